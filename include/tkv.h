@@ -395,6 +395,119 @@ TKV_API tkv_status tkv_classify(int32_t batch, const double* scores, const uint8
 TKV_API tkv_status tkv_quantize_rows(const void* x, int32_t kv_dtype, int64_t rows, int32_t row_len,
                              int8_t* codes, void* scales, int32_t scale_dtype, tkv_stream stream);
 
+/* ---- prompts, shared prefixes and the pages behind them ------------------
+ * Stateless operators for one prompt that several chains continue: attend the
+ * prompt, fork its pages, decode over the shared pages, compact what eviction
+ * (Methodology 1, T3) left, free what is done. All are enqueued on `stream`,
+ * touch only the buffers they are given and may be captured into a graph;
+ * calls that overlap on the GPU need scratch buffers of their own. Pool, page
+ * table and slot masks are those of tkv_paged_attention. */
+
+/* Causal attention over packed prompts: token i of a sequence with k_len keys
+ * and q_len queries sees keys 0 .. i + k_len - q_len (its own keys end at the
+ * last query, so keys ahead of the queries are an already cached part):
+ *   out_i = sum_j softmax_j(q_i . k_j / sqrt(d)) v_j.
+ * It is the prefill of the cache tkv_append fills (Problem statement; the
+ * paper scores decode steps only, so no score is formed).
+ *   q_lens, k_lens  HOST int32 [batch], 0 <= q_len <= k_len; batch 1 .. 64
+ *   q    device [sum q_len][Hq][d], consecutive tokens q_stride elements apart
+ *   k, v device [sum k_len][Hkv][d], tokens k_stride / v_stride elements apart
+ *   out  device [sum q_len][Hq][d], tokens out_stride elements apart
+ * Strides let q, k and v be views of one fused projection; they are multiples
+ * of 16 bytes and all four pointers are 16-byte aligned. Hq = 1 .. 64 times
+ * Hkv, d 64 or 128, F32 or BF16 (products of BF16 accumulate in fp32; the
+ * softmax weights are rounded to BF16 for the product with V). A NaN or
+ * infinity in K or V reaches exactly the rows that see it.
+ *   scratch  device, tkv_prompt_attention_scratch_size bytes (256-aligned;
+ *            may be NULL when that is 0): partials of calls with too few rows
+ *            to fill the device, whose keys are split
+ *   status   device int32 or NULL: set to 1 (never cleared) if a bounded
+ *            device wait gave up; the rows concerned are not valid then */
+TKV_API tkv_status tkv_prompt_attention_scratch_size(int32_t batch, const int32_t* q_lens, const int32_t* k_lens,
+                                                     int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                                     int32_t kv_dtype, size_t* scratch_bytes);
+TKV_API tkv_status tkv_prompt_attention(int32_t batch, const int32_t* q_lens, const int32_t* k_lens, int32_t n_q_heads,
+                                        int32_t n_kv_heads, int32_t head_dim, int32_t kv_dtype, const void* q,
+                                        int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                        int64_t v_stride, void* out, int64_t out_stride, void* scratch,
+                                        size_t scratch_bytes, int32_t* status, tkv_stream stream);
+
+/* tkv_paged_attention for sequences whose first shared_pages pages are the
+ * same (row 0 of the table is read for them): the prefix is read once for the
+ * whole batch, each sequence's own pages once, and the parts are joined.
+ * Arguments are those of tkv_paged_attention, except:
+ *   pool_pages   pages of the pool; a listed id outside reads as an empty page
+ *   page_counts  HOST int32 [B], shared_pages <= count <= max_pages (0 pages: output 0)
+ *   n_q_heads    1 .. 64 times n_kv_heads
+ *   alpha_sum    as there, for the slots behind the prefix only (a shared
+ *                prefix is a prompt and so protected, Methodology 1: its
+ *                tokens need no score); the prefix's entries are not touched
+ *   scratch      tkv_shared_prefix_attention_scratch_size bytes (256-aligned)
+ *   status       as for tkv_prompt_attention
+ * Empty slots may hold any bits. A sequence without a valid slot gives 0. */
+TKV_API tkv_status tkv_shared_prefix_attention_scratch_size(int32_t batch, int32_t n_q_heads, int32_t n_kv_heads,
+                                                            int32_t head_dim, int32_t kv_dtype,
+                                                            const int32_t* page_counts, int32_t max_pages,
+                                                            int32_t shared_pages, int32_t want_alpha,
+                                                            size_t* scratch_bytes);
+TKV_API tkv_status tkv_shared_prefix_attention(int32_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                               int32_t kv_dtype, const void* q, const void* pool, int64_t pool_pages,
+                                               const int32_t* page_table, const uint32_t* slot_mask,
+                                               const int32_t* page_counts, int32_t max_pages, int32_t shared_pages,
+                                               void* out, float* alpha_sum, void* scratch, size_t scratch_bytes,
+                                               int32_t* status, tkv_stream stream);
+
+/* The page operators work on
+ *   pool        device [n_layers][pool_pages][Hkv][2][16][d] (16-byte aligned)
+ *   page_table  device int32 [rows][max_pages], max_pages <= 16384
+ *   page_counts HOST int32 [rows]: entries in use per row
+ *   page_refs   device int32 [pool_pages]: rows that list a page, 0 = free
+ *   slot_mask   device uint32 [pool_pages], positions device int32
+ *               [pool_pages][16] or NULL (the position each slot holds)
+ * and up to 64 sequences per call. The paper fixes no allocator; a new page is
+ * the lowest free id, as in the handle's slot rule. */
+
+/* Forks row parents[i] into the empty row children[i] (HOST int32 [n_forks];
+ * children distinct, none a parent; page_counts[child] == 0). share != 0: the
+ * child lists the parent's pages (counted once more), but a last page that
+ * still has free slots is copied, so that both can append. share == 0: every
+ * page is copied. Copies take K/V of all layers, mask and positions. The
+ * child's count is the parent's. *status (device) becomes 0; or the number of
+ * pages lacking; or -1 if a parent's row lists a page that is not held. If it
+ * is not 0 nothing else has changed. */
+TKV_API tkv_status tkv_fork_sequences_scratch_size(int32_t rows, int32_t max_pages, const int32_t* page_counts,
+                                                   int32_t n_forks, const int32_t* parents, const int32_t* children,
+                                                   int32_t share, size_t* scratch_bytes);
+TKV_API tkv_status tkv_fork_sequences(void* pool, int32_t n_layers, int64_t pool_pages, int32_t n_kv_heads,
+                                      int32_t head_dim, int32_t kv_dtype, int32_t* page_table, int32_t rows,
+                                      int32_t max_pages, const int32_t* page_counts, int32_t* page_refs,
+                                      uint32_t* slot_mask, int32_t* positions, int32_t n_forks, const int32_t* parents,
+                                      const int32_t* children, int32_t share, void* scratch, size_t scratch_bytes,
+                                      int32_t* status, tkv_stream stream);
+
+/* Frees rows seqs[i] (HOST int32 [n_seqs], distinct): every page they list is
+ * counted once less, a page at 0 is free and its mask 0, and the rows' entries
+ * become -1. *status (device) becomes 0, or -1 if a row listed a page that was
+ * not held (that entry is dropped). */
+TKV_API tkv_status tkv_free_sequences(int32_t* page_table, int32_t rows, int32_t max_pages, const int32_t* page_counts,
+                                      int64_t pool_pages, int32_t* page_refs, uint32_t* slot_mask, int32_t n_seqs,
+                                      const int32_t* seqs, int32_t* status, tkv_stream stream);
+
+/* Compacts every row after tokens left it (Methodology 1, T3): of the pages a
+ * row lists alone, the first ceil(tokens / 16) stay and the valid slots of the
+ * others, in order, move into their holes, in order; the emptied pages are
+ * freed (mask 0, positions -1, count 0) and leave the row, whose freed entries
+ * become -1. Pages listed by other rows too stay as they are. page_refs NULL:
+ * no page is shared. new_counts device int32 [rows]: entries left, or -1 for a
+ * row that lists a page that is not held (that row is not changed). */
+TKV_API tkv_status tkv_compact_sequences_scratch_size(int32_t rows, int32_t max_pages, const int32_t* page_counts,
+                                                      size_t* scratch_bytes);
+TKV_API tkv_status tkv_compact_sequences(void* pool, int32_t n_layers, int64_t pool_pages, int32_t n_kv_heads,
+                                         int32_t head_dim, int32_t kv_dtype, int32_t* page_table, int32_t rows,
+                                         int32_t max_pages, const int32_t* page_counts, int32_t* page_refs,
+                                         uint32_t* slot_mask, int32_t* positions, int32_t* new_counts, void* scratch,
+                                         size_t scratch_bytes, tkv_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -90,6 +90,20 @@ _SIGS = {
     "tkv_classify_scratch_size": [c_i32, c_i64, ctypes.POINTER(c_sz)],
     "tkv_classify": [c_i32, c_vp, c_vp, c_vp, c_i64, c_vp, c_i32, c_i32, c_vp, c_sz, c_vp],
     "tkv_quantize_rows": [c_vp, c_i32, c_i64, c_i32, c_vp, c_vp, c_i32, c_vp],
+    "tkv_prompt_attention_scratch_size": [c_i32, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, ctypes.POINTER(c_sz)],
+    "tkv_prompt_attention": [c_i32, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64,
+                             c_vp, c_i64, c_vp, c_sz, c_vp, c_vp],
+    "tkv_shared_prefix_attention_scratch_size": [c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_i32, c_i32, c_i32,
+                                                 ctypes.POINTER(c_sz)],
+    "tkv_shared_prefix_attention": [c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_i64, c_vp, c_vp, c_vp, c_i32,
+                                    c_i32, c_vp, c_vp, c_vp, c_sz, c_vp, c_vp],
+    "tkv_fork_sequences_scratch_size": [c_i32, c_i32, c_vp, c_i32, c_vp, c_vp, c_i32, ctypes.POINTER(c_sz)],
+    "tkv_fork_sequences": [c_vp, c_i32, c_i64, c_i32, c_i32, c_i32, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_i32,
+                           c_vp, c_vp, c_i32, c_vp, c_sz, c_vp, c_vp],
+    "tkv_free_sequences": [c_vp, c_i32, c_i32, c_vp, c_i64, c_vp, c_vp, c_i32, c_vp, c_vp, c_vp],
+    "tkv_compact_sequences_scratch_size": [c_i32, c_i32, c_vp, ctypes.POINTER(c_sz)],
+    "tkv_compact_sequences": [c_vp, c_i32, c_i64, c_i32, c_i32, c_i32, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp,
+                              c_vp, c_vp, c_sz, c_vp],
 }
 
 _lib = None

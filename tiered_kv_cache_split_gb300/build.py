@@ -20,7 +20,7 @@ BUILD = os.path.join(HERE, "_build")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libtkv.so")
 LIB_DEBUG = os.path.join(HERE, "libtkv_debug.so")
-SOURCES = ["attention.cu", "classify.cu", "movement.cu", "runtime.cu"]
+SOURCES = ["attention.cu", "classify.cu", "movement.cu", "pages.cu", "runtime.cu", "tile_attention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I" + INCLUDE, "-I" + CSRC]
@@ -46,7 +46,8 @@ def build(verbose: bool = False, force: bool = False, debug: bool = False) -> st
     lib = LIB_DEBUG if debug else LIB
     flags = FLAGS + (["-DTKV_DEBUG"] if debug else [])
     os.makedirs(out_dir, exist_ok=True)
-    headers = [os.path.join(CSRC, "tkv_internal.h"), os.path.join(INCLUDE, "tkv.h")]
+    headers = [os.path.join(CSRC, "tkv_internal.h"), os.path.join(CSRC, "tile_attention.h"),
+               os.path.join(INCLUDE, "tkv.h")]
     jobs = []
     for s in SOURCES:
         src = os.path.join(CSRC, s)

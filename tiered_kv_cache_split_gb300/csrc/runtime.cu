@@ -325,6 +325,20 @@ tkv_status fail_cuda(tkv_ctx* h, const char* what, cudaError_t e) {
   return fail(h, TKV_ERR_CUDA, "%s failed: %s", what, cudaGetErrorString(e));
 }
 
+}  // namespace
+
+int tkv::report(int status, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  std::vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  g_last_error = buf;
+  return status;
+}
+
+namespace {
+
 // ---- host-side fault injection (tkv_test_inject_fault, TKV_FAULT)
 
 // Set-up calls of the next tkv_create until one is reported as failed (0: off).

@@ -1,0 +1,642 @@
+// Prompt attention and shared-prefix decode attention: planning, the C ABI, the
+// fp32 kernel and the merge of partials (see tile_attention.h for the terms).
+//
+// For a row with logits l_j = q . k_j log2(e) / sqrt(d) over its keys,
+//   m = max l_j,  Z = sum 2^(l_j - m),  O = sum 2^(l_j - m) v_j,  out = O / Z,
+// all of it in one pass over the keys: when a block raises m, Z and O are
+// scaled by 2^(m_old - m_new). Partials of disjoint key ranges join the same
+// way. A row without a key has m = -inf, Z = 0 and gives 0.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "tile_attention.h"
+#include "tkv.h"
+
+namespace tkv {
+namespace {
+
+constexpr int kFmaThreads = 256;
+constexpr int kFmaRows = 64;   // rows of a tile
+constexpr int kFmaKeys = 64;   // keys staged at once (half a key block)
+constexpr int kSms = 152;      // SMs of a GB300: what the plan fills (results do not depend on the device)
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xffff0000u));
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  uint2 w;
+  w.x = *reinterpret_cast<const uint32_t*>(&a);
+  w.y = *reinterpret_cast<const uint32_t*>(&b);
+  *reinterpret_cast<uint2*>(p) = w;
+}
+__device__ __forceinline__ bool finite1(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
+
+// fp32 FMA kernel: 64 rows x 64 keys at a time, 256 threads as 16 x 16, each
+// with a 4 x 4 patch of S and 4 rows x D / 16 columns of O.
+template <typename T, int D>
+__global__ void __launch_bounds__(kFmaThreads) tile_fma_kernel(const __grid_constant__ TileParams p) {
+  constexpr int LD = D + 4, LP = kFmaKeys + 4, C4 = D / 4, NC = D / 64;
+  extern __shared__ float4 smem4[];
+  float* sq = reinterpret_cast<float*>(smem4);
+  float* sk = sq + kFmaRows * LD;
+  float* sv = sk + kFmaKeys * LD;
+  float* sp = sv + kFmaKeys * LD;
+  __shared__ int64_t s_page[kFmaKeys / kPage];   // page of each 16 keys of the stage, -1: none
+  __shared__ uint32_t s_bits[kFmaKeys / kPage];  // its valid slots
+  // keys that only some rows of the tile see and whose V row is not finite
+  __shared__ uint32_t s_flag[kFmaRows / 32 + 1];
+
+  const TileUnit t = tile_unit(p, blockIdx.x);
+  const TileSeg& sg = p.seg[t.seg];
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const T* q = static_cast<const T*>(p.q);
+  const int G = p.G;
+
+  for (int i = tid; i < kFmaRows * C4; i += kFmaThreads) {
+    const int r = i / C4, c = i % C4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < t.rows) {
+      const int row = t.row0 + r;
+      x = load4(q + static_cast<int64_t>(sg.tok0 + row / G) * p.q_stride + (t.h * G + row % G) * D + c * 4);
+    }
+    store4(sq + r * LD + c * 4, x);
+  }
+  if (tid <= kFmaRows / 32) s_flag[tid] = 0;
+
+  int lim[4];
+  float m[4], z[4], o[4][NC * 4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    lim[i] = tile_row_limit(p, sg, t.row0 + min(ty * 4 + i, t.rows - 1));
+    m[i] = -INFINITY;
+    z[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < NC * 4; ++c) o[i][c] = 0.f;
+  }
+  const int lim_first = tile_row_limit(p, sg, t.row0);
+  const int kend = min(t.j1 * kKeyBlock, tile_row_limit(p, sg, t.row0 + t.rows - 1));
+
+  for (int k0 = t.j0 * kKeyBlock; k0 < kend; k0 += kFmaKeys) {
+    __syncthreads();
+    if (tid < kFmaKeys / kPage) {
+      const int pg = k0 / kPage + tid;
+      int64_t id = -1;
+      uint32_t bits = 0;
+      if (p.paged) {
+        if (pg < sg.nkeys / kPage) {
+          id = p.table[sg.key0 + pg];
+          if (id < 0 || id >= p.pages) id = -1;
+          if (id >= 0) bits = p.mask[id] & 0xffffu;
+        }
+      } else {
+        const int left = sg.nkeys - pg * kPage;
+        bits = left >= kPage ? 0xffffu : left > 0 ? (1u << left) - 1 : 0u;
+      }
+      s_page[tid] = id;
+      s_bits[tid] = bits;
+    }
+    __syncthreads();
+    for (int i = tid; i < kFmaKeys * C4; i += kFmaThreads) {
+      const int kk = i / C4, c = i % C4;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+      if ((s_bits[kk / kPage] >> (kk % kPage)) & 1u) {
+        if (p.paged) {
+          const T* at = static_cast<const T*>(p.pool) + ((s_page[kk / kPage] * p.Hkv + t.h) * 2 * kPage + kk % kPage) * D + c * 4;
+          a = load4(at);
+          b = load4(at + kPage * D);
+        } else {
+          const int64_t tok = sg.key0 + k0 + kk;
+          a = load4(static_cast<const T*>(p.k) + tok * p.k_stride + t.h * D + c * 4);
+          b = load4(static_cast<const T*>(p.v) + tok * p.v_stride + t.h * D + c * 4);
+        }
+        const int part = k0 + kk - lim_first;  // >= 0: the tile's first row does not see this key
+        if (part >= 0 && !(finite1(b.x) && finite1(b.y) && finite1(b.z) && finite1(b.w))) {
+          // 0 * inf must not reach the rows that do not see the key: the rows that do get it below
+          if (!finite1(b.x)) b.x = 0.f;
+          if (!finite1(b.y)) b.y = 0.f;
+          if (!finite1(b.z)) b.z = 0.f;
+          if (!finite1(b.w)) b.w = 0.f;
+          if (part < kFmaRows) atomicOr(&s_flag[part >> 5], 1u << (part & 31));
+        }
+      }
+      store4(sk + kk * LD + c * 4, a);
+      store4(sv + kk * LD + c * 4, b);
+    }
+    __syncthreads();
+    float s[4][4] = {};
+#pragma unroll 4
+    for (int c = 0; c < C4; ++c) {
+      float4 a[4], b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = load4(sq + (ty * 4 + i) * LD + c * 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = load4(sk + (tx + 16 * j) * LD + c * 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
+          s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
+          s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
+          s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+        }
+    }
+    // key tx + 16 j is slot tx of page j of the stage
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool seen = ((s_bits[j] >> tx) & 1u) && k0 + 16 * j + tx < lim[i];
+        s[i][j] = seen ? s[i][j] * p.qscale : -INFINITY;
+        top = fmaxf(top, s[i][j]);
+      }
+#pragma unroll
+      for (int d = 8; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      const float mn = fmaxf(m[i], top);
+      const float base = mn == -INFINITY ? 0.f : mn;
+      const float f = exp2f(m[i] - base);
+      m[i] = mn;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (sg.spill0 >= 0 && ty * 4 + i < t.rows && k0 + 16 * j + tx < sg.nkeys)
+          p.spill[sg.spill0 + static_cast<int64_t>(t.h * G + (t.row0 + ty * 4 + i) % G) * sg.nkeys + k0 + 16 * j + tx] = s[i][j];
+        const float e = exp2f(s[i][j] - base);
+        sum += e;
+        sp[(ty * 4 + i) * LP + tx + 16 * j] = e;
+      }
+#pragma unroll
+      for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      z[i] = z[i] * f + sum;
+#pragma unroll
+      for (int c = 0; c < NC * 4; ++c) o[i][c] *= f;
+    }
+    __syncwarp();  // a row's weights are written and read by the same half warp
+#pragma unroll 4
+    for (int kk = 0; kk < kFmaKeys; ++kk) {
+      float4 v[NC];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) v[c] = load4(sv + kk * LD + c * 64 + tx * 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float e = sp[(ty * 4 + i) * LP + kk];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          o[i][c * 4 + 0] = fmaf(e, v[c].x, o[i][c * 4 + 0]);
+          o[i][c * 4 + 1] = fmaf(e, v[c].y, o[i][c * 4 + 1]);
+          o[i][c * 4 + 2] = fmaf(e, v[c].z, o[i][c * 4 + 2]);
+          o[i][c * 4 + 3] = fmaf(e, v[c].w, o[i][c * 4 + 3]);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  // the non-finite values of partly seen keys, for the rows that see them
+  for (int part = 0; part < kFmaRows; ++part) {
+    if (!((s_flag[part >> 5] >> (part & 31)) & 1u)) continue;
+    const int64_t tok = sg.key0 + lim_first + part;
+#pragma unroll
+    for (int c = 0; c < NC * 4; ++c) {
+      const int col = (c / 4) * 64 + tx * 4 + c % 4;
+      const float x = static_cast<float>(static_cast<const T*>(p.v)[tok * p.v_stride + t.h * D + col]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (lim_first + part < lim[i] && !finite1(x)) o[i][c] += x;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = ty * 4 + i, row = t.row0 + r;
+    if (r >= t.rows) continue;
+    if (p.direct) {
+      const float inv = z[i] > 0.f || z[i] != z[i] ? 1.f / z[i] : 0.f;
+      T* at = static_cast<T*>(p.out) + static_cast<int64_t>(sg.tok0 + row / G) * p.out_stride + (t.h * G + row % G) * D + tx * 4;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        store4(at + c * 64, make_float4(o[i][c * 4] * inv, o[i][c * 4 + 1] * inv, o[i][c * 4 + 2] * inv, o[i][c * 4 + 3] * inv));
+    } else {
+      const int64_t pr = tile_part_row(p, sg, t.grp, t.h, t.split, 0) + r;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        store4(p.part_o + pr * D + c * 64 + tx * 4, make_float4(o[i][c * 4], o[i][c * 4 + 1], o[i][c * 4 + 2], o[i][c * 4 + 3]));
+      if (tx == 0) {
+        p.part_m[pr] = m[i];
+        p.part_z[pr] = z[i];
+      }
+    }
+  }
+}
+
+// ---- merge: one CTA per (query token, KV head), one warp per query head at a
+// time; out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) Z_i. A decode token of
+// the shared-prefix form joins the prefix's partials and its own, and adds the
+// softmax weights of its own slots, summed over the G heads, to alpha.
+constexpr int kMergeThreads = 256;
+
+struct PartList {
+  int64_t first, step;  // partial row i is first + i * step
+  int n;
+};
+
+__device__ __forceinline__ PartList part_list(const TileParams& p, const TileSeg& s, int h, int row) {
+  PartList l;
+  if (s.pair) {
+    l.first = tile_part_row(p, s, 0, h, 0, 0) + row;
+    l.step = s.part_rows;
+    l.n = s.splits * 2;
+  } else {
+    const int per = p.tile_rows * p.tpg, grp = row / per, tile = row % per / p.tile_rows;
+    l.first = tile_part_row(p, s, grp, h, 0, tile) + row % p.tile_rows;
+    l.step = static_cast<int64_t>(p.tpg) * s.part_rows;
+    l.n = s.splits;
+  }
+  return l;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kMergeThreads) tile_merge_kernel(const __grid_constant__ TileParams p) {
+  constexpr int E = D / 32;
+  __shared__ float s_m[kMaxGroup], s_inv[kMaxGroup];
+  const int tok = blockIdx.x, h = blockIdx.y, G = p.G;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int own;  // the token's segment (paged: segment 0 is the prefix of all tokens)
+  if (p.paged) {
+    own = tok + 1;
+  } else {
+    int lo = 0, hi = p.nseg - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.seg[mid].tok0 <= tok) lo = mid; else hi = mid - 1;
+    }
+    own = lo;
+  }
+  for (int g = warp; g < G; g += kMergeThreads / 32) {
+    PartList l[2];
+    int nl = 0;
+    if (p.paged && p.seg[0].splits > 0) l[nl++] = part_list(p, p.seg[0], h, tok * G + g);
+    const TileSeg& so = p.seg[own];
+    if (so.splits > 0) l[nl++] = part_list(p, so, h, (tok - so.tok0) * G + g);
+    float M = -INFINITY;
+    for (int a = 0; a < nl; ++a)
+      for (int i = lane; i < l[a].n; i += 32) M = fmaxf(M, p.part_m[l[a].first + i * l[a].step]);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    const float base = M == -INFINITY ? 0.f : M;
+    float Z = 0.f, acc[E] = {};
+    for (int a = 0; a < nl; ++a)
+      for (int i0 = 0; i0 < l[a].n; i0 += 32) {
+        const int mine = i0 + lane;
+        float w = 0.f, wz = 0.f;
+        if (mine < l[a].n) {
+          const int64_t r = l[a].first + mine * l[a].step;
+          w = exp2f(p.part_m[r] - base);
+          wz = w * p.part_z[r];
+        }
+        Z += wz;
+        const int n = min(32, l[a].n - i0);
+        for (int i = 0; i < n; ++i) {
+          const float wi = __shfl_sync(0xffffffffu, w, i);
+          const float* at = p.part_o + (l[a].first + (i0 + i) * l[a].step) * D + lane * E;
+          if (wi == 0.f) continue;  // an empty range's O is all zero
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(wi, at[e], acc[e]);
+        }
+      }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) Z += __shfl_xor_sync(0xffffffffu, Z, d);
+    const float inv = Z > 0.f || Z != Z ? 1.f / Z : 0.f;
+    T* at = static_cast<T*>(p.out) + static_cast<int64_t>(tok) * p.out_stride + (h * G + g) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) at[e] = static_cast<T>(acc[e] * inv);
+    if (lane == 0) {
+      s_m[g] = base;
+      s_inv[g] = inv;
+    }
+  }
+  if (!p.alpha || p.seg[own].splits == 0) return;
+  __syncthreads();
+  const TileSeg& so = p.seg[own];
+  const float* l = p.spill + so.spill0 + static_cast<int64_t>(h) * G * so.nkeys;
+  float* at = p.alpha + (static_cast<int64_t>(tok) * p.Hkv + h) * p.alpha_stride_h + p.alpha_first;
+  for (int i = threadIdx.x * 4; i < so.nkeys; i += kMergeThreads * 4) {
+    float4 sum = *reinterpret_cast<const float4*>(at + i);
+    for (int g = 0; g < G; ++g) {
+      const float4 x = *reinterpret_cast<const float4*>(l + static_cast<int64_t>(g) * so.nkeys + i);
+      sum.x += exp2f(x.x - s_m[g]) * s_inv[g];
+      sum.y += exp2f(x.y - s_m[g]) * s_inv[g];
+      sum.z += exp2f(x.z - s_m[g]) * s_inv[g];
+      sum.w += exp2f(x.w - s_m[g]) * s_inv[g];
+    }
+    *reinterpret_cast<float4*>(at + i) = sum;
+  }
+}
+
+// ---- planning (host)
+
+struct TilePlan {
+  int64_t part_rows, spill;  // partial rows, spilled floats
+  int64_t units;
+};
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct TileShape {
+  int rows, tpg, slots, min_blocks;
+};
+TileShape tile_shape(int) { return {kFmaRows, 1, 2 * kSms, 2}; }
+
+int64_t seg_groups(const TileSeg& s, int G, const TileShape& ts) {
+  return ceil_div(static_cast<int64_t>(s.ntok) * G, static_cast<int64_t>(ts.rows) * ts.tpg);
+}
+
+// Key blocks of all units of a segment for one KV head.
+int64_t seg_blocks(const TileParams& p, const TileSeg& s, const TileShape& ts) {
+  const int64_t g = seg_groups(s, p.G, ts);
+  if (!p.causal) return g * ceil_div(s.nkeys, kKeyBlock);
+  int64_t n = 0;
+  const int64_t per = static_cast<int64_t>(ts.rows) * ts.tpg, rows = static_cast<int64_t>(s.ntok) * p.G;
+  if (g > 4096) return g * ceil_div(s.nkeys, kKeyBlock);  // far more units than SMs: the exact count decides nothing
+  for (int64_t i = 0; i < g; ++i) {
+    const int64_t last = std::min((i + 1) * per, rows) - 1;
+    n += ceil_div(s.see0 + last / p.G + 1, kKeyBlock);
+  }
+  return n;
+}
+
+// Cuts the segments (tok0, ntok, nkeys, see0 set) into units. Where the rows
+// alone give a prompt fewer units than the device has places, and always for
+// paged segments, the keys are split too, into ranges of about equal length
+// that fill the places once, no shorter than min_blocks key blocks.
+TilePlan plan_units(TileParams& p, const TileShape& ts, bool want_spill) {
+  TilePlan out{0, 0, 0};
+  p.tile_rows = ts.rows;
+  p.tpg = ts.tpg;
+  int64_t units = 0, blocks = 0;
+  for (int i = 0; i < p.nseg; ++i) {
+    TileSeg& s = p.seg[i];
+    if (s.ntok == 0 || (s.nkeys == 0 && p.paged)) continue;
+    units += seg_groups(s, p.G, ts) * p.Hkv;
+    blocks += seg_blocks(p, s, ts) * p.Hkv;
+  }
+  int64_t per = INT32_MAX;  // key blocks per unit
+  if (p.paged || units < ts.slots) per = std::max<int64_t>(ts.min_blocks, ceil_div(blocks, ts.slots));
+  bool split = p.paged;
+  for (int i = 0; i < p.nseg; ++i)
+    if (p.seg[i].ntok && ceil_div(p.seg[i].nkeys, kKeyBlock) > per) split = true;
+  p.direct = !split;
+  for (int i = 0; i < p.nseg; ++i) {
+    TileSeg& s = p.seg[i];
+    s.unit0 = static_cast<int32_t>(out.units);
+    s.part0 = out.part_rows;
+    s.spill0 = -1;
+    s.splits = s.groups = s.part_rows = s.pair = 0;
+    if (s.ntok == 0 || (s.nkeys == 0 && p.paged)) continue;
+    s.groups = static_cast<int32_t>(seg_groups(s, p.G, ts));
+    s.splits = split ? static_cast<int32_t>(std::max<int64_t>(1, ceil_div(ceil_div(s.nkeys, kKeyBlock), per))) : 1;
+    const int64_t rows = static_cast<int64_t>(s.ntok) * p.G;
+    s.pair = !p.direct && ts.tpg == 2 && rows <= ts.rows;
+    s.part_rows = static_cast<int32_t>(std::min<int64_t>(ts.rows, rows));
+    const int64_t n = static_cast<int64_t>(s.groups) * p.Hkv * s.splits;
+    out.units += n;
+    if (!p.direct) out.part_rows += n * ts.tpg * s.part_rows;
+    if (want_spill && p.paged && i > 0) {
+      s.spill0 = out.spill;
+      out.spill += static_cast<int64_t>(s.nkeys) * p.Hq;
+    }
+  }
+  return out;
+}
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct TileScratch {
+  size_t o_m, o_z, o_spill, bytes;
+};
+TileScratch tile_scratch(const TilePlan& pl, int D) {
+  TileScratch s;
+  s.o_m = align256(static_cast<size_t>(pl.part_rows) * D * 4);
+  s.o_z = s.o_m + align256(static_cast<size_t>(pl.part_rows) * 4);
+  s.o_spill = s.o_z + align256(static_cast<size_t>(pl.part_rows) * 4);
+  s.bytes = s.o_spill + align256(static_cast<size_t>(pl.spill) * 4);
+  return s;
+}
+
+int check_heads(int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype) {
+  if (Hkv < 1 || Hq < 1 || Hkv > 65535 || Hq % Hkv || Hq / Hkv > kMaxGroup)
+    return report(TKV_ERR_INVALID_ARG, "n_q_heads must be 1 to %d times n_kv_heads", kMaxGroup);
+  if (D != 64 && D != 128) return report(TKV_ERR_INVALID_ARG, "head_dim must be 64 or 128");
+  if (dtype != TKV_DTYPE_F32 && dtype != TKV_DTYPE_BF16) return report(TKV_ERR_INVALID_ARG, "kv_dtype");
+  return TKV_OK;
+}
+
+int plan_prompt(TileParams& p, TilePlan* plan, int32_t batch, const int32_t* q_lens, const int32_t* k_lens, int32_t Hq,
+                int32_t Hkv, int32_t D, int32_t dtype, int64_t* tokens, int64_t* keys) {
+  if (batch < 1 || batch > kMaxBatch) return report(TKV_ERR_INVALID_ARG, "batch must be 1 to %d", kMaxBatch);
+  if (int st = check_heads(Hq, Hkv, D, dtype)) return st;
+  if (!q_lens || !k_lens) return report(TKV_ERR_INVALID_ARG, "null pointer");
+  p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv;
+  p.causal = 1;
+  p.nseg = batch;
+  p.qscale = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
+  int64_t tq = 0, tk = 0;
+  for (int i = 0; i < batch; ++i) {
+    if (q_lens[i] < 0 || k_lens[i] < q_lens[i]) return report(TKV_ERR_INVALID_ARG, "sequence %d: 0 <= q_len <= k_len", i);
+    p.seg[i].tok0 = static_cast<int32_t>(tq);
+    p.seg[i].ntok = q_lens[i];
+    p.seg[i].key0 = tk;
+    p.seg[i].nkeys = k_lens[i];
+    p.seg[i].see0 = k_lens[i] - q_lens[i];
+    tq += q_lens[i];
+    tk += k_lens[i];
+    if (tq * p.G > INT32_MAX || tk > INT32_MAX - 2 * kKeyBlock)
+      return report(TKV_ERR_INVALID_ARG, "more than 2^31 rows or keys in one call");
+  }
+  *tokens = tq;
+  *keys = tk;
+  *plan = plan_units(p, tile_shape(dtype), false);
+  if (plan->units > INT32_MAX) return report(TKV_ERR_INVALID_ARG, "more than 2^31 units of work in one call");
+  p.units = static_cast<int32_t>(plan->units);
+  return TKV_OK;
+}
+
+int plan_shared(TileParams& p, TilePlan* plan, int32_t batch, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype,
+                const int32_t* page_counts, int32_t max_pages, int32_t shared_pages, int want_alpha) {
+  if (batch < 1 || batch > kMaxBatch) return report(TKV_ERR_INVALID_ARG, "batch must be 1 to %d", kMaxBatch);
+  if (int st = check_heads(Hq, Hkv, D, dtype)) return st;
+  if (max_pages < 1 || max_pages > kMaxSeqPages) return report(TKV_ERR_INVALID_ARG, "max_pages must be 1 to %d", kMaxSeqPages);
+  if (!page_counts) return report(TKV_ERR_INVALID_ARG, "null pointer");
+  if (shared_pages < 0 || shared_pages > max_pages) return report(TKV_ERR_INVALID_ARG, "shared_pages out of 0..max_pages");
+  p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv;
+  p.paged = 1;
+  p.nseg = batch + 1;
+  p.qscale = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
+  p.seg[0].ntok = batch;
+  p.seg[0].nkeys = shared_pages * kPage;
+  for (int b = 0; b < batch; ++b) {
+    if (page_counts[b] < shared_pages || page_counts[b] > max_pages)
+      return report(TKV_ERR_INVALID_ARG, "page_counts[%d] out of shared_pages..max_pages", b);
+    TileSeg& s = p.seg[b + 1];
+    s.tok0 = b;
+    s.ntok = 1;
+    s.key0 = static_cast<int64_t>(b) * max_pages + shared_pages;
+    s.nkeys = (page_counts[b] - shared_pages) * kPage;
+  }
+  *plan = plan_units(p, tile_shape(dtype), want_alpha != 0);
+  p.units = static_cast<int32_t>(plan->units);
+  return TKV_OK;
+}
+
+template <typename T, int D>
+cudaError_t launch_fma(const TileParams& p, cudaStream_t s) {
+  constexpr int bytes = ((kFmaRows + 2 * kFmaKeys) * (D + 4) + kFmaRows * (kFmaKeys + 4)) * 4;
+  cudaError_t e = cudaFuncSetAttribute(tile_fma_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  tile_fma_kernel<T, D><<<static_cast<unsigned>(p.units), kFmaThreads, bytes, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_tiles(const TileParams& p, int D, int tokens, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  if (p.units > 0) {
+    e = D == 64 ? launch_fma<T, 64>(p, s) : launch_fma<T, 128>(p, s);
+    if (e != cudaSuccess) return e;
+  }
+  if (!p.direct && tokens > 0) {
+    const dim3 grid(tokens, p.Hkv);
+    if (D == 64) tile_merge_kernel<T, 64><<<grid, kMergeThreads, 0, s>>>(p);
+    else tile_merge_kernel<T, 128><<<grid, kMergeThreads, 0, s>>>(p);
+    e = cudaGetLastError();
+  }
+  return e;
+}
+
+cudaError_t launch_dtype(const TileParams& p, int dtype, int D, int tokens, cudaStream_t s) {
+  return dtype == TKV_DTYPE_BF16 ? launch_tiles<__nv_bfloat16>(p, D, tokens, s) : launch_tiles<float>(p, D, tokens, s);
+}
+
+bool misaligned(const void* ptr, size_t to) { return reinterpret_cast<uintptr_t>(ptr) % to != 0; }
+
+int bind_scratch(TileParams& p, const TilePlan& plan, int D, void* scratch, size_t bytes) {
+  const TileScratch s = tile_scratch(plan, D);
+  if (s.bytes == 0) return TKV_OK;
+  if (!scratch) return report(TKV_ERR_INVALID_ARG, "null scratch: need %zu bytes", s.bytes);
+  if (bytes < s.bytes) return report(TKV_ERR_CAPACITY, "scratch too small: need %zu bytes", s.bytes);
+  if (misaligned(scratch, 256)) return report(TKV_ERR_INVALID_ARG, "scratch not 256-byte aligned");
+  char* at = static_cast<char*>(scratch);
+  p.part_o = reinterpret_cast<float*>(at);
+  p.part_m = reinterpret_cast<float*>(at + s.o_m);
+  p.part_z = reinterpret_cast<float*>(at + s.o_z);
+  p.spill = reinterpret_cast<float*>(at + s.o_spill);
+  return TKV_OK;
+}
+
+}  // namespace
+}  // namespace tkv
+
+using namespace tkv;
+
+extern "C" {
+
+tkv_status tkv_prompt_attention_scratch_size(int32_t batch, const int32_t* q_lens, const int32_t* k_lens,
+                                             int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t kv_dtype,
+                                             size_t* scratch_bytes) {
+  if (!scratch_bytes) return tkv_status(report(TKV_ERR_INVALID_ARG, "null pointer"));
+  TileParams p{};
+  TilePlan plan;
+  int64_t tq, tk;
+  if (int st = plan_prompt(p, &plan, batch, q_lens, k_lens, n_q_heads, n_kv_heads, head_dim, kv_dtype, &tq, &tk))
+    return tkv_status(st);
+  *scratch_bytes = tile_scratch(plan, head_dim).bytes;
+  return TKV_OK;
+}
+
+tkv_status tkv_prompt_attention(int32_t batch, const int32_t* q_lens, const int32_t* k_lens, int32_t n_q_heads,
+                                int32_t n_kv_heads, int32_t head_dim, int32_t kv_dtype, const void* q, int64_t q_stride,
+                                const void* k, int64_t k_stride, const void* v, int64_t v_stride, void* out,
+                                int64_t out_stride, void* scratch, size_t scratch_bytes, int32_t* status,
+                                tkv_stream stream) {
+  TileParams p{};
+  TilePlan plan;
+  int64_t tq, tk;
+  if (int st = plan_prompt(p, &plan, batch, q_lens, k_lens, n_q_heads, n_kv_heads, head_dim, kv_dtype, &tq, &tk))
+    return tkv_status(st);
+  if (tq == 0) return TKV_OK;
+  if (!q || !k || !v || !out) return tkv_status(report(TKV_ERR_INVALID_ARG, "null pointer"));
+  const int64_t unit = kv_dtype == TKV_DTYPE_BF16 ? 8 : 4;  // elements of 16 bytes
+  if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(out, 16))
+    return tkv_status(report(TKV_ERR_INVALID_ARG, "q, k, v and out must be 16-byte aligned"));
+  const int64_t qrow = static_cast<int64_t>(n_q_heads) * head_dim, krow = static_cast<int64_t>(n_kv_heads) * head_dim;
+  if (q_stride < qrow || out_stride < qrow || k_stride < krow || v_stride < krow || q_stride % unit || out_stride % unit ||
+      k_stride % unit || v_stride % unit || (q_stride | out_stride | k_stride | v_stride) >> 36)
+    return tkv_status(report(TKV_ERR_INVALID_ARG, "token strides must hold a token and be multiples of 16 bytes"));
+  if (int st = bind_scratch(p, plan, head_dim, scratch, scratch_bytes)) return tkv_status(st);
+  p.q = q; p.q_stride = q_stride;
+  p.k = k; p.k_stride = k_stride;
+  p.v = v; p.v_stride = v_stride;
+  p.out = out; p.out_stride = out_stride;
+  p.status = status;
+  p.wait_limit_ns = 2000000000ull;
+  const cudaError_t e = launch_dtype(p, kv_dtype, head_dim, static_cast<int>(tq), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return tkv_status(report(TKV_ERR_CUDA, "prompt attention launch failed: %s", cudaGetErrorString(e)));
+  return TKV_OK;
+}
+
+tkv_status tkv_shared_prefix_attention_scratch_size(int32_t batch, int32_t n_q_heads, int32_t n_kv_heads,
+                                                    int32_t head_dim, int32_t kv_dtype, const int32_t* page_counts,
+                                                    int32_t max_pages, int32_t shared_pages, int32_t want_alpha,
+                                                    size_t* scratch_bytes) {
+  if (!scratch_bytes) return tkv_status(report(TKV_ERR_INVALID_ARG, "null pointer"));
+  TileParams p{};
+  TilePlan plan;
+  if (int st = plan_shared(p, &plan, batch, n_q_heads, n_kv_heads, head_dim, kv_dtype, page_counts, max_pages, shared_pages,
+                           want_alpha))
+    return tkv_status(st);
+  *scratch_bytes = tile_scratch(plan, head_dim).bytes;
+  return TKV_OK;
+}
+
+tkv_status tkv_shared_prefix_attention(int32_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                       int32_t kv_dtype, const void* q, const void* pool, int64_t pool_pages,
+                                       const int32_t* page_table, const uint32_t* slot_mask, const int32_t* page_counts,
+                                       int32_t max_pages, int32_t shared_pages, void* out, float* alpha_sum,
+                                       void* scratch, size_t scratch_bytes, int32_t* status, tkv_stream stream) {
+  TileParams p{};
+  TilePlan plan;
+  if (int st = plan_shared(p, &plan, batch, n_q_heads, n_kv_heads, head_dim, kv_dtype, page_counts, max_pages, shared_pages,
+                           alpha_sum != nullptr))
+    return tkv_status(st);
+  if (!q || !pool || !page_table || !slot_mask || !out) return tkv_status(report(TKV_ERR_INVALID_ARG, "null pointer"));
+  if (pool_pages < 1 || pool_pages > (int64_t(1) << 30) / n_kv_heads)
+    return tkv_status(report(TKV_ERR_INVALID_ARG, "pool_pages x n_kv_heads must be 1 to 2^30"));
+  if (misaligned(q, 16) || misaligned(pool, 16) || misaligned(out, 16) || misaligned(alpha_sum, 16))
+    return tkv_status(report(TKV_ERR_INVALID_ARG, "q, pool, out and alpha_sum must be 16-byte aligned"));
+  if (int st = bind_scratch(p, plan, head_dim, scratch, scratch_bytes)) return tkv_status(st);
+  p.q = q; p.q_stride = static_cast<int64_t>(n_q_heads) * head_dim;
+  p.out = out; p.out_stride = p.q_stride;
+  p.pool = pool;
+  p.pages = pool_pages;
+  p.table = page_table;
+  p.mask = slot_mask;
+  p.alpha = alpha_sum;
+  p.alpha_stride_h = static_cast<int64_t>(max_pages) * kPage;
+  p.alpha_first = static_cast<int64_t>(shared_pages) * kPage;
+  p.status = status;
+  p.wait_limit_ns = 2000000000ull;
+  const cudaError_t e = launch_dtype(p, kv_dtype, head_dim, batch, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess)
+    return tkv_status(report(TKV_ERR_CUDA, "shared-prefix attention launch failed: %s", cudaGetErrorString(e)));
+  return TKV_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,111 @@
+// Shared by the tiled attention kernels (prompt attention and shared-prefix
+// decode attention): how a call is cut into segments, units and partials.
+//
+// A SEGMENT is a run of query tokens over one list of keys: a packed prompt, a
+// prefix seen by the whole batch, or a sequence's own pages. The G query heads
+// that share a KV head are rows of one matrix, row = token * G + g, so a K / V
+// element is read once for all of them and a short segment still fills a tile.
+// A UNIT (one CTA) is (segment, row group, KV head, split): the rows of the
+// group over a range of 128-key blocks. A unit that covers all keys of its rows
+// writes the output; otherwise it writes a PARTIAL (m, Z, unnormalised O) per
+// row, in base 2, and the merge kernel joins the partials of each row.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "tkv_internal.h"
+
+namespace tkv {
+
+constexpr int kKeyBlock = 128;              // keys of a block, the unit of splitting
+constexpr int kMaxSegs = kMaxBatch + 1;
+constexpr int kMaxGroup = 64;               // query heads per KV head
+
+struct TileSeg {
+  int64_t key0;      // packed: first key token; paged: first entry of its pages in the page table
+  int64_t part0;     // first partial row
+  int64_t spill0;    // first spilled logit of head 0 (row stride nkeys per query head), -1: none
+  int32_t tok0;      // first query token
+  int32_t ntok;      // query tokens
+  int32_t nkeys;     // keys (paged: 16 per page)
+  int32_t see0;      // causal: token i sees keys [0, see0 + i]
+  int32_t splits;    // key ranges per row group (0: the segment has no unit)
+  int32_t groups;    // row groups
+  int32_t unit0;     // first unit
+  int32_t part_rows; // rows per partial tile
+  int32_t pair;      // 1: one row tile, its two halves of the CTA take alternate key blocks
+};
+
+struct TileParams {
+  const void* q;
+  int64_t q_stride;            // elements from one token to the next
+  void* out;
+  int64_t out_stride;
+  const void *k, *v;           // packed keys and values [token][Hkv][D]
+  int64_t k_stride, v_stride;
+  const void* pool;            // paged: [pages][Hkv][2][16][D]
+  const int32_t* table;
+  const uint32_t* mask;
+  int64_t pages;               // pool pages: ids outside read as empty pages
+  float *part_o, *part_m, *part_z;
+  float* spill;
+  float* alpha;                // [B][Hkv][alpha slots], or null
+  int64_t alpha_stride_h;
+  int64_t alpha_first;         // slots ahead of a sequence's own pages
+  int32_t* status;             // set to 1 by a wait that gave up, or null
+  unsigned long long wait_limit_ns;
+  float qscale;                // log2(e) / sqrt(D): logits are kept in base 2
+  int32_t Hq, Hkv, G;
+  int32_t nseg, units;
+  int32_t paged, causal;
+  int32_t direct;              // 1: no splits, units write the output
+  int32_t tile_rows, tpg;      // rows of a tile, tiles of a row group
+  TileSeg seg[kMaxSegs];
+};
+
+struct TileUnit {
+  int seg, h, split;
+  int grp;
+  int row0, rows;  // rows of the segment's matrix
+  int j0, j1;      // key blocks
+};
+
+// keys seen by row r of a segment
+__device__ __forceinline__ int tile_row_limit(const TileParams& p, const TileSeg& s, int row) {
+  return p.causal ? min(s.nkeys, s.see0 + row / p.G + 1) : s.nkeys;
+}
+
+__device__ __forceinline__ TileUnit tile_unit(const TileParams& p, int u) {
+  TileUnit t;
+  int lo = 0, hi = p.nseg - 1;  // last segment whose first unit is <= u (segments without units share it)
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.seg[mid].unit0 <= u) lo = mid; else hi = mid - 1;
+  }
+  t.seg = lo;
+  const TileSeg& s = p.seg[lo];
+  int r = u - s.unit0;
+  t.split = r % s.splits;
+  r /= s.splits;
+  t.h = r % p.Hkv;
+  t.grp = s.groups - 1 - r / p.Hkv;  // a causal segment's last rows see most keys: they go first
+  const int per = s.pair ? p.tile_rows : p.tile_rows * p.tpg;
+  t.row0 = t.grp * per;
+  t.rows = min(per, s.ntok * p.G - t.row0);
+  const int nb = (tile_row_limit(p, s, t.row0 + t.rows - 1) + kKeyBlock - 1) / kKeyBlock;
+  t.j0 = static_cast<int>(static_cast<int64_t>(nb) * t.split / s.splits);
+  t.j1 = static_cast<int>(static_cast<int64_t>(nb) * (t.split + 1) / s.splits);
+  return t;
+}
+
+// first partial row of tile `tile` of a unit
+__device__ __forceinline__ int64_t tile_part_row(const TileParams& p, const TileSeg& s, int grp, int h, int split, int tile) {
+  return s.part0 + (((static_cast<int64_t>(grp) * p.Hkv + h) * s.splits + split) * p.tpg + tile) * s.part_rows;
+}
+
+// tile_attention.cu
+// tile_attention_mma.cu
+cudaError_t launch_tile_mma(const TileParams& p, int D, cudaStream_t s);
+
+}  // namespace tkv

@@ -8,6 +8,9 @@
 
 namespace tkv {
 
+// runtime.cu: sets the message tkv_last_error(NULL) returns; gives back `status` (a tkv_status).
+int report(int status, const char* fmt, ...);
+
 constexpr int kPage = 16;          // tokens per page
 constexpr int kMaxBatch = 64;      // sequences per handle (kernel parameters carry per-sequence arrays)
 #ifndef TKV_ATTN_WARPS
