@@ -25,24 +25,12 @@ constexpr int kFmaKeys = 64;   // keys staged at once (half a key block)
 constexpr int kSms = 152;      // SMs of a GB300: what the plan fills (results do not depend on the device)
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                     __uint_as_float(w.y & 0xffff0000u));
-}
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-  uint2 w;
-  w.x = *reinterpret_cast<const uint32_t*>(&a);
-  w.y = *reinterpret_cast<const uint32_t*>(&b);
-  *reinterpret_cast<uint2*>(p) = w;
-}
 __device__ __forceinline__ bool finite1(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 
 // fp32 FMA kernel: 64 rows x 64 keys at a time, 256 threads as 16 x 16, each
 // with a 4 x 4 patch of S and 4 rows x D / 16 columns of O.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kFmaThreads) tile_fma_kernel(const __grid_constant__ TileParams p) {
   constexpr int LD = D + 4, LP = kFmaKeys + 4, C4 = D / 4, NC = D / 64;
   extern __shared__ float4 smem4[];
@@ -58,7 +46,7 @@ __global__ void __launch_bounds__(kFmaThreads) tile_fma_kernel(const __grid_cons
   const TileUnit t = tile_unit(p, blockIdx.x);
   const TileSeg& sg = p.seg[t.seg];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const T* q = static_cast<const T*>(p.q);
+  const float* q = static_cast<const float*>(p.q);
   const int G = p.G;
 
   for (int i = tid; i < kFmaRows * C4; i += kFmaThreads) {
@@ -110,13 +98,13 @@ __global__ void __launch_bounds__(kFmaThreads) tile_fma_kernel(const __grid_cons
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
       if ((s_bits[kk / kPage] >> (kk % kPage)) & 1u) {
         if (p.paged) {
-          const T* at = static_cast<const T*>(p.pool) + ((s_page[kk / kPage] * p.Hkv + t.h) * 2 * kPage + kk % kPage) * D + c * 4;
+          const float* at = static_cast<const float*>(p.pool) + ((s_page[kk / kPage] * p.Hkv + t.h) * 2 * kPage + kk % kPage) * D + c * 4;
           a = load4(at);
           b = load4(at + kPage * D);
         } else {
           const int64_t tok = sg.key0 + k0 + kk;
-          a = load4(static_cast<const T*>(p.k) + tok * p.k_stride + t.h * D + c * 4);
-          b = load4(static_cast<const T*>(p.v) + tok * p.v_stride + t.h * D + c * 4);
+          a = load4(static_cast<const float*>(p.k) + tok * p.k_stride + t.h * D + c * 4);
+          b = load4(static_cast<const float*>(p.v) + tok * p.v_stride + t.h * D + c * 4);
         }
         const int part = k0 + kk - lim_first;  // >= 0: the tile's first row does not see this key
         if (part >= 0 && !(finite1(b.x) && finite1(b.y) && finite1(b.z) && finite1(b.w))) {
@@ -208,7 +196,7 @@ __global__ void __launch_bounds__(kFmaThreads) tile_fma_kernel(const __grid_cons
 #pragma unroll
     for (int c = 0; c < NC * 4; ++c) {
       const int col = (c / 4) * 64 + tx * 4 + c % 4;
-      const float x = static_cast<float>(static_cast<const T*>(p.v)[tok * p.v_stride + t.h * D + col]);
+      const float x = static_cast<float>(static_cast<const float*>(p.v)[tok * p.v_stride + t.h * D + col]);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (lim_first + part < lim[i] && !finite1(x)) o[i][c] += x;
@@ -220,7 +208,7 @@ __global__ void __launch_bounds__(kFmaThreads) tile_fma_kernel(const __grid_cons
     if (r >= t.rows) continue;
     if (p.direct) {
       const float inv = z[i] > 0.f || z[i] != z[i] ? 1.f / z[i] : 0.f;
-      T* at = static_cast<T*>(p.out) + static_cast<int64_t>(sg.tok0 + row / G) * p.out_stride + (t.h * G + row % G) * D + tx * 4;
+      float* at = static_cast<float*>(p.out) + static_cast<int64_t>(sg.tok0 + row / G) * p.out_stride + (t.h * G + row % G) * D + tx * 4;
 #pragma unroll
       for (int c = 0; c < NC; ++c)
         store4(at + c * 64, make_float4(o[i][c * 4] * inv, o[i][c * 4 + 1] * inv, o[i][c * 4 + 2] * inv, o[i][c * 4 + 3] * inv));
@@ -307,7 +295,7 @@ __global__ void __launch_bounds__(kMergeThreads) tile_merge_kernel(const __grid_
         for (int i = 0; i < n; ++i) {
           const float wi = __shfl_sync(0xffffffffu, w, i);
           const float* at = p.part_o + (l[a].first + (i0 + i) * l[a].step) * D + lane * E;
-          if (wi == 0.f) continue;  // an empty range's O is all zero
+          if (wi == 0.f && __shfl_sync(0xffffffffu, wz, i) == 0.f) continue;  // nothing, or nothing that counts
 #pragma unroll
           for (int e = 0; e < E; ++e) acc[e] = fmaf(wi, at[e], acc[e]);
         }
@@ -353,7 +341,10 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 struct TileShape {
   int rows, tpg, slots, min_blocks;
 };
-TileShape tile_shape(int) { return {kFmaRows, 1, 2 * kSms, 2}; }
+TileShape tile_shape(int dtype) {
+  if (dtype == TKV_DTYPE_BF16) return {128, 2, kSms, 4};
+  return {kFmaRows, 1, 2 * kSms, 2};
+}
 
 int64_t seg_groups(const TileSeg& s, int G, const TileShape& ts) {
   return ceil_div(static_cast<int64_t>(s.ntok) * G, static_cast<int64_t>(ts.rows) * ts.tpg);
@@ -496,20 +487,21 @@ int plan_shared(TileParams& p, TilePlan* plan, int32_t batch, int32_t Hq, int32_
   return TKV_OK;
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_fma(const TileParams& p, cudaStream_t s) {
   constexpr int bytes = ((kFmaRows + 2 * kFmaKeys) * (D + 4) + kFmaRows * (kFmaKeys + 4)) * 4;
-  cudaError_t e = cudaFuncSetAttribute(tile_fma_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  cudaError_t e = cudaFuncSetAttribute(tile_fma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  tile_fma_kernel<T, D><<<static_cast<unsigned>(p.units), kFmaThreads, bytes, s>>>(p);
+  tile_fma_kernel<D><<<static_cast<unsigned>(p.units), kFmaThreads, bytes, s>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_tiles(const TileParams& p, int D, int tokens, cudaStream_t s) {
+cudaError_t launch_tiles(const TileParams& p, int D, int tokens, int64_t keys, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (p.units > 0) {
-    e = D == 64 ? launch_fma<T, 64>(p, s) : launch_fma<T, 128>(p, s);
+    if (sizeof(T) == 2) e = launch_tile_mma(p, D, keys, s);
+    else e = D == 64 ? launch_fma<64>(p, s) : launch_fma<128>(p, s);
     if (e != cudaSuccess) return e;
   }
   if (!p.direct && tokens > 0) {
@@ -521,8 +513,8 @@ cudaError_t launch_tiles(const TileParams& p, int D, int tokens, cudaStream_t s)
   return e;
 }
 
-cudaError_t launch_dtype(const TileParams& p, int dtype, int D, int tokens, cudaStream_t s) {
-  return dtype == TKV_DTYPE_BF16 ? launch_tiles<__nv_bfloat16>(p, D, tokens, s) : launch_tiles<float>(p, D, tokens, s);
+cudaError_t launch_dtype(const TileParams& p, int dtype, int D, int tokens, int64_t keys, cudaStream_t s) {
+  return dtype == TKV_DTYPE_BF16 ? launch_tiles<__nv_bfloat16>(p, D, tokens, keys, s) : launch_tiles<float>(p, D, tokens, keys, s);
 }
 
 bool misaligned(const void* ptr, size_t to) { return reinterpret_cast<uintptr_t>(ptr) % to != 0; }
@@ -587,7 +579,7 @@ tkv_status tkv_prompt_attention(int32_t batch, const int32_t* q_lens, const int3
   p.out = out; p.out_stride = out_stride;
   p.status = status;
   p.wait_limit_ns = 2000000000ull;
-  const cudaError_t e = launch_dtype(p, kv_dtype, head_dim, static_cast<int>(tq), static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_dtype(p, kv_dtype, head_dim, static_cast<int>(tq), tk, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return tkv_status(report(TKV_ERR_CUDA, "prompt attention launch failed: %s", cudaGetErrorString(e)));
   return TKV_OK;
 }
@@ -617,8 +609,8 @@ tkv_status tkv_shared_prefix_attention(int32_t batch, int32_t n_q_heads, int32_t
                            alpha_sum != nullptr))
     return tkv_status(st);
   if (!q || !pool || !page_table || !slot_mask || !out) return tkv_status(report(TKV_ERR_INVALID_ARG, "null pointer"));
-  if (pool_pages < 1 || pool_pages > (int64_t(1) << 30) / n_kv_heads)
-    return tkv_status(report(TKV_ERR_INVALID_ARG, "pool_pages x n_kv_heads must be 1 to 2^30"));
+  if (pool_pages < 1 || pool_pages > (int64_t(1) << 29) / n_kv_heads)
+    return tkv_status(report(TKV_ERR_INVALID_ARG, "pool_pages x n_kv_heads must be 1 to 2^29"));
   if (misaligned(q, 16) || misaligned(pool, 16) || misaligned(out, 16) || misaligned(alpha_sum, 16))
     return tkv_status(report(TKV_ERR_INVALID_ARG, "q, pool, out and alpha_sum must be 16-byte aligned"));
   if (int st = bind_scratch(p, plan, head_dim, scratch, scratch_bytes)) return tkv_status(st);
@@ -633,7 +625,7 @@ tkv_status tkv_shared_prefix_attention(int32_t batch, int32_t n_q_heads, int32_t
   p.alpha_first = static_cast<int64_t>(shared_pages) * kPage;
   p.status = status;
   p.wait_limit_ns = 2000000000ull;
-  const cudaError_t e = launch_dtype(p, kv_dtype, head_dim, batch, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_dtype(p, kv_dtype, head_dim, batch, 0, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess)
     return tkv_status(report(TKV_ERR_CUDA, "shared-prefix attention launch failed: %s", cudaGetErrorString(e)));
   return TKV_OK;

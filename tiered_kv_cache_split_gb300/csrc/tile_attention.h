@@ -104,8 +104,7 @@ __device__ __forceinline__ int64_t tile_part_row(const TileParams& p, const Tile
   return s.part0 + (((static_cast<int64_t>(grp) * p.Hkv + h) * s.splits + split) * p.tpg + tile) * s.part_rows;
 }
 
-// tile_attention.cu
-// tile_attention_mma.cu
-cudaError_t launch_tile_mma(const TileParams& p, int D, cudaStream_t s);
+// tile_attention_mma.cu: the units of a bf16 call; keys: packed key tokens
+cudaError_t launch_tile_mma(const TileParams& p, int D, int64_t keys, cudaStream_t s);
 
 }  // namespace tkv
