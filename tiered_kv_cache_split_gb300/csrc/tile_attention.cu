@@ -339,51 +339,72 @@ struct TilePlan {
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct TileShape {
-  int rows, tpg, slots, min_blocks;
+  int rows, tpg;     // rows of a tile, tiles of a row group
+  int slots;         // units the device runs at once
+  int unit_cost;     // fixed time of a unit, in key blocks (a block: 64 KB of K and V at d = 128)
 };
+// bf16: one CTA per SM; a unit's start and end take about 5 us, a block about 1.5 us.
+// fp32: two 64-row CTAs per SM, whose blocks take several times as long.
 TileShape tile_shape(int dtype) {
-  if (dtype == TKV_DTYPE_BF16) return {128, 2, kSms, 4};
-  return {kFmaRows, 1, 2 * kSms, 2};
+  if (dtype == TKV_DTYPE_BF16) return {128, 2, kSms, 3};
+  return {kFmaRows, 1, 2 * kSms, 1};
 }
 
-int64_t seg_groups(const TileSeg& s, int G, const TileShape& ts) {
-  return ceil_div(static_cast<int64_t>(s.ntok) * G, static_cast<int64_t>(ts.rows) * ts.tpg);
-}
-
-// Key blocks of all units of a segment for one KV head.
-int64_t seg_blocks(const TileParams& p, const TileSeg& s, const TileShape& ts) {
-  const int64_t g = seg_groups(s, p.G, ts);
-  if (!p.causal) return g * ceil_div(s.nkeys, kKeyBlock);
-  int64_t n = 0;
+struct SegWork {
+  int64_t groups, most, blocks;  // row groups; key blocks of the longest; of all of them
+};
+SegWork seg_work(const TileParams& p, const TileSeg& s, const TileShape& ts) {
+  SegWork w{0, 0, 0};
+  if (s.ntok == 0 || (s.nkeys == 0 && p.paged)) return w;
   const int64_t per = static_cast<int64_t>(ts.rows) * ts.tpg, rows = static_cast<int64_t>(s.ntok) * p.G;
-  if (g > 4096) return g * ceil_div(s.nkeys, kKeyBlock);  // far more units than SMs: the exact count decides nothing
-  for (int64_t i = 0; i < g; ++i) {
-    const int64_t last = std::min((i + 1) * per, rows) - 1;
-    n += ceil_div(s.see0 + last / p.G + 1, kKeyBlock);
-  }
-  return n;
+  w.groups = ceil_div(rows, per);
+  w.most = ceil_div(s.nkeys, kKeyBlock);
+  // a causal segment's groups see from see0 to all of its keys, evenly spread
+  w.blocks = p.causal ? ceil_div(w.groups * (s.see0 + s.nkeys), 2 * kKeyBlock) : w.groups * w.most;
+  return w;
 }
 
-// Cuts the segments (tok0, ntok, nkeys, see0 set) into units. Where the rows
-// alone give a prompt fewer units than the device has places, and always for
-// paged segments, the keys are split too, into ranges of about equal length
-// that fill the places once, no shorter than min_blocks key blocks.
+// Key blocks per unit. A unit costs its blocks and unit_cost; the device runs
+// them in waves of `slots`. Rows alone leave a decode step, or a short piece of
+// a prompt, with a few long units, so their keys are split: the candidate with
+// the shortest makespan wins. More than four waves of units are never split.
+int64_t blocks_per_unit(const SegWork* w, int n, int hkv, const TileShape& ts, bool paged) {
+  int64_t whole = 0, most = 1, blocks = 0;
+  for (int i = 0; i < n; ++i) {
+    whole += w[i].groups * hkv;
+    most = std::max(most, w[i].most);
+    blocks += w[i].blocks * hkv;
+  }
+  if (whole >= 4 * ts.slots) return most;
+  int64_t best = most;
+  double best_time = 1e300;
+  for (int64_t cut = 1; cut <= most; cut += 1 + cut / 8) {
+    const int64_t per = ceil_div(most, cut);
+    int64_t units = 0;
+    for (int i = 0; i < n; ++i)
+      if (w[i].groups) units += w[i].groups * hkv * ceil_div(w[i].most, per);
+    const double work = static_cast<double>(blocks) + static_cast<double>(ts.unit_cost) * units;
+    double time = units <= ts.slots ? static_cast<double>(per + ts.unit_cost)
+                                    : std::max(static_cast<double>(per + ts.unit_cost), ceil_div(units, ts.slots) * (work / units));
+    if (!paged && cut > 1) time += ts.unit_cost;  // the merge launch
+    if (time < best_time) {
+      best_time = time;
+      best = per;
+    }
+  }
+  return best;
+}
+
+// Cuts the segments (tok0, ntok, nkeys, see0 set) into units.
 TilePlan plan_units(TileParams& p, const TileShape& ts, bool want_spill) {
   TilePlan out{0, 0, 0};
+  SegWork work[kMaxSegs];
   p.tile_rows = ts.rows;
   p.tpg = ts.tpg;
-  int64_t units = 0, blocks = 0;
-  for (int i = 0; i < p.nseg; ++i) {
-    TileSeg& s = p.seg[i];
-    if (s.ntok == 0 || (s.nkeys == 0 && p.paged)) continue;
-    units += seg_groups(s, p.G, ts) * p.Hkv;
-    blocks += seg_blocks(p, s, ts) * p.Hkv;
-  }
-  int64_t per = INT32_MAX;  // key blocks per unit
-  if (p.paged || units < ts.slots) per = std::max<int64_t>(ts.min_blocks, ceil_div(blocks, ts.slots));
   bool split = p.paged;
-  for (int i = 0; i < p.nseg; ++i)
-    if (p.seg[i].ntok && ceil_div(p.seg[i].nkeys, kKeyBlock) > per) split = true;
+  for (int i = 0; i < p.nseg; ++i) work[i] = seg_work(p, p.seg[i], ts);
+  const int64_t per = blocks_per_unit(work, p.nseg, p.Hkv, ts, p.paged);
+  for (int i = 0; i < p.nseg; ++i) split |= work[i].groups && work[i].most > per;
   p.direct = !split;
   for (int i = 0; i < p.nseg; ++i) {
     TileSeg& s = p.seg[i];
@@ -391,9 +412,9 @@ TilePlan plan_units(TileParams& p, const TileShape& ts, bool want_spill) {
     s.part0 = out.part_rows;
     s.spill0 = -1;
     s.splits = s.groups = s.part_rows = s.pair = 0;
-    if (s.ntok == 0 || (s.nkeys == 0 && p.paged)) continue;
-    s.groups = static_cast<int32_t>(seg_groups(s, p.G, ts));
-    s.splits = split ? static_cast<int32_t>(std::max<int64_t>(1, ceil_div(ceil_div(s.nkeys, kKeyBlock), per))) : 1;
+    if (!work[i].groups) continue;
+    s.groups = static_cast<int32_t>(work[i].groups);
+    s.splits = static_cast<int32_t>(std::max<int64_t>(1, ceil_div(work[i].most, per)));
     const int64_t rows = static_cast<int64_t>(s.ntok) * p.G;
     s.pair = !p.direct && ts.tpg == 2 && rows <= ts.rows;
     s.part_rows = static_cast<int32_t>(std::min<int64_t>(ts.rows, rows));

@@ -2,17 +2,20 @@
 // tile_attention.h; the mathematics: tile_attention.cu).
 //
 // One CTA per SM runs one unit: up to 256 rows as two tiles of 128 against a
-// stream of 128-key blocks. Ten warps:
+// stream of 128-key blocks. Eleven warps:
 //   0-3, 4-7  softmax of tile 0 / 1: one thread per row (TMEM lane), so row
 //             maxima and sums need no exchange between threads
 //   8         producer: TMA of K and V blocks into a ring of shared-memory slots
-//   9         issues tcgen05.mma: S = Q K^T from shared memory, O += P V with P
-//             read from TMEM
-// TMEM holds, per tile, S (128 fp32 columns) and O (D columns); P (bf16)
-// overwrites the S it came from. While one tile is in its softmax the tensor
-// cores work for the other. A segment of at most 128 rows that is split anyway
-// (a decode step) runs as a PAIR: both halves hold the same rows and take
-// alternate key blocks, each with a partial of its own.
+//   9, 10     issue tcgen05.mma for tile 0 / 1: S = Q K^T from shared memory,
+//             O += P V with P read from TMEM. The tensor core takes few MMAs
+//             ahead, so a lone issuer's waits would idle it: with two, one waits
+//             while the other's MMAs run
+// A key block is taken in two halves of 64 keys. TMEM holds, per tile, S of two
+// halves (2 x 64 fp32 columns) and O (D columns); P (bf16) overwrites the S it
+// came from. S of the next half is computed while the softmax works on this
+// one, so a softmax warp finds its next S ready. A segment of at most 128 rows
+// that is split anyway (a decode step) runs as a PAIR: both halves of the CTA
+// hold the same rows and take alternate key blocks, each with a partial of its own.
 //
 // Running maximum: O is rescaled only when a row's maximum has risen by more
 // than 2^8 over the one its weights refer to (or at the first key): the weights
@@ -42,9 +45,10 @@ namespace tkv {
 namespace {
 
 constexpr int kRows = 128;
-constexpr int kThreads = 320;
-constexpr int kProducer = 8, kIssuer = 9;
+constexpr int kThreads = 352;
+constexpr int kProducer = 8, kIssuer = 9;  // warps; one issuer per tile
 constexpr int kBoxBytes = kKeyBlock * 128;  // 128 rows of 64 bf16 columns, 128-byte swizzle
+constexpr int kHalf = 64;                   // keys of one S
 constexpr int kBatch = 4;                   // key blocks whose page ids are fetched together
 constexpr int kMaskBatches = 4;             // batches the mask ring holds
 
@@ -59,8 +63,10 @@ struct Cfg {
   __host__ __device__ static constexpr uint32_t col_o(int t) { return 256 + t * D; }
 };
 
+// Barriers of alternate halves come in pairs: a parity wait tells two phases
+// apart, and up to two halves of a tile are under way.
 struct Shared {
-  uint64_t full[8], empty[8], s_full[2], p_full[2], o_full[2], q_full, drain, ids[kMaskBatches];
+  uint64_t full[8], empty[8], s_full[2][2], p_full[2][2], o_full[2][2], q_full, drain[2], ids[kMaskBatches];
   uint32_t tmem;
   int abort;
   uint32_t flag[8];                       // partly seen keys with non-finite V values
@@ -133,21 +139,31 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint
 __host__ __device__ constexpr uint32_t instr_desc(int n, bool b_mn_major) {
   return 1u << 4 | 1u << 7 | 1u << 10 | (b_mn_major ? 1u << 16 : 0u) | static_cast<uint32_t>(n >> 3) << 17 | (kRows >> 4) << 24;
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// The issuing warp runs its loop with all lanes, so that descriptors stay in
+// uniform registers; `leader` (one elected lane) predicates the instructions.
+__device__ __forceinline__ uint32_t elect_leader() {
+  uint32_t is;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(is));
+  return is;
+}
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b),
-      "r"(idesc), "r"(acc)
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b),
-      "r"(idesc), "r"(acc)
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader)
       : "memory");
 }
-// Arrives on bar once the MMAs issued so far by this thread are done.
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+// Arrives on bar once the MMAs issued so far by the leader are done.
+__device__ __forceinline__ void mma_commit(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.u32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)), "r"(leader)
+      : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -173,6 +189,11 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
+// 16 bytes to shared memory; bytes = 0 writes zeros
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -183,7 +204,33 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ bool bf16_finite(uint32_t bits) { return (bits & 0x7f80u) != 0x7f80u; }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+// Zeroes the non-finite ones of two bf16 values; whether there was one.
+__device__ __forceinline__ bool strip(uint32_t& w) {
+  const bool lo = (w & 0x7f80u) == 0x7f80u, hi = (w & 0x7f800000u) == 0x7f800000u;
+  if (lo) w &= 0xffff0000u;
+  if (hi) w &= 0x0000ffffu;
+  return lo || hi;
+}
 
 // Ring position of the i-th K / V block: K blocks run `ahead` blocks ahead of V.
 __device__ __forceinline__ int pos_k(int i, int ahead) { return i + max(0, i - ahead + 1); }
@@ -198,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Shared sh;
   char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t s_q = smem_u32(smem), s_ring = s_q + 2 * C::tile;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   volatile int* abort = &sh.abort;
   const uint64_t limit = p.wait_limit_ns;
 
@@ -209,16 +256,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < C::slots; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.empty[i], 2);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&sh.s_full[t], 1);
-      mbar_init(&sh.p_full[t], 4);
-      mbar_init(&sh.o_full[t], 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&sh.s_full[t][b], 1);
+        mbar_init(&sh.p_full[t][b], 4);
+        mbar_init(&sh.o_full[t][b], 1);
+      }
+      mbar_init(&sh.drain[t], 1);
     }
     for (int i = 0; i < kMaskBatches; ++i) mbar_init(&sh.ids[i], 1);
     mbar_init(&sh.q_full, 8);
-    mbar_init(&sh.drain, 1);
     sh.abort = 0;
     for (int i = 0; i < 8; ++i) sh.flag[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -227,22 +276,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
 
   const TileUnit u = tile_unit(p, blockIdx.x);
   const TileSeg& sg = p.seg[u.seg];
   const int pair = sg.pair, ahead = pair ? 2 : 1;
   const int n = u.j1 - u.j0;  // key blocks
-  // blocks of each tile: a causal tile 0 may end before tile 1
-  int nt[2];
+  // halves each tile works on: a causal tile 0 may end before tile 1
+  int ns[2];
   if (pair) {
-    nt[0] = (n + 1) / 2;
-    nt[1] = n / 2;
+    ns[0] = (n + 1) / 2 * 2;
+    ns[1] = n / 2 * 2;
   } else {
     for (int t = 0; t < 2; ++t) {
       const int last = min((t + 1) * kRows, u.rows) - 1;
-      nt[t] = last < t * kRows ? 0 : min(n, (tile_row_limit(p, sg, u.row0 + last) + kKeyBlock - 1) / kKeyBlock - u.j0);
-      nt[t] = max(nt[t], 0);
+      const int halves = (tile_row_limit(p, sg, u.row0 + last) + kHalf - 1) / kHalf - 2 * u.j0;
+      ns[t] = last < t * kRows ? 0 : max(min(2 * n, halves), 0);
     }
   }
 
@@ -304,81 +353,86 @@ __global__ void __launch_bounds__(kThreads, 1)
     // an aborted CTA lets the copies in flight land before it ends
     if (*abort)
       for (int q = max(0, pos - C::slots); q < pos; ++q) warp_wait(&sh.full[q % C::slots], (q / C::slots) & 1, nullptr, limit);
-  } else if (warp == kIssuer) {
-    if (lane == 0) {
-      constexpr uint32_t kIdescS = instr_desc(kKeyBlock, false), kIdescO = instr_desc(D, true);
-      auto slot_ready = [&](int pos) { return mbar_wait(&sh.full[pos % C::slots], (pos / C::slots) & 1, abort, limit); };
-      auto qk = [&](int t, int pos) {
-        const uint32_t a = s_q + (pair ? 0 : t) * C::tile, b = s_ring + pos % C::slots * C::tile;
+  } else if (warp >= kIssuer) {
+    {
+      const uint32_t leader = elect_leader();
+      const int t = warp - kIssuer;
+      constexpr uint32_t kIdescS = instr_desc(kHalf, false), kIdescO = instr_desc(D, true);
+      const uint64_t desc_q = smem_desc(s_q + (pair ? 0 : t) * C::tile, 16, 1024);
+      const uint32_t t_s = tmem + t * kKeyBlock, t_o = tmem + C::col_o(t);
+      auto slot_ready = [&](int pos) { return warp_wait(&sh.full[pos % C::slots], (pos / C::slots) & 1, abort, limit); };
+      // S of the h-th half = Q K^T over half h & 1 of the K block at ring position pos
+      auto qk = [&](int h, int pos) {
+        const uint64_t b = smem_desc(s_ring + pos % C::slots * C::tile + (h & 1) * (kHalf * 128), 16, 1024);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k / 4) * kBoxBytes + (k % 4) * 32;
-          mma_ss(tmem + t * kKeyBlock, smem_desc(a + off, 16, 1024), smem_desc(b + off, 16, 1024), kIdescS, k > 0);
+          const uint32_t off = ((k / 4) * kBoxBytes + (k % 4) * 32) >> 4;
+          mma_ss(leader, t_s + (h & 1) * kHalf, desc_q + off, b + off, kIdescS, k > 0);
         }
-        mma_commit(&sh.s_full[t]);
+        mma_commit(leader, &sh.s_full[t][h & 1]);
       };
-      auto pv = [&](int t, int pos, bool acc) {
-        const uint32_t b = s_ring + pos % C::slots * C::tile;
+      // O += P V over the same half of the V block
+      auto pv = [&](int h, int pos) {
+        const uint64_t b = smem_desc(s_ring + pos % C::slots * C::tile + (h & 1) * (kHalf * 128), kBoxBytes, 1024);
 #pragma unroll
-        for (int k = 0; k < kKeyBlock / 16; ++k)
-          mma_ts(tmem + C::col_o(t), tmem + t * kKeyBlock + k * 8, smem_desc(b + k * 2048, kBoxBytes, 1024), kIdescO, acc || k > 0);
-        mma_commit(&sh.o_full[t]);
+        for (int k = 0; k < kHalf / 16; ++k)
+          mma_ts(leader, t_o, t_s + (h & 1) * kHalf + k * 8, b + k * (2048 >> 4), kIdescO, h > 0 || k > 0);
+        mma_commit(leader, &sh.o_full[t][h & 1]);
+      };
+      auto p_ready = [&](int h) {
+        const bool ready = warp_wait(&sh.p_full[t][h & 1], (h >> 1) & 1, abort, limit);
+        fence_after();
+        return ready;
+      };
+      // Both issuers pass every ring slot in turn and give it back: one that does
+      // not use it at once, but never before it is full. A slot no later block
+      // takes is not given back: nobody would wait for that arrival, and it could
+      // reach the shared memory of the next CTA on this SM.
+      auto release = [&](int pos) {
+        if (pos + C::slots < 2 * n) mma_commit(leader, &sh.empty[pos % C::slots]);
       };
       auto run = [&]() {
-        if (n == 0) return;
-        if (!mbar_wait(&sh.q_full, 0, abort, limit)) return;
+        if (n == 0 || !warp_wait(&sh.q_full, 0, abort, limit)) return;
         fence_after();
-        if (pair) {
-          for (int i = 0; i < min(2, n); ++i) {
-            const int pk = pos_k(i, 2);
-            if (!slot_ready(pk)) return;
-            qk(i, pk);
-            mma_commit(&sh.empty[pk % C::slots]);
+        const int mine = ns[t];
+        for (int i = 0; i < min(ahead, n); ++i) {
+          if (!slot_ready(i)) return;
+          if (!pair || i == t) {
+            if (0 < mine) qk(0, i);
+            if (1 < mine) qk(1, i);
           }
-          for (int i = 0; i < n; ++i) {
-            const int t = i & 1, pvs = pos_v(i, 2, n);
-            if (!slot_ready(pvs)) return;
-            if (!mbar_wait(&sh.p_full[t], (i >> 1) & 1, abort, limit)) return;
-            fence_after();
-            pv(t, pvs, i >= 2);
-            mma_commit(&sh.empty[pvs % C::slots]);
-            if (i + 2 < n) {
-              const int pk = pos_k(i + 2, 2);
-              if (!slot_ready(pk)) return;
-              qk(t, pk);
-              mma_commit(&sh.empty[pk % C::slots]);
-            }
-          }
-          return;
+          release(i);
         }
-        if (!slot_ready(0)) return;
-        for (int t = 0; t < 2; ++t)
-          if (nt[t] > 0) qk(t, 0);
-        mma_commit(&sh.empty[0]);
         for (int i = 0; i < n; ++i) {
-          const int pvs = pos_v(i, 1, n), pk = pos_k(i + 1, 1);
-          if (!slot_ready(pvs)) return;
-          for (int t = 0; t < 2; ++t) {
-            if (i >= nt[t]) continue;
-            if (!mbar_wait(&sh.p_full[t], i & 1, abort, limit)) return;
-            fence_after();
-            pv(t, pvs, i > 0);
-            if (i + 1 < nt[t]) {
-              if (!slot_ready(pk)) return;
-              qk(t, pk);
-            }
+          const int at = pos_v(i, ahead, n), pk = pos_k(i + ahead, ahead);
+          const bool more = i + ahead < n, use = !pair || (i & 1) == t;
+          const int h = pair ? i >> 1 << 1 : 2 * i;  // the tile's halves of block i: h, h + 1
+          if (!slot_ready(at)) return;
+          if (use && h < mine) {
+            if (!p_ready(h)) return;
+            pv(h, at);
           }
-          mma_commit(&sh.empty[pvs % C::slots]);
-          if (i + 1 < n) mma_commit(&sh.empty[pk % C::slots]);
+          if (more) {
+            if (!slot_ready(pk)) return;
+            if (use && h + 2 < mine) qk(h + 2, pk);
+          }
+          if (use && h + 1 < mine) {
+            if (!p_ready(h + 1)) return;
+            pv(h + 1, at);
+          }
+          release(at);
+          if (more) {
+            if (use && h + 3 < mine) qk(h + 3, pk);
+            release(pk);
+          }
         }
       };
       run();
       if (*abort) {
-        mma_commit(&sh.drain);
-        mbar_wait(&sh.drain, 0, nullptr, limit);
+        mma_commit(leader, &sh.drain[t]);
+        warp_wait(&sh.drain[t], 0, nullptr, limit);
       }
     }
-    __syncwarp();
   } else {
     const int t = warp >> 2, r = tid & 127;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp & 3) << 21);
@@ -389,19 +443,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = u.row0 + first + min(r, max(rows - 1, 0));
     const bool valid = r < rows;
     // Q tile into shared memory in the swizzled layout; rows past the end are 0
+    const int tok_base = sg.tok0 + u.row0 / G, g_base = u.row0 % G;  // of the unit's first row
+    const uint32_t gmul = (65535 + G) / G;  // (x * gmul) >> 16 = x / G for x < 320, G <= 64
     if (!pair || t == 0) {
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + u.h * G * D;
       constexpr int kChunks = D / 8;
-#pragma unroll 4
-      for (int i = r; i < kRows * kChunks; i += kRows) {
-        const int rr = i / kChunks, c = i % kChunks;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (rr < rows) {
-          const int at = u.row0 + first + rr;
-          x = *reinterpret_cast<const uint4*>(q + static_cast<int64_t>(sg.tok0 + at / G) * p.q_stride + (u.h * G + at % G) * D + c * 8);
-        }
-        *reinterpret_cast<uint4*>(smem + t * C::tile + (c >> 3) * kBoxBytes + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = x;
+      const int c = r % kChunks;
+      const uint32_t dst = s_q + t * C::tile + (c >> 3) * kBoxBytes;
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const int rr = r / kChunks + i * (kRows / kChunks), x = g_base + first + rr, tok = (x * gmul) >> 16;
+        const __nv_bfloat16* src = rr < rows ? q + static_cast<int64_t>(tok_base + tok) * p.q_stride + (x - tok * G) * D + c * 8 : q;
+        cp_async16(dst + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), src, rr < rows ? 16 : 0);
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy();
     }
     __syncwarp();
@@ -413,54 +468,60 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float qs = p.qscale;
     float ref = -INFINITY, z = 0.f;  // maximum the weights refer to (unscaled logits), sum of weights
     bool ok = true;
-    for (int k = 0; ok && k < nt[t]; ++k) {
-      const int i = pair ? 2 * k + t : k;
-      const int k0 = (u.j0 + i) * kKeyBlock;
-      uint32_t live[4] = {~0u, ~0u, ~0u, ~0u};
+    for (int h = 0; ok && h < ns[t]; ++h) {
+      const int i = pair ? (h >> 1) * 2 + t : h >> 1, half = h & 1;
+      const int k0 = (u.j0 + i) * kKeyBlock + half * kHalf;
+      uint32_t live[2] = {~0u, ~0u};
       if (kPaged) {
         const int b = i / kBatch;
         if (!(ok = warp_wait(&sh.ids[b % kMaskBatches], (b / kMaskBatches) & 1, abort, limit))) break;
-        const uint4 w = *reinterpret_cast<const uint4*>(&sh.mask[b % kMaskBatches * 32 + i % kBatch * 8]);
-        live[0] = w.x; live[1] = w.y; live[2] = w.z; live[3] = w.w;
+        const uint2 w = *reinterpret_cast<const uint2*>(&sh.mask[b % kMaskBatches * 32 + i % kBatch * 8 + half * 4]);
+        live[0] = w.x;
+        live[1] = w.y;
       }
-      const bool holes = kPaged && (live[0] & live[1] & live[2] & live[3]) != ~0u;
-      const bool cut = !kPaged && k0 + kKeyBlock > lim_warp;
-      const bool clean = (holes || (!kPaged && k0 + kKeyBlock > lim_first)) && (pair || t == 0 || i >= nt[0]);
+      const bool holes = kPaged && (live[0] & live[1]) != ~0u;
+      const bool cut = !kPaged && k0 + kHalf > lim_warp;
+      const bool clean = holes || (!kPaged && k0 + kHalf > lim_first);
 
-      if (!(ok = warp_wait(&sh.s_full[t], k & 1, abort, limit))) break;
+      if (!(ok = warp_wait(&sh.s_full[t][half], (h >> 1) & 1, abort, limit))) break;
       fence_after();
-      uint32_t s[128];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, s + c * 32);
+      uint32_t s[kHalf];
+      tmem_ld32(t_s + half * kHalf, s);
+      tmem_ld32(t_s + half * kHalf + 32, s + 32);
       wait_ld();
       if (cut) {
         const int m = lim - k0;
 #pragma unroll
-        for (int c = 0; c < 128; ++c) s[c] = c < m ? s[c] : 0xff800000u;
+        for (int c = 0; c < kHalf; ++c) s[c] = c < m ? s[c] : 0xff800000u;
       }
       if (holes) {
 #pragma unroll
-        for (int c = 0; c < 128; ++c) s[c] = (live[c / 32] >> (c % 32)) & 1u ? s[c] : 0xff800000u;
+        for (int c = 0; c < kHalf; ++c) s[c] = (live[c / 32] >> (c % 32)) & 1u ? s[c] : 0xff800000u;
       }
-      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int c = 0; c < 128; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(s[c]));
-      const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
       if (kPaged && sg.spill0 >= 0 && valid) {
         float4* at = reinterpret_cast<float4*>(p.spill + sg.spill0 + static_cast<int64_t>(u.h * G + row % G) * sg.nkeys + k0);
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
+        for (int c = 0; c < kHalf / 4; ++c)
           if (k0 + c * 4 < sg.nkeys)
             at[c] = make_float4(__uint_as_float(s[c * 4]) * qs, __uint_as_float(s[c * 4 + 1]) * qs,
                                 __uint_as_float(s[c * 4 + 2]) * qs, __uint_as_float(s[c * 4 + 3]) * qs);
       }
-      const float next = fmaxf(ref, mx);
+      float top[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) top[c] = max3(__uint_as_float(s[c]), __uint_as_float(s[c + 4]), __uint_as_float(s[c + 8]));
+#pragma unroll
+      for (int c = 12; c < 60; c += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top[e] = max3(top[e], __uint_as_float(s[c + e]), __uint_as_float(s[c + 4 + e]));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], __uint_as_float(s[60 + e]));
+      const float next = fmaxf(max3(ref, top[0], top[1]), fmaxf(top[2], top[3]));
       if (__any_sync(0xffffffffu, (next - ref) * qs > 8.f)) {
         const float f = next == -INFINITY ? 1.f : ex2((ref - next) * qs);
-        if (k > 0) {
-          if (!(ok = warp_wait(&sh.o_full[t], (k - 1) & 1, abort, limit))) break;
+        if (h > 0) {
+          if (!(ok = warp_wait(&sh.o_full[t][(h - 1) & 1], ((h - 1) >> 1) & 1, abort, limit))) break;
           fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
             tmem_ld32(t_o + c, o);
@@ -474,43 +535,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         ref = next;
       }
       const float base = ref == -INFINITY ? 0.f : ref * qs;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const float2 qs2 = make_float2(qs, qs), base2 = make_float2(-base, -base);
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float a = ex2(fmaf(__uint_as_float(s[h * 64 + 2 * c]), qs, -base));
-          const float b = ex2(fmaf(__uint_as_float(s[h * 64 + 2 * c + 1]), qs, -base));
-          sum[c & 3] += a + b;
-          s[h * 32 + c] = pack2(a, b);
-        }
-        tmem_st32(t_s + h * 32, s + h * 32);
+      for (int c = 0; c < kHalf / 2; ++c) {
+        float2 x = fma2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), qs2, base2);
+        x.x = ex2(x.x);
+        x.y = ex2(x.y);
+        sum[c & 1] = add2(sum[c & 1], x);
+        s[c] = pack2(x.x, x.y);
       }
-      z += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_st32(t_s + half * kHalf, s);
+      z += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       if (clean) {
-        const int pv = pos_v(i, ahead, n), key = k0 + r;
+        const int pv = pos_v(i, ahead, n), kr = half * kHalf + (r & 63), key = k0 + (r & 63);
         if (!(ok = warp_wait(&sh.full[pv % C::slots], (pv / C::slots) & 1, abort, limit))) break;
-        const bool none = kPaged ? !((live[r >> 5] >> (r & 31)) & 1u) : key >= lim_last;
+        const bool none = kPaged ? !((live[(r & 63) >> 5] >> (r & 31)) & 1u) : key >= lim_last;
         if (none || (!kPaged && key >= lim_first)) {
-          char* at = smem + (2 + pv % C::slots) * C::tile + r * 128;
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            uint4* w = reinterpret_cast<uint4*>(at + (c >> 3) * kBoxBytes + (((c + r) & 7) << 4));
+          // two threads per key, half of its columns each; where both tiles use the
+          // block both clean it, with the same result
+          char* at = smem + (2 + pv % C::slots) * C::tile + kr * 128;
+#pragma unroll 2
+          for (int e = 0; e < D / 16; ++e) {
+            const int c = (r >> 6) * (D / 16) + e;
+            uint4* w = reinterpret_cast<uint4*>(at + (c >> 3) * kBoxBytes + (((c + kr) & 7) << 4));
             if (none) {
               *w = make_uint4(0, 0, 0, 0);
               continue;
             }
             uint4 x = *w;
-            uint32_t* e = &x.x;
-            bool bad = false;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (!bf16_finite(e[j])) { e[j] &= 0xffff0000u; bad = true; }
-              if (!bf16_finite(e[j] >> 16)) { e[j] &= 0x0000ffffu; bad = true; }
-            }
-            if (bad) {
-              *w = x;
+            const bool bad = strip(x.x) | strip(x.y) | strip(x.z) | strip(x.w);
+            if (bad) {  // the flag first: who reads the stripped value finds the flag set
               atomicOr(&sh.flag[(key - lim_first) >> 5], 1u << ((key - lim_first) & 31));
+              __threadfence_block();
+              *w = x;
             }
           }
         }
@@ -519,31 +577,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait_st();
       fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.p_full[t]);
+      if (lane == 0) mbar_arrive(&sh.p_full[t][half]);
     }
-    // flags set by either half (tile 0's, which tile 1 needs, are complete here)
+    // every key this tile's rows see has been looked at by its own warps, or was
+    // found stripped with its flag set before
     if (!kPaged) {
-      if (t == 0) asm volatile("bar.sync 2, 128;" ::: "memory");
-      if (t == 0) asm volatile("bar.arrive 1, 256;" ::: "memory");
-      else asm volatile("bar.sync 1, 256;" ::: "memory");
+      __threadfence_block();
+      asm volatile("bar.sync %0, 128;" ::"r"(t + 1) : "memory");
     }
-    if (ok && nt[t] > 0) {
-      ok = warp_wait(&sh.o_full[t], (nt[t] - 1) & 1, abort, limit);
+    if (ok && ns[t] > 0) {
+      ok = warp_wait(&sh.o_full[t][(ns[t] - 1) & 1], ((ns[t] - 1) >> 1) & 1, abort, limit);
       fence_after();
     }
-    if (ok && (rows > 0)) {
+    if (ok && rows > 0) {
       const float inv = z > 0.f || z != z ? 1.f / z : 0.f;
-      const int64_t part = p.direct ? 0 : tile_part_row(p, sg, u.grp, u.h, u.split, t) + r;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + static_cast<int64_t>(sg.tok0 + row / G) * p.out_stride + (u.h * G + row % G) * D;
+      const int64_t part = p.direct ? 0 : tile_part_row(p, sg, u.grp, u.h, u.split, t);
+      // A thread holds a row; rows leave through shared memory, a piece of D bytes
+      // of the warp's 32 rows at a time, so that stores are whole sectors of
+      // neighbouring lanes. The Q tile is free by now (a pair's second one always is).
+      constexpr int kPiece = D, kChunk = kPiece / 16;
+      char* stage = smem + (pair ? C::tile + warp * 32 * kPiece : t * C::tile + (warp & 3) * 32 * kPiece);
+      const int row_in_warp = lane / kChunk, ch = lane % kChunk, warp_row = (warp & 3) * 32;
+      constexpr int kCols = 32;  // TMEM columns read at once
 #pragma unroll
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        if (nt[t] > 0) {
+      for (int c = 0; c < D; c += kCols) {
+        uint32_t o[kCols];
+        if (ns[t] > 0) {
           tmem_ld32(t_o + c, o);
           wait_ld();
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0;
+          for (int e = 0; e < kCols; ++e) o[e] = 0;
         }
         if (!kPaged) {
           for (int w = 0; w < 8; ++w)
@@ -552,33 +616,52 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (key >= lim) continue;
               const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + (sg.key0 + key) * p.v_stride + u.h * D + c;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
+              for (int e = 0; e < kCols; ++e) {
                 const float x = __bfloat162float(v[e]);
                 if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
               }
             }
         }
-        if (!valid) continue;
+        // what this chunk is in the output's type: kCols values, in pieces of kPiece bytes per row
+        const int out_bytes = p.direct ? kCols * 2 : kCols * 4;
+        const int at = p.direct ? (c % (kPiece / 2)) * 2 : 0;  // bytes of earlier chunks in the piece
         if (p.direct) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint4 w;
-            w.x = pack2(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-            w.y = pack2(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-            w.z = pack2(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-            w.w = pack2(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-            *reinterpret_cast<uint4*>(out + c + e) = w;
-          }
-        } else {
-          float* at = p.part_o + part * D + c;
+          for (int e = 0; e < kCols / 2; ++e)
+            o[e] = pack2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+        }
+        for (int b0 = 0; b0 < out_bytes; b0 += kPiece) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<uint4*>(at + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          for (int e = 0; e < kCols / 4; ++e) {
+            const int byte = at + e * 16 - b0;
+            if (byte >= 0 && byte < kPiece && e * 16 < out_bytes)
+              *reinterpret_cast<uint4*>(stage + lane * kPiece + (((byte >> 4) ^ (lane % kChunk)) << 4)) =
+                  make_uint4(o[e * 4], o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]);
+          }
+          if (at + out_bytes < kPiece) break;  // the next chunk completes the piece
+          __syncwarp();
+          const int col_byte = p.direct ? c * 2 - at : c * 4 + b0;  // where the piece starts in a row
+#pragma unroll
+          for (int i = 0; i < kChunk; ++i) {
+            const int rr = row_in_warp + i * (32 / kChunk), tile_row = warp_row + rr;
+            const uint4 w = *reinterpret_cast<const uint4*>(stage + rr * kPiece + ((ch ^ (rr % kChunk)) << 4));
+            if (tile_row >= rows) continue;
+            char* to;
+            if (p.direct) {
+              const int x = g_base + first + tile_row, tok = (x * gmul) >> 16;
+              to = reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(p.out) + static_cast<int64_t>(tok_base + tok) * p.out_stride +
+                                           (u.h * G + x - tok * G) * D);
+            } else {
+              to = reinterpret_cast<char*>(p.part_o + (part + tile_row) * D);
+            }
+            *reinterpret_cast<uint4*>(to + col_byte + ch * 16) = w;
+          }
+          __syncwarp();
         }
       }
       if (!p.direct && valid) {
-        p.part_m[part] = ref * qs;
-        p.part_z[part] = z;
+        p.part_m[part + r] = ref * qs;
+        p.part_z[part + r] = z;
       }
     }
     fence_before();
