@@ -69,7 +69,7 @@ struct Shared {
   uint64_t full[8], empty[8], s_full[2][2], p_full[2][2], o_full[2][2], q_full, drain[2], ids[kMaskBatches];
   uint32_t tmem;
   int abort;
-  uint32_t flag[8];                       // partly seen keys with non-finite V values
+  alignas(16) uint32_t flag[8];           // partly seen keys with non-finite V values
   int32_t id[kMaskBatches * 32];          // page ids of recent blocks, -1: none
   alignas(16) uint16_t mask[kMaskBatches * 32];  // their slot masks
 };
@@ -181,6 +181,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
       : TKV_R8(r, 0), TKV_R8(r, 8), TKV_R8(r, 16), TKV_R8(r, 24)
       : "r"(addr));
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : TKV_R8(r, 0), TKV_R8(r, 8)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::TKV_W8(r, 0),
+      TKV_W8(r, 8), "r"(addr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
@@ -235,6 +247,22 @@ __device__ __forceinline__ bool strip(uint32_t& w) {
 // Ring position of the i-th K / V block: K blocks run `ahead` blocks ahead of V.
 __device__ __forceinline__ int pos_k(int i, int ahead) { return i + max(0, i - ahead + 1); }
 __device__ __forceinline__ int pos_v(int i, int ahead, int n) { return i + min(n, i + ahead); }
+
+// Adds the non-finite V values of flagged keys (partly seen by the unit) to 16
+// columns of a row that sees keys below lim.
+__device__ __noinline__ void add_flagged(const TileParams& p, const uint32_t* flag, int lim_first, int lim, int64_t key0, int col,
+                                         uint32_t* o) {
+  for (int w = 0; w < 8; ++w)
+    for (uint32_t left = flag[w]; left; left &= left - 1) {
+      const int key = lim_first + w * 32 + __ffs(left) - 1;
+      if (key >= lim) continue;
+      const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + (key0 + key) * p.v_stride + col;
+      for (int e = 0; e < 16; ++e) {
+        const float x = __bfloat162float(v[e]);
+        if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
+      }
+    }
+}
 
 template <int D, bool kPaged>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -450,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kChunks = D / 8;
       const int c = r % kChunks;
       const uint32_t dst = s_q + t * C::tile + (c >> 3) * kBoxBytes;
-#pragma unroll
+#pragma unroll 4
       for (int i = 0; i < kChunks; ++i) {
         const int rr = r / kChunks + i * (kRows / kChunks), x = g_base + first + rr, tok = (x * gmul) >> 16;
         const __nv_bfloat16* src = rr < rows ? q + static_cast<int64_t>(tok_base + tok) * p.q_stride + (x - tok * G) * D + c * 8 : q;
@@ -594,68 +622,90 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t part = p.direct ? 0 : tile_part_row(p, sg, u.grp, u.h, u.split, t);
       // A thread holds a row; rows leave through shared memory, a piece of D bytes
       // of the warp's 32 rows at a time, so that stores are whole sectors of
-      // neighbouring lanes. The Q tile is free by now (a pair's second one always is).
-      constexpr int kPiece = D, kChunk = kPiece / 16;
-      char* stage = smem + (pair ? C::tile + warp * 32 * kPiece : t * C::tile + (warp & 3) * 32 * kPiece);
-      const int row_in_warp = lane / kChunk, ch = lane % kChunk, warp_row = (warp & 3) * 32;
-      constexpr int kCols = 32;  // TMEM columns read at once
-#pragma unroll
-      for (int c = 0; c < D; c += kCols) {
-        uint32_t o[kCols];
-        if (ns[t] > 0) {
-          tmem_ld32(t_o + c, o);
+      // neighbouring lanes. The Q tile is free by now (a pair's second one always
+      // is). Loops stay rolled: this runs once per unit, from a cold instruction cache.
+      constexpr int kChunk = D / 16;
+      char* stage = smem + (pair ? C::tile + warp * 32 * D : t * C::tile + (warp & 3) * 32 * D);
+      uint32_t flagged = 0;
+      if (!kPaged)
+        for (int w = 0; w < 8; w += 4) {
+          const uint4 f = *reinterpret_cast<const uint4*>(&sh.flag[w]);
+          flagged |= f.x | f.y | f.z | f.w;
+        }
+      if (ns[t] == 0 || (!kPaged && flagged)) {
+        // no key: O was never written; or non-finite values to add, in place
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          uint32_t o[16];
+          tmem_ld16(t_o + c, o);
           wait_ld();
-        } else {
+          if (ns[t] == 0) {
 #pragma unroll
-          for (int e = 0; e < kCols; ++e) o[e] = 0;
-        }
-        if (!kPaged) {
-          for (int w = 0; w < 8; ++w)
-            for (uint32_t left = sh.flag[w]; left; left &= left - 1) {
-              const int key = lim_first + w * 32 + __ffs(left) - 1;
-              if (key >= lim) continue;
-              const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + (sg.key0 + key) * p.v_stride + u.h * D + c;
-#pragma unroll
-              for (int e = 0; e < kCols; ++e) {
-                const float x = __bfloat162float(v[e]);
-                if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
-              }
-            }
-        }
-        // what this chunk is in the output's type: kCols values, in pieces of kPiece bytes per row
-        const int out_bytes = p.direct ? kCols * 2 : kCols * 4;
-        const int at = p.direct ? (c % (kPiece / 2)) * 2 : 0;  // bytes of earlier chunks in the piece
-        if (p.direct) {
-#pragma unroll
-          for (int e = 0; e < kCols / 2; ++e)
-            o[e] = pack2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-        }
-        for (int b0 = 0; b0 < out_bytes; b0 += kPiece) {
-#pragma unroll
-          for (int e = 0; e < kCols / 4; ++e) {
-            const int byte = at + e * 16 - b0;
-            if (byte >= 0 && byte < kPiece && e * 16 < out_bytes)
-              *reinterpret_cast<uint4*>(stage + lane * kPiece + (((byte >> 4) ^ (lane % kChunk)) << 4)) =
-                  make_uint4(o[e * 4], o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]);
+            for (int e = 0; e < 16; ++e) o[e] = 0;
+          } else {
+            add_flagged(p, sh.flag, lim_first, lim, sg.key0, u.h * D + c, o);
           }
-          if (at + out_bytes < kPiece) break;  // the next chunk completes the piece
+          tmem_st16(t_o + c, o);
+        }
+        wait_st();
+      }
+      const int ch = lane % kChunk, row_lane = lane / kChunk, swz = lane % kChunk;
+      char* mine = stage + lane * D;
+      if (p.direct) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += D / 2) {
+#pragma unroll
+          for (int half = 0; half < D / 64; ++half) {
+            uint32_t o[32];
+            tmem_ld32(t_o + c + half * 32, o);
+            wait_ld();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                w[j] = pack2(__uint_as_float(o[e * 8 + 2 * j]) * inv, __uint_as_float(o[e * 8 + 2 * j + 1]) * inv);
+              *reinterpret_cast<uint4*>(mine + (((half * 4 + e) ^ swz) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
           __syncwarp();
-          const int col_byte = p.direct ? c * 2 - at : c * 4 + b0;  // where the piece starts in a row
+          uint4 w[kChunk];
 #pragma unroll
           for (int i = 0; i < kChunk; ++i) {
-            const int rr = row_in_warp + i * (32 / kChunk), tile_row = warp_row + rr;
-            const uint4 w = *reinterpret_cast<const uint4*>(stage + rr * kPiece + ((ch ^ (rr % kChunk)) << 4));
-            if (tile_row >= rows) continue;
-            char* to;
-            if (p.direct) {
-              const int x = g_base + first + tile_row, tok = (x * gmul) >> 16;
-              to = reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(p.out) + static_cast<int64_t>(tok_base + tok) * p.out_stride +
-                                           (u.h * G + x - tok * G) * D);
-            } else {
-              to = reinterpret_cast<char*>(p.part_o + (part + tile_row) * D);
-            }
-            *reinterpret_cast<uint4*>(to + col_byte + ch * 16) = w;
+            const int rr = row_lane + i * (32 / kChunk);
+            w[i] = *reinterpret_cast<const uint4*>(stage + rr * D + ((ch ^ (rr % kChunk)) << 4));
           }
+#pragma unroll
+          for (int i = 0; i < kChunk; ++i) {
+            const int tile_row = (warp & 3) * 32 + row_lane + i * (32 / kChunk);
+            const int x = g_base + first + tile_row, tok = (x * gmul) >> 16;
+            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + static_cast<int64_t>(tok_base + tok) * p.out_stride;
+            if (tile_row < rows) *reinterpret_cast<uint4*>(to + (u.h * G + x - tok * G) * D + c + ch * 8) = w[i];
+          }
+          __syncwarp();
+        }
+      } else {
+        float* to = p.part_o + (part + (warp & 3) * 32 + row_lane) * D + ch * 4;
+        const int left = rows - (warp & 3) * 32 - row_lane;
+#pragma unroll 1
+        for (int c = 0; c < D; c += D / 4) {
+          uint32_t o[D / 4];
+          if (D == 128) tmem_ld32(t_o + c, o);
+          else tmem_ld16(t_o + c, o);
+          wait_ld();
+#pragma unroll
+          for (int e = 0; e < kChunk; ++e)
+            *reinterpret_cast<uint4*>(mine + ((e ^ swz) << 4)) = make_uint4(o[e * 4], o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]);
+          __syncwarp();
+          uint4 w[kChunk];
+#pragma unroll
+          for (int i = 0; i < kChunk; ++i) {
+            const int rr = row_lane + i * (32 / kChunk);
+            w[i] = *reinterpret_cast<const uint4*>(stage + rr * D + ((ch ^ (rr % kChunk)) << 4));
+          }
+#pragma unroll
+          for (int i = 0; i < kChunk; ++i)
+            if (i * (32 / kChunk) < left) *reinterpret_cast<uint4*>(to + i * (32 / kChunk) * D + c) = w[i];
           __syncwarp();
         }
       }
