@@ -343,10 +343,10 @@ struct TileShape {
   int slots;         // units the device runs at once
   int unit_cost;     // fixed time of a unit, in key blocks (a block: 64 KB of K and V at d = 128)
 };
-// bf16: one CTA per SM; a unit's start and end take about 5 us, a block about 1.5 us.
+// bf16: one CTA per SM; a unit's end takes about 2 us, a block about 1.5 us.
 // fp32: two 64-row CTAs per SM, whose blocks take several times as long.
 TileShape tile_shape(int dtype) {
-  if (dtype == TKV_DTYPE_BF16) return {128, 2, kSms, 3};
+  if (dtype == TKV_DTYPE_BF16) return {128, 2, kSms, 2};
   return {kFmaRows, 1, 2 * kSms, 1};
 }
 
@@ -598,6 +598,7 @@ tkv_status tkv_prompt_attention(int32_t batch, const int32_t* q_lens, const int3
   p.k = k; p.k_stride = k_stride;
   p.v = v; p.v_stride = v_stride;
   p.out = out; p.out_stride = out_stride;
+  p.out_sectors = !misaligned(out, 32) && out_stride % (2 * unit) == 0;
   p.status = status;
   p.wait_limit_ns = 2000000000ull;
   const cudaError_t e = launch_dtype(p, kv_dtype, head_dim, static_cast<int>(tq), tk, static_cast<cudaStream_t>(stream));
@@ -637,6 +638,7 @@ tkv_status tkv_shared_prefix_attention(int32_t batch, int32_t n_q_heads, int32_t
   if (int st = bind_scratch(p, plan, head_dim, scratch, scratch_bytes)) return tkv_status(st);
   p.q = q; p.q_stride = static_cast<int64_t>(n_q_heads) * head_dim;
   p.out = out; p.out_stride = p.q_stride;
+  p.out_sectors = !misaligned(out, 32);
   p.pool = pool;
   p.pages = pool_pages;
   p.table = page_table;

@@ -42,6 +42,7 @@ struct TileParams {
   int64_t q_stride;            // elements from one token to the next
   void* out;
   int64_t out_stride;
+  int32_t out_sectors;         // 1: rows of out start on multiples of 32 bytes
   const void *k, *v;           // packed keys and values [token][Hkv][D]
   int64_t k_stride, v_stride;
   const void* pool;            // paged: [pages][Hkv][2][16][D]

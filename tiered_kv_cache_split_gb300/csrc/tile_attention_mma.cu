@@ -1,26 +1,36 @@
 // bf16 tiled attention on the 5th-generation tensor cores (terms and plan:
 // tile_attention.h; the mathematics: tile_attention.cu).
 //
-// One CTA per SM runs one unit: up to 256 rows as two tiles of 128 against a
-// stream of 128-key blocks. Eleven warps:
+// One CTA per SM runs unit after unit: up to 256 rows as two tiles of 128
+// against a stream of 128-key blocks, each in two halves of 64. Eleven warps:
 //   0-3, 4-7  softmax of tile 0 / 1: one thread per row (TMEM lane), so row
-//             maxima and sums need no exchange between threads
-//   8         producer: TMA of K and V blocks into a ring of shared-memory slots
+//             maxima and sums need no exchange between threads; they also load
+//             the tile's Q and write its result
+//   8         producer: TMA of K and V blocks into a ring of shared-memory slots,
+//             running ahead into the next unit
 //   9, 10     issue tcgen05.mma for tile 0 / 1: S = Q K^T from shared memory,
 //             O += P V with P read from TMEM. The tensor core takes few MMAs
 //             ahead, so a lone issuer's waits would idle it: with two, one waits
 //             while the other's MMAs run
-// A key block is taken in two halves of 64 keys. TMEM holds, per tile, S of two
-// halves (2 x 64 fp32 columns) and O (D columns); P (bf16) overwrites the S it
-// came from. S of the next half is computed while the softmax works on this
-// one, so a softmax warp finds its next S ready. A segment of at most 128 rows
-// that is split anyway (a decode step) runs as a PAIR: both halves of the CTA
-// hold the same rows and take alternate key blocks, each with a partial of its own.
+// TMEM holds, per tile, S of two halves (2 x 64 fp32 columns) and O (D
+// columns); P (bf16) overwrites the S it came from. S of the next half is
+// computed while the softmax works on this one, so a softmax warp finds its
+// next S ready; the next unit's first two are computed while the last O is
+// written out. A segment of at most 128 rows that is split anyway (a decode
+// step) runs as a PAIR: both tiles hold the same rows, tile t takes half t of
+// every block, and each has a partial of its own.
+//
+// The grid has a CTA per unit; a running CTA takes the units of CTAs that have
+// not started (cluster launch control), so units are handed out in grid order,
+// longest first, without a counter in memory, and a unit's start-up overlaps
+// the end of the one before.
 //
 // Running maximum: O is rescaled only when a row's maximum has risen by more
-// than 2^8 over the one its weights refer to (or at the first key): the weights
-// stay below 2^8, far inside bf16 and fp32, and O and Z always refer to the
-// same maximum, so nothing is lost and most blocks touch O with the MMA alone.
+// than kRise (base 2) over the one its weights refer to, or at the first key.
+// O and Z always refer to the same maximum, and a weight's relative error does
+// not depend on its size, so nothing is lost; weights stay below 2^20 and sums
+// of 2^18 of them below 2^38, far inside fp32. With a rise of 8 one half in six
+// was rescaled, at about 1500 cycles each (prompt of 8192, normal queries).
 //
 // The weights are rounded to bf16 (half a step 2^-8 each, unbiased) because the
 // MMA takes P and V in one type; Z sums them before that rounding, in fp32.
@@ -47,31 +57,37 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kThreads = 352;
 constexpr int kProducer = 8, kIssuer = 9;  // warps; one issuer per tile
-constexpr int kBoxBytes = kKeyBlock * 128;  // 128 rows of 64 bf16 columns, 128-byte swizzle
-constexpr int kHalf = 64;                   // keys of one S
-constexpr int kBatch = 4;                   // key blocks whose page ids are fetched together
-constexpr int kMaskBatches = 4;             // batches the mask ring holds
+constexpr int kHalf = 64;                  // keys of one S
+constexpr int kBlockPages = kKeyBlock / kPage;
+constexpr int kBox = 128 * 128;            // a box: 128 rows of 64 bf16 columns, 128-byte swizzled
+constexpr int kBatch = 4;                  // blocks whose page ids are fetched together
+constexpr float kRise = 20.f;
+constexpr int kSched = 4;                  // units the producer may be ahead of the slowest role
+constexpr int kBatches = 8;                // batches the id ring holds: the producer is at most kSched units and a
+                                           // ring of slots (a batch or two) ahead of the softmax
 
 template <int D>
 struct Cfg {
-  static constexpr int boxes = D / 64;
-  static constexpr int tile = boxes * kBoxBytes;  // bytes of a Q, K or V tile
-  // Q takes 2 tiles; the ring gets what is left of 227 KB (at D = 64 eight
-  // slots keep as many bytes in flight as five do at D = 128)
+  static constexpr int boxes = D / 64, tile = boxes * kBox;  // bytes of a Q, K or V tile
+  // what Q leaves of 227 KB (four slots, with room to stage the output, ran 10 %
+  // slower); at D = 64 eight slots are about as many bytes
   static constexpr int slots = D == 128 ? 5 : 8;
-  static constexpr int smem = 1024 + (2 + slots) * tile;
+  static constexpr int o_ring = 2 * tile, o_shared = o_ring + slots * tile;
   __host__ __device__ static constexpr uint32_t col_o(int t) { return 256 + t * D; }
 };
 
 // Barriers of alternate halves come in pairs: a parity wait tells two phases
 // apart, and up to two halves of a tile are under way.
 struct Shared {
-  uint64_t full[8], empty[8], s_full[2][2], p_full[2][2], o_full[2][2], q_full, drain[2], ids[kMaskBatches];
+  uint64_t full[8], empty[8], s_full[2][2], p_full[2][2], o_prev[2], o_last[2], q_full[2], wg[2], drain[2];
+  uint64_t ids[kBatches], sched_full[kSched], sched_empty[kSched];
+  alignas(16) uint4 response[kSched];
   uint32_t tmem;
   int abort;
-  alignas(16) uint32_t flag[8];           // partly seen keys with non-finite V values
-  int32_t id[kMaskBatches * 32];          // page ids of recent blocks, -1: none
-  alignas(16) uint16_t mask[kMaskBatches * 32];  // their slot masks
+  uint32_t slot_flag[8][4];                  // keys of a V slot whose values were stripped of non-finite ones
+  alignas(16) uint32_t flag[2][8];           // per tile: the unit's partly seen keys with such values
+  int32_t id[kBatches * 32];                 // page ids of recent blocks, -1: none
+  alignas(16) uint16_t mask[kBatches * 32];  // their slot masks
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -201,9 +217,19 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
-// 16 bytes to shared memory; bytes = 0 writes zeros
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+// 16 bytes to shared memory
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// 32 bytes to global memory, in one access where `whole` says the address is a multiple of 32
+__device__ __forceinline__ void store32(void* at, const uint32_t* v, int whole) {
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), TKV_W8(v, 0) : "memory");
+  } else {
+    reinterpret_cast<uint4*>(at)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(at)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -244,9 +270,57 @@ __device__ __forceinline__ bool strip(uint32_t& w) {
   return lo || hi;
 }
 
-// Ring position of the i-th K / V block: K blocks run `ahead` blocks ahead of V.
-__device__ __forceinline__ int pos_k(int i, int ahead) { return i + max(0, i - ahead + 1); }
+// Ring position, from the unit's first, of its i-th V block: K runs `ahead` blocks ahead of V.
 __device__ __forceinline__ int pos_v(int i, int ahead, int n) { return i + min(n, i + ahead); }
+
+// Asks for the unit of a CTA that has not started; 16 bytes arrive at `to`.
+__device__ __forceinline__ void request_unit(uint4* to, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(smem_u32(to)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+// The unit in a response, or -1.
+__device__ __forceinline__ int response_unit(const uint4* at) {
+  uint32_t got, x = 0;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b128 r;\n ld.shared.b128 r, [%2];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}\n"
+      : "=r"(got), "=r"(x)
+      : "r"(smem_u32(at))
+      : "memory");
+  return got ? static_cast<int>(x) : -1;
+}
+
+// What the roles need to know of a unit.
+struct Work {
+  int seg, h, grp, split, row0, rows;
+  int pair, ahead;
+  int block0, n;  // first key block, blocks
+  int ns[2];      // halves each tile works on: a causal tile 0 may end before tile 1
+};
+__device__ __forceinline__ Work unit_work(const TileParams& p, int unit) {
+  const TileUnit u = tile_unit(p, unit);
+  const TileSeg& sg = p.seg[u.seg];
+  Work w;
+  w.seg = u.seg; w.h = u.h; w.grp = u.grp; w.split = u.split; w.row0 = u.row0; w.rows = u.rows;
+  w.pair = sg.pair;
+  w.ahead = w.pair ? 2 : 1;  // two halves per tile
+  w.block0 = u.j0;
+  w.n = u.j1 - u.j0;
+  auto halves = [&](int row) {  // that row `row` sees, from block0
+    return min(2 * w.n, max(0, (tile_row_limit(p, sg, row) + kHalf - 1) / kHalf - 2 * w.block0));
+  };
+  const int all = halves(u.row0 + u.rows - 1);
+  if (w.pair) {
+    w.ns[0] = (all + 1) / 2;
+    w.ns[1] = all / 2;
+  } else {
+    w.ns[0] = u.rows > kRows ? halves(u.row0 + kRows - 1) : all;
+    w.ns[1] = u.rows > kRows ? all : 0;
+  }
+  return w;
+}
 
 // Adds the non-finite V values of flagged keys (partly seen by the unit) to 16
 // columns of a row that sees keys below lim.
@@ -269,10 +343,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tile_mma_kernel(const __grid_constant__ TileParams p, const __grid_constant__ CUtensorMap map_k,
                     const __grid_constant__ CUtensorMap map_v) {
   using C = Cfg<D>;
-  extern __shared__ char smem_raw[];
-  __shared__ Shared sh;
-  char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t s_q = smem_u32(smem), s_ring = s_q + 2 * C::tile;
+  extern __shared__ __align__(1024) char smem[];
+  Shared& sh = *reinterpret_cast<Shared*>(smem + C::o_shared);
+  const uint32_t s_q = smem_u32(smem), s_ring = s_q + C::o_ring;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   volatile int* abort = &sh.abort;
   const uint64_t limit = p.wait_limit_ns;
@@ -290,14 +363,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int b = 0; b < 2; ++b) {
         mbar_init(&sh.s_full[t][b], 1);
         mbar_init(&sh.p_full[t][b], 4);
-        mbar_init(&sh.o_full[t][b], 1);
       }
+      mbar_init(&sh.o_prev[t], 1);
+      mbar_init(&sh.o_last[t], 1);
+      mbar_init(&sh.q_full[t], 4);
+      mbar_init(&sh.wg[t], 4);
       mbar_init(&sh.drain[t], 1);
+      for (int i = 0; i < 8; ++i) sh.flag[t][i] = 0;
     }
-    for (int i = 0; i < kMaskBatches; ++i) mbar_init(&sh.ids[i], 1);
-    mbar_init(&sh.q_full, 8);
+    for (int i = 0; i < kBatches; ++i) mbar_init(&sh.ids[i], 1);
+    for (int i = 0; i < kSched; ++i) {
+      mbar_init(&sh.sched_full[i], 1);
+      mbar_init(&sh.sched_empty[i], 10);  // every warp but the producer's
+    }
     sh.abort = 0;
-    for (int i = 0; i < 8; ++i) sh.flag[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy();
   }
@@ -306,413 +385,460 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
 
-  const TileUnit u = tile_unit(p, blockIdx.x);
-  const TileSeg& sg = p.seg[u.seg];
-  const int pair = sg.pair, ahead = pair ? 2 : 1;
-  const int n = u.j1 - u.j0;  // key blocks
-  // halves each tile works on: a causal tile 0 may end before tile 1
-  int ns[2];
-  if (pair) {
-    ns[0] = (n + 1) / 2 * 2;
-    ns[1] = n / 2 * 2;
-  } else {
-    for (int t = 0; t < 2; ++t) {
-      const int last = min((t + 1) * kRows, u.rows) - 1;
-      const int halves = (tile_row_limit(p, sg, u.row0 + last) + kHalf - 1) / kHalf - 2 * u.j0;
-      ns[t] = last < t * kRows ? 0 : max(min(2 * n, halves), 0);
-    }
-  }
+  // The unit after the CTA's k-th, or -1 at the end or on an abort.
+  auto next_unit = [&](int k) {
+    const int r = k % kSched;
+    if (!warp_wait(&sh.sched_full[r], (k / kSched) & 1, abort, limit)) return -1;
+    const int u = __shfl_sync(0xffffffffu, response_unit(&sh.response[r]), 0);
+    if (warp != kProducer && lane == 0) mbar_arrive(&sh.sched_empty[r]);
+    return u;
+  };
 
   if (warp == kProducer) {
-    int pos = 0;
-    bool ok = true;
-    // page ids and masks, two batches of blocks ahead of their use
-    int32_t id_next = -1, id_after = -1;
-    uint32_t mask_next = 0;
-    const int npages = sg.nkeys / kPage;
-    auto fetch_id = [&](int batch) {
-      const int pg = (u.j0 + batch * kBatch) * (kKeyBlock / kPage) + lane;
-      if (batch * kBatch >= n || pg >= npages) return -1;
-      const int32_t id = p.table[sg.key0 + pg];
-      return id < 0 || id >= p.pages ? -1 : id;
-    };
-    auto fetch_mask = [&](int32_t id) { return id < 0 ? 0u : p.mask[id] & 0xffffu; };
-    if (kPaged) {
-      id_next = fetch_id(0);
-      id_after = fetch_id(1);
-      mask_next = fetch_mask(id_next);
-    }
-    auto load = [&](int i, bool is_v) {
-      if (kPaged && !is_v && i % kBatch == 0) {
-        const int b = i / kBatch, at = b % kMaskBatches * 32 + lane;
-        sh.id[at] = id_next;
-        sh.mask[at] = static_cast<uint16_t>(mask_next);
-        id_next = id_after;
-        mask_next = fetch_mask(id_next);
-        id_after = fetch_id(b + 2);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.ids[b % kMaskBatches]);
+    int pos = 0, batches = 0;
+    int asked = -1;  // a request not answered yet
+    for (int k = 0, unit = blockIdx.x; unit >= 0; ++k) {
+      const int r = k % kSched;
+      if (k >= kSched && !warp_wait(&sh.sched_empty[r], (k / kSched - 1) & 1, abort, limit)) break;
+      if (lane == 0) {
+        fence_proxy();
+        mbar_expect(&sh.sched_full[r], 16);
+        request_unit(&sh.response[r], &sh.sched_full[r]);
       }
-      const int slot = pos % C::slots, round = pos / C::slots;
-      ++pos;
-      if (round > 0 && !warp_wait(&sh.empty[slot], (round - 1) & 1, abort, limit)) return false;
-      const uint32_t dst = s_ring + slot * C::tile;
-      if (lane == 0) mbar_expect(&sh.full[slot], C::tile);
       __syncwarp();
+      asked = k;
+      const Work w = unit_work(p, unit);
+      const TileSeg& sg = p.seg[w.seg];
+      // page ids and masks, a batch ahead of their use
+      int32_t id_next = -1, id_after = -1;
+      uint32_t mask_next = 0;
+      const int npages = sg.nkeys / kPage, page0 = w.block0 * kBlockPages;
+      auto fetch_id = [&](int batch) {
+        const int pg = page0 + batch * 32 + lane;
+        if (batch * kBatch >= w.n || pg >= npages) return -1;
+        const int32_t id = p.table[sg.key0 + pg];
+        return id < 0 || id >= p.pages ? -1 : id;
+      };
+      auto fetch_mask = [&](int32_t id) { return id < 0 ? 0u : p.mask[id] & 0xffffu; };
       if (kPaged) {
-        const int pg = lane & 7, c = lane >> 3;
-        if (c < C::boxes) {
-          const int32_t id = sh.id[(i / kBatch % kMaskBatches) * 32 + i % kBatch * 8 + pg];
-          const int64_t z = id < 0 ? p.pages * p.Hkv * 2 : (static_cast<int64_t>(id) * p.Hkv + u.h) * 2 + is_v;
-          tma_3d(dst + c * kBoxBytes + pg * (kPage * 128), &map_k, c * 64, 0, static_cast<int>(z), &sh.full[slot]);
-        }
-      } else if (lane < C::boxes) {
-        tma_3d(dst + lane * kBoxBytes, is_v ? &map_v : &map_k, lane * 64, u.h, static_cast<int>(sg.key0) + (u.j0 + i) * kKeyBlock,
-               &sh.full[slot]);
+        id_next = fetch_id(0);
+        id_after = fetch_id(1);
+        mask_next = fetch_mask(id_next);
       }
+      auto load = [&](int i, bool is_v) {
+        if (kPaged && !is_v && i % kBatch == 0) {
+          const int b = (batches + i / kBatch) % kBatches, at = b * 32 + lane;
+          sh.id[at] = id_next;
+          sh.mask[at] = static_cast<uint16_t>(mask_next);
+          id_next = id_after;
+          mask_next = fetch_mask(id_next);
+          id_after = fetch_id(i / kBatch + 2);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.ids[b]);
+        }
+        const int slot = pos % C::slots, round = pos / C::slots;
+        if (round > 0 && !warp_wait(&sh.empty[slot], (round - 1) & 1, abort, limit)) return false;
+        ++pos;
+        const uint32_t dst = s_ring + slot * C::tile;
+        if (lane < 4) sh.slot_flag[slot][lane] = 0;
+        __syncwarp();
+        if (lane == 0) mbar_expect(&sh.full[slot], C::tile);
+        __syncwarp();
+        if (kPaged) {
+          const int pg = lane % kBlockPages, c = lane / kBlockPages;
+          if (c < C::boxes) {
+            const int32_t id = sh.id[(batches + i / kBatch) % kBatches * 32 + i % kBatch * kBlockPages + pg];
+            const int64_t z = id < 0 ? p.pages * p.Hkv * 2 : (static_cast<int64_t>(id) * p.Hkv + w.h) * 2 + is_v;
+            tma_3d(dst + c * kBox + pg * (kPage * 128), &map_k, c * 64, 0, static_cast<int>(z), &sh.full[slot]);
+          }
+        } else if (lane < C::boxes) {
+          tma_3d(dst + lane * kBox, is_v ? &map_v : &map_k, lane * 64, w.h, static_cast<int>(sg.key0) + (w.block0 + i) * kKeyBlock,
+                 &sh.full[slot]);
+        }
+        return true;
+      };
+      bool ok = true;
+      for (int i = 0; ok && i < min(w.ahead, w.n); ++i) ok = load(i, false);
+      for (int i = 0; ok && i < w.n; ++i) {
+        ok = load(i, true);
+        if (ok && i + w.ahead < w.n) ok = load(i + w.ahead, false);
+      }
+      if (!ok) break;
+      batches += (w.n + kBatch - 1) / kBatch;
+      unit = next_unit(k);
+      if (!__any_sync(0xffffffffu, *abort)) asked = -1;
+    }
+    // the issuers' arrivals on the last slots come before this shared memory is another CTA's
+    for (int q = max(0, pos - C::slots); q < pos; ++q)
+      if (!warp_wait(&sh.empty[q % C::slots], (q / C::slots) & 1, abort, limit)) break;
+    // an aborted CTA lets what is in flight land before it ends
+    if (__any_sync(0xffffffffu, *abort)) {
+      if (asked >= 0) warp_wait(&sh.sched_full[asked % kSched], (asked / kSched) & 1, nullptr, limit);
+      for (int q = max(0, pos - C::slots); q < pos; ++q) warp_wait(&sh.full[q % C::slots], (q / C::slots) & 1, nullptr, limit);
+    }
+  } else if (warp >= kIssuer) {
+    const uint32_t leader = elect_leader();
+    const int t = warp - kIssuer;
+    constexpr uint32_t kIdescS = instr_desc(kHalf, false), kIdescO = instr_desc(D, true);
+    const uint64_t desc_q = smem_desc(s_q + t * C::tile, 16, 1024);
+    const uint32_t t_s = tmem + t * 2 * kHalf, t_o = tmem + C::col_o(t);
+    int g0 = 0, used = 0;          // halves and units of this tile so far
+    int slot = 0, slot_phase = 0;  // the ring slot to take next
+    // Both issuers take every ring slot in turn and give it back, one that does
+    // not use it as soon as it is full.
+    auto take = [&](int* at) {
+      *at = slot;
+      const bool ready = warp_wait(&sh.full[slot], slot_phase, abort, limit);
+      if (++slot == C::slots) {
+        slot = 0;
+        slot_phase ^= 1;
+      }
+      return ready;
+    };
+    auto release = [&](int at) { mma_commit(leader, &sh.empty[at]); };
+    // S of the tile's g-th half = Q K^T over one half of the K block
+    auto qk = [&](int g, int at, int half) {
+      const uint64_t b = smem_desc(s_ring + at * C::tile + half * (kHalf * 128), 16, 1024);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t off = ((k / 4) * kBox + (k % 4) * 32) >> 4;
+        mma_ss(leader, t_s + (g & 1) * kHalf, desc_q + off, b + off, kIdescS, k > 0);
+      }
+      mma_commit(leader, &sh.s_full[t][g & 1]);
+    };
+    // O (+)= P V for the unit's h-th half of this tile
+    auto pv = [&](int h, int at, int half, int mine) {
+      const int g = g0 + h;
+      if (!warp_wait(&sh.p_full[t][g & 1], (g >> 1) & 1, abort, limit)) return false;
+      fence_after();
+      const uint64_t b = smem_desc(s_ring + at * C::tile + half * (kHalf * 128), kBox, 1024);
+#pragma unroll
+      for (int k = 0; k < kHalf / 16; ++k)
+        mma_ts(leader, t_o, t_s + (g & 1) * kHalf + k * 8, b + k * (2048 >> 4), kIdescO, h > 0 || k > 0);
+      if (h == mine - 2) mma_commit(leader, &sh.o_prev[t]);
+      if (h == mine - 1) mma_commit(leader, &sh.o_last[t]);
       return true;
     };
-    for (int i = 0; ok && i < min(ahead, n); ++i) ok = load(i, false);
-    for (int i = 0; ok && i < n; ++i) {
-      ok = load(i, true);
-      if (ok && i + ahead < n) ok = load(i + ahead, false);
-    }
-    if (!ok) --pos;  // the load that gave up was not issued
-    // an aborted CTA lets the copies in flight land before it ends
-    if (*abort)
-      for (int q = max(0, pos - C::slots); q < pos; ++q) warp_wait(&sh.full[q % C::slots], (q / C::slots) & 1, nullptr, limit);
-  } else if (warp >= kIssuer) {
-    {
-      const uint32_t leader = elect_leader();
-      const int t = warp - kIssuer;
-      constexpr uint32_t kIdescS = instr_desc(kHalf, false), kIdescO = instr_desc(D, true);
-      const uint64_t desc_q = smem_desc(s_q + (pair ? 0 : t) * C::tile, 16, 1024);
-      const uint32_t t_s = tmem + t * kKeyBlock, t_o = tmem + C::col_o(t);
-      auto slot_ready = [&](int pos) { return warp_wait(&sh.full[pos % C::slots], (pos / C::slots) & 1, abort, limit); };
-      // S of the h-th half = Q K^T over half h & 1 of the K block at ring position pos
-      auto qk = [&](int h, int pos) {
-        const uint64_t b = smem_desc(s_ring + pos % C::slots * C::tile + (h & 1) * (kHalf * 128), 16, 1024);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = ((k / 4) * kBoxBytes + (k % 4) * 32) >> 4;
-          mma_ss(leader, t_s + (h & 1) * kHalf, desc_q + off, b + off, kIdescS, k > 0);
-        }
-        mma_commit(leader, &sh.s_full[t][h & 1]);
-      };
-      // O += P V over the same half of the V block
-      auto pv = [&](int h, int pos) {
-        const uint64_t b = smem_desc(s_ring + pos % C::slots * C::tile + (h & 1) * (kHalf * 128), kBoxBytes, 1024);
-#pragma unroll
-        for (int k = 0; k < kHalf / 16; ++k)
-          mma_ts(leader, t_o, t_s + (h & 1) * kHalf + k * 8, b + k * (2048 >> 4), kIdescO, h > 0 || k > 0);
-        mma_commit(leader, &sh.o_full[t][h & 1]);
-      };
-      auto p_ready = [&](int h) {
-        const bool ready = warp_wait(&sh.p_full[t][h & 1], (h >> 1) & 1, abort, limit);
+    for (int k = 0, unit = blockIdx.x; unit >= 0; ++k) {
+      const Work w = unit_work(p, unit);
+      const int mine = w.ns[t];
+      // a tile without rows or keys in this unit leaves the barriers of Q, S, P and O alone
+      if (mine > 0) {
+        if (!warp_wait(&sh.q_full[t], used++ & 1, abort, limit)) break;
         fence_after();
-        return ready;
-      };
-      // Both issuers pass every ring slot in turn and give it back: one that does
-      // not use it at once, but never before it is full. A slot no later block
-      // takes is not given back: nobody would wait for that arrival, and it could
-      // reach the shared memory of the next CTA on this SM.
-      auto release = [&](int pos) {
-        if (pos + C::slots < 2 * n) mma_commit(leader, &sh.empty[pos % C::slots]);
-      };
-      auto run = [&]() {
-        if (n == 0 || !warp_wait(&sh.q_full, 0, abort, limit)) return;
-        fence_after();
-        const int mine = ns[t];
-        for (int i = 0; i < min(ahead, n); ++i) {
-          if (!slot_ready(i)) return;
-          if (!pair || i == t) {
-            if (0 < mine) qk(0, i);
-            if (1 < mine) qk(1, i);
-          }
-          release(i);
-        }
-        for (int i = 0; i < n; ++i) {
-          const int at = pos_v(i, ahead, n), pk = pos_k(i + ahead, ahead);
-          const bool more = i + ahead < n, use = !pair || (i & 1) == t;
-          const int h = pair ? i >> 1 << 1 : 2 * i;  // the tile's halves of block i: h, h + 1
-          if (!slot_ready(at)) return;
-          if (use && h < mine) {
-            if (!p_ready(h)) return;
-            pv(h, at);
-          }
-          if (more) {
-            if (!slot_ready(pk)) return;
-            if (use && h + 2 < mine) qk(h + 2, pk);
-          }
-          if (use && h + 1 < mine) {
-            if (!p_ready(h + 1)) return;
-            pv(h + 1, at);
-          }
+      }
+      bool ok = true;
+      if (w.pair) {
+        for (int i = 0, at; i < min(2, w.n); ++i) {
+          if (!(ok = take(&at))) break;
+          if (i < mine) qk(g0 + i, at, t);
           release(at);
-          if (more) {
-            if (use && h + 3 < mine) qk(h + 3, pk);
-            release(pk);
-          }
         }
-      };
-      run();
-      if (*abort) {
-        mma_commit(leader, &sh.drain[t]);
-        warp_wait(&sh.drain[t], 0, nullptr, limit);
-      }
-    }
-  } else {
-    const int t = warp >> 2, r = tid & 127;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp & 3) << 21);
-    const uint32_t t_s = lane_base + t * kKeyBlock, t_o = lane_base + C::col_o(t);
-    const int G = p.G;
-    const int first = pair ? 0 : t * kRows;  // the tile's first row in the unit
-    const int rows = min(kRows, u.rows - first);
-    const int row = u.row0 + first + min(r, max(rows - 1, 0));
-    const bool valid = r < rows;
-    // Q tile into shared memory in the swizzled layout; rows past the end are 0
-    const int tok_base = sg.tok0 + u.row0 / G, g_base = u.row0 % G;  // of the unit's first row
-    const uint32_t gmul = (65535 + G) / G;  // (x * gmul) >> 16 = x / G for x < 320, G <= 64
-    if (!pair || t == 0) {
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + u.h * G * D;
-      constexpr int kChunks = D / 8;
-      const int c = r % kChunks;
-      const uint32_t dst = s_q + t * C::tile + (c >> 3) * kBoxBytes;
-#pragma unroll 4
-      for (int i = 0; i < kChunks; ++i) {
-        const int rr = r / kChunks + i * (kRows / kChunks), x = g_base + first + rr, tok = (x * gmul) >> 16;
-        const __nv_bfloat16* src = rr < rows ? q + static_cast<int64_t>(tok_base + tok) * p.q_stride + (x - tok * G) * D + c * 8 : q;
-        cp_async16(dst + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), src, rr < rows ? 16 : 0);
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_proxy();
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.q_full);
-
-    const int lim = tile_row_limit(p, sg, row);
-    const int lim_first = tile_row_limit(p, sg, u.row0), lim_last = tile_row_limit(p, sg, u.row0 + u.rows - 1);
-    const int lim_warp = __shfl_sync(0xffffffffu, lim, 0);  // limits rise with the row
-    const float qs = p.qscale;
-    float ref = -INFINITY, z = 0.f;  // maximum the weights refer to (unscaled logits), sum of weights
-    bool ok = true;
-    for (int h = 0; ok && h < ns[t]; ++h) {
-      const int i = pair ? (h >> 1) * 2 + t : h >> 1, half = h & 1;
-      const int k0 = (u.j0 + i) * kKeyBlock + half * kHalf;
-      uint32_t live[2] = {~0u, ~0u};
-      if (kPaged) {
-        const int b = i / kBatch;
-        if (!(ok = warp_wait(&sh.ids[b % kMaskBatches], (b / kMaskBatches) & 1, abort, limit))) break;
-        const uint2 w = *reinterpret_cast<const uint2*>(&sh.mask[b % kMaskBatches * 32 + i % kBatch * 8 + half * 4]);
-        live[0] = w.x;
-        live[1] = w.y;
-      }
-      const bool holes = kPaged && (live[0] & live[1]) != ~0u;
-      const bool cut = !kPaged && k0 + kHalf > lim_warp;
-      const bool clean = holes || (!kPaged && k0 + kHalf > lim_first);
-
-      if (!(ok = warp_wait(&sh.s_full[t][half], (h >> 1) & 1, abort, limit))) break;
-      fence_after();
-      uint32_t s[kHalf];
-      tmem_ld32(t_s + half * kHalf, s);
-      tmem_ld32(t_s + half * kHalf + 32, s + 32);
-      wait_ld();
-      if (cut) {
-        const int m = lim - k0;
-#pragma unroll
-        for (int c = 0; c < kHalf; ++c) s[c] = c < m ? s[c] : 0xff800000u;
-      }
-      if (holes) {
-#pragma unroll
-        for (int c = 0; c < kHalf; ++c) s[c] = (live[c / 32] >> (c % 32)) & 1u ? s[c] : 0xff800000u;
-      }
-      if (kPaged && sg.spill0 >= 0 && valid) {
-        float4* at = reinterpret_cast<float4*>(p.spill + sg.spill0 + static_cast<int64_t>(u.h * G + row % G) * sg.nkeys + k0);
-#pragma unroll
-        for (int c = 0; c < kHalf / 4; ++c)
-          if (k0 + c * 4 < sg.nkeys)
-            at[c] = make_float4(__uint_as_float(s[c * 4]) * qs, __uint_as_float(s[c * 4 + 1]) * qs,
-                                __uint_as_float(s[c * 4 + 2]) * qs, __uint_as_float(s[c * 4 + 3]) * qs);
-      }
-      float top[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) top[c] = max3(__uint_as_float(s[c]), __uint_as_float(s[c + 4]), __uint_as_float(s[c + 8]));
-#pragma unroll
-      for (int c = 12; c < 60; c += 8)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) top[e] = max3(top[e], __uint_as_float(s[c + e]), __uint_as_float(s[c + 4 + e]));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], __uint_as_float(s[60 + e]));
-      const float next = fmaxf(max3(ref, top[0], top[1]), fmaxf(top[2], top[3]));
-      if (__any_sync(0xffffffffu, (next - ref) * qs > 8.f)) {
-        const float f = next == -INFINITY ? 1.f : ex2((ref - next) * qs);
-        if (h > 0) {
-          if (!(ok = warp_wait(&sh.o_full[t][(h - 1) & 1], ((h - 1) >> 1) & 1, abort, limit))) break;
-          fence_after();
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(t_o + c, o);
-            wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(t_o + c, o);
+        for (int i = 0, at; ok && i < w.n; ++i) {
+          if (!(ok = take(&at))) break;
+          if (i < mine && !(ok = pv(i, at, t, mine))) break;
+          release(at);
+          if (i + 2 < w.n) {
+            if (!(ok = take(&at))) break;
+            if (i + 2 < mine) qk(g0 + i + 2, at, t);
+            release(at);
           }
-          z *= f;
-        }
-        ref = next;
-      }
-      const float base = ref == -INFINITY ? 0.f : ref * qs;
-      const float2 qs2 = make_float2(qs, qs), base2 = make_float2(-base, -base);
-      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-      for (int c = 0; c < kHalf / 2; ++c) {
-        float2 x = fma2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), qs2, base2);
-        x.x = ex2(x.x);
-        x.y = ex2(x.y);
-        sum[c & 1] = add2(sum[c & 1], x);
-        s[c] = pack2(x.x, x.y);
-      }
-      tmem_st32(t_s + half * kHalf, s);
-      z += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-      if (clean) {
-        const int pv = pos_v(i, ahead, n), kr = half * kHalf + (r & 63), key = k0 + (r & 63);
-        if (!(ok = warp_wait(&sh.full[pv % C::slots], (pv / C::slots) & 1, abort, limit))) break;
-        const bool none = kPaged ? !((live[(r & 63) >> 5] >> (r & 31)) & 1u) : key >= lim_last;
-        if (none || (!kPaged && key >= lim_first)) {
-          // two threads per key, half of its columns each; where both tiles use the
-          // block both clean it, with the same result
-          char* at = smem + (2 + pv % C::slots) * C::tile + kr * 128;
-#pragma unroll 2
-          for (int e = 0; e < D / 16; ++e) {
-            const int c = (r >> 6) * (D / 16) + e;
-            uint4* w = reinterpret_cast<uint4*>(at + (c >> 3) * kBoxBytes + (((c + kr) & 7) << 4));
-            if (none) {
-              *w = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            uint4 x = *w;
-            const bool bad = strip(x.x) | strip(x.y) | strip(x.z) | strip(x.w);
-            if (bad) {  // the flag first: who reads the stripped value finds the flag set
-              atomicOr(&sh.flag[(key - lim_first) >> 5], 1u << ((key - lim_first) & 31));
-              __threadfence_block();
-              *w = x;
-            }
-          }
-        }
-        fence_proxy();
-      }
-      wait_st();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.p_full[t][half]);
-    }
-    // every key this tile's rows see has been looked at by its own warps, or was
-    // found stripped with its flag set before
-    if (!kPaged) {
-      __threadfence_block();
-      asm volatile("bar.sync %0, 128;" ::"r"(t + 1) : "memory");
-    }
-    if (ok && ns[t] > 0) {
-      ok = warp_wait(&sh.o_full[t][(ns[t] - 1) & 1], ((ns[t] - 1) >> 1) & 1, abort, limit);
-      fence_after();
-    }
-    if (ok && rows > 0) {
-      const float inv = z > 0.f || z != z ? 1.f / z : 0.f;
-      const int64_t part = p.direct ? 0 : tile_part_row(p, sg, u.grp, u.h, u.split, t);
-      // A thread holds a row; rows leave through shared memory, a piece of D bytes
-      // of the warp's 32 rows at a time, so that stores are whole sectors of
-      // neighbouring lanes. The Q tile is free by now (a pair's second one always
-      // is). Loops stay rolled: this runs once per unit, from a cold instruction cache.
-      constexpr int kChunk = D / 16;
-      char* stage = smem + (pair ? C::tile + warp * 32 * D : t * C::tile + (warp & 3) * 32 * D);
-      uint32_t flagged = 0;
-      if (!kPaged)
-        for (int w = 0; w < 8; w += 4) {
-          const uint4 f = *reinterpret_cast<const uint4*>(&sh.flag[w]);
-          flagged |= f.x | f.y | f.z | f.w;
-        }
-      if (ns[t] == 0 || (!kPaged && flagged)) {
-        // no key: O was never written; or non-finite values to add, in place
-#pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          uint32_t o[16];
-          tmem_ld16(t_o + c, o);
-          wait_ld();
-          if (ns[t] == 0) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = 0;
-          } else {
-            add_flagged(p, sh.flag, lim_first, lim, sg.key0, u.h * D + c, o);
-          }
-          tmem_st16(t_o + c, o);
-        }
-        wait_st();
-      }
-      const int ch = lane % kChunk, row_lane = lane / kChunk, swz = lane % kChunk;
-      char* mine = stage + lane * D;
-      if (p.direct) {
-#pragma unroll 1
-        for (int c = 0; c < D; c += D / 2) {
-#pragma unroll
-          for (int half = 0; half < D / 64; ++half) {
-            uint32_t o[32];
-            tmem_ld32(t_o + c + half * 32, o);
-            wait_ld();
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t w[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                w[j] = pack2(__uint_as_float(o[e * 8 + 2 * j]) * inv, __uint_as_float(o[e * 8 + 2 * j + 1]) * inv);
-              *reinterpret_cast<uint4*>(mine + (((half * 4 + e) ^ swz) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
-          __syncwarp();
-          uint4 w[kChunk];
-#pragma unroll
-          for (int i = 0; i < kChunk; ++i) {
-            const int rr = row_lane + i * (32 / kChunk);
-            w[i] = *reinterpret_cast<const uint4*>(stage + rr * D + ((ch ^ (rr % kChunk)) << 4));
-          }
-#pragma unroll
-          for (int i = 0; i < kChunk; ++i) {
-            const int tile_row = (warp & 3) * 32 + row_lane + i * (32 / kChunk);
-            const int x = g_base + first + tile_row, tok = (x * gmul) >> 16;
-            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + static_cast<int64_t>(tok_base + tok) * p.out_stride;
-            if (tile_row < rows) *reinterpret_cast<uint4*>(to + (u.h * G + x - tok * G) * D + c + ch * 8) = w[i];
-          }
-          __syncwarp();
         }
       } else {
-        float* to = p.part_o + (part + (warp & 3) * 32 + row_lane) * D + ch * 4;
-        const int left = rows - (warp & 3) * 32 - row_lane;
-#pragma unroll 1
-        for (int c = 0; c < D; c += D / 4) {
-          uint32_t o[D / 4];
-          if (D == 128) tmem_ld32(t_o + c, o);
-          else tmem_ld16(t_o + c, o);
-          wait_ld();
-#pragma unroll
-          for (int e = 0; e < kChunk; ++e)
-            *reinterpret_cast<uint4*>(mine + ((e ^ swz) << 4)) = make_uint4(o[e * 4], o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]);
-          __syncwarp();
-          uint4 w[kChunk];
-#pragma unroll
-          for (int i = 0; i < kChunk; ++i) {
-            const int rr = row_lane + i * (32 / kChunk);
-            w[i] = *reinterpret_cast<const uint4*>(stage + rr * D + ((ch ^ (rr % kChunk)) << 4));
+        int at_k, at_v;
+        if (w.n > 0) {
+          if (!take(&at_k)) break;
+          if (0 < mine) qk(g0, at_k, 0);
+          if (1 < mine) qk(g0 + 1, at_k, 1);
+          release(at_k);
+        }
+        for (int i = 0; i < w.n; ++i) {
+          const int h = 2 * i;
+          if (!(ok = take(&at_v))) break;
+          if (h < mine && !(ok = pv(h, at_v, 0, mine))) break;
+          if (i + 1 < w.n) {
+            if (!(ok = take(&at_k))) break;
+            if (h + 2 < mine) qk(g0 + h + 2, at_k, 0);
           }
-#pragma unroll
-          for (int i = 0; i < kChunk; ++i)
-            if (i * (32 / kChunk) < left) *reinterpret_cast<uint4*>(to + i * (32 / kChunk) * D + c) = w[i];
-          __syncwarp();
+          if (h + 1 < mine && !(ok = pv(h + 1, at_v, 1, mine))) break;
+          release(at_v);
+          if (i + 1 < w.n) {
+            if (h + 3 < mine) qk(g0 + h + 3, at_k, 1);
+            release(at_k);
+          }
         }
       }
-      if (!p.direct && valid) {
-        p.part_m[part + r] = ref * qs;
-        p.part_z[part + r] = z;
+      if (!ok) break;
+      g0 += mine;
+      unit = next_unit(k);
+    }
+    if (__any_sync(0xffffffffu, *abort)) {
+      mma_commit(leader, &sh.drain[t]);
+      warp_wait(&sh.drain[t], 0, nullptr, limit);
+    }
+  } else {
+    const int t = warp >> 2, r = tid & 127, wq = warp & 3;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(wq) << 21);
+    const uint32_t t_s = lane_base + t * 2 * kHalf, t_o = lane_base + C::col_o(t);
+    const int G = p.G;
+    const uint32_t gmul = (65535 + G) / G;  // (x * gmul) >> 16 = x / G for x < 320, G <= 64
+    const float qs = p.qscale;
+    // Q rows of a unit into the tile's shared memory, swizzled; rows past the end
+    // keep what is there: a row's S, P and O depend on its own Q alone
+    auto load_q = [&](const Work& w) {
+      const TileSeg& sg = p.seg[w.seg];
+      const int first = w.pair ? 0 : t * kRows, rows = min(kRows, w.rows - first);
+      const int tok_base = sg.tok0 + w.row0 / G, g_base = w.row0 % G + first;
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + w.h * G * D;
+      constexpr int kChunks = D / 8;
+      const int c = r % kChunks;
+      const uint32_t dst = s_q + t * C::tile + (c >> 3) * kBox;
+#pragma unroll 4
+      for (int rr = r / kChunks; rr < rows; rr += kRows / kChunks) {
+        const int x = g_base + rr, tok = (x * gmul) >> 16;
+        cp_async16(dst + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), q + static_cast<int64_t>(tok_base + tok) * p.q_stride + (x - tok * G) * D + c * 8);
       }
+    };
+    int syncs = 0;
+    auto tile_sync = [&]() {  // the tile's four warps
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.wg[t]);
+      return warp_wait(&sh.wg[t], syncs++ & 1, abort, limit);
+    };
+    int pos0 = 0, g0 = 0, batches = 0, used = 0, used2 = 0;  // used2: units with two halves or more
+    int unit = blockIdx.x;
+    Work w = unit_work(p, unit);
+    load_q(w);
+    for (int k = 0; unit >= 0; ++k) {
+      const TileSeg& sg = p.seg[w.seg];
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy();
+      __syncwarp();
+      if (lane == 0 && w.ns[t] > 0) mbar_arrive(&sh.q_full[t]);
+
+      const int first = w.pair ? 0 : t * kRows;  // the tile's first row in the unit
+      const int rows = min(kRows, w.rows - first), mine = w.ns[t];
+      const int row = w.row0 + first + min(r, max(rows - 1, 0));
+      const bool valid = r < rows, active = wq * 32 < rows;  // active: the warp has rows at all
+      const int lim = tile_row_limit(p, sg, row);
+      const int lim_first = tile_row_limit(p, sg, w.row0), lim_last = tile_row_limit(p, sg, w.row0 + w.rows - 1);
+      const int lim_warp = __shfl_sync(0xffffffffu, lim, 0);  // limits rise with the row
+      float ref = -INFINITY, z = 0.f;  // maximum the weights refer to (unscaled logits), sum of weights
+      bool ok = true;
+      for (int h = 0; h < mine; ++h) {
+        const int i = w.pair ? h : h >> 1, half = w.pair ? t : h & 1, g = g0 + h, buf = g & 1;
+        const int k0 = (w.block0 + i) * kKeyBlock + half * kHalf;
+        uint32_t live[2] = {~0u, ~0u};
+        if (kPaged) {
+          const int b = batches + i / kBatch;
+          if (!(ok = warp_wait(&sh.ids[b % kBatches], (b / kBatches) & 1, abort, limit))) break;
+          const uint2 x = *reinterpret_cast<const uint2*>(&sh.mask[b % kBatches * 32 + i % kBatch * kBlockPages + half * (kBlockPages / 2)]);
+          live[0] = x.x;
+          live[1] = x.y;
+        }
+        const bool holes = kPaged && (live[0] & live[1]) != ~0u;
+        const bool cut = !kPaged && k0 + kHalf > lim_warp;
+        const bool clean = holes || (!kPaged && k0 + kHalf > lim_first);
+
+        if (!(ok = warp_wait(&sh.s_full[t][buf], (g >> 1) & 1, abort, limit))) break;
+        fence_after();
+        if (active) {
+          uint32_t s[kHalf];
+          tmem_ld32(t_s + buf * kHalf, s);
+          tmem_ld32(t_s + buf * kHalf + 32, s + 32);
+          wait_ld();
+          if (cut) {
+            const int m = lim - k0;
+#pragma unroll
+            for (int c = 0; c < kHalf; ++c) s[c] = c < m ? s[c] : 0xff800000u;
+          }
+          if (holes) {
+#pragma unroll
+            for (int c = 0; c < kHalf; ++c) s[c] = (live[c / 32] >> (c % 32)) & 1u ? s[c] : 0xff800000u;
+          }
+          if (kPaged && sg.spill0 >= 0 && valid) {
+            float4* at = reinterpret_cast<float4*>(p.spill + sg.spill0 + static_cast<int64_t>(w.h * G + row % G) * sg.nkeys + k0);
+#pragma unroll
+            for (int c = 0; c < kHalf / 4; ++c)
+              if (k0 + c * 4 < sg.nkeys)
+                at[c] = make_float4(__uint_as_float(s[c * 4]) * qs, __uint_as_float(s[c * 4 + 1]) * qs,
+                                    __uint_as_float(s[c * 4 + 2]) * qs, __uint_as_float(s[c * 4 + 3]) * qs);
+          }
+          float top[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) top[c] = max3(__uint_as_float(s[c]), __uint_as_float(s[c + 4]), __uint_as_float(s[c + 8]));
+#pragma unroll
+          for (int c = 12; c < 60; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top[e] = max3(top[e], __uint_as_float(s[c + e]), __uint_as_float(s[c + 4 + e]));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], __uint_as_float(s[60 + e]));
+          const float next = fmaxf(max3(ref, top[0], top[1]), fmaxf(top[2], top[3]));
+          if (__any_sync(0xffffffffu, valid && (next - ref) * qs > kRise)) {
+            const float f = next == -INFINITY ? 1.f : ex2((ref - next) * qs);
+            if (h > 0) {
+              // the product before: behind it comes S of the next half, or for the last half its own signal
+              if (h < mine - 1) ok = warp_wait(&sh.s_full[t][(g + 1) & 1], ((g + 1) >> 1) & 1, abort, limit);
+              else ok = warp_wait(&sh.o_prev[t], used2 & 1, abort, limit);
+              if (!ok) break;
+              fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(t_o + c, o);
+                wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st32(t_o + c, o);
+              }
+              z *= f;
+            }
+            ref = next;
+          }
+          const float base = ref == -INFINITY ? 0.f : ref * qs;
+          const float2 qs2 = make_float2(qs, qs), base2 = make_float2(-base, -base);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < kHalf / 2; ++c) {
+            float2 x = fma2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), qs2, base2);
+            x.x = ex2(x.x);
+            x.y = ex2(x.y);
+            sum[c & 1] = add2(sum[c & 1], x);
+            s[c] = pack2(x.x, x.y);
+          }
+          tmem_st32(t_s + buf * kHalf, s);
+          z += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        }
+        if (clean) {
+          const int at_v = pos0 + pos_v(i, w.ahead, w.n), slot = at_v % C::slots, round = at_v / C::slots;
+          const int kr = half * kHalf + (r & 63), key = k0 + (r & 63);
+          if (!(ok = warp_wait(&sh.full[slot], round & 1, abort, limit))) break;
+          const bool none = kPaged ? !((live[(r & 63) >> 5] >> (r & 31)) & 1u) : key >= lim_last;
+          if (none || (!kPaged && key >= lim_first)) {
+            // two threads per key, half of its columns each; where both tiles use the
+            // half both clean it, with the same result
+            char* at = smem + C::o_ring + slot * C::tile + kr * 128;
+#pragma unroll 2
+            for (int e = 0; e < D / 16; ++e) {
+              const int c = (r >> 6) * (D / 16) + e;
+              uint4* v = reinterpret_cast<uint4*>(at + (c >> 3) * kBox + (((c + kr) & 7) << 4));
+              if (none) {
+                *v = make_uint4(0, 0, 0, 0);
+                continue;
+              }
+              uint4 x = *v;
+              const bool bad = strip(x.x) | strip(x.y) | strip(x.z) | strip(x.w);
+              if (bad) {  // the flag first: who reads the stripped value finds the flag set
+                atomicOr(&sh.slot_flag[slot][kr >> 5], 1u << (kr & 31));
+                __threadfence_block();
+                *v = x;
+              }
+            }
+          }
+          if (!kPaged) {
+            // every value of the half has been looked at by this tile's warps, or was
+            // found stripped with its flag set: note the flags before the slot goes
+            __threadfence_block();
+            if (!(ok = tile_sync())) break;
+            const uint32_t f = lane < 2 ? sh.slot_flag[slot][half * 2 + lane] : 0;
+            if (wq == 0)
+              for (uint32_t left = f; left; left &= left - 1) {
+                const int part = k0 + lane * 32 + __ffs(left) - 1 - lim_first;
+                atomicOr(&sh.flag[t][part >> 5], 1u << (part & 31));
+              }
+          }
+          fence_proxy();
+        }
+        wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[t][buf]);
+      }
+      // Q is free: the tile's last S has been seen. Load the next unit's while this one's O is finished.
+      Work next_w;
+      int next = -1;
+      if (ok) {
+        next = next_unit(k);
+        if (next >= 0) {
+          next_w = unit_work(p, next);
+          load_q(next_w);
+        }
+        ok = !__any_sync(0xffffffffu, *abort);
+      }
+      if (ok && mine > 0) {
+        ok = warp_wait(&sh.o_last[t], used & 1, abort, limit);
+        fence_after();
+      }
+      uint32_t flagged = 0;
+      if (!kPaged && ok && w.rows > 0) {
+        __threadfence_block();
+        ok = tile_sync();
+        for (int i = 0; i < 8; i += 4) {
+          const uint4 f = *reinterpret_cast<const uint4*>(&sh.flag[t][i]);
+          flagged |= f.x | f.y | f.z | f.w;
+        }
+      }
+      if (!ok) break;
+      if (active && rows > 0) {
+        const float inv = z > 0.f || z != z ? 1.f / z : 0.f;
+        const int64_t part = p.direct ? 0 : tile_part_row(p, sg, w.grp, w.h, w.split, t);
+        if (mine == 0 || (!kPaged && flagged)) {
+          // no key: O was never written; or non-finite values to add, in place
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(t_o + c, o);
+            wait_ld();
+            if (mine == 0) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = 0;
+            } else {
+              add_flagged(p, sh.flag[t], lim_first, lim, sg.key0, w.h * D + c, o);
+            }
+            tmem_st16(t_o + c, o);
+          }
+          wait_st();
+        }
+        // a thread holds a row and stores it by whole 32-byte sectors
+        const int x = w.row0 % G + first + r, tok = (x * gmul) >> 16;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + static_cast<int64_t>(sg.tok0 + w.row0 / G + tok) * p.out_stride +
+                             (w.h * G + x - tok * G) * D;
+        float* po = p.part_o + (part + r) * D;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(t_o + c, o);
+          wait_ld();
+          if (!valid) continue;
+          if (p.direct) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = pack2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+            store32(out + c, o, p.out_sectors);
+            store32(out + c + 16, o + 8, p.out_sectors);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) store32(po + c + e * 8, o + e * 8, 1);
+          }
+        }
+        if (!p.direct && valid) {
+          p.part_m[part + r] = ref * qs;
+          p.part_z[part + r] = z;
+        }
+      }
+      if (!kPaged && flagged) {  // clear the tile's flags once all of its warps have used them
+        if (!tile_sync()) break;
+        if (wq == 0 && lane < 8) sh.flag[t][lane] = 0;
+        __threadfence_block();
+        if (!tile_sync()) break;
+      }
+      fence_before();
+      pos0 += 2 * w.n;
+      g0 += mine;
+      used += mine > 0;
+      used2 += mine > 1;
+      batches += (w.n + kBatch - 1) / kBatch;
+      unit = next;
+      w = next_w;
     }
     fence_before();
   }
@@ -752,7 +878,8 @@ bool encode(CUtensorMap* map, const void* base, int d, uint64_t n1, uint64_t n2,
 
 template <int D, bool kPaged>
 cudaError_t launch(const TileParams& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
-  constexpr int bytes = Cfg<D>::smem;
+  constexpr int bytes = Cfg<D>::o_shared + static_cast<int>(sizeof(Shared));
+  static_assert(bytes <= 227 * 1024, "shared memory");
   const cudaError_t e = cudaFuncSetAttribute(tile_mma_kernel<D, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   tile_mma_kernel<D, kPaged><<<static_cast<unsigned>(p.units), kThreads, bytes, s>>>(p, k, v);
