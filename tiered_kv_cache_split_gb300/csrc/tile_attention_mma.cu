@@ -2,16 +2,18 @@
 // tile_attention.h; the mathematics: tile_attention.cu).
 //
 // One CTA per SM runs unit after unit: up to 256 rows as two tiles of 128
-// against a stream of 128-key blocks, each in two halves of 64. Eleven warps:
+// against a stream of 128-key blocks, each in two halves of 64. Twelve warps:
 //   0-3, 4-7  softmax of tile 0 / 1: one thread per row (TMEM lane), so row
 //             maxima and sums need no exchange between threads; they also load
 //             the tile's Q and write its result
-//   8         producer: TMA of K and V blocks into a ring of shared-memory slots,
-//             running ahead into the next unit
+//   8         producer: takes units and publishes them to the other warps; TMA of
+//             K and V blocks into a ring of shared-memory slots, running ahead
+//             into the next unit
 //   9, 10     issue tcgen05.mma for tile 0 / 1: S = Q K^T from shared memory,
 //             O += P V with P read from TMEM. The tensor core takes few MMAs
 //             ahead, so a lone issuer's waits would idle it: with two, one waits
 //             while the other's MMAs run
+//   11        helper: cleans V blocks (below)
 // TMEM holds, per tile, S of two halves (2 x 64 fp32 columns) and O (D
 // columns); P (bf16) overwrites the S it came from. S of the next half is
 // computed while the softmax works on this one, so a softmax warp finds its
@@ -35,10 +37,10 @@
 // The weights are rounded to bf16 (half a step 2^-8 each, unbiased) because the
 // MMA takes P and V in one type; Z sums them before that rounding, in fp32.
 //
-// Keys that no row of the unit sees (holes, the end of a sequence) have their V
-// rows zeroed in shared memory, since 0 * NaN would reach O; keys that only
-// some rows see have their non-finite V values taken out there and added at the
-// end to the rows that see them.
+// 0 * NaN must not reach O: the V rows of holes are zeroed in shared memory, and
+// keys past a sequence's end or that only some rows see have their non-finite V
+// values taken out there; those are added at the end to the rows that see them. The helper warp does this between a V block's
+// arrival and its product, and passes on blocks that need nothing.
 //
 // Every wait is bounded: on running out it raises the CTA's abort flag and the
 // caller's status word; each role then leaves its loop, the copies and MMAs in
@@ -55,15 +57,15 @@ namespace tkv {
 namespace {
 
 constexpr int kRows = 128;
-constexpr int kThreads = 352;
-constexpr int kProducer = 8, kIssuer = 9;  // warps; one issuer per tile
+constexpr int kThreads = 384;
+constexpr int kProducer = 8, kIssuer = 9, kHelper = 11;  // warps; one issuer per tile
 constexpr int kHalf = 64;                  // keys of one S
 constexpr int kBlockPages = kKeyBlock / kPage;
 constexpr int kBox = 128 * 128;            // a box: 128 rows of 64 bf16 columns, 128-byte swizzled
 constexpr int kBatch = 4;                  // blocks whose page ids are fetched together
 constexpr float kRise = 20.f;
-constexpr int kSched = 4;                  // units the producer may be ahead of the slowest role
-constexpr int kBatches = 8;                // batches the id ring holds: the producer is at most kSched units and a
+constexpr int kUnits = 4;                  // units the producer may be ahead of the slowest warp
+constexpr int kBatches = 8;                // batches the id ring holds: the producer is at most kUnits units and a
                                            // ring of slots (a batch or two) ahead of the softmax
 
 template <int D>
@@ -76,16 +78,27 @@ struct Cfg {
   __host__ __device__ static constexpr uint32_t col_o(int t) { return 256 + t * D; }
 };
 
+// What the warps need to know of a unit.
+struct Work {
+  int unit;           // -1: no more units
+  int seg, h, grp, split, row0, rows;
+  int pair, ahead;
+  int block0, n;      // first key block, blocks
+  int ns[2];          // halves each tile works on: a causal tile 0 may end before tile 1
+  int pad[3];
+};
+
 // Barriers of alternate halves come in pairs: a parity wait tells two phases
 // apart, and up to two halves of a tile are under way.
 struct Shared {
-  uint64_t full[8], empty[8], s_full[2][2], p_full[2][2], o_prev[2], o_last[2], q_full[2], wg[2], drain[2];
-  uint64_t ids[kBatches], sched_full[kSched], sched_empty[kSched];
-  alignas(16) uint4 response[kSched];
+  uint64_t full[8], empty[8], s_full[2][2], p_full[2][2], o_prev[2], o_last[2], q_full[2], drain[2];
+  uint64_t v_clean[8];  // of the V blocks in turn; the helper is fewer than 8 ahead of any reader
+  uint64_t ids[kBatches], work_full[kUnits], work_empty[kUnits], response_full;
+  alignas(16) uint4 response;
+  alignas(16) Work work[kUnits];
   uint32_t tmem;
   int abort;
-  uint32_t slot_flag[8][4];                  // keys of a V slot whose values were stripped of non-finite ones
-  alignas(16) uint32_t flag[2][8];           // per tile: the unit's partly seen keys with such values
+  alignas(16) uint32_t flag[2 * kUnits][8];  // per unit: partly seen keys with non-finite V values
   int32_t id[kBatches * 32];                 // page ids of recent blocks, -1: none
   alignas(16) uint16_t mask[kBatches * 32];  // their slot masks
 };
@@ -262,6 +275,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
+// The larger magnitudes of two pairs of bf16 values; NaN wins.
+__device__ __forceinline__ uint32_t max_abs(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b & 0x7fff7fffu));
+  return r;
+}
 // Zeroes the non-finite ones of two bf16 values; whether there was one.
 __device__ __forceinline__ bool strip(uint32_t& w) {
   const bool lo = (w & 0x7f80u) == 0x7f80u, hi = (w & 0x7f800000u) == 0x7f800000u;
@@ -292,17 +311,11 @@ __device__ __forceinline__ int response_unit(const uint4* at) {
   return got ? static_cast<int>(x) : -1;
 }
 
-// What the roles need to know of a unit.
-struct Work {
-  int seg, h, grp, split, row0, rows;
-  int pair, ahead;
-  int block0, n;  // first key block, blocks
-  int ns[2];      // halves each tile works on: a causal tile 0 may end before tile 1
-};
 __device__ __forceinline__ Work unit_work(const TileParams& p, int unit) {
   const TileUnit u = tile_unit(p, unit);
   const TileSeg& sg = p.seg[u.seg];
   Work w;
+  w.unit = unit;
   w.seg = u.seg; w.h = u.h; w.grp = u.grp; w.split = u.split; w.row0 = u.row0; w.rows = u.rows;
   w.pair = sg.pair;
   w.ahead = w.pair ? 2 : 1;  // two halves per tile
@@ -367,14 +380,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.o_prev[t], 1);
       mbar_init(&sh.o_last[t], 1);
       mbar_init(&sh.q_full[t], 4);
-      mbar_init(&sh.wg[t], 4);
       mbar_init(&sh.drain[t], 1);
-      for (int i = 0; i < 8; ++i) sh.flag[t][i] = 0;
     }
+    mbar_init(&sh.response_full, 1);
+    for (int i = 0; i < 8; ++i) mbar_init(&sh.v_clean[i], 1);
     for (int i = 0; i < kBatches; ++i) mbar_init(&sh.ids[i], 1);
-    for (int i = 0; i < kSched; ++i) {
-      mbar_init(&sh.sched_full[i], 1);
-      mbar_init(&sh.sched_empty[i], 10);  // every warp but the producer's
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(&sh.work_full[i], 1);
+      mbar_init(&sh.work_empty[i], kThreads / 32 - 1);  // every warp but the producer
     }
     sh.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -385,29 +398,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
 
-  // The unit after the CTA's k-th, or -1 at the end or on an abort.
-  auto next_unit = [&](int k) {
-    const int r = k % kSched;
-    if (!warp_wait(&sh.sched_full[r], (k / kSched) & 1, abort, limit)) return -1;
-    const int u = __shfl_sync(0xffffffffu, response_unit(&sh.response[r]), 0);
-    if (warp != kProducer && lane == 0) mbar_arrive(&sh.sched_empty[r]);
-    return u;
+  // The CTA's k-th unit as the producer published it; unit -1 at the end or on an abort.
+  auto next_work = [&](int k) {
+    const int r = k % kUnits;
+    Work w;
+    w.unit = -1;
+    if (!warp_wait(&sh.work_full[r], (k / kUnits) & 1, abort, limit)) return w;
+    w = sh.work[r];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.work_empty[r]);
+    return w;
   };
 
   if (warp == kProducer) {
     int pos = 0, batches = 0;
     int asked = -1;  // a request not answered yet
-    for (int k = 0, unit = blockIdx.x; unit >= 0; ++k) {
-      const int r = k % kSched;
-      if (k >= kSched && !warp_wait(&sh.sched_empty[r], (k / kSched - 1) & 1, abort, limit)) break;
+    for (int k = 0, unit = blockIdx.x;; ++k) {
+      const int r = k % kUnits;
+      if (k >= kUnits && !warp_wait(&sh.work_empty[r], (k / kUnits - 1) & 1, abort, limit)) break;
+      Work w;
+      w.unit = -1;
+      if (unit >= 0) w = unit_work(p, unit);
+      if (lane == 0) {
+        sh.work[r] = w;
+        mbar_arrive(&sh.work_full[r]);
+      }
+      if (unit < 0) break;
       if (lane == 0) {
         fence_proxy();
-        mbar_expect(&sh.sched_full[r], 16);
-        request_unit(&sh.response[r], &sh.sched_full[r]);
+        mbar_expect(&sh.response_full, 16);
+        request_unit(&sh.response, &sh.response_full);
       }
       __syncwarp();
       asked = k;
-      const Work w = unit_work(p, unit);
       const TileSeg& sg = p.seg[w.seg];
       // page ids and masks, a batch ahead of their use
       int32_t id_next = -1, id_after = -1;
@@ -440,8 +463,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (round > 0 && !warp_wait(&sh.empty[slot], (round - 1) & 1, abort, limit)) return false;
         ++pos;
         const uint32_t dst = s_ring + slot * C::tile;
-        if (lane < 4) sh.slot_flag[slot][lane] = 0;
-        __syncwarp();
         if (lane == 0) mbar_expect(&sh.full[slot], C::tile);
         __syncwarp();
         if (kPaged) {
@@ -465,25 +486,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       batches += (w.n + kBatch - 1) / kBatch;
-      unit = next_unit(k);
-      if (!__any_sync(0xffffffffu, *abort)) asked = -1;
+      if (!warp_wait(&sh.response_full, k & 1, abort, limit)) break;
+      unit = __shfl_sync(0xffffffffu, response_unit(&sh.response), 0);
+      asked = -1;
     }
     // the issuers' arrivals on the last slots come before this shared memory is another CTA's
     for (int q = max(0, pos - C::slots); q < pos; ++q)
       if (!warp_wait(&sh.empty[q % C::slots], (q / C::slots) & 1, abort, limit)) break;
     // an aborted CTA lets what is in flight land before it ends
     if (__any_sync(0xffffffffu, *abort)) {
-      if (asked >= 0) warp_wait(&sh.sched_full[asked % kSched], (asked / kSched) & 1, nullptr, limit);
+      if (asked >= 0) warp_wait(&sh.response_full, asked & 1, nullptr, limit);
       for (int q = max(0, pos - C::slots); q < pos; ++q) warp_wait(&sh.full[q % C::slots], (q / C::slots) & 1, nullptr, limit);
     }
-  } else if (warp >= kIssuer) {
+  } else if (warp == kIssuer || warp == kIssuer + 1) {
     const uint32_t leader = elect_leader();
     const int t = warp - kIssuer;
     constexpr uint32_t kIdescS = instr_desc(kHalf, false), kIdescO = instr_desc(D, true);
     const uint64_t desc_q = smem_desc(s_q + t * C::tile, 16, 1024);
     const uint32_t t_s = tmem + t * 2 * kHalf, t_o = tmem + C::col_o(t);
-    int g0 = 0, used = 0;          // halves and units of this tile so far
-    int slot = 0, slot_phase = 0;  // the ring slot to take next
+    int g0 = 0, blocks = 0, used = 0;  // halves of this tile, V blocks and units of this tile so far
+    int slot = 0, slot_phase = 0;      // the ring slot to take next
     // Both issuers take every ring slot in turn and give it back, one that does
     // not use it as soon as it is full.
     auto take = [&](int* at) {
@@ -494,6 +516,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         slot_phase ^= 1;
       }
       return ready;
+    };
+    auto take_v = [&](int* at) {
+      const int i = blocks++;
+      return take(at) && warp_wait(&sh.v_clean[i & 7], (i >> 3) & 1, abort, limit);
     };
     auto release = [&](int at) { mma_commit(leader, &sh.empty[at]); };
     // S of the tile's g-th half = Q K^T over one half of the K block
@@ -519,8 +545,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (h == mine - 1) mma_commit(leader, &sh.o_last[t]);
       return true;
     };
-    for (int k = 0, unit = blockIdx.x; unit >= 0; ++k) {
-      const Work w = unit_work(p, unit);
+    for (int k = 0;; ++k) {
+      const Work w = next_work(k);
+      if (w.unit < 0) break;
       const int mine = w.ns[t];
       // a tile without rows or keys in this unit leaves the barriers of Q, S, P and O alone
       if (mine > 0) {
@@ -535,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           release(at);
         }
         for (int i = 0, at; ok && i < w.n; ++i) {
-          if (!(ok = take(&at))) break;
+          if (!(ok = take_v(&at))) break;
           if (i < mine && !(ok = pv(i, at, t, mine))) break;
           release(at);
           if (i + 2 < w.n) {
@@ -546,35 +573,101 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         int at_k, at_v;
+        auto qk_half = [&](int h, int half) {
+          if (h < mine) qk(g0 + h, at_k, half);
+        };
         if (w.n > 0) {
           if (!take(&at_k)) break;
-          if (0 < mine) qk(g0, at_k, 0);
-          if (1 < mine) qk(g0 + 1, at_k, 1);
+          qk_half(0, 0);
+          qk_half(1, 1);
           release(at_k);
         }
         for (int i = 0; i < w.n; ++i) {
           const int h = 2 * i;
-          if (!(ok = take(&at_v))) break;
+          if (!(ok = take_v(&at_v))) break;
           if (h < mine && !(ok = pv(h, at_v, 0, mine))) break;
           if (i + 1 < w.n) {
             if (!(ok = take(&at_k))) break;
-            if (h + 2 < mine) qk(g0 + h + 2, at_k, 0);
+            qk_half(h + 2, 0);
           }
           if (h + 1 < mine && !(ok = pv(h + 1, at_v, 1, mine))) break;
           release(at_v);
           if (i + 1 < w.n) {
-            if (h + 3 < mine) qk(g0 + h + 3, at_k, 1);
+            qk_half(h + 3, 1);
             release(at_k);
           }
         }
       }
       if (!ok) break;
       g0 += mine;
-      unit = next_unit(k);
     }
     if (__any_sync(0xffffffffu, *abort)) {
       mma_commit(leader, &sh.drain[t]);
       warp_wait(&sh.drain[t], 0, nullptr, limit);
+    }
+  } else if (warp == kHelper) {
+    int pos0 = 0, vb = 0, batches = 0;
+    for (int k = 0;; ++k) {
+      const Work w = next_work(k);
+      if (w.unit < 0) break;
+      const TileSeg& sg = p.seg[w.seg];
+      const int lim_first = tile_row_limit(p, sg, w.row0), lim_last = tile_row_limit(p, sg, w.row0 + w.rows - 1);
+      uint32_t* flag = sh.flag[k % (2 * kUnits)];
+      if (lane < 8) flag[lane] = 0;
+      __syncwarp();
+      bool ok = true;
+      for (int i = 0; i < w.n; ++i, ++vb) {
+        const int at = pos0 + pos_v(i, w.ahead, w.n), slot = at % C::slots;
+        if (!(ok = warp_wait(&sh.full[slot], (at / C::slots) & 1, abort, limit))) break;
+        const int k0 = (w.block0 + i) * kKeyBlock;
+        if (kPaged) {
+          const int b = batches + i / kBatch;
+          if (!(ok = warp_wait(&sh.ids[b % kBatches], (b / kBatches) & 1, abort, limit))) break;
+          const int at0 = b % kBatches * 32 + i % kBatch * kBlockPages;
+          const uint16_t* mask = &sh.mask[at0];
+          // two lanes per key, half of its columns each
+          for (int pg = 0; pg < kBlockPages; ++pg) {
+            if (mask[pg] == 0xffffu || sh.id[at0 + pg] < 0) continue;  // a page that is not there arrived as zeros
+            const int key = pg * kPage + (lane >> 1);
+            if ((mask[pg] >> (lane >> 1)) & 1u) continue;
+            char* v = smem + C::o_ring + slot * C::tile + key * 128;
+#pragma unroll 4
+            for (int e = 0; e < D / 16; ++e) {
+              const int c = (lane & 1) * (D / 16) + e;
+              *reinterpret_cast<uint4*>(v + (c >> 3) * kBox + (((c + key) & 7) << 4)) = make_uint4(0, 0, 0, 0);
+            }
+          }
+          fence_proxy();
+        } else if (k0 + kKeyBlock > lim_first) {
+          for (int key = max(0, lim_first - k0) + (lane >> 1); key < kKeyBlock; key += 16) {
+            char* v = smem + C::o_ring + slot * C::tile + key * 128;
+            uint32_t top[2] = {0, 0};  // largest magnitudes; NaN stays
+#pragma unroll
+            for (int e = 0; e < D / 16; ++e) {
+              const int c = (lane & 1) * (D / 16) + e;
+              const uint4 x = *reinterpret_cast<const uint4*>(v + (c >> 3) * kBox + (((c + key) & 7) << 4));
+              top[0] = max_abs(max_abs(top[0], x.x), x.y);
+              top[1] = max_abs(max_abs(top[1], x.z), x.w);
+            }
+            top[0] = max_abs(top[0], top[1]);
+            if (!strip(top[0])) continue;
+#pragma unroll 1
+            for (int e = 0; e < D / 16; ++e) {
+              const int c = (lane & 1) * (D / 16) + e;
+              uint4* x = reinterpret_cast<uint4*>(v + (c >> 3) * kBox + (((c + key) & 7) << 4));
+              strip(x->x), strip(x->y), strip(x->z), strip(x->w);
+            }
+            const int part = k0 + key - lim_first;
+            if (k0 + key < lim_last) atomicOr(&flag[part >> 5], 1u << (part & 31));
+          }
+          fence_proxy();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.v_clean[vb & 7]);
+      }
+      if (!ok) break;
+      pos0 += 2 * w.n;
+      batches += (w.n + kBatch - 1) / kBatch;
     }
   } else {
     const int t = warp >> 2, r = tid & 127, wq = warp & 3;
@@ -586,6 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Q rows of a unit into the tile's shared memory, swizzled; rows past the end
     // keep what is there: a row's S, P and O depend on its own Q alone
     auto load_q = [&](const Work& w) {
+      if (w.unit < 0) return;
       const TileSeg& sg = p.seg[w.seg];
       const int first = w.pair ? 0 : t * kRows, rows = min(kRows, w.rows - first);
       const int tok_base = sg.tok0 + w.row0 / G, g_base = w.row0 % G + first;
@@ -599,29 +693,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         cp_async16(dst + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), q + static_cast<int64_t>(tok_base + tok) * p.q_stride + (x - tok * G) * D + c * 8);
       }
     };
-    int syncs = 0;
-    auto tile_sync = [&]() {  // the tile's four warps
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.wg[t]);
-      return warp_wait(&sh.wg[t], syncs++ & 1, abort, limit);
-    };
-    int pos0 = 0, g0 = 0, batches = 0, used = 0, used2 = 0;  // used2: units with two halves or more
-    int unit = blockIdx.x;
-    Work w = unit_work(p, unit);
+    int g0 = 0, vb = 0, batches = 0, used = 0, used2 = 0;  // used2: units with two halves or more
+    Work w = next_work(0);
     load_q(w);
-    for (int k = 0; unit >= 0; ++k) {
+    for (int k = 0; w.unit >= 0; ++k) {
       const TileSeg& sg = p.seg[w.seg];
       asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy();
       __syncwarp();
       if (lane == 0 && w.ns[t] > 0) mbar_arrive(&sh.q_full[t]);
-
       const int first = w.pair ? 0 : t * kRows;  // the tile's first row in the unit
       const int rows = min(kRows, w.rows - first), mine = w.ns[t];
       const int row = w.row0 + first + min(r, max(rows - 1, 0));
       const bool valid = r < rows, active = wq * 32 < rows;  // active: the warp has rows at all
       const int lim = tile_row_limit(p, sg, row);
-      const int lim_first = tile_row_limit(p, sg, w.row0), lim_last = tile_row_limit(p, sg, w.row0 + w.rows - 1);
       const int lim_warp = __shfl_sync(0xffffffffu, lim, 0);  // limits rise with the row
       float ref = -INFINITY, z = 0.f;  // maximum the weights refer to (unscaled logits), sum of weights
       bool ok = true;
@@ -638,7 +723,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const bool holes = kPaged && (live[0] & live[1]) != ~0u;
         const bool cut = !kPaged && k0 + kHalf > lim_warp;
-        const bool clean = holes || (!kPaged && k0 + kHalf > lim_first);
 
         if (!(ok = warp_wait(&sh.s_full[t][buf], (g >> 1) & 1, abort, limit))) break;
         fence_after();
@@ -709,72 +793,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st32(t_s + buf * kHalf, s);
           z += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         }
-        if (clean) {
-          const int at_v = pos0 + pos_v(i, w.ahead, w.n), slot = at_v % C::slots, round = at_v / C::slots;
-          const int kr = half * kHalf + (r & 63), key = k0 + (r & 63);
-          if (!(ok = warp_wait(&sh.full[slot], round & 1, abort, limit))) break;
-          const bool none = kPaged ? !((live[(r & 63) >> 5] >> (r & 31)) & 1u) : key >= lim_last;
-          if (none || (!kPaged && key >= lim_first)) {
-            // two threads per key, half of its columns each; where both tiles use the
-            // half both clean it, with the same result
-            char* at = smem + C::o_ring + slot * C::tile + kr * 128;
-#pragma unroll 2
-            for (int e = 0; e < D / 16; ++e) {
-              const int c = (r >> 6) * (D / 16) + e;
-              uint4* v = reinterpret_cast<uint4*>(at + (c >> 3) * kBox + (((c + kr) & 7) << 4));
-              if (none) {
-                *v = make_uint4(0, 0, 0, 0);
-                continue;
-              }
-              uint4 x = *v;
-              const bool bad = strip(x.x) | strip(x.y) | strip(x.z) | strip(x.w);
-              if (bad) {  // the flag first: who reads the stripped value finds the flag set
-                atomicOr(&sh.slot_flag[slot][kr >> 5], 1u << (kr & 31));
-                __threadfence_block();
-                *v = x;
-              }
-            }
-          }
-          if (!kPaged) {
-            // every value of the half has been looked at by this tile's warps, or was
-            // found stripped with its flag set: note the flags before the slot goes
-            __threadfence_block();
-            if (!(ok = tile_sync())) break;
-            const uint32_t f = lane < 2 ? sh.slot_flag[slot][half * 2 + lane] : 0;
-            if (wq == 0)
-              for (uint32_t left = f; left; left &= left - 1) {
-                const int part = k0 + lane * 32 + __ffs(left) - 1 - lim_first;
-                atomicOr(&sh.flag[t][part >> 5], 1u << (part & 31));
-              }
-          }
-          fence_proxy();
-        }
         wait_st();
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.p_full[t][buf]);
       }
-      // Q is free: the tile's last S has been seen. Load the next unit's while this one's O is finished.
-      Work next_w;
-      int next = -1;
-      if (ok) {
-        next = next_unit(k);
-        if (next >= 0) {
-          next_w = unit_work(p, next);
-          load_q(next_w);
-        }
-        ok = !__any_sync(0xffffffffu, *abort);
-      }
-      if (ok && mine > 0) {
+      // Q is free, its last S has been seen: load the next unit's while this one's O is finished
+      if (!ok) break;
+      const Work next = next_work(k + 1);
+      load_q(next);
+      if (mine > 0) {
         ok = warp_wait(&sh.o_last[t], used & 1, abort, limit);
         fence_after();
       }
+      const uint32_t* flag = sh.flag[k % (2 * kUnits)];
       uint32_t flagged = 0;
-      if (!kPaged && ok && w.rows > 0) {
-        __threadfence_block();
-        ok = tile_sync();
+      if (!kPaged && ok && mine > 0) {
+        // the helper is done with the unit's V blocks, and so with its flags
+        const int last = vb + w.n - 1;
+        ok = warp_wait(&sh.v_clean[last & 7], (last >> 3) & 1, abort, limit);
         for (int i = 0; i < 8; i += 4) {
-          const uint4 f = *reinterpret_cast<const uint4*>(&sh.flag[t][i]);
+          const uint4 f = *reinterpret_cast<const uint4*>(&flag[i]);
           flagged |= f.x | f.y | f.z | f.w;
         }
       }
@@ -793,16 +832,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 16; ++e) o[e] = 0;
             } else {
-              add_flagged(p, sh.flag[t], lim_first, lim, sg.key0, w.h * D + c, o);
+              add_flagged(p, flag, tile_row_limit(p, sg, w.row0), lim, sg.key0, w.h * D + c, o);
             }
             tmem_st16(t_o + c, o);
           }
           wait_st();
         }
         // a thread holds a row and stores it by whole 32-byte sectors
-        const int x = w.row0 % G + first + r, tok = (x * gmul) >> 16;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + static_cast<int64_t>(sg.tok0 + w.row0 / G + tok) * p.out_stride +
-                             (w.h * G + x - tok * G) * D;
+        const int at = w.row0 + first + r, tok = at / G;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + static_cast<int64_t>(sg.tok0 + tok) * p.out_stride +
+                             (w.h * G + at - tok * G) * D;
         float* po = p.part_o + (part + r) * D;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -825,20 +864,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.part_z[part + r] = z;
         }
       }
-      if (!kPaged && flagged) {  // clear the tile's flags once all of its warps have used them
-        if (!tile_sync()) break;
-        if (wq == 0 && lane < 8) sh.flag[t][lane] = 0;
-        __threadfence_block();
-        if (!tile_sync()) break;
-      }
       fence_before();
-      pos0 += 2 * w.n;
+      vb += w.n;
       g0 += mine;
       used += mine > 0;
       used2 += mine > 1;
       batches += (w.n + kBatch - 1) / kBatch;
-      unit = next;
-      w = next_w;
+      w = next;
     }
     fence_before();
   }
