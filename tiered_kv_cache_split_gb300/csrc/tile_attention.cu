@@ -225,108 +225,173 @@ __global__ void __launch_bounds__(kFmaThreads) tile_fma_kernel(const __grid_cons
   }
 }
 
-// ---- merge: one CTA per (query token, KV head), one warp per query head at a
-// time; out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) Z_i. A decode token of
-// the shared-prefix form joins the prefix's partials and its own, and adds the
-// softmax weights of its own slots, summed over the G heads, to alpha.
-constexpr int kMergeThreads = 256;
+// ---- merge: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) Z_i over a row's
+// partials. Four warps share a row's partials where a row has many (few rows,
+// split far), else each takes a row. Bound by reading the partials, which the
+// L2 mostly still holds; eight loads per lane are in flight.
+// A second kind of CTA serves decode steps with alpha: 512 own slots of a
+// (sequence, KV head), adding the softmax weights of their spilled logits
+// summed over the G heads; it forms M and Z of the G heads for itself.
+constexpr int kMergeThreads = 128;
+constexpr int kMergeWarps = kMergeThreads / 32;
+constexpr int kAlphaSlots = kMergeThreads * 4;
+constexpr int kShareParts = 16;  // partials from which four warps share a row
 
 struct PartList {
-  int64_t first, step;  // partial row i is first + i * step
-  int n;
+  int64_t first[2], step[2];  // partial row i of a list is first + i * step
+  int n0, n;                  // those of the first list, all
+  __device__ __forceinline__ int64_t at(int i) const { return i < n0 ? first[0] + i * step[0] : first[1] + (i - n0) * step[1]; }
 };
 
-__device__ __forceinline__ PartList part_list(const TileParams& p, const TileSeg& s, int h, int row) {
-  PartList l;
+__device__ __forceinline__ void add_parts(PartList& l, int which, const TileParams& p, const TileSeg& s, int h, int row) {
+  if (s.splits == 0) return;
+  int n;
   if (s.pair) {
-    l.first = tile_part_row(p, s, 0, h, 0, 0) + row;
-    l.step = s.part_rows;
-    l.n = s.splits * 2;
+    l.first[which] = tile_part_row(p, s, 0, h, 0, 0) + row;
+    l.step[which] = s.part_rows;
+    n = s.splits * 2;
   } else {
     const int per = p.tile_rows * p.tpg, grp = row / per, tile = row % per / p.tile_rows;
-    l.first = tile_part_row(p, s, grp, h, 0, tile) + row % p.tile_rows;
-    l.step = static_cast<int64_t>(p.tpg) * s.part_rows;
-    l.n = s.splits;
+    l.first[which] = tile_part_row(p, s, grp, h, 0, tile) + row % p.tile_rows;
+    l.step[which] = static_cast<int64_t>(p.tpg) * s.part_rows;
+    n = s.splits;
+  }
+  if (which == 0) l.n0 = n;
+  l.n += n;
+}
+
+// The partials of query head h * G + g of token tok.
+__device__ PartList part_list(const TileParams& p, int tok, int h, int g) {
+  PartList l{};
+  if (p.paged) {  // segment 0 is the prefix of all tokens
+    add_parts(l, 0, p, p.seg[0], h, tok * p.G + g);
+    add_parts(l, 1, p, p.seg[tok + 1], h, g);
+  } else {
+    int own = 0;
+    for (int i = 0; i < p.nseg; ++i)
+      if (tok >= p.seg[i].tok0 && tok < p.seg[i].tok0 + p.seg[i].ntok) own = i;
+    add_parts(l, 0, p, p.seg[own], h, (tok - p.seg[own].tok0) * p.G + g);
   }
   return l;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kMergeThreads) tile_merge_kernel(const __grid_constant__ TileParams p) {
-  constexpr int E = D / 32;
-  __shared__ float s_m[kMaxGroup], s_inv[kMaxGroup];
-  const int tok = blockIdx.x, h = blockIdx.y, G = p.G;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int own;  // the token's segment (paged: segment 0 is the prefix of all tokens)
-  if (p.paged) {
-    own = tok + 1;
-  } else {
-    int lo = 0, hi = p.nseg - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (p.seg[mid].tok0 <= tok) lo = mid; else hi = mid - 1;
-    }
-    own = lo;
-  }
-  for (int g = warp; g < G; g += kMergeThreads / 32) {
-    PartList l[2];
-    int nl = 0;
-    if (p.paged && p.seg[0].splits > 0) l[nl++] = part_list(p, p.seg[0], h, tok * G + g);
-    const TileSeg& so = p.seg[own];
-    if (so.splits > 0) l[nl++] = part_list(p, so, h, (tok - so.tok0) * G + g);
-    float M = -INFINITY;
-    for (int a = 0; a < nl; ++a)
-      for (int i = lane; i < l[a].n; i += 32) M = fmaxf(M, p.part_m[l[a].first + i * l[a].step]);
+// M (0 where there is no key) of a row, by one warp.
+__device__ __forceinline__ float parts_max(const TileParams& p, const PartList& l, int lane) {
+  float m = -INFINITY;
+  for (int i = lane; i < l.n; i += 32) m = fmaxf(m, p.part_m[l.at(i)]);
 #pragma unroll
-    for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    const float base = M == -INFINITY ? 0.f : M;
-    float Z = 0.f, acc[E] = {};
-    for (int a = 0; a < nl; ++a)
-      for (int i0 = 0; i0 < l[a].n; i0 += 32) {
-        const int mine = i0 + lane;
-        float w = 0.f, wz = 0.f;
-        if (mine < l[a].n) {
-          const int64_t r = l[a].first + mine * l[a].step;
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  return m == -INFINITY ? 0.f : m;
+}
+__device__ __forceinline__ float parts_inv(float z) { return z > 0.f || z != z ? 1.f / z : 0.f; }
+
+template <typename T, int D, int kShare>
+__global__ void __launch_bounds__(kMergeThreads) tile_merge_kernel(const __grid_constant__ TileParams p, int64_t rows, int row_ctas) {
+  constexpr int E = D / 32, kAhead = 8;
+  __shared__ float s_acc[kMergeWarps][D], s_z[kMergeWarps], s_m[kMaxGroup], s_inv[kMaxGroup];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = p.G;
+  cudaGridDependencySynchronize();
+  if (static_cast<int>(blockIdx.x) < row_ctas) {
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kMergeWarps / kShare) + warp / kShare;
+    const bool live = row < rows;
+    float acc[E] = {}, z = 0.f;
+    const int tok = live ? static_cast<int>(row / p.Hq) : 0, hq = live ? static_cast<int>(row % p.Hq) : 0;
+    if (live) {
+      const PartList l = part_list(p, tok, hq / G, hq % G);
+      const float base = parts_max(p, l, lane);
+      for (int i0 = warp % kShare * kAhead; i0 < l.n; i0 += kShare * kAhead) {
+        float w = 0.f;
+        if (lane < kAhead && i0 + lane < l.n) {
+          const int64_t r = l.at(i0 + lane);
           w = exp2f(p.part_m[r] - base);
-          wz = w * p.part_z[r];
+          z += w * p.part_z[r];
         }
-        Z += wz;
-        const int n = min(32, l[a].n - i0);
-        for (int i = 0; i < n; ++i) {
-          const float wi = __shfl_sync(0xffffffffu, w, i);
-          const float* at = p.part_o + (l[a].first + (i0 + i) * l[a].step) * D + lane * E;
-          if (wi == 0.f && __shfl_sync(0xffffffffu, wz, i) == 0.f) continue;  // nothing, or nothing that counts
+        float v[kAhead][E];
 #pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] = fmaf(wi, at[e], acc[e]);
+        for (int i = 0; i < kAhead; ++i) {
+          if (i0 + i < l.n) {
+            const float* at = p.part_o + l.at(i0 + i) * D + lane * E;
+            if constexpr (E == 4) {
+              const float4 x = *reinterpret_cast<const float4*>(at);
+              v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+            } else {
+              const float2 x = *reinterpret_cast<const float2*>(at);
+              v[i][0] = x.x, v[i][1] = x.y;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[i][e] = 0.f;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const float wi = __shfl_sync(0xffffffffu, w, i);
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(wi, v[i][e], acc[e]);
         }
       }
 #pragma unroll
-    for (int d = 16; d; d >>= 1) Z += __shfl_xor_sync(0xffffffffu, Z, d);
-    const float inv = Z > 0.f || Z != Z ? 1.f / Z : 0.f;
-    T* at = static_cast<T*>(p.out) + static_cast<int64_t>(tok) * p.out_stride + (h * G + g) * D + lane * E;
+      for (int d = kAhead / 2; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+      z = __shfl_sync(0xffffffffu, z, 0);
+    }
+    if constexpr (kShare > 1) {
+      if (warp > 0) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) at[e] = static_cast<T>(acc[e] * inv);
+        for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
+        if (lane == 0) s_z[warp] = z;
+      }
+      __syncthreads();
+      if (warp > 0) return;
+      for (int o = 1; o < kMergeWarps; ++o) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += s_acc[o][lane * E + e];
+        z += s_z[o];
+      }
+    }
+    if (!live) return;
+    const float inv = parts_inv(z);
+    T* at = static_cast<T*>(p.out) + static_cast<int64_t>(tok) * p.out_stride + hq * D + lane * E;
+    if constexpr (sizeof(T) == 2 && E == 4) {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv), b = __floats2bfloat162_rn(acc[2] * inv, acc[3] * inv);
+      *reinterpret_cast<uint2*>(at) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) at[e] = static_cast<T>(acc[e] * inv);
+    }
+    return;
+  }
+  // alpha
+  const int per = (static_cast<int>(gridDim.x) - row_ctas) / (static_cast<int>(rows / p.Hq) * p.Hkv);  // CTAs of a (sequence, KV head)
+  const int item = blockIdx.x - row_ctas, tok = item / per / p.Hkv, h = item / per % p.Hkv;
+  const TileSeg& so = p.seg[tok + 1];
+  const int i = item % per * kAlphaSlots + threadIdx.x * 4;
+  if (item % per * kAlphaSlots >= so.nkeys) return;
+  for (int g = warp; g < G; g += kMergeWarps) {
+    const PartList l = part_list(p, tok, h, g);
+    const float base = parts_max(p, l, lane);
+    float z = 0.f;
+    for (int k = lane; k < l.n; k += 32) z += exp2f(p.part_m[l.at(k)] - base) * p.part_z[l.at(k)];
+#pragma unroll
+    for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
     if (lane == 0) {
       s_m[g] = base;
-      s_inv[g] = inv;
+      s_inv[g] = parts_inv(z);
     }
   }
-  if (!p.alpha || p.seg[own].splits == 0) return;
   __syncthreads();
-  const TileSeg& so = p.seg[own];
-  const float* l = p.spill + so.spill0 + static_cast<int64_t>(h) * G * so.nkeys;
-  float* at = p.alpha + (static_cast<int64_t>(tok) * p.Hkv + h) * p.alpha_stride_h + p.alpha_first;
-  for (int i = threadIdx.x * 4; i < so.nkeys; i += kMergeThreads * 4) {
-    float4 sum = *reinterpret_cast<const float4*>(at + i);
-    for (int g = 0; g < G; ++g) {
-      const float4 x = *reinterpret_cast<const float4*>(l + static_cast<int64_t>(g) * so.nkeys + i);
-      sum.x += exp2f(x.x - s_m[g]) * s_inv[g];
-      sum.y += exp2f(x.y - s_m[g]) * s_inv[g];
-      sum.z += exp2f(x.z - s_m[g]) * s_inv[g];
-      sum.w += exp2f(x.w - s_m[g]) * s_inv[g];
-    }
-    *reinterpret_cast<float4*>(at + i) = sum;
+  if (i >= so.nkeys) return;
+  const float* l = p.spill + so.spill0 + static_cast<int64_t>(h) * G * so.nkeys + i;
+  float4* at = reinterpret_cast<float4*>(p.alpha + (static_cast<int64_t>(tok) * p.Hkv + h) * p.alpha_stride_h + p.alpha_first + i);
+  float4 sum = *at;
+#pragma unroll 4
+  for (int g = 0; g < G; ++g) {
+    const float4 x = *reinterpret_cast<const float4*>(l + static_cast<int64_t>(g) * so.nkeys);
+    sum.x += exp2f(x.x - s_m[g]) * s_inv[g];
+    sum.y += exp2f(x.y - s_m[g]) * s_inv[g];
+    sum.z += exp2f(x.z - s_m[g]) * s_inv[g];
+    sum.w += exp2f(x.w - s_m[g]) * s_inv[g];
   }
+  *at = sum;
 }
 
 // ---- planning (host)
@@ -364,30 +429,43 @@ SegWork seg_work(const TileParams& p, const TileSeg& s, const TileShape& ts) {
   return w;
 }
 
-// Key blocks per unit. A unit costs its blocks and unit_cost; the device runs
-// them in waves of `slots`. Rows alone leave a decode step, or a short piece of
-// a prompt, with a few long units, so their keys are split: the candidate with
-// the shortest makespan wins. More than four waves of units are never split.
-int64_t blocks_per_unit(const SegWork* w, int n, int hkv, const TileShape& ts, bool paged) {
+// What a unit costs beside its blocks, in blocks: the fixed part, and its
+// partial rows written and read again where keys are split.
+double unit_cost(const TileShape& ts, int64_t rows, bool split) {
+  return ts.unit_cost + (split ? static_cast<double>(std::min<int64_t>(rows, static_cast<int64_t>(ts.rows) * ts.tpg)) / 64 : 0.0);
+}
+
+// Key blocks per unit. Units are handed out longest first to `slots` places, so
+// the time is about the larger of what one place gets on average and of the
+// waves the longest kind of unit makes. Rows alone leave a decode step, or a
+// short piece of a prompt, with a few long units: then keys are split, and the
+// candidate with the shortest time wins. More than four waves are never split.
+int64_t blocks_per_unit(const TileParams& p, const SegWork* w, const TileShape& ts) {
   int64_t whole = 0, most = 1, blocks = 0;
-  for (int i = 0; i < n; ++i) {
-    whole += w[i].groups * hkv;
+  for (int i = 0; i < p.nseg; ++i) {
+    whole += w[i].groups * p.Hkv;
     most = std::max(most, w[i].most);
-    blocks += w[i].blocks * hkv;
+    blocks += w[i].blocks * p.Hkv;
   }
   if (whole >= 4 * ts.slots) return most;
   int64_t best = most;
   double best_time = 1e300;
   for (int64_t cut = 1; cut <= most; cut += 1 + cut / 8) {
     const int64_t per = ceil_div(most, cut);
-    int64_t units = 0;
-    for (int i = 0; i < n; ++i)
-      if (w[i].groups) units += w[i].groups * hkv * ceil_div(w[i].most, per);
-    const double work = static_cast<double>(blocks) + static_cast<double>(ts.unit_cost) * units;
-    double time = units <= ts.slots ? static_cast<double>(per + ts.unit_cost)
-                                    : std::max(static_cast<double>(per + ts.unit_cost), ceil_div(units, ts.slots) * (work / units));
-    if (!paged && cut > 1) time += ts.unit_cost;  // the merge launch
-    if (time < best_time) {
+    const bool split = p.paged || cut > 1;
+    double work = static_cast<double>(blocks), longest = 0;
+    int64_t n_longest = 0;
+    for (int i = 0; i < p.nseg; ++i) {
+      if (!w[i].groups) continue;
+      const int64_t parts = ceil_div(w[i].most, per), units = w[i].groups * p.Hkv * parts;
+      const double cost = unit_cost(ts, static_cast<int64_t>(p.seg[i].ntok) * p.G, split);
+      const double time = static_cast<double>(ceil_div(w[i].most, parts)) + cost;
+      work += cost * units;
+      if (time > longest * 1.01) longest = time, n_longest = units;
+      else if (time > longest * 0.99) n_longest += units;
+    }
+    const double time = std::max(work / ts.slots, longest * ceil_div(n_longest, ts.slots)) + (!p.paged && split ? ts.unit_cost : 0);
+    if (time < best_time * 0.999) {
       best_time = time;
       best = per;
     }
@@ -403,7 +481,7 @@ TilePlan plan_units(TileParams& p, const TileShape& ts, bool want_spill) {
   p.tpg = ts.tpg;
   bool split = p.paged;
   for (int i = 0; i < p.nseg; ++i) work[i] = seg_work(p, p.seg[i], ts);
-  const int64_t per = blocks_per_unit(work, p.nseg, p.Hkv, ts, p.paged);
+  const int64_t per = blocks_per_unit(p, work, ts);
   for (int i = 0; i < p.nseg; ++i) split |= work[i].groups && work[i].most > per;
   p.direct = !split;
   for (int i = 0; i < p.nseg; ++i) {
@@ -473,6 +551,8 @@ int plan_prompt(TileParams& p, TilePlan* plan, int32_t batch, const int32_t* q_l
     if (tq * p.G > INT32_MAX || tk > INT32_MAX - 2 * kKeyBlock)
       return report(TKV_ERR_INVALID_ARG, "more than 2^31 rows or keys in one call");
   }
+  // longest first
+  std::stable_sort(p.seg, p.seg + batch, [](const TileSeg& a, const TileSeg& b) { return a.nkeys > b.nkeys; });
   *tokens = tq;
   *keys = tk;
   *plan = plan_units(p, tile_shape(dtype), false);
@@ -511,10 +591,38 @@ int plan_shared(TileParams& p, TilePlan* plan, int32_t batch, int32_t Hq, int32_
 template <int D>
 cudaError_t launch_fma(const TileParams& p, cudaStream_t s) {
   constexpr int bytes = ((kFmaRows + 2 * kFmaKeys) * (D + 4) + kFmaRows * (kFmaKeys + 4)) * 4;
-  cudaError_t e = cudaFuncSetAttribute(tile_fma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  static SharedMemoryOptIn opt_in;
+  const cudaError_t e = opt_in.once(reinterpret_cast<const void*>(tile_fma_kernel<D>), bytes);
   if (e != cudaSuccess) return e;
   tile_fma_kernel<D><<<static_cast<unsigned>(p.units), kFmaThreads, bytes, s>>>(p);
   return cudaGetLastError();
+}
+
+// The merge may start while the units' kernel ends; it waits for it before it reads.
+template <typename T, int D>
+cudaError_t launch_merge(const TileParams& p, int tokens, cudaStream_t s) {
+  int parts = 0, slots = 0;  // most partials of a row, most own slots of a sequence
+  for (int i = 0; i < p.nseg; ++i) {
+    const int n = p.seg[i].splits * (p.seg[i].pair ? 2 : 1) + (p.paged && i > 0 ? p.seg[0].splits * (p.seg[0].pair ? 2 : 1) : 0);
+    parts = std::max(parts, n);
+    if (p.paged && i > 0) slots = std::max(slots, p.seg[i].nkeys);
+  }
+  const int64_t rows = static_cast<int64_t>(tokens) * p.Hq;
+  const bool share = parts >= kShareParts;
+  const int64_t row_ctas = share ? rows : ceil_div(rows, kMergeWarps);
+  const int64_t alpha_ctas = p.alpha ? static_cast<int64_t>(tokens) * p.Hkv * ceil_div(slots, kAlphaSlots) : 0;
+  if (row_ctas + alpha_ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(row_ctas + alpha_ctas));
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.units > 0 ? 1 : 0;
+  return share ? cudaLaunchKernelEx(&cfg, tile_merge_kernel<T, D, kMergeWarps>, p, rows, static_cast<int>(row_ctas))
+               : cudaLaunchKernelEx(&cfg, tile_merge_kernel<T, D, 1>, p, rows, static_cast<int>(row_ctas));
 }
 
 template <typename T>
@@ -525,12 +633,7 @@ cudaError_t launch_tiles(const TileParams& p, int D, int tokens, int64_t keys, c
     else e = D == 64 ? launch_fma<64>(p, s) : launch_fma<128>(p, s);
     if (e != cudaSuccess) return e;
   }
-  if (!p.direct && tokens > 0) {
-    const dim3 grid(tokens, p.Hkv);
-    if (D == 64) tile_merge_kernel<T, 64><<<grid, kMergeThreads, 0, s>>>(p);
-    else tile_merge_kernel<T, 128><<<grid, kMergeThreads, 0, s>>>(p);
-    e = cudaGetLastError();
-  }
+  if (!p.direct && tokens > 0) e = D == 64 ? launch_merge<T, 64>(p, tokens, s) : launch_merge<T, 128>(p, tokens, s);
   return e;
 }
 

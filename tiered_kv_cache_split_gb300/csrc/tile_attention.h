@@ -12,6 +12,8 @@
 #pragma once
 
 #include <cuda_runtime.h>
+
+#include <atomic>
 #include <cstdint>
 
 #include "tkv_internal.h"
@@ -104,6 +106,20 @@ __device__ __forceinline__ TileUnit tile_unit(const TileParams& p, int u) {
 __device__ __forceinline__ int64_t tile_part_row(const TileParams& p, const TileSeg& s, int grp, int h, int split, int tile) {
   return s.part0 + (((static_cast<int64_t>(grp) * p.Hkv + h) * s.splits + split) * p.tpg + tile) * s.part_rows;
 }
+
+// The dynamic shared memory limit of a kernel, raised once per device.
+struct SharedMemoryOptIn {
+  std::atomic<bool> done[64] = {};
+  cudaError_t once(const void* kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_release);
+    return e;
+  }
+};
 
 // tile_attention_mma.cu: the units of a bf16 call; keys: packed key tokens
 cudaError_t launch_tile_mma(const TileParams& p, int D, int64_t keys, cudaStream_t s);

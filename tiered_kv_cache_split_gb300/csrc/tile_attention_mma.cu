@@ -912,7 +912,8 @@ template <int D, bool kPaged>
 cudaError_t launch(const TileParams& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
   constexpr int bytes = Cfg<D>::o_shared + static_cast<int>(sizeof(Shared));
   static_assert(bytes <= 227 * 1024, "shared memory");
-  const cudaError_t e = cudaFuncSetAttribute(tile_mma_kernel<D, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  static SharedMemoryOptIn opt_in;
+  const cudaError_t e = opt_in.once(reinterpret_cast<const void*>(tile_mma_kernel<D, kPaged>), bytes);
   if (e != cudaSuccess) return e;
   tile_mma_kernel<D, kPaged><<<static_cast<unsigned>(p.units), kThreads, bytes, s>>>(p, k, v);
   return cudaGetLastError();

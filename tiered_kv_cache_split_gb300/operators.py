@@ -10,6 +10,7 @@ or device; the library's own checks raise TkvError.
 from __future__ import annotations
 
 import ctypes
+from array import array
 
 import torch
 
@@ -24,22 +25,30 @@ def _need(ok, message):
 
 
 def _ints(values, n, name):
-    """Host integers as a C int32 array."""
+    """(C int32 array, entries) of host integers."""
     if isinstance(values, torch.Tensor):
         _need(values.device.type == "cpu", f"{name}: host integers")
         values = values.tolist()
-    values = [int(v) for v in values]
-    _need(n is None or len(values) == n, f"{name}: one entry per sequence")
-    _need(all(-(1 << 31) <= v < (1 << 31) for v in values), f"{name}: out of int32")
-    return (ctypes.c_int32 * max(len(values), 1))(*values), len(values)
+    try:
+        values = array("i", values)
+    except (TypeError, OverflowError) as e:
+        raise ValueError(f"{name}: host integers of 32 bits ({e})") from None
+    k = len(values)
+    if n is not None and k != n:
+        raise ValueError(f"{name}: one entry per sequence")
+    return (ctypes.c_int32 * k).from_buffer(values) if k else None, k
 
 
 def _dense(t, name, dtypes, device, shape=None):
-    """A contiguous tensor of the given kind."""
-    _need(isinstance(t, torch.Tensor) and t.dtype in dtypes, f"{name}: wrong dtype")
-    _need(t.device == device, f"{name}: on another device")
-    _need(t.is_contiguous(), f"{name}: not contiguous")
-    _need(shape is None or tuple(t.shape) == tuple(shape), f"{name}: shape must be {list(shape or ())}")
+    """The address of a contiguous tensor of the given kind."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
+        raise ValueError(f"{name}: wrong dtype")
+    if t.device != device:
+        raise ValueError(f"{name}: on another device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: shape must be {list(shape)}")
     return t.data_ptr()
 
 
@@ -55,29 +64,36 @@ def _tokens(t, name, like=None):
 
 
 class _On:
-    """The call's device made current, and its stream."""
+    """The call's device made current if it is not, and its stream."""
+
+    __slots__ = ("device", "guard", "given", "raw")
 
     def __init__(self, device, stream):
         _need(device.type == "cuda", "the tensors must be on a CUDA device")
-        self.guard = torch.cuda.device(device)
-        self.given, self.device = stream, device
+        self.device, self.given, self.guard = device, stream, None
+        if torch.cuda.current_device() != device.index:
+            self.guard = torch.cuda.device(device)
 
     def __enter__(self):
-        self.guard.__enter__()
-        current = torch.cuda.current_stream(self.device)
-        self.stream = current if self.given is None else self.given
-        _need(self.stream.device == self.device, "stream: of another device")
-        self.other = self.stream != current
+        if self.guard is not None:
+            self.guard.__enter__()
+        self.raw = torch.cuda.current_stream(self.device).cuda_stream
+        if self.given is not None:
+            _need(self.given.device == self.device, "stream: of another device")
+            if self.given.cuda_stream == self.raw:
+                self.given = None
+            else:
+                self.raw = self.given.cuda_stream
         return self
 
     def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
+        return self.guard.__exit__(*exc) if self.guard is not None else None
 
     def empty(self, shape, dtype):
         """A buffer made for this call."""
         t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self.other:
-            t.record_stream(self.stream)
+        if self.given is not None:
+            t.record_stream(self.given)
         return t
 
     def scratch(self, given, need):
@@ -112,8 +128,8 @@ def prompt_attention(q, k, v, q_lens, k_lens=None, out=None, scratch=None, statu
     _need(k.shape == v.shape, "v: shape must be that of k")
     ql, batch = _ints(q_lens, None, "q_lens")
     kl, _ = (ql, batch) if k_lens is None else _ints(k_lens, batch, "k_lens")
-    _need(sum(ql[:batch]) == q.shape[0], "q_lens: must add up to the tokens of q")
-    _need(sum(kl[:batch]) == k.shape[0], "k_lens: must add up to the tokens of k")
+    _need(sum(ql or ()) == q.shape[0], "q_lens: must add up to the tokens of q")
+    _need(sum(kl or ()) == k.shape[0], "k_lens: must add up to the tokens of k")
     hq, hkv, d, dt = q.shape[1], k.shape[1], q.shape[2], _DTYPES[q.dtype]
     with _On(q.device, stream) as on:
         need = ctypes.c_size_t()
@@ -124,7 +140,7 @@ def prompt_attention(q, k, v, q_lens, k_lens=None, out=None, scratch=None, statu
         _need(out.shape == q.shape, "out: shape must be that of q")
         scratch = on.scratch(scratch, need.value)
         L.check(lib.tkv_prompt_attention(batch, ql, kl, hq, hkv, d, dt, pq, sq, pk, sk, pv, sv, po, so,
-                                         *_bytes(scratch), _status(status, q.device), on.stream.cuda_stream))
+                                         *_bytes(scratch), _status(status, q.device), on.raw))
     return out
 
 
@@ -165,7 +181,7 @@ def shared_prefix_attention(q, pool, page_table, slot_mask, page_counts, shared_
         scratch = on.scratch(scratch, need.value)
         L.check(lib.tkv_shared_prefix_attention(batch, hq, hkv, d, dt, pq, pp, pages, pt, pm, counts, max_pages,
                                                 shared_pages, po, pa, *_bytes(scratch), _status(status, dev),
-                                                on.stream.cuda_stream))
+                                                on.raw))
     return out
 
 
@@ -213,7 +229,7 @@ def fork_sequences(pool, page_table, page_counts, page_refs, slot_mask, parents,
         scratch = on.scratch(scratch, need.value)
         status = on.empty(1, torch.int32)
         L.check(lib.tkv_fork_sequences(pp, layers, pages, hkv, d, dt, pt, rows, max_pages, counts, pr, pm, pos, n, par,
-                                       chi, bool(share), *_bytes(scratch), status.data_ptr(), on.stream.cuda_stream))
+                                       chi, bool(share), *_bytes(scratch), status.data_ptr(), on.raw))
     return status
 
 
@@ -233,7 +249,7 @@ def free_sequences(page_table, page_counts, page_refs, slot_mask, seqs, stream=N
     with _On(dev, stream) as on:
         status = on.empty(1, torch.int32)
         L.check(lib.tkv_free_sequences(pt, rows, max_pages, counts, pages, pr, pm, n, seq, status.data_ptr(),
-                                       on.stream.cuda_stream))
+                                       on.raw))
     return status
 
 
@@ -255,5 +271,5 @@ def compact_sequences(pool, page_table, page_counts, page_refs, slot_mask, posit
         scratch = on.scratch(scratch, need.value)
         new = on.empty(rows, torch.int32)
         L.check(lib.tkv_compact_sequences(pp, layers, pages, hkv, d, dt, pt, rows, max_pages, counts, pr, pm, pos,
-                                          new.data_ptr(), *_bytes(scratch), on.stream.cuda_stream))
+                                          new.data_ptr(), *_bytes(scratch), on.raw))
     return new
