@@ -17,26 +17,30 @@ import torch
 from . import _lib as L
 
 _DTYPES = {torch.float32: L.DTYPE_F32, torch.bfloat16: L.DTYPE_BF16}
-
-
-def _need(ok, message):
-    if not ok:
-        raise ValueError(message)
+_I32 = (torch.int32,)
+_MASK = (torch.int32, torch.uint32)
+# The small calls are bound by this file, so it stays flat: cheap checks first,
+# names and messages only on the way out.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
 def _ints(values, n, name):
-    """(C int32 array, entries) of host integers."""
+    """Host integers as an array of C ints."""
     if isinstance(values, torch.Tensor):
-        _need(values.device.type == "cpu", f"{name}: host integers")
+        if values.device.type != "cpu":
+            raise ValueError(f"{name}: host integers")
         values = values.tolist()
     try:
         values = array("i", values)
     except (TypeError, OverflowError) as e:
         raise ValueError(f"{name}: host integers of 32 bits ({e})") from None
-    k = len(values)
-    if n is not None and k != n:
+    if n is not None and len(values) != n:
         raise ValueError(f"{name}: one entry per sequence")
-    return (ctypes.c_int32 * k).from_buffer(values) if k else None, k
+    return values
+
+
+def _at(ints):
+    return ints.buffer_info()[0]
 
 
 def _dense(t, name, dtypes, device, shape=None):
@@ -53,63 +57,62 @@ def _dense(t, name, dtypes, device, shape=None):
 
 
 def _tokens(t, name, like=None):
-    """(pointer, token stride) of [tokens, heads, d] whose tokens are dense."""
-    _need(isinstance(t, torch.Tensor) and t.dim() == 3, f"{name}: must be [tokens, heads, d]")
-    _need(like is None or (t.dtype == like.dtype and t.device == like.device and t.shape[2] == like.shape[2]),
-          f"{name}: dtype, device and d must be those of q")
+    """(tokens, heads, d, token stride) of [tokens, heads, d] whose tokens are dense."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name}: must be [tokens, heads, d]")
+    if like is not None and (t.dtype is not like.dtype or t.device != like.device):
+        raise ValueError(f"{name}: dtype and device must be those of q")
     n, h, d = t.shape
-    st = t.stride()
-    _need((st[2] == 1 or d == 1) and (st[1] == d or h == 1), f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), (st[0] if n > 1 else h * d)
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d != 1) or (s1 != d and h != 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return n, h, d, (s0 if n > 1 else h * d)
 
 
 class _On:
-    """The call's device made current if it is not, and its stream."""
+    """The call's device made current if it is not, its stream, and buffers made
+    for the call (kept alive for a stream other than the current one)."""
 
     __slots__ = ("device", "guard", "given", "raw")
 
     def __init__(self, device, stream):
-        _need(device.type == "cuda", "the tensors must be on a CUDA device")
-        self.device, self.given, self.guard = device, stream, None
-        if torch.cuda.current_device() != device.index:
-            self.guard = torch.cuda.device(device)
+        if device.type != "cuda":
+            raise ValueError("the tensors must be on a CUDA device")
+        self.device = device
+        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        self.given = None
+        self.raw = _raw_stream(device.index)
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError("stream: of another device")
+            if stream.cuda_stream != self.raw:
+                self.given, self.raw = stream, stream.cuda_stream
 
     def __enter__(self):
         if self.guard is not None:
             self.guard.__enter__()
-        self.raw = torch.cuda.current_stream(self.device).cuda_stream
-        if self.given is not None:
-            _need(self.given.device == self.device, "stream: of another device")
-            if self.given.cuda_stream == self.raw:
-                self.given = None
-            else:
-                self.raw = self.given.cuda_stream
         return self
 
     def __exit__(self, *exc):
-        return self.guard.__exit__(*exc) if self.guard is not None else None
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
 
     def empty(self, shape, dtype):
-        """A buffer made for this call."""
         t = torch.empty(shape, dtype=dtype, device=self.device)
         if self.given is not None:
             t.record_stream(self.given)
         return t
 
     def scratch(self, given, need):
+        """(tensor, address, bytes)"""
         if given is None:
-            return self.empty(need, torch.uint8) if need else None
-        _need(isinstance(given, torch.Tensor) and given.is_contiguous() and given.device == self.device,
-              "scratch: a contiguous tensor on the call's device")
-        return given
-
-
-def _bytes(t):
-    return (t.data_ptr(), t.numel() * t.element_size()) if t is not None else (None, 0)
-
-
-def _status(status, device):
-    return None if status is None else _dense(status, "status", (torch.int32,), device, (1,))
+            if need == 0:
+                return None, None, 0
+            given = self.empty(need, torch.uint8)
+            return given, given.data_ptr(), need
+        if not isinstance(given, torch.Tensor) or not given.is_contiguous() or given.device != self.device:
+            raise ValueError("scratch: a contiguous tensor on the call's device")
+        return given, given.data_ptr(), given.numel() * given.element_size()
 
 
 def prompt_attention(q, k, v, q_lens, k_lens=None, out=None, scratch=None, status=None, stream=None):
@@ -121,26 +124,41 @@ def prompt_attention(q, k, v, q_lens, k_lens=None, out=None, scratch=None, statu
     strided, as views of a fused projection are.
     """
     lib = L.load()
-    pq, sq = _tokens(q, "q")
-    pk, sk = _tokens(k, "k", q)
-    pv, sv = _tokens(v, "v", q)
-    _need(q.dtype in _DTYPES, "q: float32 or bfloat16")
-    _need(k.shape == v.shape, "v: shape must be that of k")
-    ql, batch = _ints(q_lens, None, "q_lens")
-    kl, _ = (ql, batch) if k_lens is None else _ints(k_lens, batch, "k_lens")
-    _need(sum(ql or ()) == q.shape[0], "q_lens: must add up to the tokens of q")
-    _need(sum(kl or ()) == k.shape[0], "k_lens: must add up to the tokens of k")
-    hq, hkv, d, dt = q.shape[1], k.shape[1], q.shape[2], _DTYPES[q.dtype]
-    with _On(q.device, stream) as on:
-        need = ctypes.c_size_t()
-        L.check(lib.tkv_prompt_attention_scratch_size(batch, ql, kl, hq, hkv, d, dt, ctypes.byref(need)))
+    tq, hq, d, sq = _tokens(q, "q")
+    tk, hkv, dk, sk = _tokens(k, "k", q)
+    tv, hv, dv, sv = _tokens(v, "v", q)
+    dt = _DTYPES.get(q.dtype)
+    if dt is None:
+        raise ValueError("q: float32 or bfloat16")
+    if dk != d:
+        raise ValueError("k: d must be that of q")
+    if tv != tk or hv != hkv or dv != d:
+        raise ValueError("v: shape must be that of k")
+    ql = _ints(q_lens, None, "q_lens")
+    batch = len(ql)
+    kl = ql if k_lens is None else _ints(k_lens, batch, "k_lens")
+    if sum(ql) != tq:
+        raise ValueError("q_lens: must add up to the tokens of q")
+    if sum(kl) != tk:
+        raise ValueError("k_lens: must add up to the tokens of k")
+    dev = q.device
+    with _On(dev, stream) as on:
         if out is None:
-            out = on.empty(q.shape, q.dtype)
-        po, so = _tokens(out, "out", q)
-        _need(out.shape == q.shape, "out: shape must be that of q")
-        scratch = on.scratch(scratch, need.value)
-        L.check(lib.tkv_prompt_attention(batch, ql, kl, hq, hkv, d, dt, pq, sq, pk, sk, pv, sv, po, so,
-                                         *_bytes(scratch), _status(status, q.device), on.raw))
+            out, so = on.empty((tq, hq, d), q.dtype), hq * d
+        else:
+            to, ho, do, so = _tokens(out, "out", q)
+            if to != tq or ho != hq or do != d:
+                raise ValueError("out: shape must be that of q")
+        a, b, need = _at(ql), _at(kl), ctypes.c_size_t()
+        st = lib.tkv_prompt_attention_scratch_size(batch, a, b, hq, hkv, d, dt, ctypes.byref(need))
+        if st:
+            L.check(st)
+        keep, scratch, nbytes = on.scratch(scratch, need.value)
+        st = lib.tkv_prompt_attention(batch, a, b, hq, hkv, d, dt, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv,
+                                      out.data_ptr(), so, scratch, nbytes,
+                                      None if status is None else _dense(status, "status", _I32, dev, (1,)), on.raw)
+        if st:
+            L.check(st)
     return out
 
 
@@ -156,54 +174,64 @@ def shared_prefix_attention(q, pool, page_table, slot_mask, page_counts, shared_
     behind the prefix).
     """
     lib = L.load()
-    dev = q.device
-    _need(q.dim() == 3 and q.dtype in _DTYPES, "q: float32 or bfloat16 [B, Hq, d]")
+    dt = _DTYPES.get(q.dtype)
+    if dt is None or q.dim() != 3:
+        raise ValueError("q: float32 or bfloat16 [B, Hq, d]")
+    if pool.dim() != 5:
+        raise ValueError("pool: must be [pages, Hkv, 2, 16, d]")
+    if page_table.dim() != 2 or page_table.shape[0] != q.shape[0]:
+        raise ValueError("page_table: must be [B, max_pages]")
+    dev, dtypes = q.device, (q.dtype,)
     batch, hq, d = q.shape
-    pq = _dense(q, "q", (q.dtype,), dev)
-    _need(pool.dim() == 5, "pool: must be [pages, Hkv, 2, 16, d]")
     pages, hkv = pool.shape[:2]
-    pp = _dense(pool, "pool", (q.dtype,), dev, (pages, hkv, 2, 16, d))
-    _need(page_table.dim() == 2 and page_table.shape[0] == batch, "page_table: must be [B, max_pages]")
-    pt = _dense(page_table, "page_table", (torch.int32,), dev)
-    pm = _dense(slot_mask, "slot_mask", (torch.int32, torch.uint32), dev, (pages,))
-    max_pages, dt = page_table.shape[1], _DTYPES[q.dtype]
-    counts, _ = _ints(page_counts, batch, "page_counts")
-    pa = None
-    if alpha_sum is not None:
-        pa = _dense(alpha_sum, "alpha_sum", (torch.float32,), dev, (batch, hkv, max_pages * 16))
+    max_pages = page_table.shape[1]
+    pq = _dense(q, "q", dtypes, dev)
+    pp = _dense(pool, "pool", dtypes, dev, (pages, hkv, 2, 16, d))
+    pt = _dense(page_table, "page_table", _I32, dev)
+    pm = _dense(slot_mask, "slot_mask", _MASK, dev, (pages,))
+    pa = None if alpha_sum is None else _dense(alpha_sum, "alpha_sum", (torch.float32,), dev, (batch, hkv, max_pages * 16))
+    counts = _ints(page_counts, batch, "page_counts")
     with _On(dev, stream) as on:
-        need = ctypes.c_size_t()
-        L.check(lib.tkv_shared_prefix_attention_scratch_size(batch, hq, hkv, d, dt, counts, max_pages, shared_pages,
-                                                             pa is not None, ctypes.byref(need)))
         if out is None:
-            out = on.empty(q.shape, q.dtype)
-        po = _dense(out, "out", (q.dtype,), dev, q.shape)
-        scratch = on.scratch(scratch, need.value)
-        L.check(lib.tkv_shared_prefix_attention(batch, hq, hkv, d, dt, pq, pp, pages, pt, pm, counts, max_pages,
-                                                shared_pages, po, pa, *_bytes(scratch), _status(status, dev),
-                                                on.raw))
+            out = on.empty((batch, hq, d), q.dtype)
+            po = out.data_ptr()
+        else:
+            po = _dense(out, "out", dtypes, dev, (batch, hq, d))
+        c, need = _at(counts), ctypes.c_size_t()
+        st = lib.tkv_shared_prefix_attention_scratch_size(batch, hq, hkv, d, dt, c, max_pages, shared_pages, pa is not None,
+                                                          ctypes.byref(need))
+        if st:
+            L.check(st)
+        keep, scratch, nbytes = on.scratch(scratch, need.value)
+        st = lib.tkv_shared_prefix_attention(batch, hq, hkv, d, dt, pq, pp, pages, pt, pm, c, max_pages, shared_pages, po, pa,
+                                             scratch, nbytes,
+                                             None if status is None else _dense(status, "status", _I32, dev, (1,)), on.raw)
+        if st:
+            L.check(st)
     return out
 
 
 def _pool(pool):
-    """(pointer, layers, pages, Hkv, d, dtype) of [layers, pages, Hkv, 2, 16, d], or of one layer of it."""
-    _need(isinstance(pool, torch.Tensor) and pool.dim() in (5, 6) and tuple(pool.shape[-3:-1]) == (2, 16),
-          "pool: must be [layers, pages, Hkv, 2, 16, d] or one layer of it")
-    _need(pool.dtype in _DTYPES, "pool: float32 or bfloat16")
-    _need(pool.is_contiguous(), "pool: not contiguous")
-    shape = pool.shape if pool.dim() == 6 else (1, *pool.shape)
-    return pool.data_ptr(), shape[0], shape[1], shape[2], shape[5], _DTYPES[pool.dtype]
+    """(address, layers, pages, Hkv, d, dtype) of [layers, pages, Hkv, 2, 16, d], or of one layer of it."""
+    shape = tuple(pool.shape) if isinstance(pool, torch.Tensor) else ()
+    if len(shape) == 5:
+        shape = (1, *shape)
+    if len(shape) != 6 or shape[3:5] != (2, 16):
+        raise ValueError("pool: must be [layers, pages, Hkv, 2, 16, d] or one layer of it")
+    dt = _DTYPES.get(pool.dtype)
+    if dt is None:
+        raise ValueError("pool: float32 or bfloat16")
+    if not pool.is_contiguous():
+        raise ValueError("pool: not contiguous")
+    return pool.data_ptr(), shape[0], shape[1], shape[2], shape[5], dt
 
 
 def _book(page_table, page_refs, slot_mask, device, pages):
-    _need(isinstance(page_table, torch.Tensor) and page_table.dim() == 2, "page_table: must be [rows, max_pages]")
-    return (_dense(page_table, "page_table", (torch.int32,), device),
-            None if page_refs is None else _dense(page_refs, "page_refs", (torch.int32,), device, (pages,)),
-            _dense(slot_mask, "slot_mask", (torch.int32, torch.uint32), device, (pages,)))
-
-
-def _positions(positions, device, pages):
-    return None if positions is None else _dense(positions, "positions", (torch.int32,), device, (pages, 16))
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table: must be [rows, max_pages]")
+    return (_dense(page_table, "page_table", _I32, device),
+            None if page_refs is None else _dense(page_refs, "page_refs", _I32, device, (pages,)),
+            _dense(slot_mask, "slot_mask", _MASK, device, (pages,)))
 
 
 def fork_sequences(pool, page_table, page_counts, page_refs, slot_mask, parents, children, share=True,
@@ -217,19 +245,26 @@ def fork_sequences(pool, page_table, page_counts, page_refs, slot_mask, parents,
     """
     lib = L.load()
     pp, layers, pages, hkv, d, dt = _pool(pool)
-    pt, pr, pm = _book(page_table, page_refs, slot_mask, pool.device, pages)
+    dev = pool.device
+    pt, pr, pm = _book(page_table, page_refs, slot_mask, dev, pages)
     rows, max_pages = page_table.shape
-    counts, _ = _ints(page_counts, rows, "page_counts")
-    par, n = _ints(parents, None, "parents")
-    chi, _ = _ints(children, n, "children")
-    pos = _positions(positions, pool.device, pages)
-    with _On(pool.device, stream) as on:
-        need = ctypes.c_size_t()
-        L.check(lib.tkv_fork_sequences_scratch_size(rows, max_pages, counts, n, par, chi, bool(share), ctypes.byref(need)))
-        scratch = on.scratch(scratch, need.value)
+    counts = _ints(page_counts, rows, "page_counts")
+    par = _ints(parents, None, "parents")
+    n = len(par)
+    chi = _ints(children, n, "children")
+    pos = None if positions is None else _dense(positions, "positions", _I32, dev, (pages, 16))
+    share = bool(share)
+    with _On(dev, stream) as on:
+        c, a, b, need = _at(counts), _at(par), _at(chi), ctypes.c_size_t()
+        st = lib.tkv_fork_sequences_scratch_size(rows, max_pages, c, n, a, b, share, ctypes.byref(need))
+        if st:
+            L.check(st)
+        keep, scratch, nbytes = on.scratch(scratch, need.value)
         status = on.empty(1, torch.int32)
-        L.check(lib.tkv_fork_sequences(pp, layers, pages, hkv, d, dt, pt, rows, max_pages, counts, pr, pm, pos, n, par,
-                                       chi, bool(share), *_bytes(scratch), status.data_ptr(), on.raw))
+        st = lib.tkv_fork_sequences(pp, layers, pages, hkv, d, dt, pt, rows, max_pages, c, pr, pm, pos, n, a, b, share,
+                                    scratch, nbytes, status.data_ptr(), on.raw)
+        if st:
+            L.check(st)
     return status
 
 
@@ -240,16 +275,19 @@ def free_sequences(page_table, page_counts, page_refs, slot_mask, seqs, stream=N
     """
     lib = L.load()
     dev = page_table.device
-    _need(page_refs is not None and page_refs.dim() == 1, "page_refs: must be [pages]")
+    if not isinstance(page_refs, torch.Tensor) or page_refs.dim() != 1:
+        raise ValueError("page_refs: must be [pages]")
     pages = page_refs.shape[0]
     pt, pr, pm = _book(page_table, page_refs, slot_mask, dev, pages)
     rows, max_pages = page_table.shape
-    counts, _ = _ints(page_counts, rows, "page_counts")
-    seq, n = _ints(seqs, None, "seqs")
+    counts = _ints(page_counts, rows, "page_counts")
+    seq = _ints(seqs, None, "seqs")
     with _On(dev, stream) as on:
         status = on.empty(1, torch.int32)
-        L.check(lib.tkv_free_sequences(pt, rows, max_pages, counts, pages, pr, pm, n, seq, status.data_ptr(),
-                                       on.raw))
+        st = lib.tkv_free_sequences(pt, rows, max_pages, _at(counts), pages, pr, pm, len(seq), _at(seq), status.data_ptr(),
+                                    on.raw)
+        if st:
+            L.check(st)
     return status
 
 
@@ -261,15 +299,20 @@ def compact_sequences(pool, page_table, page_counts, page_refs, slot_mask, posit
     """
     lib = L.load()
     pp, layers, pages, hkv, d, dt = _pool(pool)
-    pt, pr, pm = _book(page_table, page_refs, slot_mask, pool.device, pages)
+    dev = pool.device
+    pt, pr, pm = _book(page_table, page_refs, slot_mask, dev, pages)
     rows, max_pages = page_table.shape
-    counts, _ = _ints(page_counts, rows, "page_counts")
-    pos = _positions(positions, pool.device, pages)
-    with _On(pool.device, stream) as on:
-        need = ctypes.c_size_t()
-        L.check(lib.tkv_compact_sequences_scratch_size(rows, max_pages, counts, ctypes.byref(need)))
-        scratch = on.scratch(scratch, need.value)
+    counts = _ints(page_counts, rows, "page_counts")
+    pos = None if positions is None else _dense(positions, "positions", _I32, dev, (pages, 16))
+    with _On(dev, stream) as on:
+        c, need = _at(counts), ctypes.c_size_t()
+        st = lib.tkv_compact_sequences_scratch_size(rows, max_pages, c, ctypes.byref(need))
+        if st:
+            L.check(st)
+        keep, scratch, nbytes = on.scratch(scratch, need.value)
         new = on.empty(rows, torch.int32)
-        L.check(lib.tkv_compact_sequences(pp, layers, pages, hkv, d, dt, pt, rows, max_pages, counts, pr, pm, pos,
-                                          new.data_ptr(), *_bytes(scratch), on.raw))
+        st = lib.tkv_compact_sequences(pp, layers, pages, hkv, d, dt, pt, rows, max_pages, c, pr, pm, pos, new.data_ptr(),
+                                       scratch, nbytes, on.raw)
+        if st:
+            L.check(st)
     return new
