@@ -16,7 +16,8 @@ def attend(q, k, v, seen, dtype):
     Returns (o, bound, p). The bound counts, with u = half a step of the dtype
     and e = 2^-24, A = sum_j p_j |v_j| per row:
       output rounding        u |o|
-      weights rounded to bf16 for the product with V (bf16 only)  u A
+      weights rounded to bf16, w (1 + t) with |t| <= u, in the product with V and in
+      their sum (bf16 only): sum t w v - o sum t w, at most u (A + |o|)
       a logit is a d-term fp32 sum: off by D = (d + 2) e max_j sum|q k| / sqrt(d),
       so each weight and the sum of weights by a relative D + 4 e (exp2, its
       argument): 2 (D + 4 e) A, and 2^-20 for arguments up to 16 in base 2
@@ -39,7 +40,7 @@ def attend(q, k, v, seen, dtype):
     o, a = p @ v0, p @ np.abs(v0)
     mag = np.where(seen, mag, 0.0).max(1, keepdims=True)
     delta = (d + 2) * e * mag + 4 * e + e * mag * 1.5
-    bound = u * np.abs(o) + (u * a if dtype == torch.bfloat16 else 0.0) + (2 * delta + 2 * m * e) * a
+    bound = u * np.abs(o) + (u * (a + np.abs(o)) if dtype == torch.bfloat16 else 0.0) + (2 * delta + 2 * m * e) * a
     return o, bound * (1 + 2.0 ** -6) + 1e-30, p
 
 

@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kMergeThreads) tile_merge_kernel(const __grid_
     const PartList l = part_list(p, tok, h, g);
     const float base = parts_max(p, l, lane);
     float z = 0.f;
-    for (int k = lane; k < l.n; k += 32) z += exp2f(p.part_m[l.at(k)] - base) * p.part_z[l.at(k)];
+    for (int k = lane; k < l.n; k += 32) z += exp2f(p.part_m[l.at(k)] - base) * p.part_ze[l.at(k)];
 #pragma unroll
     for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
     if (lane == 0) {
@@ -510,13 +510,15 @@ TilePlan plan_units(TileParams& p, const TileShape& ts, bool want_spill) {
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct TileScratch {
-  size_t o_m, o_z, o_spill, bytes;
+  size_t o_m, o_z, o_ze, o_spill, bytes;
 };
 TileScratch tile_scratch(const TilePlan& pl, int D) {
+  const size_t column = align256(static_cast<size_t>(pl.part_rows) * 4);
   TileScratch s;
   s.o_m = align256(static_cast<size_t>(pl.part_rows) * D * 4);
-  s.o_z = s.o_m + align256(static_cast<size_t>(pl.part_rows) * 4);
-  s.o_spill = s.o_z + align256(static_cast<size_t>(pl.part_rows) * 4);
+  s.o_z = s.o_m + column;
+  s.o_ze = s.o_z + column;
+  s.o_spill = s.o_ze + (pl.spill ? column : 0);
   s.bytes = s.o_spill + align256(static_cast<size_t>(pl.spill) * 4);
   return s;
 }
@@ -643,7 +645,7 @@ cudaError_t launch_dtype(const TileParams& p, int dtype, int D, int tokens, int6
 
 bool misaligned(const void* ptr, size_t to) { return reinterpret_cast<uintptr_t>(ptr) % to != 0; }
 
-int bind_scratch(TileParams& p, const TilePlan& plan, int D, void* scratch, size_t bytes) {
+int bind_scratch(TileParams& p, const TilePlan& plan, int D, bool fp32, void* scratch, size_t bytes) {
   const TileScratch s = tile_scratch(plan, D);
   if (s.bytes == 0) return TKV_OK;
   if (!scratch) return report(TKV_ERR_INVALID_ARG, "null scratch: need %zu bytes", s.bytes);
@@ -653,6 +655,7 @@ int bind_scratch(TileParams& p, const TilePlan& plan, int D, void* scratch, size
   p.part_o = reinterpret_cast<float*>(at);
   p.part_m = reinterpret_cast<float*>(at + s.o_m);
   p.part_z = reinterpret_cast<float*>(at + s.o_z);
+  p.part_ze = fp32 ? p.part_z : reinterpret_cast<float*>(at + s.o_ze);
   p.spill = reinterpret_cast<float*>(at + s.o_spill);
   return TKV_OK;
 }
@@ -696,7 +699,7 @@ tkv_status tkv_prompt_attention(int32_t batch, const int32_t* q_lens, const int3
   if (q_stride < qrow || out_stride < qrow || k_stride < krow || v_stride < krow || q_stride % unit || out_stride % unit ||
       k_stride % unit || v_stride % unit || (q_stride | out_stride | k_stride | v_stride) >> 36)
     return tkv_status(report(TKV_ERR_INVALID_ARG, "token strides must hold a token and be multiples of 16 bytes"));
-  if (int st = bind_scratch(p, plan, head_dim, scratch, scratch_bytes)) return tkv_status(st);
+  if (int st = bind_scratch(p, plan, head_dim, kv_dtype == TKV_DTYPE_F32, scratch, scratch_bytes)) return tkv_status(st);
   p.q = q; p.q_stride = q_stride;
   p.k = k; p.k_stride = k_stride;
   p.v = v; p.v_stride = v_stride;
@@ -738,7 +741,7 @@ tkv_status tkv_shared_prefix_attention(int32_t batch, int32_t n_q_heads, int32_t
     return tkv_status(report(TKV_ERR_INVALID_ARG, "pool_pages x n_kv_heads must be 1 to 2^29"));
   if (misaligned(q, 16) || misaligned(pool, 16) || misaligned(out, 16) || misaligned(alpha_sum, 16))
     return tkv_status(report(TKV_ERR_INVALID_ARG, "q, pool, out and alpha_sum must be 16-byte aligned"));
-  if (int st = bind_scratch(p, plan, head_dim, scratch, scratch_bytes)) return tkv_status(st);
+  if (int st = bind_scratch(p, plan, head_dim, kv_dtype == TKV_DTYPE_F32, scratch, scratch_bytes)) return tkv_status(st);
   p.q = q; p.q_stride = static_cast<int64_t>(n_q_heads) * head_dim;
   p.out = out; p.out_stride = p.q_stride;
   p.out_sectors = !misaligned(out, 32);

@@ -52,6 +52,7 @@ struct TileParams {
   const uint32_t* mask;
   int64_t pages;               // pool pages: ids outside read as empty pages
   float *part_o, *part_m, *part_z;
+  float* part_ze;              // Z of unrounded weights, for alpha (fp32: part_z)
   float* spill;
   float* alpha;                // [B][Hkv][alpha slots], or null
   int64_t alpha_stride_h;

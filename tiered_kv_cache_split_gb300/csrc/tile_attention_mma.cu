@@ -34,8 +34,12 @@
 // of 2^18 of them below 2^38, far inside fp32. With a rise of 8 one half in six
 // was rescaled, at about 1500 cycles each (prompt of 8192, normal queries).
 //
-// The weights are rounded to bf16 (half a step 2^-8 each, unbiased) because the
-// MMA takes P and V in one type; Z sums them before that rounding, in fp32.
+// The weights are rounded to bf16 (half a step 2^-8 each) because the MMA takes
+// P and V in one type. Z sums the rounded weights, in fp32: where few keys carry
+// a row, their errors then leave the quotient (0.0018 off the 64-bit result in
+// the 2-norm, against 0.0023 with Z of the unrounded ones; output rounding alone
+// is 0.0016). alpha is made of unrounded weights: calls that ask for it keep
+// their sum too.
 //
 // 0 * NaN must not reach O: the V rows of holes are zeroed in shared memory, and
 // keys past a sequence's end or that only some rows see have their non-finite V
@@ -50,6 +54,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "tile_attention.h"
 
@@ -708,7 +713,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool valid = r < rows, active = wq * 32 < rows;  // active: the warp has rows at all
       const int lim = tile_row_limit(p, sg, row);
       const int lim_warp = __shfl_sync(0xffffffffu, lim, 0);  // limits rise with the row
-      float ref = -INFINITY, z = 0.f;  // maximum the weights refer to (unscaled logits), sum of weights
+      float ref = -INFINITY;           // maximum the weights refer to (unscaled logits)
+      float z = 0.f, z_exact = 0.f;    // sums of the weights: rounded, not rounded
       bool ok = true;
       for (int h = 0; h < mine; ++h) {
         const int i = w.pair ? h : h >> 1, half = w.pair ? t : h & 1, g = g0 + h, buf = g & 1;
@@ -776,20 +782,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st32(t_o + c, o);
               }
               z *= f;
+              z_exact *= f;
             }
             ref = next;
           }
           const float base = ref == -INFINITY ? 0.f : ref * qs;
           const float2 qs2 = make_float2(qs, qs), base2 = make_float2(-base, -base);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          auto weights = [&](auto exact) {
+            float2 whole[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int c = 0; c < kHalf / 2; ++c) {
-            float2 x = fma2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), qs2, base2);
-            x.x = ex2(x.x);
-            x.y = ex2(x.y);
-            sum[c & 1] = add2(sum[c & 1], x);
-            s[c] = pack2(x.x, x.y);
-          }
+            for (int c = 0; c < kHalf / 2; ++c) {
+              float2 x = fma2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), qs2, base2);
+              x.x = ex2(x.x);
+              x.y = ex2(x.y);
+              s[c] = pack2(x.x, x.y);
+              if constexpr (decltype(exact)::value) whole[c & 1] = add2(whole[c & 1], x);
+              sum[c & 1] = add2(sum[c & 1], make_float2(__uint_as_float(s[c] << 16), __uint_as_float(s[c] & 0xffff0000u)));
+            }
+            if constexpr (decltype(exact)::value) z_exact += (whole[0].x + whole[0].y) + (whole[1].x + whole[1].y);
+          };
+          if (kPaged && p.alpha) weights(std::true_type{});
+          else weights(std::false_type{});
           tmem_st32(t_s + buf * kHalf, s);
           z += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         }
@@ -862,6 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!p.direct && valid) {
           p.part_m[part + r] = ref * qs;
           p.part_z[part + r] = z;
+          if (kPaged && p.alpha) p.part_ze[part + r] = z_exact;
         }
       }
       fence_before();
