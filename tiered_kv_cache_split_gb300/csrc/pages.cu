@@ -254,29 +254,28 @@ struct CompactParams {
   int32_t* new_counts;
 };
 
-constexpr int kPagesPerThread = kMaxSeqPages / kPlanThreads;
-
-// One CTA per sequence. Private pages in list order keep the first
+// One CTA per sequence, kPer consecutive pages per thread (a row of 288 pages took
+// 19 us with 16 per thread for all, 16384 pages being the most). Private pages in list order keep the first
 // ceil(tokens / 16) of them; the valid slots of the rest, in order, fill the
 // holes of those kept, in order. Shared pages stay as they are.
+template <int kPer>
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid_constant__ CompactParams p) {
   __shared__ unsigned long long s_warp[kPlanWarps];
   __shared__ int s_bad;
   const int b = blockIdx.x, tid = threadIdx.x, n = p.count[b];
   int32_t* row = p.table + b * p.stride;
-  const int per = (n + kPlanThreads - 1) / kPlanThreads;  // consecutive pages of each thread
-  const int j0 = tid * per;
+  const int j0 = tid * kPer;
   if (tid == 0) s_bad = 0;
   __syncthreads();
-  int32_t id[kPagesPerThread];
-  uint32_t bits[kPagesPerThread];
+  int32_t id[kPer];
+  uint32_t bits[kPer];
   uint32_t mine = 0;  // bit i: page j0 + i is private
   unsigned long long sum = 0;
 #pragma unroll
-  for (int i = 0; i < kPagesPerThread; ++i) {
+  for (int i = 0; i < kPer; ++i) {
     id[i] = -1;
     bits[i] = 0;
-    if (i >= per || j0 + i >= n) continue;
+    if (j0 + i >= n) continue;
     id[i] = row[j0 + i];
     if (id[i] < 0 || id[i] >= p.pages) {
       s_bad = 1;
@@ -304,7 +303,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid
   unsigned long long hm = 0;
   int stay = 0;
 #pragma unroll
-  for (int i = 0; i < kPagesPerThread; ++i) {
+  for (int i = 0; i < kPer; ++i) {
     if (id[i] < 0) continue;
     if (!((mine >> i) & 1u)) {
       ++stay;
@@ -313,21 +312,21 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid
     if (rank++ < keep) {
       front |= 1u << i;
       ++stay;
-      hm += static_cast<unsigned long long>(kPage - __popc(bits[i])) << 32;
+      hm += static_cast<unsigned long long>(kPage - __popc(bits[i])) << 40;
     } else {
-      hm += __popc(bits[i]);
+      hm += static_cast<unsigned long long>(__popc(bits[i])) << 20;
     }
   }
-  unsigned long long hm_total, stay_total;
-  const unsigned long long hm_at = block_scan(hm, s_warp, &hm_total);
-  int at = static_cast<int>(block_scan(static_cast<unsigned long long>(stay), s_warp, &stay_total));
-  int hole = static_cast<int>(hm_at >> 32), mover = static_cast<int>(hm_at & 0xffffffffu);
-  const int movers = static_cast<int>(hm_total & 0xffffffffu), kept = static_cast<int>(stay_total);
+  // holes of the pages kept, tokens that move, pages that stay: 24, 20 and 20 bits
+  unsigned long long all;
+  const unsigned long long before = block_scan(hm | static_cast<unsigned long long>(stay), s_warp, &all);
+  int at = static_cast<int>(before & 0xfffffu), mover = static_cast<int>(before >> 20 & 0xfffffu), hole = static_cast<int>(before >> 40);
+  const int kept = static_cast<int>(all & 0xfffffu), movers = static_cast<int>(all >> 20 & 0xfffffu);
   int32_t* from = p.from + p.move0[b];
   int32_t* to = p.to + p.move0[b];
   // every read of the row came before the scans' barriers
 #pragma unroll
-  for (int i = 0; i < kPagesPerThread; ++i) {
+  for (int i = 0; i < kPer; ++i) {
     if (id[i] < 0) continue;
     const bool is_front = (front >> i) & 1u, is_tail = ((mine >> i) & 1u) && !is_front;
     if (is_front) {
@@ -344,6 +343,9 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid
       for (uint32_t left = bits[i]; left; left &= left - 1) from[mover++] = id[i] * kPage + __ffs(left) - 1;
       p.mask[id[i]] = 0;
       if (p.refs) p.refs[id[i]] = 0;
+      if (p.positions)  // its tokens' slots are emptied by the move
+        for (uint32_t left = ~bits[i] & kFullMask; left; left &= left - 1)
+          p.positions[static_cast<int64_t>(id[i]) * kPage + __ffs(left) - 1] = -1;
     }
     if (!is_tail) row[at++] = id[i];
   }
@@ -353,13 +355,6 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid
     p.moves[b] = movers;
     p.new_counts[b] = kept;
   }
-  if (!p.positions) return;
-  for (int i = tid; i < movers; i += kPlanThreads) p.positions[to[i]] = p.positions[from[i]];
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kPagesPerThread; ++i)
-    if (id[i] >= 0 && ((mine >> i) & 1u) && !((front >> i) & 1u))
-      for (int s = 0; s < kPage; ++s) p.positions[static_cast<int64_t>(id[i]) * kPage + s] = -1;
 }
 
 // One warp per (layer, moved token): its 2 * Hkv rows, 16 bytes per lane.
@@ -388,6 +383,10 @@ __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const __grid
       if (s_first[mid] <= k) lo = mid; else hi = mid - 1;
     }
     const int32_t from = p.from[p.move0[lo] + k - s_first[lo]], to = p.to[p.move0[lo] + k - s_first[lo]];
+    if (layer == 0 && p.positions && lane == 0) {  // a token's slot is read here alone, so it can be emptied here
+      p.positions[to] = p.positions[from];
+      p.positions[from] = -1;
+    }
     char* base = p.pool.base + layer * p.pool.layer_bytes;
     const char* src = base + (from / kPage) * p.pool.page_bytes + (from % kPage) * p.pool.row_bytes;
     char* dst = base + (to / kPage) * p.pool.page_bytes + (to % kPage) * p.pool.row_bytes;
@@ -627,7 +626,10 @@ tkv_status tkv_compact_sequences(void* pool, int32_t n_layers, int64_t pool_page
   p.to = reinterpret_cast<int32_t*>(static_cast<char*>(scratch) + sc.o_to);
   p.new_counts = new_counts;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  compact_plan_kernel<<<rows, kPlanThreads, 0, st>>>(p);
+  const int32_t most = *std::max_element(page_counts, page_counts + rows);
+  if (most <= kPlanThreads) compact_plan_kernel<1><<<rows, kPlanThreads, 0, st>>>(p);
+  else if (most <= 4 * kPlanThreads) compact_plan_kernel<4><<<rows, kPlanThreads, 0, st>>>(p);
+  else compact_plan_kernel<kMaxSeqPages / kPlanThreads><<<rows, kPlanThreads, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return tkv_status(launched("compact plan", e));
   return tkv_status(launched("compact", launch_after(compact_move_kernel, p, ctas_for(pages * n_layers), st)));

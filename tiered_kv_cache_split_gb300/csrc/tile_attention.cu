@@ -429,10 +429,11 @@ SegWork seg_work(const TileParams& p, const TileSeg& s, const TileShape& ts) {
   return w;
 }
 
-// What a unit costs beside its blocks, in blocks: the fixed part, and its
-// partial rows written and read again where keys are split.
+// What a unit costs beside its blocks, in blocks: the fixed part (half of it for
+// a tile of few rows), and its partial rows written and read again where keys are split.
 double unit_cost(const TileShape& ts, int64_t rows, bool split) {
-  return ts.unit_cost + (split ? static_cast<double>(std::min<int64_t>(rows, static_cast<int64_t>(ts.rows) * ts.tpg)) / 64 : 0.0);
+  const int64_t most = static_cast<int64_t>(ts.rows) * ts.tpg;
+  return ts.unit_cost * (rows <= ts.rows ? 0.5 : 1.0) + (split ? static_cast<double>(std::min(rows, most)) / 64 : 0.0);
 }
 
 // Key blocks per unit. Units are handed out longest first to `slots` places, so
@@ -484,21 +485,30 @@ TilePlan plan_units(TileParams& p, const TileShape& ts, bool want_spill) {
   const int64_t per = blocks_per_unit(p, work, ts);
   for (int i = 0; i < p.nseg; ++i) split |= work[i].groups && work[i].most > per;
   p.direct = !split;
+  int32_t length[kMaxSegs];
+  for (int i = 0; i < p.nseg; ++i) {
+    const int64_t parts = work[i].groups ? std::max<int64_t>(1, ceil_div(work[i].most, per)) : 0;
+    p.seg[i].splits = split ? static_cast<int32_t>(parts) : work[i].groups > 0;
+    length[i] = parts ? static_cast<int32_t>(ceil_div(work[i].most, p.seg[i].splits)) + 1 : 0;
+    p.order[i] = static_cast<uint8_t>(i);
+  }
+  std::stable_sort(p.order, p.order + p.nseg, [&](uint8_t a, uint8_t b) { return length[a] > length[b]; });
+  for (int at = 0; at < p.nseg; ++at) {
+    const int i = p.order[at];
+    p.first_unit[at] = static_cast<int32_t>(out.units);
+    out.units += work[i].groups * p.Hkv * p.seg[i].splits;
+  }
   for (int i = 0; i < p.nseg; ++i) {
     TileSeg& s = p.seg[i];
-    s.unit0 = static_cast<int32_t>(out.units);
     s.part0 = out.part_rows;
     s.spill0 = -1;
-    s.splits = s.groups = s.part_rows = s.pair = 0;
+    s.groups = s.part_rows = s.pair = 0;
     if (!work[i].groups) continue;
     s.groups = static_cast<int32_t>(work[i].groups);
-    s.splits = static_cast<int32_t>(std::max<int64_t>(1, ceil_div(work[i].most, per)));
     const int64_t rows = static_cast<int64_t>(s.ntok) * p.G;
     s.pair = !p.direct && ts.tpg == 2 && rows <= ts.rows;
     s.part_rows = static_cast<int32_t>(std::min<int64_t>(ts.rows, rows));
-    const int64_t n = static_cast<int64_t>(s.groups) * p.Hkv * s.splits;
-    out.units += n;
-    if (!p.direct) out.part_rows += n * ts.tpg * s.part_rows;
+    if (!p.direct) out.part_rows += static_cast<int64_t>(s.groups) * p.Hkv * s.splits * ts.tpg * s.part_rows;
     if (want_spill && p.paged && i > 0) {
       s.spill0 = out.spill;
       out.spill += static_cast<int64_t>(s.nkeys) * p.Hq;
@@ -553,8 +563,6 @@ int plan_prompt(TileParams& p, TilePlan* plan, int32_t batch, const int32_t* q_l
     if (tq * p.G > INT32_MAX || tk > INT32_MAX - 2 * kKeyBlock)
       return report(TKV_ERR_INVALID_ARG, "more than 2^31 rows or keys in one call");
   }
-  // longest first
-  std::stable_sort(p.seg, p.seg + batch, [](const TileSeg& a, const TileSeg& b) { return a.nkeys > b.nkeys; });
   *tokens = tq;
   *keys = tk;
   *plan = plan_units(p, tile_shape(dtype), false);

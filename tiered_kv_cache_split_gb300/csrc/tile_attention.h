@@ -34,7 +34,6 @@ struct TileSeg {
   int32_t see0;      // causal: token i sees keys [0, see0 + i]
   int32_t splits;    // key ranges per row group (0: the segment has no unit)
   int32_t groups;    // row groups
-  int32_t unit0;     // first unit
   int32_t part_rows; // rows per partial tile
   int32_t pair;      // 1: one row tile, its two halves of the CTA take alternate key blocks
 };
@@ -66,6 +65,10 @@ struct TileParams {
   int32_t direct;              // 1: no splits, units write the output
   int32_t tile_rows, tpg;      // rows of a tile, tiles of a row group
   TileSeg seg[kMaxSegs];
+  // units are numbered by segments in this order, longest units first: the
+  // i-th has units first_unit[i] ..
+  int32_t first_unit[kMaxSegs];
+  uint8_t order[kMaxSegs];
 };
 
 struct TileUnit {
@@ -82,24 +85,26 @@ __device__ __forceinline__ int tile_row_limit(const TileParams& p, const TileSeg
 
 __device__ __forceinline__ TileUnit tile_unit(const TileParams& p, int u) {
   TileUnit t;
-  int lo = 0, hi = p.nseg - 1;  // last segment whose first unit is <= u (segments without units share it)
+  int lo = 0, hi = p.nseg - 1;  // the last whose first unit is <= u (those without units come last)
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (p.seg[mid].unit0 <= u) lo = mid; else hi = mid - 1;
+    if (p.first_unit[mid] <= u) lo = mid; else hi = mid - 1;
   }
-  t.seg = lo;
-  const TileSeg& s = p.seg[lo];
-  int r = u - s.unit0;
-  t.split = r % s.splits;
-  r /= s.splits;
-  t.h = r % p.Hkv;
-  t.grp = s.groups - 1 - r / p.Hkv;  // a causal segment's last rows see most keys: they go first
+  t.seg = p.order[lo];
+  const TileSeg& s = p.seg[t.seg];
+  uint32_t r = u - p.first_unit[lo];
+  t.split = r % static_cast<uint32_t>(s.splits);
+  r /= static_cast<uint32_t>(s.splits);
+  t.h = r % static_cast<uint32_t>(p.Hkv);
+  t.grp = s.groups - 1 - static_cast<int>(r / static_cast<uint32_t>(p.Hkv));  // a causal segment's last rows see most keys: they go first
   const int per = s.pair ? p.tile_rows : p.tile_rows * p.tpg;
   t.row0 = t.grp * per;
   t.rows = min(per, s.ntok * p.G - t.row0);
   const int nb = (tile_row_limit(p, s, t.row0 + t.rows - 1) + kKeyBlock - 1) / kKeyBlock;
-  t.j0 = static_cast<int>(static_cast<int64_t>(nb) * t.split / s.splits);
-  t.j1 = static_cast<int>(static_cast<int64_t>(nb) * (t.split + 1) / s.splits);
+  // even ranges, the first nb % splits one block longer
+  const int per_split = nb / s.splits, longer = nb % s.splits;
+  t.j0 = t.split * per_split + min(t.split, longer);
+  t.j1 = t.j0 + per_split + (t.split < longer);
   return t;
 }
 
