@@ -275,20 +275,30 @@ __device__ PartList part_list(const TileParams& p, int tok, int h, int g) {
   return l;
 }
 
-// M (0 where there is no key) of a row, by one warp.
-__device__ __forceinline__ float parts_max(const TileParams& p, const PartList& l, int lane) {
-  float m = -INFINITY;
-  for (int i = lane; i < l.n; i += 32) m = fmaxf(m, p.part_m[l.at(i)]);
+// M (0 where there is no key) and Z of a row, by one warp in one pass.
+__device__ __forceinline__ float2 parts_sum(const TileParams& p, const PartList& l, const float* part_z, int lane) {
+  float m = -INFINITY, z = 0.f;
+  for (int i = lane; i < l.n; i += 32) {
+    const float mi = p.part_m[l.at(i)], zi = part_z[l.at(i)], next = fmaxf(m, mi);
+    if (next == -INFINITY) continue;
+    z = z * exp2f(m - next) + zi * exp2f(mi - next);
+    m = next;
+  }
+  float M = m;
 #pragma unroll
-  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  return m == -INFINITY ? 0.f : m;
+  for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  M = M == -INFINITY ? 0.f : M;
+  z *= exp2f(m - M);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+  return make_float2(M, z);
 }
 __device__ __forceinline__ float parts_inv(float z) { return z > 0.f || z != z ? 1.f / z : 0.f; }
 
 template <typename T, int D, int kShare>
 __global__ void __launch_bounds__(kMergeThreads) tile_merge_kernel(const __grid_constant__ TileParams p, int64_t rows, int row_ctas) {
   constexpr int E = D / 32, kAhead = 8;
-  __shared__ float s_acc[kMergeWarps][D], s_z[kMergeWarps], s_m[kMaxGroup], s_inv[kMaxGroup];
+  __shared__ float s_acc[kMergeWarps][D], s_m[kMaxGroup], s_inv[kMaxGroup];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = p.G;
   cudaGridDependencySynchronize();
   if (static_cast<int>(blockIdx.x) < row_ctas) {
@@ -298,14 +308,11 @@ __global__ void __launch_bounds__(kMergeThreads) tile_merge_kernel(const __grid_
     const int tok = live ? static_cast<int>(row / p.Hq) : 0, hq = live ? static_cast<int>(row % p.Hq) : 0;
     if (live) {
       const PartList l = part_list(p, tok, hq / G, hq % G);
-      const float base = parts_max(p, l, lane);
+      const float2 mz = parts_sum(p, l, p.part_z, lane);
+      z = mz.y;
       for (int i0 = warp % kShare * kAhead; i0 < l.n; i0 += kShare * kAhead) {
         float w = 0.f;
-        if (lane < kAhead && i0 + lane < l.n) {
-          const int64_t r = l.at(i0 + lane);
-          w = exp2f(p.part_m[r] - base);
-          z += w * p.part_z[r];
-        }
+        if (lane < kAhead && i0 + lane < l.n) w = exp2f(p.part_m[l.at(i0 + lane)] - mz.x);
         float v[kAhead][E];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
@@ -330,22 +337,17 @@ __global__ void __launch_bounds__(kMergeThreads) tile_merge_kernel(const __grid_
           for (int e = 0; e < E; ++e) acc[e] = fmaf(wi, v[i][e], acc[e]);
         }
       }
-#pragma unroll
-      for (int d = kAhead / 2; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-      z = __shfl_sync(0xffffffffu, z, 0);
     }
     if constexpr (kShare > 1) {
       if (warp > 0) {
 #pragma unroll
         for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
-        if (lane == 0) s_z[warp] = z;
       }
       __syncthreads();
       if (warp > 0) return;
       for (int o = 1; o < kMergeWarps; ++o) {
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] += s_acc[o][lane * E + e];
-        z += s_z[o];
       }
     }
     if (!live) return;
@@ -367,15 +369,10 @@ __global__ void __launch_bounds__(kMergeThreads) tile_merge_kernel(const __grid_
   const int i = item % per * kAlphaSlots + threadIdx.x * 4;
   if (item % per * kAlphaSlots >= so.nkeys) return;
   for (int g = warp; g < G; g += kMergeWarps) {
-    const PartList l = part_list(p, tok, h, g);
-    const float base = parts_max(p, l, lane);
-    float z = 0.f;
-    for (int k = lane; k < l.n; k += 32) z += exp2f(p.part_m[l.at(k)] - base) * p.part_ze[l.at(k)];
-#pragma unroll
-    for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+    const float2 mz = parts_sum(p, part_list(p, tok, h, g), p.part_ze, lane);
     if (lane == 0) {
-      s_m[g] = base;
-      s_inv[g] = parts_inv(z);
+      s_m[g] = mz.x;
+      s_inv[g] = parts_inv(mz.y);
     }
   }
   __syncthreads();

@@ -429,13 +429,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&sh.work_full[r]);
       }
       if (unit < 0) break;
-      if (lane == 0) {
-        fence_proxy();
-        mbar_expect(&sh.response_full, 16);
-        request_unit(&sh.response, &sh.response_full);
-      }
-      __syncwarp();
-      asked = k;
       const TileSeg& sg = p.seg[w.seg];
       // page ids and masks, a batch ahead of their use
       int32_t id_next = -1, id_after = -1;
@@ -491,6 +484,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       batches += (w.n + kBatch - 1) / kBatch;
+      // Ask for the next unit only now, with this one's last blocks on their way: a
+      // unit claimed earlier would wait behind this one while another SM runs dry
+      // (69 -> 55 us on a decode step of 128 long units and 256 short ones).
+      if (lane == 0) {
+        fence_proxy();
+        mbar_expect(&sh.response_full, 16);
+        request_unit(&sh.response, &sh.response_full);
+      }
+      __syncwarp();
+      asked = k;
       if (!warp_wait(&sh.response_full, k & 1, abort, limit)) break;
       unit = __shfl_sync(0xffffffffu, response_unit(&sh.response), 0);
       asked = -1;
