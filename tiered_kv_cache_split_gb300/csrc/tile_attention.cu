@@ -448,7 +448,7 @@ int64_t blocks_per_unit(const TileParams& p, const SegWork* w, const TileShape& 
   if (whole >= 4 * ts.slots) return most;
   int64_t best = most;
   double best_time = 1e300;
-  for (int64_t cut = 1; cut <= most; cut += 1 + cut / 8) {
+  for (int64_t cut = 1; cut <= most; cut += 1 + cut / 4) {
     const int64_t per = ceil_div(most, cut);
     const bool split = p.paged || cut > 1;
     double work = static_cast<double>(blocks), longest = 0;
@@ -482,18 +482,33 @@ TilePlan plan_units(TileParams& p, const TileShape& ts, bool want_spill) {
   const int64_t per = blocks_per_unit(p, work, ts);
   for (int i = 0; i < p.nseg; ++i) split |= work[i].groups && work[i].most > per;
   p.direct = !split;
-  int32_t length[kMaxSegs];
+  int live = 0;
   for (int i = 0; i < p.nseg; ++i) {
-    const int64_t parts = work[i].groups ? std::max<int64_t>(1, ceil_div(work[i].most, per)) : 0;
-    p.seg[i].splits = split ? static_cast<int32_t>(parts) : work[i].groups > 0;
-    length[i] = parts ? static_cast<int32_t>(ceil_div(work[i].most, p.seg[i].splits)) + 1 : 0;
-    p.order[i] = static_cast<uint8_t>(i);
+    p.seg[i].splits = work[i].groups ? (split ? static_cast<int32_t>(std::max<int64_t>(1, ceil_div(work[i].most, per))) : 1) : 0;
+    live += work[i].groups > 0;
   }
-  std::stable_sort(p.order, p.order + p.nseg, [&](uint8_t a, uint8_t b) { return length[a] > length[b]; });
-  for (int at = 0; at < p.nseg; ++at) {
-    const int i = p.order[at];
-    p.first_unit[at] = static_cast<int32_t>(out.units);
-    out.units += work[i].groups * p.Hkv * p.seg[i].splits;
+  struct Length {
+    int64_t blocks, groups;
+    TileParams::Band band;
+  } bands[kMaxBands];
+  p.nbands = 0;
+  for (int i = 0; i < p.nseg; ++i) {
+    const int64_t groups = work[i].groups;
+    if (!groups) continue;
+    const int64_t cut = p.causal ? std::min<int64_t>(groups, kMaxBands / live) : 1, rows = static_cast<int64_t>(ts.rows) * ts.tpg;
+    for (int64_t j = 0; j < cut; ++j) {
+      const int64_t top = groups - 1 - groups * j / cut, count = top - (groups - 1 - groups * (j + 1) / cut);
+      const int64_t seen = p.causal ? std::min<int64_t>(p.seg[i].nkeys, p.seg[i].see0 + ((top + 1) * rows - 1) / p.G + 1) : p.seg[i].nkeys;
+      bands[p.nbands++] = {ceil_div(ceil_div(seen, kKeyBlock), p.seg[i].splits), count, {0, static_cast<int32_t>(top), i}};
+    }
+  }
+  std::sort(bands, bands + p.nbands, [](const Length& a, const Length& b) {
+    return a.blocks != b.blocks ? a.blocks > b.blocks : a.band.seg != b.band.seg ? a.band.seg < b.band.seg : a.band.top > b.band.top;
+  });
+  for (int i = 0; i < p.nbands; ++i) {
+    p.band[i] = bands[i].band;
+    p.band[i].first_unit = static_cast<int32_t>(std::min<int64_t>(out.units, INT32_MAX));
+    out.units += bands[i].groups * p.Hkv * p.seg[bands[i].band.seg].splits;
   }
   for (int i = 0; i < p.nseg; ++i) {
     TileSeg& s = p.seg[i];

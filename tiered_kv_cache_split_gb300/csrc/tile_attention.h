@@ -22,6 +22,7 @@ namespace tkv {
 
 constexpr int kKeyBlock = 128;              // keys of a block, the unit of splitting
 constexpr int kMaxSegs = kMaxBatch + 1;
+constexpr int kMaxBands = 2 * kMaxSegs;
 constexpr int kMaxGroup = 64;               // query heads per KV head
 
 struct TileSeg {
@@ -65,10 +66,15 @@ struct TileParams {
   int32_t direct;              // 1: no splits, units write the output
   int32_t tile_rows, tpg;      // rows of a tile, tiles of a row group
   TileSeg seg[kMaxSegs];
-  // units are numbered by segments in this order, longest units first: the
-  // i-th has units first_unit[i] ..
-  int32_t first_unit[kMaxSegs];
-  uint8_t order[kMaxSegs];
+  // Units are numbered by bands, longest first: band i is row groups top, top - 1,
+  // .. of a segment (a causal segment's later rows see more keys), each with all
+  // KV heads and splits, and has units first_unit .. the next band's.
+  struct Band {
+    int32_t first_unit, top;
+    int32_t seg;
+  };
+  int32_t nbands;
+  Band band[kMaxBands];
 };
 
 struct TileUnit {
@@ -85,18 +91,18 @@ __device__ __forceinline__ int tile_row_limit(const TileParams& p, const TileSeg
 
 __device__ __forceinline__ TileUnit tile_unit(const TileParams& p, int u) {
   TileUnit t;
-  int lo = 0, hi = p.nseg - 1;  // the last whose first unit is <= u (those without units come last)
+  int lo = 0, hi = p.nbands - 1;  // the last band whose first unit is <= u
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (p.first_unit[mid] <= u) lo = mid; else hi = mid - 1;
+    if (p.band[mid].first_unit <= u) lo = mid; else hi = mid - 1;
   }
-  t.seg = p.order[lo];
+  t.seg = p.band[lo].seg;
   const TileSeg& s = p.seg[t.seg];
-  uint32_t r = u - p.first_unit[lo];
+  uint32_t r = u - p.band[lo].first_unit;
   t.split = r % static_cast<uint32_t>(s.splits);
   r /= static_cast<uint32_t>(s.splits);
   t.h = r % static_cast<uint32_t>(p.Hkv);
-  t.grp = s.groups - 1 - static_cast<int>(r / static_cast<uint32_t>(p.Hkv));  // a causal segment's last rows see most keys: they go first
+  t.grp = p.band[lo].top - static_cast<int>(r / static_cast<uint32_t>(p.Hkv));  // a causal segment's last rows see most keys: they go first
   const int per = s.pair ? p.tile_rows : p.tile_rows * p.tpg;
   t.row0 = t.grp * per;
   t.rows = min(per, s.ntok * p.G - t.row0);
