@@ -26,18 +26,30 @@ constexpr int kSms = 152;      // SMs of a GB300: what the plan fills (results d
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
 __device__ __forceinline__ bool finite1(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 
 // fp32 FMA kernel: 64 rows x 64 keys at a time, 256 threads as 16 x 16, each
-// with a 4 x 4 patch of S and 4 rows x D / 16 columns of O.
+// with a 4 x 4 patch of S and 4 rows x D / 16 columns of O. The weights take the
+// place of K in shared memory, so that two CTAs fit on an SM at d = 128 (four at
+// 64) and one loads while another computes. Bound by the FMA pipe and about as
+// much by shared-memory reads: tensor cores would round fp32 operands.
 template <int D>
-__global__ void __launch_bounds__(kFmaThreads) tile_fma_kernel(const __grid_constant__ TileParams p) {
+__global__ void __launch_bounds__(kFmaThreads, 2) tile_fma_kernel(const __grid_constant__ TileParams p) {
   constexpr int LD = D + 4, LP = kFmaKeys + 4, C4 = D / 4, NC = D / 64;
+  static_assert(kFmaRows * LP <= kFmaKeys * LD, "the weights fit where K was");
   extern __shared__ float4 smem4[];
   float* sq = reinterpret_cast<float*>(smem4);
   float* sk = sq + kFmaRows * LD;
   float* sv = sk + kFmaKeys * LD;
-  float* sp = sv + kFmaKeys * LD;
+  float* sp = sk;  // weights, once S is done
   __shared__ int64_t s_page[kFmaKeys / kPage];   // page of each 16 keys of the stage, -1: none
   __shared__ uint32_t s_bits[kFmaKeys / kPage];  // its valid slots
   // keys that only some rows of the tile see and whose V row is not finite
@@ -61,14 +73,15 @@ __global__ void __launch_bounds__(kFmaThreads) tile_fma_kernel(const __grid_cons
   if (tid <= kFmaRows / 32) s_flag[tid] = 0;
 
   int lim[4];
-  float m[4], z[4], o[4][NC * 4];
+  float m[4], z[4];
+  float2 o2[4][NC * 2];  // columns 4 tx .. of each 64
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     lim[i] = tile_row_limit(p, sg, t.row0 + min(ty * 4 + i, t.rows - 1));
     m[i] = -INFINITY;
     z[i] = 0.f;
 #pragma unroll
-    for (int c = 0; c < NC * 4; ++c) o[i][c] = 0.f;
+    for (int c = 0; c < NC * 2; ++c) o2[i][c] = make_float2(0.f, 0.f);
   }
   const int lim_first = tile_row_limit(p, sg, t.row0);
   const int kend = min(t.j1 * kKeyBlock, tile_row_limit(p, sg, t.row0 + t.rows - 1));
@@ -120,7 +133,7 @@ __global__ void __launch_bounds__(kFmaThreads) tile_fma_kernel(const __grid_cons
       store4(sv + kk * LD + c * 4, b);
     }
     __syncthreads();
-    float s[4][4] = {};
+    float2 s2[4][4] = {};  // even and odd columns apart
 #pragma unroll 4
     for (int c = 0; c < C4; ++c) {
       float4 a[4], b[4];
@@ -132,12 +145,16 @@ __global__ void __launch_bounds__(kFmaThreads) tile_fma_kernel(const __grid_cons
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
-          s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
-          s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
-          s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+          s2[i][j] = fma2(make_float2(a[i].x, a[i].y), make_float2(b[j].x, b[j].y), s2[i][j]);
+          s2[i][j] = fma2(make_float2(a[i].z, a[i].w), make_float2(b[j].z, b[j].w), s2[i][j]);
         }
     }
+    float s[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[i][j] = s2[i][j].x + s2[i][j].y;
+    __syncthreads();  // K is done with
     // key tx + 16 j is slot tx of page j of the stage
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -167,27 +184,39 @@ __global__ void __launch_bounds__(kFmaThreads) tile_fma_kernel(const __grid_cons
       for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       z[i] = z[i] * f + sum;
 #pragma unroll
-      for (int c = 0; c < NC * 4; ++c) o[i][c] *= f;
+      for (int c = 0; c < NC * 2; ++c) o2[i][c].x *= f, o2[i][c].y *= f;
     }
     __syncwarp();  // a row's weights are written and read by the same half warp
-#pragma unroll 4
-    for (int kk = 0; kk < kFmaKeys; ++kk) {
-      float4 v[NC];
-#pragma unroll
-      for (int c = 0; c < NC; ++c) v[c] = load4(sv + kk * LD + c * 64 + tx * 4);
+#pragma unroll 2
+    for (int kk = 0; kk < kFmaKeys; kk += 4) {
+      float e[4][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float e = sp[(ty * 4 + i) * LP + kk];
+        const float4 x = load4(sp + (ty * 4 + i) * LP + kk);
+        e[i][0] = x.x, e[i][1] = x.y, e[i][2] = x.z, e[i][3] = x.w;
+      }
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          o[i][c * 4 + 0] = fmaf(e, v[c].x, o[i][c * 4 + 0]);
-          o[i][c * 4 + 1] = fmaf(e, v[c].y, o[i][c * 4 + 1]);
-          o[i][c * 4 + 2] = fmaf(e, v[c].z, o[i][c * 4 + 2]);
-          o[i][c * 4 + 3] = fmaf(e, v[c].w, o[i][c * 4 + 3]);
+      for (int u = 0; u < 4; ++u) {
+        float4 v[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) v[c] = load4(sv + (kk + u) * LD + c * 64 + tx * 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const float2 w = make_float2(e[i][u], e[i][u]);
+            o2[i][c * 2] = fma2(w, make_float2(v[c].x, v[c].y), o2[i][c * 2]);
+            o2[i][c * 2 + 1] = fma2(w, make_float2(v[c].z, v[c].w), o2[i][c * 2 + 1]);
+          }
         }
       }
     }
   }
+  float o[4][NC * 4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int c = 0; c < NC * 2; ++c) o[i][c * 2] = o2[i][c].x, o[i][c * 2 + 1] = o2[i][c].y;
   __syncthreads();
   // the non-finite values of partly seen keys, for the rows that see them
   for (int part = 0; part < kFmaRows; ++part) {
@@ -612,7 +641,7 @@ int plan_shared(TileParams& p, TilePlan* plan, int32_t batch, int32_t Hq, int32_
 
 template <int D>
 cudaError_t launch_fma(const TileParams& p, cudaStream_t s) {
-  constexpr int bytes = ((kFmaRows + 2 * kFmaKeys) * (D + 4) + kFmaRows * (kFmaKeys + 4)) * 4;
+  constexpr int bytes = (kFmaRows + 2 * kFmaKeys) * (D + 4) * 4;
   static SharedMemoryOptIn opt_in;
   const cudaError_t e = opt_in.once(reinterpret_cast<const void*>(tile_fma_kernel<D>), bytes);
   if (e != cudaSuccess) return e;
