@@ -470,16 +470,20 @@ int fork_check(int32_t rows, int32_t max_pages, const int32_t* page_counts, int3
   if (n < 1 || n > kMaxBatch) return report(TKV_ERR_INVALID_ARG, "1 to %d forks per call", kMaxBatch);
   if (!parents || !children) return report(TKV_ERR_INVALID_ARG, "null pointer");
   *most = 0;
+  bool parent_empty = false;  // a child's row is empty, so only an empty parent can be a child too
   for (int i = 0; i < n; ++i) {
     if (parents[i] < 0 || parents[i] >= rows || children[i] < 0 || children[i] >= rows)
       return report(TKV_ERR_INVALID_ARG, "fork %d: row out of range", i);
     if (page_counts[children[i]] != 0) return report(TKV_ERR_INVALID_ARG, "fork %d: the child's row holds pages", i);
-    for (int j = 0; j < n; ++j) {
-      if (j < i && children[j] == children[i]) return report(TKV_ERR_INVALID_ARG, "fork %d: a child listed twice", i);
-      if (parents[j] == children[i]) return report(TKV_ERR_INVALID_ARG, "fork %d: a child that is a parent too", i);
-    }
+    parent_empty |= page_counts[parents[i]] == 0;
     *most += share ? 1 : page_counts[parents[i]];
   }
+  for (int i = 0; i < n; ++i)
+    for (int j = 0; j < i; ++j)
+      if (children[j] == children[i]) return report(TKV_ERR_INVALID_ARG, "fork %d: a child listed twice", i);
+  for (int i = 0; parent_empty && i < n; ++i)
+    for (int j = 0; j < n; ++j)
+      if (parents[j] == children[i]) return report(TKV_ERR_INVALID_ARG, "fork %d: a child that is a parent too", i);
   return TKV_OK;
 }
 

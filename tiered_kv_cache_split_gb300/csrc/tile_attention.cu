@@ -264,7 +264,8 @@ __global__ void __launch_bounds__(kFmaThreads, 2) tile_fma_kernel(const __grid_c
 constexpr int kMergeThreads = 128;
 constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kAlphaSlots = kMergeThreads * 4;
-constexpr int kShareParts = 16;  // partials from which four warps share a row
+// Four warps share a row from this many partials, while rows are at most one wave of CTAs.
+constexpr int kShareParts = 16, kShareRows = 152 * 8;
 
 struct PartList {
   int64_t first[2], step[2];  // partial row i of a list is first + i * step
@@ -475,18 +476,22 @@ int64_t blocks_per_unit(const TileParams& p, const SegWork* w, const TileShape& 
     blocks += w[i].blocks * p.Hkv;
   }
   if (whole >= 4 * ts.slots) return most;
+  // candidates: keys whole, and around what each place gets if all is even
+  const int64_t even = std::max<int64_t>(1, ceil_div(blocks, ts.slots));
   int64_t best = most;
   double best_time = 1e300;
-  for (int64_t cut = 1; cut <= most; cut += 1 + cut / 4) {
-    const int64_t per = ceil_div(most, cut);
-    const bool split = p.paged || cut > 1;
+  for (int c = 0; c < 8; ++c) {
+    const int64_t per = c == 0 ? most : std::max<int64_t>(1, even * (c + 1) / 4);  // even / 2 .. 2 even
+    if (per > most || (c > 1 && per == std::max<int64_t>(1, even * c / 4))) continue;
+    const bool split = p.paged || per < most;
     double work = static_cast<double>(blocks), longest = 0;
     int64_t n_longest = 0;
     for (int i = 0; i < p.nseg; ++i) {
       if (!w[i].groups) continue;
-      const int64_t parts = ceil_div(w[i].most, per), units = w[i].groups * p.Hkv * parts;
+      const uint32_t seg = static_cast<uint32_t>(w[i].most), parts = (seg + static_cast<uint32_t>(per) - 1) / static_cast<uint32_t>(per);
+      const int64_t units = w[i].groups * p.Hkv * parts;
       const double cost = unit_cost(ts, static_cast<int64_t>(p.seg[i].ntok) * p.G, split);
-      const double time = static_cast<double>(ceil_div(w[i].most, parts)) + cost;
+      const double time = static_cast<double>(parts == 1 ? seg : (seg + parts - 1) / parts) + cost;
       work += cost * units;
       if (time > longest * 1.01) longest = time, n_longest = units;
       else if (time > longest * 0.99) n_longest += units;
@@ -659,7 +664,7 @@ cudaError_t launch_merge(const TileParams& p, int tokens, cudaStream_t s) {
     if (p.paged && i > 0) slots = std::max(slots, p.seg[i].nkeys);
   }
   const int64_t rows = static_cast<int64_t>(tokens) * p.Hq;
-  const bool share = parts >= kShareParts;
+  const bool share = parts >= kShareParts && rows <= kShareRows;
   const int64_t row_ctas = share ? rows : ceil_div(rows, kMergeWarps);
   const int64_t alpha_ctas = p.alpha ? static_cast<int64_t>(tokens) * p.Hkv * ceil_div(slots, kAlphaSlots) : 0;
   if (row_ctas + alpha_ctas > INT32_MAX) return cudaErrorInvalidConfiguration;

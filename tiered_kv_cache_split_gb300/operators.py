@@ -22,6 +22,7 @@ _MASK = (torch.int32, torch.uint32)
 # The small calls are bound by this file, so it stays flat: cheap checks first,
 # names and messages only on the way out.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _ints(values, n, name):
@@ -44,10 +45,10 @@ def _at(ints):
 
 
 def _dense(t, name, dtypes, device, shape=None):
-    """The address of a contiguous tensor of the given kind."""
+    """The address of a contiguous tensor of the given kind on a device, by its index."""
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
         raise ValueError(f"{name}: wrong dtype")
-    if t.device != device:
+    if t.get_device() != device:
         raise ValueError(f"{name}: on another device")
     if not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous")
@@ -60,7 +61,7 @@ def _tokens(t, name, like=None):
     """(tokens, heads, d, token stride) of [tokens, heads, d] whose tokens are dense."""
     if not isinstance(t, torch.Tensor) or t.dim() != 3:
         raise ValueError(f"{name}: must be [tokens, heads, d]")
-    if like is not None and (t.dtype is not like.dtype or t.device != like.device):
+    if like is not None and (t.dtype is not like.dtype or t.get_device() != like.get_device()):
         raise ValueError(f"{name}: dtype and device must be those of q")
     n, h, d = t.shape
     s0, s1, s2 = t.stride()
@@ -76,14 +77,14 @@ class _On:
     __slots__ = ("device", "guard", "given", "raw")
 
     def __init__(self, device, stream):
-        if device.type != "cuda":
+        if device < 0:
             raise ValueError("the tensors must be on a CUDA device")
         self.device = device
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        self.guard = None if _current_device() == device else torch.cuda.device(device)
         self.given = None
-        self.raw = _raw_stream(device.index)
+        self.raw = _raw_stream(device)
         if stream is not None:
-            if stream.device != device:
+            if stream.device_index != device:
                 raise ValueError("stream: of another device")
             if stream.cuda_stream != self.raw:
                 self.given, self.raw = stream, stream.cuda_stream
@@ -110,7 +111,7 @@ class _On:
                 return None, None, 0
             given = self.empty(need, torch.uint8)
             return given, given.data_ptr(), need
-        if not isinstance(given, torch.Tensor) or not given.is_contiguous() or given.device != self.device:
+        if not isinstance(given, torch.Tensor) or not given.is_contiguous() or given.get_device() != self.device:
             raise ValueError("scratch: a contiguous tensor on the call's device")
         return given, given.data_ptr(), given.numel() * given.element_size()
 
@@ -141,7 +142,7 @@ def prompt_attention(q, k, v, q_lens, k_lens=None, out=None, scratch=None, statu
         raise ValueError("q_lens: must add up to the tokens of q")
     if sum(kl) != tk:
         raise ValueError("k_lens: must add up to the tokens of k")
-    dev = q.device
+    dev = q.get_device()
     with _On(dev, stream) as on:
         if out is None:
             out, so = on.empty((tq, hq, d), q.dtype), hq * d
@@ -181,7 +182,7 @@ def shared_prefix_attention(q, pool, page_table, slot_mask, page_counts, shared_
         raise ValueError("pool: must be [pages, Hkv, 2, 16, d]")
     if page_table.dim() != 2 or page_table.shape[0] != q.shape[0]:
         raise ValueError("page_table: must be [B, max_pages]")
-    dev, dtypes = q.device, (q.dtype,)
+    dev, dtypes = q.get_device(), (q.dtype,)
     batch, hq, d = q.shape
     pages, hkv = pool.shape[:2]
     max_pages = page_table.shape[1]
@@ -245,7 +246,7 @@ def fork_sequences(pool, page_table, page_counts, page_refs, slot_mask, parents,
     """
     lib = L.load()
     pp, layers, pages, hkv, d, dt = _pool(pool)
-    dev = pool.device
+    dev = pool.get_device()
     pt, pr, pm = _book(page_table, page_refs, slot_mask, dev, pages)
     rows, max_pages = page_table.shape
     counts = _ints(page_counts, rows, "page_counts")
@@ -274,7 +275,7 @@ def free_sequences(page_table, page_counts, page_refs, slot_mask, seqs, stream=N
     -1 if a row listed a page that was not held.
     """
     lib = L.load()
-    dev = page_table.device
+    dev = page_table.get_device()
     if not isinstance(page_refs, torch.Tensor) or page_refs.dim() != 1:
         raise ValueError("page_refs: must be [pages]")
     pages = page_refs.shape[0]
@@ -299,7 +300,7 @@ def compact_sequences(pool, page_table, page_counts, page_refs, slot_mask, posit
     """
     lib = L.load()
     pp, layers, pages, hkv, d, dt = _pool(pool)
-    dev = pool.device
+    dev = pool.get_device()
     pt, pr, pm = _book(page_table, page_refs, slot_mask, dev, pages)
     rows, max_pages = page_table.shape
     counts = _ints(page_counts, rows, "page_counts")
