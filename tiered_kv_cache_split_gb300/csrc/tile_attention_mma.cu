@@ -398,9 +398,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy();
   }
+  if (tid == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
+    if (!kPaged) asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v) : "memory");
+  }
   fence_before();
   __syncthreads();
   fence_after();
+  // the set-up above may overlap the end of the kernel ahead on the stream
+  cudaGridDependencySynchronize();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
 
   // The CTA's k-th unit as the producer published it; unit -1 at the end or on an abort.
@@ -837,7 +843,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       if (active && rows > 0) {
         const float inv = z > 0.f || z != z ? 1.f / z : 0.f;
-        const int64_t part = p.direct ? 0 : tile_part_row(p, sg, w.grp, w.h, w.split, t);
+        const bool direct = !kPaged && p.direct;
+        const int64_t part = direct ? 0 : tile_part_row(p, sg, w.grp, w.h, w.split, t);
         if (mine == 0 || (!kPaged && flagged)) {
           // no key: O was never written; or non-finite values to add, in place
 #pragma unroll 1
@@ -866,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(t_o + c, o);
           wait_ld();
           if (!valid) continue;
-          if (p.direct) {
+          if (direct) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] = pack2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
             store32(out + c, o, p.out_sectors);
@@ -876,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 4; ++e) store32(po + c + e * 8, o + e * 8, 1);
           }
         }
-        if (!p.direct && valid) {
+        if (!direct && valid) {
           p.part_m[part + r] = ref * qs;
           p.part_z[part + r] = z;
           if (kPaged && p.alpha) p.part_ze[part + r] = z_exact;
@@ -933,8 +940,17 @@ cudaError_t launch(const TileParams& p, const CUtensorMap& k, const CUtensorMap&
   static SharedMemoryOptIn opt_in;
   const cudaError_t e = opt_in.once(reinterpret_cast<const void*>(tile_mma_kernel<D, kPaged>), bytes);
   if (e != cudaSuccess) return e;
-  tile_mma_kernel<D, kPaged><<<static_cast<unsigned>(p.units), kThreads, bytes, s>>>(p, k, v);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.units));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tile_mma_kernel<D, kPaged>, p, k, v);
 }
 
 }  // namespace
