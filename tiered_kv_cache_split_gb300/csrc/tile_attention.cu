@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kFmaThreads = 256;
 constexpr int kFmaRows = 64;   // rows of a tile
+constexpr int kMmaRows = 128;  // rows of a bf16 tile, two to a group
 constexpr int kFmaKeys = 64;   // keys staged at once (half a key block)
 constexpr int kSms = 152;      // SMs of a GB300: what the plan fills (results do not depend on the device)
 
@@ -273,6 +274,7 @@ struct PartList {
   __device__ __forceinline__ int64_t at(int i) const { return i < n0 ? first[0] + i * step[0] : first[1] + (i - n0) * step[1]; }
 };
 
+template <bool kMma>
 __device__ __forceinline__ void add_parts(PartList& l, int which, const TileParams& p, const TileSeg& s, int h, int row) {
   if (s.splits == 0) return;
   int n;
@@ -281,8 +283,9 @@ __device__ __forceinline__ void add_parts(PartList& l, int which, const TilePara
     l.step[which] = s.part_rows;
     n = s.splits * 2;
   } else {
-    const int per = p.tile_rows * p.tpg, grp = row / per, tile = row % per / p.tile_rows;
-    l.first[which] = tile_part_row(p, s, grp, h, 0, tile) + row % p.tile_rows;
+    constexpr uint32_t kTile = kMma ? kMmaRows : kFmaRows, kPer = kMma ? 2 * kMmaRows : kFmaRows;
+    const uint32_t r = row;
+    l.first[which] = tile_part_row(p, s, r / kPer, h, 0, r % kPer / kTile) + r % kTile;
     l.step[which] = static_cast<int64_t>(p.tpg) * s.part_rows;
     n = s.splits;
   }
@@ -291,16 +294,17 @@ __device__ __forceinline__ void add_parts(PartList& l, int which, const TilePara
 }
 
 // The partials of query head h * G + g of token tok.
-__device__ PartList part_list(const TileParams& p, int tok, int h, int g) {
+template <bool kMma>
+__device__ __forceinline__ PartList part_list(const TileParams& p, int tok, int h, int g) {
   PartList l{};
   if (p.paged) {  // segment 0 is the prefix of all tokens
-    add_parts(l, 0, p, p.seg[0], h, tok * p.G + g);
-    add_parts(l, 1, p, p.seg[tok + 1], h, g);
+    add_parts<kMma>(l, 0, p, p.seg[0], h, tok * p.G + g);
+    add_parts<kMma>(l, 1, p, p.seg[tok + 1], h, g);
   } else {
     int own = 0;
     for (int i = 0; i < p.nseg; ++i)
       if (tok >= p.seg[i].tok0 && tok < p.seg[i].tok0 + p.seg[i].ntok) own = i;
-    add_parts(l, 0, p, p.seg[own], h, (tok - p.seg[own].tok0) * p.G + g);
+    add_parts<kMma>(l, 0, p, p.seg[own], h, (tok - p.seg[own].tok0) * p.G + g);
   }
   return l;
 }
@@ -326,24 +330,21 @@ __device__ __forceinline__ float2 parts_sum(const TileParams& p, const PartList&
 __device__ __forceinline__ float parts_inv(float z) { return z > 0.f || z != z ? 1.f / z : 0.f; }
 
 template <typename T, int D, int kShare>
-__global__ void __launch_bounds__(kMergeThreads) tile_merge_kernel(const __grid_constant__ TileParams p, int64_t rows, int row_ctas) {
+__global__ void __launch_bounds__(kMergeThreads) tile_merge_kernel(const __grid_constant__ TileParams p, uint32_t rows, int row_ctas) {
   constexpr int E = D / 32, kAhead = 8;
   __shared__ float s_acc[kMergeWarps][D], s_m[kMaxGroup], s_inv[kMaxGroup];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = p.G;
   cudaGridDependencySynchronize();
   if (static_cast<int>(blockIdx.x) < row_ctas) {
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kMergeWarps / kShare) + warp / kShare;
+    const uint32_t row = blockIdx.x * (kMergeWarps / kShare) + warp / kShare, hq_all = p.Hq;
     const bool live = row < rows;
     float acc[E] = {}, z = 0.f;
-    const int tok = live ? static_cast<int>(row / p.Hq) : 0, hq = live ? static_cast<int>(row % p.Hq) : 0;
+    const int tok = live ? row / hq_all : 0, hq = live ? row % hq_all : 0;
     if (live) {
-      const PartList l = part_list(p, tok, hq / G, hq % G);
-      const float2 mz = parts_sum(p, l, p.part_z, lane);
-      z = mz.y;
-      for (int i0 = warp % kShare * kAhead; i0 < l.n; i0 += kShare * kAhead) {
-        float w = 0.f;
-        if (lane < kAhead && i0 + lane < l.n) w = exp2f(p.part_m[l.at(i0 + lane)] - mz.x);
-        float v[kAhead][E];
+      const uint32_t h = static_cast<uint32_t>(hq) / static_cast<uint32_t>(G);
+      const PartList l = part_list<sizeof(T) == 2>(p, tok, h, hq - h * G);
+      float v[kAhead][E];
+      auto load = [&](int i0) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
           if (i0 + i < l.n) {
@@ -360,12 +361,21 @@ __global__ void __launch_bounds__(kMergeThreads) tile_merge_kernel(const __grid_
             for (int e = 0; e < E; ++e) v[i][e] = 0.f;
           }
         }
+      };
+      int i0 = warp % kShare * kAhead;
+      load(i0);  // on its way while M and Z are formed
+      const float2 mz = parts_sum(p, l, p.part_z, lane);
+      z = mz.y;
+      while (i0 < l.n) {
+        const float w = lane < kAhead && i0 + lane < l.n ? exp2f(p.part_m[l.at(i0 + lane)] - mz.x) : 0.f;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
           const float wi = __shfl_sync(0xffffffffu, w, i);
 #pragma unroll
           for (int e = 0; e < E; ++e) acc[e] = fmaf(wi, v[i][e], acc[e]);
         }
+        i0 += kShare * kAhead;
+        if (i0 < l.n) load(i0);
       }
     }
     if constexpr (kShare > 1) {
@@ -393,13 +403,13 @@ __global__ void __launch_bounds__(kMergeThreads) tile_merge_kernel(const __grid_
     return;
   }
   // alpha
-  const int per = (static_cast<int>(gridDim.x) - row_ctas) / (static_cast<int>(rows / p.Hq) * p.Hkv);  // CTAs of a (sequence, KV head)
+  const int per = (static_cast<int>(gridDim.x) - row_ctas) / (static_cast<int>(rows / static_cast<uint32_t>(p.Hq)) * p.Hkv);  // CTAs of a (sequence, KV head)
   const int item = blockIdx.x - row_ctas, tok = item / per / p.Hkv, h = item / per % p.Hkv;
   const TileSeg& so = p.seg[tok + 1];
   const int i = item % per * kAlphaSlots + threadIdx.x * 4;
   if (item % per * kAlphaSlots >= so.nkeys) return;
   for (int g = warp; g < G; g += kMergeWarps) {
-    const float2 mz = parts_sum(p, part_list(p, tok, h, g), p.part_ze, lane);
+    const float2 mz = parts_sum(p, part_list<sizeof(T) == 2>(p, tok, h, g), p.part_ze, lane);
     if (lane == 0) {
       s_m[g] = mz.x;
       s_inv[g] = parts_inv(mz.y);
@@ -438,7 +448,7 @@ struct TileShape {
 // bf16: one CTA per SM; a unit's end takes about 2 us, a block about 1.5 us.
 // fp32: two 64-row CTAs per SM, whose blocks take several times as long.
 TileShape tile_shape(int dtype) {
-  if (dtype == TKV_DTYPE_BF16) return {128, 2, kSms, 2};
+  if (dtype == TKV_DTYPE_BF16) return {kMmaRows, 2, kSms, 2};
   return {kFmaRows, 1, 2 * kSms, 1};
 }
 
@@ -667,7 +677,7 @@ cudaError_t launch_merge(const TileParams& p, int tokens, cudaStream_t s) {
   const bool share = parts >= kShareParts && rows <= kShareRows;
   const int64_t row_ctas = share ? rows : ceil_div(rows, kMergeWarps);
   const int64_t alpha_ctas = p.alpha ? static_cast<int64_t>(tokens) * p.Hkv * ceil_div(slots, kAlphaSlots) : 0;
-  if (row_ctas + alpha_ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  if (rows > INT32_MAX || row_ctas + alpha_ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(row_ctas + alpha_ctas));
   cfg.blockDim = dim3(kMergeThreads);
@@ -677,8 +687,8 @@ cudaError_t launch_merge(const TileParams& p, int tokens, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.units > 0 ? 1 : 0;
-  return share ? cudaLaunchKernelEx(&cfg, tile_merge_kernel<T, D, kMergeWarps>, p, rows, static_cast<int>(row_ctas))
-               : cudaLaunchKernelEx(&cfg, tile_merge_kernel<T, D, 1>, p, rows, static_cast<int>(row_ctas));
+  return share ? cudaLaunchKernelEx(&cfg, tile_merge_kernel<T, D, kMergeWarps>, p, static_cast<uint32_t>(rows), static_cast<int>(row_ctas))
+               : cudaLaunchKernelEx(&cfg, tile_merge_kernel<T, D, 1>, p, static_cast<uint32_t>(rows), static_cast<int>(row_ctas));
 }
 
 template <typename T>
