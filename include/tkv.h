@@ -417,7 +417,8 @@ TKV_API tkv_status tkv_quantize_rows(const void* x, int32_t kv_dtype, int64_t ro
  * of 16 bytes and all four pointers are 16-byte aligned. Hq = 1 .. 64 times
  * Hkv, d 64 or 128, F32 or BF16 (products of BF16 accumulate in fp32; the
  * softmax weights are rounded to BF16 for the product with V). A NaN or
- * infinity in K or V reaches exactly the rows that see it.
+ * infinity in K or V reaches exactly the rows that see it; a row whose logits
+ * are all -inf counts as one without keys and gives 0.
  *   scratch  device, tkv_prompt_attention_scratch_size bytes (256-aligned;
  *            may be NULL when that is 0): partials of calls with too few rows
  *            to fill the device, whose keys are split
@@ -456,6 +457,13 @@ TKV_API tkv_status tkv_shared_prefix_attention(int32_t batch, int32_t n_q_heads,
                                                const int32_t* page_counts, int32_t max_pages, int32_t shared_pages,
                                                void* out, float* alpha_sum, void* scratch, size_t scratch_bytes,
                                                int32_t* status, tkv_stream stream);
+
+/* Test hook for the bounded waits of the two operators above (the paper has no
+ * counterpart): in this thread's next BF16 call of either, one CTA withholds
+ * its first copy and waits give up after wait_limit_ns (1 ms .. 2 s) instead
+ * of 2 s. That CTA lands its copies, gives its tensor memory back and ends; the
+ * call's status word becomes 1. No kernel traps or hangs. */
+TKV_API tkv_status tkv_test_stall_next_tiles(uint64_t wait_limit_ns);
 
 /* The page operators work on
  *   pool        device [n_layers][pool_pages][Hkv][2][16][d] (16-byte aligned)

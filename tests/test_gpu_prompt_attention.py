@@ -151,3 +151,70 @@ def test_captured_and_replayed_on_new_inputs(q_lens, k_lens):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, prompt_attention(q2, k2, v2, q_lens, k_lens))
+
+
+def test_an_output_aligned_to_16_bytes_only():
+    from tiered_kv_cache_split_gb300 import prompt_attention
+    q_lens = [150, 40]
+    for dtype in ("bf16", "f32"):
+        q, k, v = make(14, dtype, 6, 2, 128, q_lens, q_lens)
+        unit = 16 // q.element_size()
+        buf = torch.full((190 * 6 * 128 + 64,), 5.0, dtype=q.dtype, device=DEV)
+        out = buf[unit:unit + 190 * 6 * 128].view(190, 6, 128)
+        check(q, k, v, q_lens, q_lens, out=out)
+        assert (buf[:unit] == 5).all() and (buf[unit + 190 * 6 * 128:] == 5).all()
+
+
+def test_no_query_at_all():
+    from tiered_kv_cache_split_gb300 import prompt_attention
+    q, k, v = make(15, "bf16", 4, 2, 64, [0, 0], [5, 0])
+    assert prompt_attention(q, k, v, [0, 0], [5, 0]).shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_offsets_past_32_bits(dtype):
+    """Token strides that put the last keys and rows more than 2^32 bytes in."""
+    from tiered_kv_cache_split_gb300 import prompt_attention
+    n, d = 300, 64
+    q, k, v = make(16, dtype, 2, 1, d, [n], [n])
+    stride = (1 << 33) // q.element_size() // n // 8 * 8
+    wide = torch.empty(n * stride, dtype=q.dtype, device=DEV)
+    far = lambda h: wide.as_strided((n, h, d), (stride, d, 1))   # noqa: E731
+    want, bound = prompt_reference(q, k, v, [n], [n])
+    far(1).copy_(k)
+    assert_within(prompt_attention(q, far(1), v, [n]), want, bound, "k")
+    far(1).copy_(v)
+    assert_within(prompt_attention(q, k, far(1), [n]), want, bound, "v")
+    far(2).copy_(q)
+    assert_within(prompt_attention(far(2), k, v, [n]), want, bound, "q")
+    assert_within(prompt_attention(q, k, v, [n], out=far(2)), want, bound, "out")
+
+
+def test_one_scratch_for_calls_in_turn():
+    """A caller's scratch, just large enough, used by different calls one after the other."""
+    import ctypes
+    from tiered_kv_cache_split_gb300 import _lib as L, prompt_attention
+    shapes = [([20], [3000]), ([3, 40], [900, 2000])]
+    most = 0
+    for ql, kl in shapes:
+        need = ctypes.c_size_t()
+        a, b = (ctypes.c_int32 * len(ql))(*ql), (ctypes.c_int32 * len(kl))(*kl)
+        L.check(L.load().tkv_prompt_attention_scratch_size(len(ql), a, b, 8, 2, 128, L.DTYPE_BF16, ctypes.byref(need)))
+        most = max(most, need.value)
+    scratch = torch.full((most,), 255, dtype=torch.uint8, device=DEV)      # NaN wherever it is read as float
+    for _ in range(2):
+        for i, (ql, kl) in enumerate(shapes):
+            check(*make(20 + i, "bf16", 8, 2, 128, ql, kl), ql, kl, scratch=scratch)
+    with pytest.raises(L.TkvError, match="too small"):
+        prompt_attention(*make(20, "bf16", 8, 2, 128, *shapes[0]), *shapes[0], scratch=scratch[:1024])
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_device_goes_on():
+    from tiered_kv_cache_split_gb300 import _lib as L, prompt_attention
+    q, k, v = make(17, "bf16", 8, 2, 128, [400], [400])
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    L.check(L.load().tkv_test_stall_next_tiles(5_000_000))
+    prompt_attention(q, k, v, [400], status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 1
+    check(q, k, v, [400], [400])

@@ -130,3 +130,34 @@ def test_two_streams_and_a_captured_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, two)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_pages_past_32_bits(dtype):
+    """A pool of more than 2^32 bytes (2^31 elements in bf16) whose last pages are used."""
+    from tiered_kv_cache_split_gb300 import shared_prefix_attention
+    q, pool, table, mask, counts, tb, mk = make(8, dtype, 8, 4, 128, 9, [4, 20, 1])
+    want, bound, aw, ab = prefix_reference(q, pool, tb, mk, counts, 9)
+    n = pool.shape[0]
+    record = pool[0].numel() * pool.element_size()
+    pages = (9 << 29) // record
+    big = torch.empty((pages, *pool.shape[1:]), dtype=pool.dtype, device=DEV)
+    big[pages - n:] = pool
+    bmask = torch.zeros(pages, dtype=torch.int32, device=DEV)
+    bmask[pages - n:] = mask
+    alpha = torch.zeros(3, 4, table.shape[1] * 16, device=DEV)
+    out = shared_prefix_attention(q, big, torch.where(table < n, table + (pages - n), table), bmask, counts, 9, alpha_sum=alpha)
+    assert_within(out, want, bound, "out")
+    assert_within(alpha, aw, ab, "alpha")
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_device_goes_on():
+    from tiered_kv_cache_split_gb300 import _lib as L, shared_prefix_attention
+    x = make(9, "bf16", 8, 2, 64, 40, [3, 9])[:5]
+    good = shared_prefix_attention(*x, 40)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    L.check(L.load().tkv_test_stall_next_tiles(5_000_000))
+    shared_prefix_attention(*x, 40, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 1
+    assert torch.equal(shared_prefix_attention(*x, 40), good)

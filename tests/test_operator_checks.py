@@ -155,6 +155,11 @@ def test_compact_refusals(lib, bad, words):
     refused(lib, compact(lib, **bad), L.ERR_INVALID_ARG, *words)
 
 
+def test_stall_hook_limits(lib):
+    for bad in (0, 999_999, 2_000_000_001):
+        refused(lib, lib.tkv_test_stall_next_tiles(bad), L.ERR_INVALID_ARG, "1 ms")
+
+
 def test_python_checks_name_the_argument():
     import tiered_kv_cache_split_gb300 as t
     q, k = torch.zeros(6, 4, 64), torch.zeros(6, 2, 64)

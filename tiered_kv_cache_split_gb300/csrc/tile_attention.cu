@@ -650,6 +650,7 @@ int plan_shared(TileParams& p, TilePlan* plan, int32_t batch, int32_t Hq, int32_
     s.nkeys = (page_counts[b] - shared_pages) * kPage;
   }
   *plan = plan_units(p, tile_shape(dtype), want_alpha != 0);
+  if (plan->units > INT32_MAX) return report(TKV_ERR_INVALID_ARG, "more than 2^31 units of work in one call");
   p.units = static_cast<int32_t>(plan->units);
   return TKV_OK;
 }
@@ -705,6 +706,17 @@ cudaError_t launch_tiles(const TileParams& p, int D, int tokens, int64_t keys, c
 
 cudaError_t launch_dtype(const TileParams& p, int dtype, int D, int tokens, int64_t keys, cudaStream_t s) {
   return dtype == TKV_DTYPE_BF16 ? launch_tiles<__nv_bfloat16>(p, D, tokens, keys, s) : launch_tiles<float>(p, D, tokens, keys, s);
+}
+
+thread_local uint64_t g_stall_limit_ns = 0;  // tkv_test_stall_next_tiles
+
+void set_waits(TileParams& p, int32_t dtype) {
+  p.wait_limit_ns = 2000000000ull;
+  if (g_stall_limit_ns && dtype == TKV_DTYPE_BF16) {
+    p.wait_limit_ns = g_stall_limit_ns;
+    p.stall = 1;
+    g_stall_limit_ns = 0;
+  }
 }
 
 bool misaligned(const void* ptr, size_t to) { return reinterpret_cast<uintptr_t>(ptr) % to != 0; }
@@ -770,9 +782,16 @@ tkv_status tkv_prompt_attention(int32_t batch, const int32_t* q_lens, const int3
   p.out = out; p.out_stride = out_stride;
   p.out_sectors = !misaligned(out, 32) && out_stride % (2 * unit) == 0;
   p.status = status;
-  p.wait_limit_ns = 2000000000ull;
+  set_waits(p, kv_dtype);
   const cudaError_t e = launch_dtype(p, kv_dtype, head_dim, static_cast<int>(tq), tk, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return tkv_status(report(TKV_ERR_CUDA, "prompt attention launch failed: %s", cudaGetErrorString(e)));
+  return TKV_OK;
+}
+
+tkv_status tkv_test_stall_next_tiles(uint64_t wait_limit_ns) {
+  if (wait_limit_ns < 1000000ull || wait_limit_ns > 2000000000ull)
+    return tkv_status(report(TKV_ERR_INVALID_ARG, "wait limit out of 1 ms .. 2 s"));
+  g_stall_limit_ns = wait_limit_ns;
   return TKV_OK;
 }
 
@@ -817,7 +836,7 @@ tkv_status tkv_shared_prefix_attention(int32_t batch, int32_t n_q_heads, int32_t
   p.alpha_stride_h = static_cast<int64_t>(max_pages) * kPage;
   p.alpha_first = static_cast<int64_t>(shared_pages) * kPage;
   p.status = status;
-  p.wait_limit_ns = 2000000000ull;
+  set_waits(p, kv_dtype);
   const cudaError_t e = launch_dtype(p, kv_dtype, head_dim, batch, 0, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess)
     return tkv_status(report(TKV_ERR_CUDA, "shared-prefix attention launch failed: %s", cudaGetErrorString(e)));

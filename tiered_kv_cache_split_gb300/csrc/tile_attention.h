@@ -59,6 +59,7 @@ struct TileParams {
   int64_t alpha_first;         // slots ahead of a sequence's own pages
   int32_t* status;             // set to 1 by a wait that gave up, or null
   unsigned long long wait_limit_ns;
+  int32_t stall;               // test hook: the CTA of unit 0 withholds its first copy
   float qscale;                // log2(e) / sqrt(D): logits are kept in base 2
   int32_t Hq, Hkv, G;
   int32_t nseg, units;

@@ -467,6 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (round > 0 && !warp_wait(&sh.empty[slot], (round - 1) & 1, abort, limit)) return false;
         ++pos;
         const uint32_t dst = s_ring + slot * C::tile;
+        if (p.stall && unit == 0 && i == 0 && !is_v) return true;  // the waits on this slot run out
         if (lane == 0) mbar_expect(&sh.full[slot], C::tile);
         __syncwarp();
         if (kPaged) {
@@ -897,6 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       batches += (w.n + kBatch - 1) / kBatch;
       w = next;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     fence_before();
   }
   __syncthreads();

@@ -192,6 +192,7 @@ def shared_prefix_attention(q, pool, page_table, slot_mask, page_counts, shared_
     pm = _dense(slot_mask, "slot_mask", _MASK, dev, (pages,))
     pa = None if alpha_sum is None else _dense(alpha_sum, "alpha_sum", (torch.float32,), dev, (batch, hkv, max_pages * 16))
     counts = _ints(page_counts, batch, "page_counts")
+    shared_pages = int(shared_pages)
     with _On(dev, stream) as on:
         if out is None:
             out = on.empty((batch, hq, d), q.dtype)
