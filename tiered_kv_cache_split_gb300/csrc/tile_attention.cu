@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kFmaThreads, 2) tile_fma_kernel(const __grid_c
       const int64_t pr = tile_part_row(p, sg, t.grp, t.h, t.split, 0) + r;
 #pragma unroll
       for (int c = 0; c < NC; ++c)
-        store4(p.part_o + pr * D + c * 64 + tx * 4, make_float4(o[i][c * 4], o[i][c * 4 + 1], o[i][c * 4 + 2], o[i][c * 4 + 3]));
+        store4(p.part_o + (pr - r) * D + ((c * 8 + tx / 2) * sg.part_rows + r) * 8 + (tx & 1) * 4, make_float4(o[i][c * 4], o[i][c * 4 + 1], o[i][c * 4 + 2], o[i][c * 4 + 3]));
       if (tx == 0) {
         p.part_m[pr] = m[i];
         p.part_z[pr] = z[i];
@@ -270,7 +270,8 @@ constexpr int kShareParts = 16, kShareRows = 152 * 8;
 
 struct PartList {
   int64_t first[2], step[2];  // partial row i of a list is first + i * step
-  int n0, n;                  // those of the first list, all
+  int row[2], rows[2];        // the row in its tile, rows of a partial tile
+  int n0, n;                  // partials of the first list, of both
   __device__ __forceinline__ int64_t at(int i) const { return i < n0 ? first[0] + i * step[0] : first[1] + (i - n0) * step[1]; }
 };
 
@@ -278,13 +279,16 @@ template <bool kMma>
 __device__ __forceinline__ void add_parts(PartList& l, int which, const TileParams& p, const TileSeg& s, int h, int row) {
   if (s.splits == 0) return;
   int n;
+  l.rows[which] = s.part_rows;
   if (s.pair) {
     l.first[which] = tile_part_row(p, s, 0, h, 0, 0) + row;
+    l.row[which] = row;
     l.step[which] = s.part_rows;
     n = s.splits * 2;
   } else {
     constexpr uint32_t kTile = kMma ? kMmaRows : kFmaRows, kPer = kMma ? 2 * kMmaRows : kFmaRows;
     const uint32_t r = row;
+    l.row[which] = r % kTile;
     l.first[which] = tile_part_row(p, s, r / kPer, h, 0, r % kPer / kTile) + r % kTile;
     l.step[which] = static_cast<int64_t>(p.tpg) * s.part_rows;
     n = s.splits;
@@ -343,12 +347,16 @@ __global__ void __launch_bounds__(kMergeThreads) tile_merge_kernel(const __grid_
     if (live) {
       const uint32_t h = static_cast<uint32_t>(hq) / static_cast<uint32_t>(G);
       const PartList l = part_list<sizeof(T) == 2>(p, tok, h, hq - h * G);
+      int64_t off[2];  // this lane's columns, from a partial row's number of elements
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        off[q] = (static_cast<int64_t>(lane * E / 8) * l.rows[q] + l.row[q]) * 8 + lane * E % 8 - static_cast<int64_t>(l.row[q]) * D;
       float v[kAhead][E];
       auto load = [&](int i0) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
           if (i0 + i < l.n) {
-            const float* at = p.part_o + l.at(i0 + i) * D + lane * E;
+            const float* at = p.part_o + l.at(i0 + i) * D + off[i0 + i >= l.n0];
             if constexpr (E == 4) {
               const float4 x = *reinterpret_cast<const float4*>(at);
               v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
@@ -470,7 +478,7 @@ SegWork seg_work(const TileParams& p, const TileSeg& s, const TileShape& ts) {
 // a tile of few rows), and its partial rows written and read again where keys are split.
 double unit_cost(const TileShape& ts, int64_t rows, bool split) {
   const int64_t most = static_cast<int64_t>(ts.rows) * ts.tpg;
-  return ts.unit_cost * (rows <= ts.rows ? 0.5 : 1.0) + (split ? static_cast<double>(std::min(rows, most)) / 64 : 0.0);
+  return ts.unit_cost * (rows <= ts.rows ? 0.5 : 1.0) + (split ? static_cast<double>(std::min(rows, most)) / 96 : 0.0);
 }
 
 // Key blocks per unit. Units are handed out longest first to `slots` places, so

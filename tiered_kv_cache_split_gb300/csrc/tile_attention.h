@@ -8,7 +8,9 @@
 // A UNIT (one CTA) is (segment, row group, KV head, split): the rows of the
 // group over a range of 128-key blocks. A unit that covers all keys of its rows
 // writes the output; otherwise it writes a PARTIAL (m, Z, unnormalised O) per
-// row, in base 2, and the merge kernel joins the partials of each row.
+// row, in base 2, and the merge kernel joins the partials of each row. O of a
+// partial tile lies as [D / 8][rows][8]: a thread per row then stores whole lines
+// with its neighbours (and the merge reads whole 32-byte sectors).
 #pragma once
 
 #include <cuda_runtime.h>

@@ -863,11 +863,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           wait_st();
         }
-        // a thread holds a row and stores it by whole 32-byte sectors
+        // a thread holds a row and stores it by 32-byte sectors; in a partial, neighbours' sectors touch
         const int at = w.row0 + first + r, tok = at / G;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + static_cast<int64_t>(sg.tok0 + tok) * p.out_stride +
                              (w.h * G + at - tok * G) * D;
-        float* po = p.part_o + (part + r) * D;
+        float* po = p.part_o + part * D + r * 8;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
@@ -881,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             store32(out + c + 16, o + 8, p.out_sectors);
           } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) store32(po + c + e * 8, o + e * 8, 1);
+            for (int e = 0; e < 4; ++e) store32(po + (c / 8 + e) * sg.part_rows * 8, o + e * 8, 1);
           }
         }
         if (!direct && valid) {
