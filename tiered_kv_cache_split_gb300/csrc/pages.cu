@@ -357,12 +357,14 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid
   }
 }
 
-// One warp per (layer, moved token): its 2 * Hkv rows, 16 bytes per lane.
+// One warp per moved token of the CTA's layer (blockIdx.y): its 2 * Hkv rows, 16
+// bytes per lane, four in flight. Index arithmetic is 32-bit and by shifts: with
+// divisions the issue slots, not HBM, were the bound (264 MB: 44 us).
 __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const __grid_constant__ CompactParams p) {
-  __shared__ int64_t s_first[kMaxBatch + 1];
+  __shared__ int s_first[kMaxBatch + 1];
   cudaGridDependencySynchronize();
   if (threadIdx.x == 0) {
-    int64_t at = 0;
+    int at = 0;
     for (int b = 0; b < p.n; ++b) {
       s_first[b] = at;
       at += p.moves[b];
@@ -370,38 +372,37 @@ __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const __grid
     s_first[p.n] = at;
   }
   __syncthreads();
-  const int lane = threadIdx.x & 31;
-  const int64_t tokens = s_first[p.n], items = tokens * p.pool.layers;
-  const int chunks = p.pool.row_bytes / 16, work = p.pool.kv_rows * chunks;  // 16-byte chunks of a token
-  const int64_t block = static_cast<int64_t>(kPage) * p.pool.row_bytes;
-  for (int64_t w = static_cast<int64_t>(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5); w < items;
-       w += static_cast<int64_t>(gridDim.x) * (kMoveThreads / 32)) {
-    const int64_t layer = w / tokens, k = w % tokens;
+  const int lane = threadIdx.x & 31, tokens = s_first[p.n];
+  const int log_chunks = 31 - __clz(p.pool.row_bytes / 16);  // 16-byte chunks of a row: 8, 16 or 32
+  const int work = p.pool.kv_rows << log_chunks;             // of a token
+  const int block = kPage * p.pool.row_bytes;                // from a row to the next head's, or K's to V's
+  char* base = p.pool.base + blockIdx.y * p.pool.layer_bytes;
+  for (int k = blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5); k < tokens; k += gridDim.x * (kMoveThreads / 32)) {
     int lo = 0, hi = p.n - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (s_first[mid] <= k) lo = mid; else hi = mid - 1;
     }
-    const int32_t from = p.from[p.move0[lo] + k - s_first[lo]], to = p.to[p.move0[lo] + k - s_first[lo]];
-    if (layer == 0 && p.positions && lane == 0) {  // a token's slot is read here alone, so it can be emptied here
+    const int64_t at = p.move0[lo] + k - s_first[lo];
+    const int32_t from = p.from[at], to = p.to[at];
+    if (blockIdx.y == 0 && p.positions && lane == 0) {  // a token's slot is read here alone, so it can be emptied here
       p.positions[to] = p.positions[from];
       p.positions[from] = -1;
     }
-    char* base = p.pool.base + layer * p.pool.layer_bytes;
     const char* src = base + (from / kPage) * p.pool.page_bytes + (from % kPage) * p.pool.row_bytes;
     char* dst = base + (to / kPage) * p.pool.page_bytes + (to % kPage) * p.pool.row_bytes;
     for (int i = lane; i < work; i += 32 * 4) {
       int4 x[4];
+      int off[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int c = i + 32 * u;
-        if (c < work) x[u] = *reinterpret_cast<const int4*>(src + (c / chunks) * block + (c % chunks) * 16);
+        off[u] = (c >> log_chunks) * block + (c & ((1 << log_chunks) - 1)) * 16;
+        if (c < work) x[u] = *reinterpret_cast<const int4*>(src + off[u]);
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int c = i + 32 * u;
-        if (c < work) *reinterpret_cast<int4*>(dst + (c / chunks) * block + (c % chunks) * 16) = x[u];
-      }
+      for (int u = 0; u < 4; ++u)
+        if (i + 32 * u < work) *reinterpret_cast<int4*>(dst + off[u]) = x[u];
     }
   }
 }
@@ -411,9 +412,9 @@ __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const __grid
 // Launches `kernel` so that its CTAs may start while the plan ahead of it on
 // the stream ends (each waits for the plan before it reads).
 template <typename P>
-cudaError_t launch_after(void (*kernel)(P), const P& p, int ctas, cudaStream_t s) {
+cudaError_t launch_after(void (*kernel)(P), const P& p, dim3 ctas, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
+  cfg.gridDim = ctas;
   cfg.blockDim = dim3(kMoveThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -428,7 +429,7 @@ bool misaligned(const void* ptr, size_t to) { return reinterpret_cast<uintptr_t>
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 int check_pool(PoolDesc* d, void* pool, int32_t n_layers, int64_t pool_pages, int32_t n_kv_heads, int32_t head_dim, int32_t kv_dtype) {
-  if (n_layers < 1 || n_kv_heads < 1 || n_kv_heads > 65535 || pool_pages < 1 || pool_pages > kMaxPoolPages)
+  if (n_layers < 1 || n_layers > 65535 || n_kv_heads < 1 || n_kv_heads > 65535 || pool_pages < 1 || pool_pages > kMaxPoolPages)
     return report(TKV_ERR_INVALID_ARG, "bad pool shape");
   if (head_dim != 64 && head_dim != 128) return report(TKV_ERR_INVALID_ARG, "head_dim must be 64 or 128");
   if (kv_dtype != TKV_DTYPE_F32 && kv_dtype != TKV_DTYPE_BF16) return report(TKV_ERR_INVALID_ARG, "kv_dtype");
@@ -636,7 +637,7 @@ tkv_status tkv_compact_sequences(void* pool, int32_t n_layers, int64_t pool_page
   else compact_plan_kernel<kMaxSeqPages / kPlanThreads><<<rows, kPlanThreads, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return tkv_status(launched("compact plan", e));
-  return tkv_status(launched("compact", launch_after(compact_move_kernel, p, ctas_for(pages * n_layers), st)));
+  return tkv_status(launched("compact", launch_after(compact_move_kernel, p, dim3(std::max(1, ctas_for(pages * n_layers) / n_layers), n_layers), st)));
 }
 
 }  // extern "C"
