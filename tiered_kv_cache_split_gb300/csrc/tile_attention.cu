@@ -481,6 +481,14 @@ double unit_cost(const TileShape& ts, int64_t rows, bool split) {
   return ts.unit_cost * (rows <= ts.rows ? 0.5 : 1.0) + (split ? static_cast<double>(std::min(rows, most)) / 96 : 0.0);
 }
 
+// Segments whose ranges are cut to one length, the last taking the rest: the rest
+// fills the places that whole waves leave (512 tokens behind 15872 cached, 64
+// units of 128 blocks on 152 SMs: ranges of 57, 57 and 14 against two of 64). Even ranges where the rows of a group see very different
+// numbers of keys, or keys are few.
+bool leads(const TileParams& p, int i) {
+  return p.causal ? p.seg[i].see0 >= p.seg[i].nkeys / 2 : p.paged && i == 0;
+}
+
 // Key blocks per unit. Units are handed out longest first to `slots` places, so
 // the time is about the larger of what one place gets on average and of the
 // waves the longest kind of unit makes. Rows alone leave a decode step, or a
@@ -498,23 +506,32 @@ int64_t blocks_per_unit(const TileParams& p, const SegWork* w, const TileShape& 
   const int64_t even = std::max<int64_t>(1, ceil_div(blocks, ts.slots));
   int64_t best = most;
   double best_time = 1e300;
-  for (int c = 0; c < 8; ++c) {
-    const int64_t per = c == 0 ? most : std::max<int64_t>(1, even * (c + 1) / 4);  // even / 2 .. 2 even
-    if (per > most || (c > 1 && per == std::max<int64_t>(1, even * c / 4))) continue;
+  constexpr int kSixteenths[] = {8, 12, 16, 17, 18, 20, 24, 32, 48, 64};
+  int64_t last = 0;
+  for (int c = -1; c < 10; ++c) {
+    const int64_t per = c < 0 ? most : std::max<int64_t>(1, even * kSixteenths[c] / 16);
+    if (per > most || per == last) continue;
+    last = per;
     const bool split = p.paged || per < most;
-    double work = static_cast<double>(blocks), longest = 0;
-    int64_t n_longest = 0;
+    double work = static_cast<double>(blocks), longest = 0, rest = 0;
+    int64_t n_longest = 0, n_rest = 0;
     for (int i = 0; i < p.nseg; ++i) {
       if (!w[i].groups) continue;
       const uint32_t seg = static_cast<uint32_t>(w[i].most), parts = (seg + static_cast<uint32_t>(per) - 1) / static_cast<uint32_t>(per);
       const int64_t units = w[i].groups * p.Hkv * parts;
+      const bool lead = parts > 1 && leads(p, i) && seg % static_cast<uint32_t>(per);
       const double cost = unit_cost(ts, static_cast<int64_t>(p.seg[i].ntok) * p.G, split);
-      const double time = static_cast<double>(parts == 1 ? seg : (seg + parts - 1) / parts) + cost;
+      const double time = static_cast<double>(lead ? per : (seg + parts - 1) / parts) + cost;
+      const int64_t n = lead ? units / parts * (parts - 1) : units;
       work += cost * units;
-      if (time > longest * 1.01) longest = time, n_longest = units;
-      else if (time > longest * 0.99) n_longest += units;
+      if (time > longest * 1.01) longest = time, n_longest = n;
+      else if (time > longest * 0.99) n_longest += n;
+      if (lead && !p.paged) rest = std::max(rest, static_cast<double>(seg % static_cast<uint32_t>(per)) + cost), n_rest += units - n;
     }
-    const double time = std::max(work / ts.slots, longest * ceil_div(n_longest, ts.slots)) + (!p.paged && split ? ts.unit_cost : 0);
+    double time = std::max(work / ts.slots, longest * ceil_div(n_longest, ts.slots));
+    if (n_rest && n_longest < ts.slots)  // the rests run beside the one wave, in rounds of their own
+      time = std::max(time, std::min(rest * ceil_div(n_rest, ts.slots - n_longest), longest + rest));
+    if (!p.paged && split) time += ts.unit_cost;  // the merge
     if (time < best_time * 0.999) {
       best_time = time;
       best = per;
@@ -537,6 +554,7 @@ TilePlan plan_units(TileParams& p, const TileShape& ts, bool want_spill) {
   int live = 0;
   for (int i = 0; i < p.nseg; ++i) {
     p.seg[i].splits = work[i].groups ? (split ? static_cast<int32_t>(std::max<int64_t>(1, ceil_div(work[i].most, per))) : 1) : 0;
+    p.seg[i].lead = p.seg[i].splits > 1 && leads(p, i) ? static_cast<int32_t>(per) : 0;
     live += work[i].groups > 0;
   }
   struct Length {
@@ -547,20 +565,29 @@ TilePlan plan_units(TileParams& p, const TileShape& ts, bool want_spill) {
   for (int i = 0; i < p.nseg; ++i) {
     const int64_t groups = work[i].groups;
     if (!groups) continue;
-    const int64_t cut = p.causal ? std::min<int64_t>(groups, kMaxBands / live) : 1, rows = static_cast<int64_t>(ts.rows) * ts.tpg;
+    const int64_t cut = p.causal ? std::min<int64_t>(groups, kMaxBands / live / 2) : 1, rows = static_cast<int64_t>(ts.rows) * ts.tpg;
+    const int32_t splits = p.seg[i].splits, lead = p.seg[i].lead;
     for (int64_t j = 0; j < cut; ++j) {
       const int64_t top = groups - 1 - groups * j / cut, count = top - (groups - 1 - groups * (j + 1) / cut);
       const int64_t seen = p.causal ? std::min<int64_t>(p.seg[i].nkeys, p.seg[i].see0 + ((top + 1) * rows - 1) / p.G + 1) : p.seg[i].nkeys;
-      bands[p.nbands++] = {ceil_div(ceil_div(seen, kKeyBlock), p.seg[i].splits), count, {0, static_cast<int32_t>(top), i}};
+      const int64_t nb = ceil_div(seen, kKeyBlock);
+      if (lead) {
+        bands[p.nbands++] = {std::min<int64_t>(nb, lead), count, {0, static_cast<int32_t>(top), i, 0, splits - 1}};
+        bands[p.nbands++] = {std::max<int64_t>(0, nb - static_cast<int64_t>(splits - 1) * lead), count, {0, static_cast<int32_t>(top), i, splits - 1, 1}};
+      } else {
+        bands[p.nbands++] = {ceil_div(nb, splits), count, {0, static_cast<int32_t>(top), i, 0, splits}};
+      }
     }
   }
   std::sort(bands, bands + p.nbands, [](const Length& a, const Length& b) {
-    return a.blocks != b.blocks ? a.blocks > b.blocks : a.band.seg != b.band.seg ? a.band.seg < b.band.seg : a.band.top > b.band.top;
+    if (a.blocks != b.blocks) return a.blocks > b.blocks;
+    if (a.band.seg != b.band.seg) return a.band.seg < b.band.seg;
+    return a.band.top != b.band.top ? a.band.top > b.band.top : a.band.split0 < b.band.split0;
   });
   for (int i = 0; i < p.nbands; ++i) {
     p.band[i] = bands[i].band;
     p.band[i].first_unit = static_cast<int32_t>(std::min<int64_t>(out.units, INT32_MAX));
-    out.units += bands[i].groups * p.Hkv * p.seg[bands[i].band.seg].splits;
+    out.units += bands[i].groups * p.Hkv * bands[i].band.splits;
   }
   for (int i = 0; i < p.nseg; ++i) {
     TileSeg& s = p.seg[i];

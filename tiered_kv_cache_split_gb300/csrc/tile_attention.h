@@ -36,6 +36,7 @@ struct TileSeg {
   int32_t nkeys;     // keys (paged: 16 per page)
   int32_t see0;      // causal: token i sees keys [0, see0 + i]
   int32_t splits;    // key ranges per row group (0: the segment has no unit)
+  int32_t lead;      // 0: even ranges; else blocks of each range but the last, which has the rest
   int32_t groups;    // row groups
   int32_t part_rows; // rows per partial tile
   int32_t pair;      // 1: one row tile, its two halves of the CTA take alternate key blocks
@@ -71,10 +72,11 @@ struct TileParams {
   TileSeg seg[kMaxSegs];
   // Units are numbered by bands, longest first: band i is row groups top, top - 1,
   // .. of a segment (a causal segment's later rows see more keys), each with all
-  // KV heads and splits, and has units first_unit .. the next band's.
+  // KV heads and `splits` key ranges from split0, and has units first_unit .. the
+  // next band's.
   struct Band {
     int32_t first_unit, top;
-    int32_t seg;
+    int32_t seg, split0, splits;
   };
   int32_t nbands;
   Band band[kMaxBands];
@@ -99,21 +101,26 @@ __device__ __forceinline__ TileUnit tile_unit(const TileParams& p, int u) {
     const int mid = (lo + hi + 1) >> 1;
     if (p.band[mid].first_unit <= u) lo = mid; else hi = mid - 1;
   }
-  t.seg = p.band[lo].seg;
+  const TileParams::Band& band = p.band[lo];
+  t.seg = band.seg;
   const TileSeg& s = p.seg[t.seg];
-  uint32_t r = u - p.band[lo].first_unit;
-  t.split = r % static_cast<uint32_t>(s.splits);
-  r /= static_cast<uint32_t>(s.splits);
+  uint32_t r = u - band.first_unit;
+  t.split = band.split0 + r % static_cast<uint32_t>(band.splits);
+  r /= static_cast<uint32_t>(band.splits);
   t.h = r % static_cast<uint32_t>(p.Hkv);
-  t.grp = p.band[lo].top - static_cast<int>(r / static_cast<uint32_t>(p.Hkv));  // a causal segment's last rows see most keys: they go first
+  t.grp = band.top - static_cast<int>(r / static_cast<uint32_t>(p.Hkv));  // a causal segment's last rows see most keys: they go first
   const int per = s.pair ? p.tile_rows : p.tile_rows * p.tpg;
   t.row0 = t.grp * per;
   t.rows = min(per, s.ntok * p.G - t.row0);
   const int nb = (tile_row_limit(p, s, t.row0 + t.rows - 1) + kKeyBlock - 1) / kKeyBlock;
-  // even ranges, the first nb % splits one block longer
-  const int per_split = nb / s.splits, longer = nb % s.splits;
-  t.j0 = t.split * per_split + min(t.split, longer);
-  t.j1 = t.j0 + per_split + (t.split < longer);
+  if (s.lead) {
+    t.j0 = min(nb, t.split * s.lead);
+    t.j1 = min(nb, t.j0 + s.lead);
+  } else {  // even ranges, the first nb % splits one block longer
+    const int each = nb / s.splits, longer = nb % s.splits;
+    t.j0 = t.split * each + min(t.split, longer);
+    t.j1 = t.j0 + each + (t.split < longer);
+  }
   return t;
 }
 
