@@ -209,6 +209,22 @@ def test_one_scratch_for_calls_in_turn():
         prompt_attention(*make(20, "bf16", 8, 2, 128, *shapes[0]), *shapes[0], scratch=scratch[:1024])
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(32, 32, 128), (16, 4, 128), (32, 8, 64)])
+def test_long_units_repeated_over_a_scratch_of_nan(hq, hkv, d):
+    """Many long key ranges at once, whose copies land in any order: every call
+    finishes every range (a partial that stayed unwritten would read as NaN)."""
+    from tiered_kv_cache_split_gb300 import prompt_attention
+    q_lens = [43, 51, 318, 2, 8, 5, 10, 44, 5, 32, 35, 2]
+    k_lens = [n + c for n, c in zip(q_lens, [7271, 2, 1793, 0, 2771, 5922, 0, 3, 12, 290, 0, 0])]
+    x = make(19, "bf16", hq, hkv, d, q_lens, k_lens)
+    scratch = torch.empty(256 << 20, dtype=torch.uint8, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    first = check(*x, q_lens, k_lens, scratch=scratch.fill_(255))
+    for _ in range(60):
+        assert torch.equal(prompt_attention(*x, q_lens, k_lens, scratch=scratch.fill_(255), status=status), first)
+        assert status.item() == 0
+
+
 def test_a_wait_that_runs_out_is_reported_and_the_device_goes_on():
     from tiered_kv_cache_split_gb300 import _lib as L, prompt_attention
     q, k, v = make(17, "bf16", 8, 2, 128, [400], [400])

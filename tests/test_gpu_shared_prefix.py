@@ -161,3 +161,20 @@ def test_a_wait_that_runs_out_is_reported_and_the_device_goes_on():
     torch.cuda.synchronize()
     assert status.item() == 1
     assert torch.equal(shared_prefix_attention(*x, 40), good)
+
+
+@pytest.mark.parametrize("hq,hkv,d,shared,own", [(28, 4, 128, 1200, [3, 90, 0, 17, 1] * 6), (32, 32, 128, 600, [40, 200] * 4), (16, 2, 64, 2000, [50] * 20)])
+def test_long_units_repeated_over_a_scratch_of_nan(hq, hkv, d, shared, own):
+    """Many long key ranges at once, whose copies land in any order, with holes all over."""
+    from tiered_kv_cache_split_gb300 import shared_prefix_attention
+    q, pool, table, mask, counts, tb, mk = make(3, "bf16", hq, hkv, d, shared, own)
+    scratch = torch.empty(256 << 20, dtype=torch.uint8, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    first = None
+    for _ in range(60):
+        out = shared_prefix_attention(q, pool, table, mask, counts, shared, scratch=scratch.fill_(255), status=status)
+        if first is None:
+            first = out
+            want, bound, _, _ = prefix_reference(q, pool, tb, mk, counts, shared)
+            assert_within(out, want, bound, "out")
+        assert status.item() == 0 and torch.equal(out, first)

@@ -43,8 +43,9 @@
 //
 // 0 * NaN must not reach O: the V rows of holes are zeroed in shared memory, and
 // keys past a sequence's end or that only some rows see have their non-finite V
-// values taken out there; those are added at the end to the rows that see them. The helper warp does this between a V block's
-// arrival and its product, and passes on blocks that need nothing.
+// values taken out there; those are added at the end to the rows that see them.
+// The helper warp does this between a V block's arrival and its product, and
+// passes on blocks that need nothing.
 //
 // Every wait is bounded: on running out it raises the CTA's abort flag and the
 // caller's status word; each role then leaves its loop, the copies and MMAs in
@@ -67,8 +68,8 @@ constexpr int kProducer = 8, kIssuer = 9, kHelper = 11;  // warps; one issuer pe
 constexpr int kHalf = 64;                  // keys of one S
 constexpr int kBlockPages = kKeyBlock / kPage;
 constexpr int kBox = 128 * 128;            // a box: 128 rows of 64 bf16 columns, 128-byte swizzled
+constexpr float kRise = 20.f;              // of a row's maximum, in base 2, that rescales O
 constexpr int kBatch = 4;                  // blocks whose page ids are fetched together
-constexpr float kRise = 20.f;
 constexpr int kUnits = 4;                  // units the producer may be ahead of the slowest warp
 constexpr int kBatches = 8;                // batches the id ring holds: the producer is at most kUnits units and a
                                            // ring of slots (a batch or two) ahead of the softmax
@@ -97,7 +98,8 @@ struct Work {
 // apart, and up to two halves of a tile are under way.
 struct Shared {
   uint64_t full[8], empty[8], s_full[2][2], p_full[2][2], o_prev[2], o_last[2], q_full[2], drain[2];
-  uint64_t v_clean[8];  // of the V blocks in turn; the helper is fewer than 8 ahead of any reader
+  uint64_t v_clean[8];  // of the V blocks in turn: the helper gives back every slot, so at most 8 lie between it and an issuer
+  uint64_t flags_full[2 * kUnits];  // of the units in turn: a warp is at most kUnits + 1 units behind
   uint64_t ids[kBatches], work_full[kUnits], work_empty[kUnits], response_full;
   alignas(16) uint4 response;
   alignas(16) Work work[kUnits];
@@ -294,9 +296,6 @@ __device__ __forceinline__ bool strip(uint32_t& w) {
   return lo || hi;
 }
 
-// Ring position, from the unit's first, of its i-th V block: K runs `ahead` blocks ahead of V.
-__device__ __forceinline__ int pos_v(int i, int ahead, int n) { return i + min(n, i + ahead); }
-
 // Asks for the unit of a CTA that has not started; 16 bytes arrive at `to`.
 __device__ __forceinline__ void request_unit(uint4* to, uint64_t* bar) {
   asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(smem_u32(to)),
@@ -375,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < C::slots; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 2);
+      mbar_init(&sh.empty[i], 3);  // both issuers and the helper
     }
     for (int t = 0; t < 2; ++t) {
       for (int b = 0; b < 2; ++b) {
@@ -389,6 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&sh.response_full, 1);
     for (int i = 0; i < 8; ++i) mbar_init(&sh.v_clean[i], 1);
+    for (int i = 0; i < 2 * kUnits; ++i) mbar_init(&sh.flags_full[i], 1);
     for (int i = 0; i < kBatches; ++i) mbar_init(&sh.ids[i], 1);
     for (int i = 0; i < kUnits; ++i) {
       mbar_init(&sh.work_full[i], 1);
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       unit = __shfl_sync(0xffffffffu, response_unit(&sh.response), 0);
       asked = -1;
     }
-    // the issuers' arrivals on the last slots come before this shared memory is another CTA's
+    // the arrivals on the last slots come before this shared memory is another CTA's
     for (int q = max(0, pos - C::slots); q < pos; ++q)
       if (!warp_wait(&sh.empty[q % C::slots], (q / C::slots) & 1, abort, limit)) break;
     // an aborted CTA lets what is in flight land before it ends
@@ -621,7 +621,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       warp_wait(&sh.drain[t], 0, nullptr, limit);
     }
   } else if (warp == kHelper) {
-    int pos0 = 0, vb = 0, batches = 0;
+    // Takes every ring slot in turn, K blocks too, and gives it back: a parity wait
+    // on a slot is right only for who has seen its phase before and is not lapped.
+    int slot = 0, slot_phase = 0, vb = 0, batches = 0;
+    auto ready = [&] { return warp_wait(&sh.full[slot], slot_phase, abort, limit); };
+    auto release = [&] {
+      if (lane == 0) mbar_arrive(&sh.empty[slot]);
+      if (++slot == C::slots) {
+        slot = 0;
+        slot_phase ^= 1;
+      }
+    };
+    auto pass_k = [&] {
+      if (!ready()) return false;
+      release();
+      return true;
+    };
     for (int k = 0;; ++k) {
       const Work w = next_work(k);
       if (w.unit < 0) break;
@@ -631,9 +646,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane < 8) flag[lane] = 0;
       __syncwarp();
       bool ok = true;
-      for (int i = 0; i < w.n; ++i, ++vb) {
-        const int at = pos0 + pos_v(i, w.ahead, w.n), slot = at % C::slots;
-        if (!(ok = warp_wait(&sh.full[slot], (at / C::slots) & 1, abort, limit))) break;
+      for (int i = 0; ok && i < min(w.ahead, w.n); ++i) ok = pass_k();
+      for (int i = 0; ok && i < w.n; ++i, ++vb) {
+        if (!(ok = ready())) break;
         const int k0 = (w.block0 + i) * kKeyBlock;
         if (kPaged) {
           const int b = batches + i / kBatch;
@@ -679,9 +694,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.v_clean[vb & 7]);
+        release();
+        if (i + w.ahead < w.n) ok = pass_k();
       }
       if (!ok) break;
-      pos0 += 2 * w.n;
+      if (lane == 0) mbar_arrive(&sh.flags_full[k % (2 * kUnits)]);
       batches += (w.n + kBatch - 1) / kBatch;
     }
   } else {
@@ -708,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         cp_async16(dst + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), q + static_cast<int64_t>(tok_base + tok) * p.q_stride + (x - tok * G) * D + c * 8);
       }
     };
-    int g0 = 0, vb = 0, batches = 0, used = 0, used2 = 0;  // used2: units with two halves or more
+    int g0 = 0, batches = 0, used = 0, used2 = 0;  // used2: units with two halves or more
     Work w = next_work(0);
     load_q(w);
     for (int k = 0; w.unit >= 0; ++k) {
@@ -833,9 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t* flag = sh.flag[k % (2 * kUnits)];
       uint32_t flagged = 0;
       if (!kPaged && ok && mine > 0) {
-        // the helper is done with the unit's V blocks, and so with its flags
-        const int last = vb + w.n - 1;
-        ok = warp_wait(&sh.v_clean[last & 7], (last >> 3) & 1, abort, limit);
+        ok = warp_wait(&sh.flags_full[k % (2 * kUnits)], k / (2 * kUnits) & 1, abort, limit);
         for (int i = 0; i < 8; i += 4) {
           const uint4 f = *reinterpret_cast<const uint4*>(&flag[i]);
           flagged |= f.x | f.y | f.z | f.w;
@@ -891,7 +906,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       fence_before();
-      vb += w.n;
       g0 += mine;
       used += mine > 0;
       used2 += mine > 1;
