@@ -409,7 +409,7 @@ TKV_API tkv_status tkv_quantize_rows(const void* x, int32_t kv_dtype, int64_t ro
  *   out_i = sum_j softmax_j(q_i . k_j / sqrt(d)) v_j.
  * It is the prefill of the cache tkv_append fills (Problem statement; the
  * paper scores decode steps only, so no score is formed).
- *   q_lens, k_lens  HOST int32 [batch], 0 <= q_len <= k_len; batch 1 .. 64
+ *   q_lens, k_lens  HOST int32 [batch], 0 <= q_len <= k_len <= 2^26; batch 1 .. 64
  *   q    device [sum q_len][Hq][d], consecutive tokens q_stride elements apart
  *   k, v device [sum k_len][Hkv][d], tokens k_stride / v_stride elements apart
  *   out  device [sum q_len][Hq][d], tokens out_stride elements apart

@@ -45,8 +45,9 @@ def prompt(lib, batch=2, ql=(5, 7), kl=(5, 9), hq=8, hkv=2, d=64, dt=L.DTYPE_BF1
     (dict(q=I + 8), ("aligned",)), (dict(v=I + 2), ("aligned",)), (dict(out=I + 4), ("aligned",)),
     (dict(sq=504), ("strides",)), (dict(sk=120), ("strides",)), (dict(sv=1025), ("strides",)), (dict(so=-1024), ("strides",)),
     (dict(sk=1 << 37), ("strides",)),
-    (dict(batch=2, ql=(1 << 30, 1 << 30), kl=(1 << 30, 1 << 30)), ("2^31",)),
-    (dict(batch=2, ql=(1, 1), kl=(1 << 30, (1 << 30) + 5)), ("2^31",)),
+    (dict(batch=2, ql=(1, 1), kl=(1 << 26, (1 << 26) + 1)), ("sequence 1", "2^26")),
+    (dict(batch=64, ql=(1,) * 64, kl=(1 << 26,) * 64), ("2^31",)),
+    (dict(batch=9, ql=(1 << 26,) * 9, kl=(1 << 26,) * 9), ("2^31",)),
 ])
 def test_prompt_refusals(lib, bad, words):
     refused(lib, prompt(lib, **bad), L.ERR_INVALID_ARG, *words)

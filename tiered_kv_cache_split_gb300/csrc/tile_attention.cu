@@ -23,6 +23,7 @@ constexpr int kFmaThreads = 256;
 constexpr int kFmaRows = 64;   // rows of a tile
 constexpr int kMmaRows = 128;  // rows of a bf16 tile, two to a group
 constexpr int kFmaKeys = 64;   // keys staged at once (half a key block)
+constexpr int kMaxPromptKeys = 1 << 26;  // a unit over all of them runs under a second, inside the waits' limit
 constexpr int kSms = 152;      // SMs of a GB300: what the plan fills (results do not depend on the device)
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
@@ -644,6 +645,7 @@ int plan_prompt(TileParams& p, TilePlan* plan, int32_t batch, const int32_t* q_l
   int64_t tq = 0, tk = 0;
   for (int i = 0; i < batch; ++i) {
     if (q_lens[i] < 0 || k_lens[i] < q_lens[i]) return report(TKV_ERR_INVALID_ARG, "sequence %d: 0 <= q_len <= k_len", i);
+    if (k_lens[i] > kMaxPromptKeys) return report(TKV_ERR_INVALID_ARG, "sequence %d: k_len above 2^26", i);
     p.seg[i].tok0 = static_cast<int32_t>(tq);
     p.seg[i].ntok = q_lens[i];
     p.seg[i].key0 = tk;
