@@ -502,10 +502,20 @@ bool leads(const TileParams& p, int i) {
 // candidate with the shortest time wins. More than four waves are never split.
 int64_t blocks_per_unit(const TileParams& p, const SegWork* w, const TileShape& ts) {
   int64_t whole = 0, most = 1, blocks = 0;
+  struct Live {
+    int64_t units;         // with keys whole
+    double whole, split;   // what a unit costs beside its blocks
+    uint32_t most;
+    bool lead;
+  } live[kMaxSegs];
+  int nlive = 0;
   for (int i = 0; i < p.nseg; ++i) {
+    if (!w[i].groups) continue;
     whole += w[i].groups * p.Hkv;
     most = std::max(most, w[i].most);
     blocks += w[i].blocks * p.Hkv;
+    const int64_t rows = static_cast<int64_t>(p.seg[i].ntok) * p.G;
+    live[nlive++] = {w[i].groups * p.Hkv, unit_cost(ts, rows, false), unit_cost(ts, rows, true), static_cast<uint32_t>(w[i].most), leads(p, i)};
   }
   if (whole >= 4 * ts.slots) return most;
   // candidates: keys whole, and around what each place gets if all is even
@@ -521,18 +531,26 @@ int64_t blocks_per_unit(const TileParams& p, const SegWork* w, const TileShape& 
     const bool split = p.paged || per < most;
     double work = static_cast<double>(blocks), longest = 0, rest = 0;
     int64_t n_longest = 0, n_rest = 0;
-    for (int i = 0; i < p.nseg; ++i) {
-      if (!w[i].groups) continue;
-      const uint32_t seg = static_cast<uint32_t>(w[i].most), parts = (seg + static_cast<uint32_t>(per) - 1) / static_cast<uint32_t>(per);
-      const int64_t units = w[i].groups * p.Hkv * parts;
-      const bool lead = parts > 1 && leads(p, i) && seg % static_cast<uint32_t>(per);
-      const double cost = unit_cost(ts, static_cast<int64_t>(p.seg[i].ntok) * p.G, split);
-      const double time = static_cast<double>(lead ? per : (seg + parts - 1) / parts) + cost;
-      const int64_t n = lead ? units / parts * (parts - 1) : units;
+    for (int i = 0; i < nlive; ++i) {
+      const Live& l = live[i];
+      const double cost = split ? l.split : l.whole;
+      double time = static_cast<double>(l.most) + cost;
+      int64_t units = l.units, n = units;
+      if (l.most > per) {
+        const uint32_t cut = static_cast<uint32_t>(per), parts = (l.most + cut - 1) / cut, left = l.most % cut;
+        units *= parts;
+        if (l.lead && left) {
+          n = units - l.units;
+          time = static_cast<double>(cut) + cost;
+          if (!p.paged) rest = std::max(rest, static_cast<double>(left) + cost), n_rest += l.units;
+        } else {
+          n = units;
+          time = static_cast<double>((l.most + parts - 1) / parts) + cost;
+        }
+      }
       work += cost * units;
       if (time > longest * 1.01) longest = time, n_longest = n;
       else if (time > longest * 0.99) n_longest += n;
-      if (lead && !p.paged) rest = std::max(rest, static_cast<double>(seg % static_cast<uint32_t>(per)) + cost), n_rest += units - n;
     }
     double time = std::max(work / ts.slots, longest * ceil_div(n_longest, ts.slots));
     if (n_rest && n_longest < ts.slots)  // the rests run beside the one wave, in rounds of their own
