@@ -209,6 +209,20 @@ def test_one_scratch_for_calls_in_turn():
         prompt_attention(*make(20, "bf16", 8, 2, 128, *shapes[0]), *shapes[0], scratch=scratch[:1024])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hkv,d", [(7, 1, 128), (8, 2, 64), (4, 4, 128)])
+def test_prompts_beside_decoding_sequences(dtype, hq, hkv, d):
+    """Sequences whose keys are split, ones whose units write the output and
+    ones of few rows in one call; the scratch starts as NaN, the output too."""
+    q_lens = [400, 1, 0, 90, 260, 1, 17]
+    k_lens = [n + c for n, c in zip(q_lens, [0, 9000, 5, 6000, 100, 0, 4000])]
+    x = make(23, dtype, hq, hkv, d, q_lens, k_lens)
+    scratch = torch.full((64 << 20,), 255, dtype=torch.uint8, device=DEV)
+    out = torch.full((sum(q_lens) + 3, hq, d), float("nan"), dtype=x[0].dtype, device=DEV)
+    check(*x, q_lens, k_lens, scratch=scratch, out=out[:-3])
+    assert out[-3:].isnan().all()
+
+
 @pytest.mark.parametrize("hq,hkv,d", [(32, 32, 128), (16, 4, 128), (32, 8, 64)])
 def test_long_units_repeated_over_a_scratch_of_nan(hq, hkv, d):
     """Many long key ranges at once, whose copies land in any order: every call

@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kFmaThreads, 2) tile_fma_kernel(const __grid_c
   for (int i = 0; i < 4; ++i) {
     const int r = ty * 4 + i, row = t.row0 + r;
     if (r >= t.rows) continue;
-    if (p.direct) {
+    if (sg.direct) {
       const float inv = z[i] > 0.f || z[i] != z[i] ? 1.f / z[i] : 0.f;
       float* at = static_cast<float*>(p.out) + static_cast<int64_t>(sg.tok0 + row / G) * p.out_stride + (t.h * G + row % G) * D + tx * 4;
 #pragma unroll
@@ -302,18 +302,22 @@ __device__ __forceinline__ void add_parts(PartList& l, int which, const TilePara
   l.n += n;
 }
 
-// The partials of query head h * G + g of token tok.
+// The partials of query head h * G + g of the n-th token that has partials; *tok: that token.
 template <bool kMma>
-__device__ __forceinline__ PartList part_list(const TileParams& p, int tok, int h, int g) {
+__device__ __forceinline__ PartList part_list(const TileParams& p, int n, int h, int g, int* tok) {
   PartList l{};
+  *tok = n;
   if (p.paged) {  // segment 0 is the prefix of all tokens
-    add_parts<kMma>(l, 0, p, p.seg[0], h, tok * p.G + g);
-    add_parts<kMma>(l, 1, p, p.seg[tok + 1], h, g);
+    add_parts<kMma>(l, 0, p, p.seg[0], h, n * p.G + g);
+    add_parts<kMma>(l, 1, p, p.seg[n + 1], h, g);
   } else {
     int own = 0;
-    for (int i = 0; i < p.nseg; ++i)
-      if (tok >= p.seg[i].tok0 && tok < p.seg[i].tok0 + p.seg[i].ntok) own = i;
-    add_parts<kMma>(l, 0, p, p.seg[own], h, (tok - p.seg[own].tok0) * p.G + g);
+    for (int i = 0, at = 0; i < p.nseg; ++i) {
+      if (p.seg[i].direct) continue;
+      if (n >= at && n < at + p.seg[i].ntok) own = i, *tok = p.seg[i].tok0 + n - at;
+      at += p.seg[i].ntok;
+    }
+    add_parts<kMma>(l, 0, p, p.seg[own], h, (*tok - p.seg[own].tok0) * p.G + g);
   }
   return l;
 }
@@ -348,10 +352,11 @@ __global__ void __launch_bounds__(kMergeThreads) tile_merge_kernel(const __grid_
     const uint32_t row = blockIdx.x * (kMergeWarps / kShare) + warp / kShare, hq_all = p.Hq;
     const bool live = row < rows;
     float acc[E] = {}, z = 0.f;
-    const int tok = live ? row / hq_all : 0, hq = live ? row % hq_all : 0;
+    int tok = 0;
+    const int hq = live ? row % hq_all : 0;
     if (live) {
       const uint32_t h = static_cast<uint32_t>(hq) / static_cast<uint32_t>(G);
-      const PartList l = part_list<sizeof(T) == 2>(p, tok, h, hq - h * G);
+      const PartList l = part_list<sizeof(T) == 2>(p, row / hq_all, h, hq - h * G, &tok);
       int64_t off[2];  // this lane's columns, from a partial row's number of elements
 #pragma unroll
       for (int q = 0; q < 2; ++q)
@@ -422,7 +427,8 @@ __global__ void __launch_bounds__(kMergeThreads) tile_merge_kernel(const __grid_
   const int i = item % per * kAlphaSlots + threadIdx.x * 4;
   if (item % per * kAlphaSlots >= so.nkeys) return;
   for (int g = warp; g < G; g += kMergeWarps) {
-    const float2 mz = parts_sum(p, part_list<sizeof(T) == 2>(p, tok, h, g), p.part_ze, lane);
+    int same;
+    const float2 mz = parts_sum(p, part_list<sizeof(T) == 2>(p, tok, h, g, &same), p.part_ze, lane);
     if (lane == 0) {
       s_m[g] = mz.x;
       s_inv[g] = parts_inv(mz.y);
@@ -495,6 +501,14 @@ bool leads(const TileParams& p, int i) {
   return p.causal ? p.seg[i].see0 >= p.seg[i].nkeys / 2 : p.paged && i == 0;
 }
 
+// A segment whose keys are not split, in a call where others are: its units write
+// the output themselves (a 2048-token prompt beside one token behind 32768 keys,
+// 28 / 4 heads: 78 -> 46 us), unless its rows are one tile, which a pair finishes
+// sooner by way of partials.
+bool whole_is_direct(const TileParams& p, const TileSeg& s, const TileShape& ts) {
+  return !p.paged && (ts.tpg == 1 || static_cast<int64_t>(s.ntok) * p.G > ts.rows);
+}
+
 // Key blocks per unit. Units are handed out longest first to `slots` places, so
 // the time is about the larger of what one place gets on average and of the
 // waves the longest kind of unit makes. Rows alone leave a decode step, or a
@@ -506,7 +520,7 @@ int64_t blocks_per_unit(const TileParams& p, const SegWork* w, const TileShape& 
     int64_t units;         // with keys whole
     double whole, split;   // what a unit costs beside its blocks
     uint32_t most;
-    bool lead;
+    bool lead, direct;     // direct: writes the output where its keys are whole
   } live[kMaxSegs];
   int nlive = 0;
   for (int i = 0; i < p.nseg; ++i) {
@@ -515,7 +529,8 @@ int64_t blocks_per_unit(const TileParams& p, const SegWork* w, const TileShape& 
     most = std::max(most, w[i].most);
     blocks += w[i].blocks * p.Hkv;
     const int64_t rows = static_cast<int64_t>(p.seg[i].ntok) * p.G;
-    live[nlive++] = {w[i].groups * p.Hkv, unit_cost(ts, rows, false), unit_cost(ts, rows, true), static_cast<uint32_t>(w[i].most), leads(p, i)};
+    live[nlive++] = {w[i].groups * p.Hkv, unit_cost(ts, rows, false), unit_cost(ts, rows, true), static_cast<uint32_t>(w[i].most), leads(p, i),
+                     whole_is_direct(p, p.seg[i], ts)};
   }
   if (whole >= 4 * ts.slots) return most;
   // candidates: keys whole, and around what each place gets if all is even
@@ -533,7 +548,7 @@ int64_t blocks_per_unit(const TileParams& p, const SegWork* w, const TileShape& 
     int64_t n_longest = 0, n_rest = 0;
     for (int i = 0; i < nlive; ++i) {
       const Live& l = live[i];
-      const double cost = split ? l.split : l.whole;
+      const double cost = split && !(l.direct && l.most <= per) ? l.split : l.whole;
       double time = static_cast<double>(l.most) + cost;
       int64_t units = l.units, n = units;
       if (l.most > per) {
@@ -574,7 +589,7 @@ TilePlan plan_units(TileParams& p, const TileShape& ts, bool want_spill) {
   for (int i = 0; i < p.nseg; ++i) work[i] = seg_work(p, p.seg[i], ts);
   const int64_t per = blocks_per_unit(p, work, ts);
   for (int i = 0; i < p.nseg; ++i) split |= work[i].groups && work[i].most > per;
-  p.direct = !split;
+  p.merge_tokens = p.paged ? p.seg[0].ntok : 0;
   int live = 0;
   for (int i = 0; i < p.nseg; ++i) {
     p.seg[i].splits = work[i].groups ? (split ? static_cast<int32_t>(std::max<int64_t>(1, ceil_div(work[i].most, per))) : 1) : 0;
@@ -617,13 +632,17 @@ TilePlan plan_units(TileParams& p, const TileShape& ts, bool want_spill) {
     TileSeg& s = p.seg[i];
     s.part0 = out.part_rows;
     s.spill0 = -1;
-    s.groups = s.part_rows = s.pair = 0;
+    s.groups = s.part_rows = s.pair = s.direct = 0;
     if (!work[i].groups) continue;
     s.groups = static_cast<int32_t>(work[i].groups);
     const int64_t rows = static_cast<int64_t>(s.ntok) * p.G;
-    s.pair = !p.direct && ts.tpg == 2 && rows <= ts.rows;
+    s.direct = s.splits == 1 && (!split || whole_is_direct(p, s, ts));
+    s.pair = !s.direct && ts.tpg == 2 && rows <= ts.rows;
     s.part_rows = static_cast<int32_t>(std::min<int64_t>(ts.rows, rows));
-    if (!p.direct) out.part_rows += static_cast<int64_t>(s.groups) * p.Hkv * s.splits * ts.tpg * s.part_rows;
+    if (!s.direct) {
+      out.part_rows += static_cast<int64_t>(s.groups) * p.Hkv * s.splits * ts.tpg * s.part_rows;
+      if (!p.paged) p.merge_tokens += s.ntok;
+    }
     if (want_spill && p.paged && i > 0) {
       s.spill0 = out.spill;
       out.spill += static_cast<int64_t>(s.nkeys) * p.Hq;
@@ -727,17 +746,17 @@ cudaError_t launch_fma(const TileParams& p, cudaStream_t s) {
 
 // The merge may start while the units' kernel ends; it waits for it before it reads.
 template <typename T, int D>
-cudaError_t launch_merge(const TileParams& p, int tokens, cudaStream_t s) {
+cudaError_t launch_merge(const TileParams& p, cudaStream_t s) {
   int parts = 0, slots = 0;  // most partials of a row, most own slots of a sequence
   for (int i = 0; i < p.nseg; ++i) {
     const int n = p.seg[i].splits * (p.seg[i].pair ? 2 : 1) + (p.paged && i > 0 ? p.seg[0].splits * (p.seg[0].pair ? 2 : 1) : 0);
     parts = std::max(parts, n);
     if (p.paged && i > 0) slots = std::max(slots, p.seg[i].nkeys);
   }
-  const int64_t rows = static_cast<int64_t>(tokens) * p.Hq;
+  const int64_t tokens = p.merge_tokens, rows = tokens * p.Hq;
   const bool share = parts >= kShareParts && rows <= kShareRows;
   const int64_t row_ctas = share ? rows : ceil_div(rows, kMergeWarps);
-  const int64_t alpha_ctas = p.alpha ? static_cast<int64_t>(tokens) * p.Hkv * ceil_div(slots, kAlphaSlots) : 0;
+  const int64_t alpha_ctas = p.alpha ? tokens * p.Hkv * ceil_div(slots, kAlphaSlots) : 0;
   if (rows > INT32_MAX || row_ctas + alpha_ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(row_ctas + alpha_ctas));
@@ -753,19 +772,19 @@ cudaError_t launch_merge(const TileParams& p, int tokens, cudaStream_t s) {
 }
 
 template <typename T>
-cudaError_t launch_tiles(const TileParams& p, int D, int tokens, int64_t keys, cudaStream_t s) {
+cudaError_t launch_tiles(const TileParams& p, int D, int64_t keys, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (p.units > 0) {
     if (sizeof(T) == 2) e = launch_tile_mma(p, D, keys, s);
     else e = D == 64 ? launch_fma<64>(p, s) : launch_fma<128>(p, s);
     if (e != cudaSuccess) return e;
   }
-  if (!p.direct && tokens > 0) e = D == 64 ? launch_merge<T, 64>(p, tokens, s) : launch_merge<T, 128>(p, tokens, s);
+  if (p.merge_tokens > 0) e = D == 64 ? launch_merge<T, 64>(p, s) : launch_merge<T, 128>(p, s);
   return e;
 }
 
-cudaError_t launch_dtype(const TileParams& p, int dtype, int D, int tokens, int64_t keys, cudaStream_t s) {
-  return dtype == TKV_DTYPE_BF16 ? launch_tiles<__nv_bfloat16>(p, D, tokens, keys, s) : launch_tiles<float>(p, D, tokens, keys, s);
+cudaError_t launch_dtype(const TileParams& p, int dtype, int D, int64_t keys, cudaStream_t s) {
+  return dtype == TKV_DTYPE_BF16 ? launch_tiles<__nv_bfloat16>(p, D, keys, s) : launch_tiles<float>(p, D, keys, s);
 }
 
 thread_local uint64_t g_stall_limit_ns = 0;  // tkv_test_stall_next_tiles
@@ -843,7 +862,7 @@ tkv_status tkv_prompt_attention(int32_t batch, const int32_t* q_lens, const int3
   p.out_sectors = !misaligned(out, 32) && out_stride % (2 * unit) == 0;
   p.status = status;
   set_waits(p, kv_dtype);
-  const cudaError_t e = launch_dtype(p, kv_dtype, head_dim, static_cast<int>(tq), tk, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_dtype(p, kv_dtype, head_dim, tk, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return tkv_status(report(TKV_ERR_CUDA, "prompt attention launch failed: %s", cudaGetErrorString(e)));
   return TKV_OK;
 }
@@ -897,7 +916,7 @@ tkv_status tkv_shared_prefix_attention(int32_t batch, int32_t n_q_heads, int32_t
   p.alpha_first = static_cast<int64_t>(shared_pages) * kPage;
   p.status = status;
   set_waits(p, kv_dtype);
-  const cudaError_t e = launch_dtype(p, kv_dtype, head_dim, batch, 0, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_dtype(p, kv_dtype, head_dim, 0, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess)
     return tkv_status(report(TKV_ERR_CUDA, "shared-prefix attention launch failed: %s", cudaGetErrorString(e)));
   return TKV_OK;

@@ -7,8 +7,9 @@
 // element is read once for all of them and a short segment still fills a tile.
 // A UNIT (one CTA) is (segment, row group, KV head, split): the rows of the
 // group over a range of 128-key blocks. A unit that covers all keys of its rows
-// writes the output; otherwise it writes a PARTIAL (m, Z, unnormalised O) per
-// row, in base 2, and the merge kernel joins the partials of each row. O of a
+// writes the output (unless it is half a pair's); otherwise it writes a PARTIAL
+// (m, Z, unnormalised O) per row, in base 2, and the merge kernel joins the
+// partials of each row. O of a
 // partial tile lies as [D / 8][rows][8]: a thread per row then stores whole lines
 // with its neighbours (and the merge reads whole 32-byte sectors).
 #pragma once
@@ -40,6 +41,7 @@ struct TileSeg {
   int32_t groups;    // row groups
   int32_t part_rows; // rows per partial tile
   int32_t pair;      // 1: one row tile, its two halves of the CTA take alternate key blocks
+  int32_t direct;    // 1: its units write the output, else partials
 };
 
 struct TileParams {
@@ -66,8 +68,8 @@ struct TileParams {
   float qscale;                // log2(e) / sqrt(D): logits are kept in base 2
   int32_t Hq, Hkv, G;
   int32_t nseg, units;
+  int32_t merge_tokens;        // of segments whose units write partials (paged: all)
   int32_t paged, causal;
-  int32_t direct;              // 1: no splits, units write the output
   int32_t tile_rows, tpg;      // rows of a tile, tiles of a row group
   TileSeg seg[kMaxSegs];
   // Units are numbered by bands, longest first: band i is row groups top, top - 1,

@@ -868,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       if (active && rows > 0) {
         const float inv = z > 0.f || z != z ? 1.f / z : 0.f;
-        const bool direct = !kPaged && p.direct;
+        const bool direct = !kPaged && sg.direct;
         const int64_t part = direct ? 0 : tile_part_row(p, sg, w.grp, w.h, w.split, t);
         if (mine == 0 || (!kPaged && flagged)) {
           // no key: O was never written; or non-finite values to add, in place
