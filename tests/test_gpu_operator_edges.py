@@ -1,0 +1,102 @@
+"""Edges of the prompt, shared-prefix and page operators: buffers of exactly the
+stated size, between guards. Bounds are those of operator_helpers."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from operator_helpers import assert_within, prefix_reference, prompt_reference
+from test_gpu_pages import Book
+from test_gpu_prompt_attention import make as make_prompt
+from test_gpu_shared_prefix import make as make_prefix
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+GUARD = 1 << 20
+
+
+class Guarded:
+    """`size` bytes of NaN between two guards."""
+
+    def __init__(self, size):
+        self.all = torch.full((size + 2 * GUARD,), 0xA5, dtype=torch.uint8, device=DEV)
+        self.mid = self.all[GUARD:GUARD + size].fill_(255)
+
+    def intact(self):
+        return bool((self.all[:GUARD] == 0xA5).all() and (self.all[GUARD + self.mid.numel():] == 0xA5).all())
+
+
+def size_of(call, *args):
+    from tiered_kv_cache_split_gb300 import _lib as L
+    n = ctypes.c_size_t()
+    L.check(getattr(L.load(), call + "_scratch_size")(*args, ctypes.byref(n)))
+    return n.value
+
+
+def ints(v):
+    return (ctypes.c_int32 * len(v))(*v)
+
+
+def code(dtype):
+    from tiered_kv_cache_split_gb300 import _lib as L
+    return L.DTYPE_BF16 if dtype == "bf16" else L.DTYPE_F32
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hkv,d,shared,own", [(28, 4, 128, 16, [0] * 31), (28, 4, 128, 256, [0] * 64), (8, 2, 64, 8, [0, 0]),
+                                                 (1, 1, 128, 1, [0]), (8, 2, 64, 20, [0, 3, 0]), (32, 32, 128, 40, [1, 9]),
+                                                 (6, 2, 64, 0, [2, 0, 5])])
+@pytest.mark.parametrize("alpha", [True, False])
+def test_a_decode_stays_inside_a_scratch_of_the_stated_size(dtype, hq, hkv, d, shared, own, alpha):
+    from tiered_kv_cache_split_gb300 import shared_prefix_attention
+    q, pool, table, mask, counts, tb, mk = make_prefix(shared, dtype, hq, hkv, d, shared, own)
+    width = table.shape[1]
+    a = torch.zeros(len(own), hkv, width * 16, device=DEV) if alpha else None
+    s = Guarded(size_of("tkv_shared_prefix_attention", len(own), hq, hkv, d, code(dtype), ints(counts), width, shared, int(alpha)))
+    out = shared_prefix_attention(q, pool, table, mask, counts, shared, alpha_sum=a, scratch=s.mid)
+    assert s.intact()
+    want, bound, aw, ab = prefix_reference(q, pool, tb, mk, counts, shared)
+    assert_within(out, want, bound, "out")
+    if alpha:
+        assert_within(a, aw, ab, "alpha")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hkv,d,q_lens,k_lens", [(8, 2, 128, [20], [3000]), (28, 4, 128, [1, 300, 0, 7], [5000, 300, 4, 900]),
+                                                    (6, 2, 64, [20], [970]), (4, 4, 64, [500], [2000])])
+def test_a_prompt_stays_inside_a_scratch_of_the_stated_size(dtype, hq, hkv, d, q_lens, k_lens):
+    from tiered_kv_cache_split_gb300 import prompt_attention
+    x = make_prompt(1, dtype, hq, hkv, d, q_lens, k_lens)
+    need = size_of("tkv_prompt_attention", len(q_lens), ints(q_lens), ints(k_lens), hq, hkv, d, code(dtype))
+    assert need > 0
+    s = Guarded(need)
+    out = prompt_attention(*x, q_lens, k_lens, scratch=s.mid)
+    assert s.intact()
+    assert_within(out, *prompt_reference(*x, q_lens, k_lens))
+
+
+@pytest.mark.parametrize("share", [True, False])
+def test_fork_and_compact_stay_inside_a_scratch_of_the_stated_size(share):
+    from tiered_kv_cache_split_gb300 import compact_sequences, fork_sequences
+    b = Book(1, 2, 400, 2, 64, "bf16", 12, 40)
+    b.fill(0, 37, last=5)
+    b.fill(1, 3, drop=0.5)
+    b.upload()
+    parents, children = [0, 1, 0, 1, 0, 0], [2, 3, 5, 7, 11, 4]
+    s = Guarded(size_of("tkv_fork_sequences", 12, 40, ints(b.counts), 6, ints(parents), ints(children), int(share)))
+    st = fork_sequences(b.dpool, b.dtable, b.counts, b.drefs, b.dmask, parents, children, share=share, positions=b.dpos, scratch=s.mid)
+    assert b.fork(parents, children, share) == st.item() == 0 and s.intact()
+    b.same()
+    for r in (6, 8):                            # empty pages ahead of as many full ones: the most moves
+        b.free = [p for p in range(400) if b.refs[p] == 0]
+        b.fill(r, 40)
+        for p in b.table[r, 0:20]:
+            b.mask[p], b.pos[p] = 0, -1
+    b.upload()
+    counts = list(b.counts)
+    s = Guarded(size_of("tkv_compact_sequences", 12, 40, ints(counts)))
+    got = compact_sequences(b.dpool, b.dtable, counts, b.drefs, b.dmask, positions=b.dpos, scratch=s.mid)
+    assert got.tolist() == b.compact() and s.intact()
+    b.same()

@@ -1,0 +1,39 @@
+"""Edges of the prompt, shared-prefix and page operators that need no GPU:
+scratch sizes, and where the buffers of a call come from."""
+import ctypes
+import os
+
+import pytest
+
+from tiered_kv_cache_split_gb300 import _lib as L
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(L.LIB_PATH):
+        from tiered_kv_cache_split_gb300 import build
+        build.build()
+    return L.load()
+
+
+def prefix_scratch(lib, dt, hq, hkv, d, counts, shared, alpha):
+    n = ctypes.c_size_t()
+    c = (ctypes.c_int32 * len(counts))(*counts)
+    L.check(lib.tkv_shared_prefix_attention_scratch_size(len(counts), hq, hkv, d, dt, c, max(counts), shared, alpha, ctypes.byref(n)))
+    return n.value
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(28, 4, 128), (8, 2, 64), (32, 32, 128), (64, 1, 64)])
+@pytest.mark.parametrize("counts,shared", [([256] * 64, 256), ([16] * 31, 16), ([1], 1), ([300] * 3, 300), ([9, 300, 9], 9)])
+def test_alpha_has_room_for_its_sums_of_weights(lib, hq, hkv, d, counts, shared):
+    """A bf16 call with alpha keeps one more float per partial row, with or
+    without pages behind the prefix (beside the logits of those pages)."""
+    without = prefix_scratch(lib, L.DTYPE_BF16, hq, hkv, d, counts, shared, 0)
+    rows = (without - 768) // (4 * (d + 2))        # at least: three columns are rounded up to 256 bytes
+    own = sum(n - shared for n in counts) * 16 * hq
+    with_alpha = prefix_scratch(lib, L.DTYPE_BF16, hq, hkv, d, counts, shared, 1)
+    assert with_alpha - without >= 4 * (rows + own)
+    assert rows > 0
+    # fp32 keeps one sum for both uses
+    with_alpha, without = (prefix_scratch(lib, L.DTYPE_F32, hq, hkv, d, counts, shared, a) for a in (1, 0))
+    assert 4 * own <= with_alpha - without < 4 * own + 256

@@ -454,6 +454,7 @@ __global__ void __launch_bounds__(kMergeThreads) tile_merge_kernel(const __grid_
 
 struct TilePlan {
   int64_t part_rows, spill;  // partial rows, spilled floats
+  int64_t exact_rows;        // partial rows with a Z of unrounded weights (bf16 with alpha: all of them, else none)
   int64_t units;
 };
 
@@ -580,8 +581,9 @@ int64_t blocks_per_unit(const TileParams& p, const SegWork* w, const TileShape& 
 }
 
 // Cuts the segments (tok0, ntok, nkeys, see0 set) into units.
-TilePlan plan_units(TileParams& p, const TileShape& ts, bool want_spill) {
-  TilePlan out{0, 0, 0};
+TilePlan plan_units(TileParams& p, int dtype, bool want_alpha) {
+  const TileShape ts = tile_shape(dtype);
+  TilePlan out{};
   SegWork work[kMaxSegs];
   p.tile_rows = ts.rows;
   p.tpg = ts.tpg;
@@ -643,11 +645,13 @@ TilePlan plan_units(TileParams& p, const TileShape& ts, bool want_spill) {
       out.part_rows += static_cast<int64_t>(s.groups) * p.Hkv * s.splits * ts.tpg * s.part_rows;
       if (!p.paged) p.merge_tokens += s.ntok;
     }
-    if (want_spill && p.paged && i > 0) {
+    if (want_alpha && p.paged && i > 0) {
       s.spill0 = out.spill;
       out.spill += static_cast<int64_t>(s.nkeys) * p.Hq;
     }
   }
+  // the units write it for every partial, the prefix's too, whether or not a sequence has slots of its own
+  out.exact_rows = want_alpha && dtype == TKV_DTYPE_BF16 ? out.part_rows : 0;
   return out;
 }
 
@@ -662,7 +666,7 @@ TileScratch tile_scratch(const TilePlan& pl, int D) {
   s.o_m = align256(static_cast<size_t>(pl.part_rows) * D * 4);
   s.o_z = s.o_m + column;
   s.o_ze = s.o_z + column;
-  s.o_spill = s.o_ze + (pl.spill ? column : 0);
+  s.o_spill = s.o_ze + align256(static_cast<size_t>(pl.exact_rows) * 4);
   s.bytes = s.o_spill + align256(static_cast<size_t>(pl.spill) * 4);
   return s;
 }
@@ -700,7 +704,7 @@ int plan_prompt(TileParams& p, TilePlan* plan, int32_t batch, const int32_t* q_l
   }
   *tokens = tq;
   *keys = tk;
-  *plan = plan_units(p, tile_shape(dtype), false);
+  *plan = plan_units(p, dtype, false);
   if (plan->units > INT32_MAX) return report(TKV_ERR_INVALID_ARG, "more than 2^31 units of work in one call");
   p.units = static_cast<int32_t>(plan->units);
   return TKV_OK;
@@ -728,7 +732,7 @@ int plan_shared(TileParams& p, TilePlan* plan, int32_t batch, int32_t Hq, int32_
     s.key0 = static_cast<int64_t>(b) * max_pages + shared_pages;
     s.nkeys = (page_counts[b] - shared_pages) * kPage;
   }
-  *plan = plan_units(p, tile_shape(dtype), want_alpha != 0);
+  *plan = plan_units(p, dtype, want_alpha != 0);
   if (plan->units > INT32_MAX) return report(TKV_ERR_INVALID_ARG, "more than 2^31 units of work in one call");
   p.units = static_cast<int32_t>(plan->units);
   return TKV_OK;
@@ -800,7 +804,7 @@ void set_waits(TileParams& p, int32_t dtype) {
 
 bool misaligned(const void* ptr, size_t to) { return reinterpret_cast<uintptr_t>(ptr) % to != 0; }
 
-int bind_scratch(TileParams& p, const TilePlan& plan, int D, bool fp32, void* scratch, size_t bytes) {
+int bind_scratch(TileParams& p, const TilePlan& plan, int D, void* scratch, size_t bytes) {
   const TileScratch s = tile_scratch(plan, D);
   if (s.bytes == 0) return TKV_OK;
   if (!scratch) return report(TKV_ERR_INVALID_ARG, "null scratch: need %zu bytes", s.bytes);
@@ -810,7 +814,7 @@ int bind_scratch(TileParams& p, const TilePlan& plan, int D, bool fp32, void* sc
   p.part_o = reinterpret_cast<float*>(at);
   p.part_m = reinterpret_cast<float*>(at + s.o_m);
   p.part_z = reinterpret_cast<float*>(at + s.o_z);
-  p.part_ze = fp32 ? p.part_z : reinterpret_cast<float*>(at + s.o_ze);
+  p.part_ze = plan.exact_rows ? reinterpret_cast<float*>(at + s.o_ze) : p.part_z;
   p.spill = reinterpret_cast<float*>(at + s.o_spill);
   return TKV_OK;
 }
@@ -854,7 +858,7 @@ tkv_status tkv_prompt_attention(int32_t batch, const int32_t* q_lens, const int3
   if (q_stride < qrow || out_stride < qrow || k_stride < krow || v_stride < krow || q_stride % unit || out_stride % unit ||
       k_stride % unit || v_stride % unit || (q_stride | out_stride | k_stride | v_stride) >> 36)
     return tkv_status(report(TKV_ERR_INVALID_ARG, "token strides must hold a token and be multiples of 16 bytes"));
-  if (int st = bind_scratch(p, plan, head_dim, kv_dtype == TKV_DTYPE_F32, scratch, scratch_bytes)) return tkv_status(st);
+  if (int st = bind_scratch(p, plan, head_dim, scratch, scratch_bytes)) return tkv_status(st);
   p.q = q; p.q_stride = q_stride;
   p.k = k; p.k_stride = k_stride;
   p.v = v; p.v_stride = v_stride;
@@ -903,7 +907,7 @@ tkv_status tkv_shared_prefix_attention(int32_t batch, int32_t n_q_heads, int32_t
     return tkv_status(report(TKV_ERR_INVALID_ARG, "pool_pages x n_kv_heads must be 1 to 2^29"));
   if (misaligned(q, 16) || misaligned(pool, 16) || misaligned(out, 16) || misaligned(alpha_sum, 16))
     return tkv_status(report(TKV_ERR_INVALID_ARG, "q, pool, out and alpha_sum must be 16-byte aligned"));
-  if (int st = bind_scratch(p, plan, head_dim, kv_dtype == TKV_DTYPE_F32, scratch, scratch_bytes)) return tkv_status(st);
+  if (int st = bind_scratch(p, plan, head_dim, scratch, scratch_bytes)) return tkv_status(st);
   p.q = q; p.q_stride = static_cast<int64_t>(n_q_heads) * head_dim;
   p.out = out; p.out_stride = p.q_stride;
   p.out_sectors = !misaligned(out, 32);
