@@ -1,5 +1,6 @@
 """Edges of the prompt, shared-prefix and page operators: buffers of exactly the
-stated size, between guards. Bounds are those of operator_helpers."""
+stated size, calls beside work on another stream. Bounds are those of
+operator_helpers."""
 import ctypes
 
 import numpy as np
@@ -100,3 +101,66 @@ def test_fork_and_compact_stay_inside_a_scratch_of_the_stated_size(share):
     got = compact_sequences(b.dpool, b.dtable, counts, b.drefs, b.dmask, positions=b.dpos, scratch=s.mid)
     assert got.tolist() == b.compact() and s.intact()
     b.same()
+
+
+class Behind:
+    """Blocks of the current stream's memory, given back while copies out of
+    them wait behind a long kernel there."""
+
+    def __init__(self, sizes):
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        blocks = [torch.full((n,), 77, dtype=torch.uint8, device=DEV) for n in sizes for _ in range(3)]
+        self.copies = [torch.zeros_like(x) for x in blocks]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(200_000_000)          # about 0.1 s
+        for x, y in zip(blocks, self.copies):
+            y.copy_(x)
+
+    def check(self):
+        torch.cuda.synchronize()
+        assert all(bool((y == 77).all()) for y in self.copies)
+
+
+def test_calls_on_another_stream_beside_work_that_still_uses_freed_blocks():
+    from tiered_kv_cache_split_gb300 import (compact_sequences, fork_sequences, free_sequences, prompt_attention,
+                                             shared_prefix_attention)
+    side = torch.cuda.Stream()
+    q_lens, k_lens = [40, 300], [3000, 300]
+    x = make_prompt(2, "bf16", 8, 2, 128, q_lens, k_lens)
+    need = size_of("tkv_prompt_attention", 2, ints(q_lens), ints(k_lens), 8, 2, 128, code("bf16"))
+    good = prompt_attention(*x, q_lens, k_lens)
+    b = Behind([need, good.numel() * 2])
+    got = prompt_attention(*x, q_lens, k_lens, stream=side)
+    b.check()
+    assert torch.equal(got, good)
+
+    q, pool, table, mask, counts = make_prefix(3, "bf16", 28, 4, 128, 40, [9, 0, 30])[:5]
+    need = size_of("tkv_shared_prefix_attention", 3, 28, 4, 128, code("bf16"), ints(counts), table.shape[1], 40, 0)
+    good = shared_prefix_attention(q, pool, table, mask, counts, 40)
+    b = Behind([need, good.numel() * 2])
+    got = shared_prefix_attention(q, pool, table, mask, counts, 40, stream=side)
+    b.check()
+    assert torch.equal(got, good)
+
+    k = Book(3, 1, 300, 2, 64, "bf16", 4, 60)
+    k.fill(0, 60, drop=0.5)
+    k.upload()
+    old = list(k.counts)
+    b = Behind([size_of("tkv_fork_sequences", 4, 60, ints(old), 2, ints([0, 0]), ints([1, 2]), 0), 4])
+    st = fork_sequences(k.dpool, k.dtable, old, k.drefs, k.dmask, [0, 0], [1, 2], share=False, positions=k.dpos, stream=side)
+    b.check()
+    assert k.fork([0, 0], [1, 2], False) == st.item() == 0
+    k.same()
+    counts = list(k.counts)
+    b = Behind([size_of("tkv_compact_sequences", 4, 60, ints(counts)), 16])
+    new = compact_sequences(k.dpool, k.dtable, counts, k.drefs, k.dmask, positions=k.dpos, stream=side)
+    b.check()
+    assert new.tolist() == k.compact()
+    k.same()
+    b = Behind([4])
+    st = free_sequences(k.dtable, k.counts, k.drefs, k.dmask, [1, 2], stream=side)
+    b.check()
+    k.free_rows([1, 2])
+    k.same()
+    assert st.item() == 0

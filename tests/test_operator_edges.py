@@ -37,3 +37,48 @@ def test_alpha_has_room_for_its_sums_of_weights(lib, hq, hkv, d, counts, shared)
     # fp32 keeps one sum for both uses
     with_alpha, without = (prefix_scratch(lib, L.DTYPE_F32, hq, hkv, d, counts, shared, a) for a in (1, 0))
     assert 4 * own <= with_alpha - without < 4 * own + 256
+
+
+class FakeStreams:
+    """torch.cuda as far as buffers for a call on another stream need it."""
+
+    def __init__(self, monkeypatch):
+        import contextlib
+
+        from tiered_kv_cache_split_gb300 import operators
+        self.now, self.made, self.recorded = "current", [], []
+
+        @contextlib.contextmanager
+        def stream(s):
+            before, self.now = self.now, s
+            yield
+            self.now = before
+
+        class Tensor:
+            def record_stream(me, s):
+                self.recorded.append(s)
+
+            def data_ptr(me):
+                return 0
+
+        def empty(*a, **k):
+            self.made.append(self.now)
+            return Tensor()
+
+        monkeypatch.setattr(operators.torch.cuda, "stream", stream)
+        monkeypatch.setattr(operators.torch.cuda, "current_stream", lambda *a: self.now)
+        monkeypatch.setattr(operators.torch, "empty", empty)
+        self.on = object.__new__(operators._On)
+        self.on.device, self.on.guard, self.on.given, self.on.raw = 0, None, "side", 1
+
+
+def test_buffers_of_a_call_come_from_its_streams_memory(monkeypatch):
+    """A block of the current stream's memory may be one that a tensor just gave
+    back while work queued on the current stream still uses it: nothing orders
+    another stream behind that work."""
+    f = FakeStreams(monkeypatch)
+    f.on.empty(4, "dtype")
+    f.on.scratch(None, 1024)
+    assert f.made == ["side", "side"]
+    assert f.recorded == ["current"]        # what is returned outlives its use on the caller's stream
+    assert f.now == "current"

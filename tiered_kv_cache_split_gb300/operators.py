@@ -3,8 +3,9 @@
 Argument marshalling only, as in cache.py: torch owns the buffers, the CUDA
 kernels of libtkv.so do the work (include/tkv.h states each operator). Every
 tensor of a call lies on one CUDA device, which need not be the current one;
-a call on a stream other than the current one keeps the buffers it made alive
-for that stream. ValueError names an argument of the wrong type, shape, layout
+a call on a stream other than the current one takes the buffers it makes from
+that stream's memory (work on the current stream waits for that stream before
+it uses them). ValueError names an argument of the wrong type, shape, layout
 or device; the library's own checks raise TkvError.
 """
 from __future__ import annotations
@@ -72,7 +73,7 @@ def _tokens(t, name, like=None):
 
 class _On:
     """The call's device made current if it is not, its stream, and buffers made
-    for the call (kept alive for a stream other than the current one)."""
+    for the call."""
 
     __slots__ = ("device", "guard", "given", "raw")
 
@@ -98,10 +99,16 @@ class _On:
         if self.guard is not None:
             self.guard.__exit__(*exc)
 
-    def empty(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self.given is not None:
-            t.record_stream(self.given)
+    def empty(self, shape, dtype, returned=True):
+        """A buffer from the memory of the stream that uses it: a block of the
+        current stream's may still be in use by work queued there. A returned
+        one may be dropped with work on the current stream outstanding."""
+        if self.given is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.given):
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+        if returned:
+            t.record_stream(torch.cuda.current_stream(self.device))
         return t
 
     def scratch(self, given, need):
@@ -109,7 +116,7 @@ class _On:
         if given is None:
             if need == 0:
                 return None, None, 0
-            given = self.empty(need, torch.uint8)
+            given = self.empty(need, torch.uint8, returned=False)
             return given, given.data_ptr(), need
         if not isinstance(given, torch.Tensor) or not given.is_contiguous() or given.get_device() != self.device:
             raise ValueError("scratch: a contiguous tensor on the call's device")
