@@ -164,3 +164,32 @@ def test_calls_on_another_stream_beside_work_that_still_uses_freed_blocks():
     k.free_rows([1, 2])
     k.same()
     assert st.item() == 0
+
+
+def test_the_other_stateless_calls_on_another_stream_beside_work_that_still_uses_freed_blocks():
+    from tiered_kv_cache_split_gb300 import classify, paged_attention, quantize_rows
+    side = torch.cuda.Stream()
+    q, pool, table, mask, counts = make_prefix(5, "bf16", 28, 4, 128, 40, [9, 2, 30])[:5]
+    table = torch.where(table < pool.shape[0], table, 0)
+    need = size_of("tkv_paged_attention", 3, 28, 4, 128, table.shape[1])
+    good = paged_attention(q, pool, table, mask, counts)
+    b = Behind([need, good.numel() * 2])
+    got = paged_attention(q, pool, table, mask, counts, stream=side)
+    b.check()
+    assert torch.equal(got, good)
+
+    x = torch.randn(3000, 512, device=DEV)
+    good = quantize_rows(x)
+    b = Behind([3000 * 512, 3000 * 4])
+    got = quantize_rows(x, stream=side)
+    b.check()
+    assert all(torch.equal(m, n) for m, n in zip(got, good))
+
+    scores = torch.rand(3, 4000, dtype=torch.float64, device=DEV)
+    tiers = torch.zeros(3, 4000, dtype=torch.uint8, device=DEV)
+    params = [[4000, 100, 500, 900, 800]] * 3
+    good = classify(scores, tiers, params, 4, 128)
+    b = Behind([size_of("tkv_classify", 3, ctypes.c_int64(4000)), 12000])
+    got = classify(scores, tiers, params, 4, 128, stream=side)
+    b.check()
+    assert torch.equal(got, good)

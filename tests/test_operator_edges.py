@@ -45,7 +45,7 @@ class FakeStreams:
     def __init__(self, monkeypatch):
         import contextlib
 
-        from tiered_kv_cache_split_gb300 import operators
+        from tiered_kv_cache_split_gb300 import operators    # its torch is everyone's
         self.now, self.made, self.recorded = "current", [], []
 
         @contextlib.contextmanager
@@ -82,3 +82,12 @@ def test_buffers_of_a_call_come_from_its_streams_memory(monkeypatch):
     assert f.made == ["side", "side"]
     assert f.recorded == ["current"]        # what is returned outlives its use on the caller's stream
     assert f.now == "current"
+
+
+def test_buffers_of_the_other_stateless_calls_too(monkeypatch):
+    from tiered_kv_cache_split_gb300 import cache
+    f = FakeStreams(monkeypatch)
+    cache._empty("side", 4, "dtype", "device")
+    assert f.made == ["side"] and f.recorded == ["current"]
+    cache._empty(None, 4, "dtype", "device")
+    assert f.made == ["side", "current"] and f.recorded == ["current"]

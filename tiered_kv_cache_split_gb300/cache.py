@@ -240,6 +240,22 @@ def inject_create_fault(countdown: int = 1):
 
 
 # ------------------------------------------------------------ stateless calls
+def _stream(stream, device):
+    return stream if stream is not None else torch.cuda.current_stream(device)
+
+
+def _empty(stream, shape, dtype, device):
+    """A buffer for a call on `stream`, from the memory of that stream: a block
+    of the current stream's may still be in use by work queued there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)                    # the caller may use and drop it there
+    return t
+
+
 def paged_attention(q, pool, page_table, slot_mask, page_counts, out=None, alpha_sum=None,
                     scratch=None, stream=None):
     """Split-K decode attention over one page pool (see tkv_paged_attention).
@@ -255,12 +271,12 @@ def paged_attention(q, pool, page_table, slot_mask, page_counts, out=None, alpha
     dt = L.DTYPE_BF16 if q.dtype == torch.bfloat16 else L.DTYPE_F32
     need = ctypes.c_size_t()
     L.check(lib.tkv_paged_attention_scratch_size(B, Hq, Hkv, d, max_pages, ctypes.byref(need)))
+    st = _stream(stream, q.device)
     if scratch is None:
-        scratch = torch.empty(need.value, dtype=torch.uint8, device=q.device)
+        scratch = _empty(stream, need.value, torch.uint8, q.device)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(stream, q.shape, q.dtype, q.device)
     counts = np.ascontiguousarray(page_counts, dtype=np.int32)
-    st = stream if stream is not None else torch.cuda.current_stream(q.device)
     L.check(lib.tkv_paged_attention(B, Hq, Hkv, d, dt, _ptr(q), _ptr(pool), _ptr(page_table),
                                     _ptr(slot_mask), counts.ctypes.data, max_pages, _ptr(out),
                                     _ptr(alpha_sum) if alpha_sum is not None else None,
@@ -274,10 +290,10 @@ def classify(scores, old_tier, params, n_sink, recent_window, stream=None):
     B, stride = scores.shape
     need = ctypes.c_size_t()
     L.check(lib.tkv_classify_scratch_size(B, stride, ctypes.byref(need)))
-    scratch = torch.empty(need.value, dtype=torch.uint8, device=scores.device)
-    new = torch.empty_like(old_tier)
+    st = _stream(stream, scores.device)
+    scratch = _empty(stream, need.value, torch.uint8, scores.device)
+    new = _empty(stream, old_tier.shape, old_tier.dtype, scores.device)
     prm = np.ascontiguousarray(params, dtype=np.int64)
-    st = stream if stream is not None else torch.cuda.current_stream(scores.device)
     L.check(lib.tkv_classify(B, _ptr(scores), _ptr(old_tier), _ptr(new), stride, prm.ctypes.data,
                              n_sink, recent_window, _ptr(scratch), scratch.numel(), st.cuda_stream))
     return new
@@ -288,9 +304,9 @@ def quantize_rows(x, scale_dtype="f32", stream=None):
     lib = L.load()
     rows, n = x.shape
     dt = L.DTYPE_BF16 if x.dtype == torch.bfloat16 else L.DTYPE_F32
-    codes = torch.empty((rows, n), dtype=torch.int8, device=x.device)
-    scales = torch.empty(rows, dtype=torch.float32 if scale_dtype == "f32" else torch.float16, device=x.device)
-    st = stream if stream is not None else torch.cuda.current_stream(x.device)
+    st = _stream(stream, x.device)
+    codes = _empty(stream, (rows, n), torch.int8, x.device)
+    scales = _empty(stream, rows, torch.float32 if scale_dtype == "f32" else torch.float16, x.device)
     L.check(lib.tkv_quantize_rows(_ptr(x), dt, rows, n, _ptr(codes), _ptr(scales),
                                   L.SCALE_F32 if scale_dtype == "f32" else L.SCALE_F16, st.cuda_stream))
     return codes, scales
