@@ -193,3 +193,20 @@ def test_the_other_stateless_calls_on_another_stream_beside_work_that_still_uses
     got = classify(scores, tiers, params, 4, 128, stream=side)
     b.check()
     assert torch.equal(got, good)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("k_len,key", [(970, 955), (970, 951), (970, 965), (1000, 990), (1025, 1010), (1025, 1022)])
+def test_an_infinite_value_at_the_end_of_a_short_piece_behind_cached_keys(dtype, k_len, key):
+    """20 rows behind cached keys, whose keys are split: the infinity reaches the
+    rows that see its key as what it is, whichever part of the last key block it
+    is in and whether or not a row sees the part behind it."""
+    from tiered_kv_cache_split_gb300 import prompt_attention
+    q, k, v = make_prompt(4, dtype, 6, 2, 64, [20], [k_len])
+    want, bound = prompt_reference(q, k, v, [20], [k_len])
+    v[key, 0, 3], v[key, 1, 9], v[key, 1, 10] = float("inf"), float("-inf"), float("nan")
+    got = prompt_attention(q, k, v, [20], [k_len]).float().cpu().numpy().astype(np.float64)
+    row = key - (k_len - 20)                    # the first row that sees it
+    assert (got[row:, :3, 3] == np.inf).all() and (got[row:, 3:, 9] == -np.inf).all() and np.isnan(got[row:, 3:, 10]).all()
+    got[row:, :3, 3], got[row:, 3:, 9:11] = want[row:, :3, 3], want[row:, 3:, 9:11]
+    assert_within(torch.from_numpy(got), want, bound)

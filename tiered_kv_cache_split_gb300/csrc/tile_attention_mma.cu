@@ -349,13 +349,15 @@ __device__ __forceinline__ Work unit_work(const TileParams& p, int unit) {
 }
 
 // Adds the non-finite V values of flagged keys (partly seen by the unit) to 16
-// columns of a row that sees keys below lim.
-__device__ __noinline__ void add_flagged(const TileParams& p, const uint32_t* flag, int lim_first, int lim, int64_t key0, int col,
-                                         uint32_t* o) {
+// columns of a row that sees keys below lim. half: of every block the tile takes
+// this half alone, -1: both. A pair's other tile adds those of the other half: a
+// row may see no key of this one, and its partial's weight is 0 then.
+__device__ __noinline__ void add_flagged(const TileParams& p, const uint32_t* flag, int lim_first, int lim, int half, int64_t key0,
+                                         int col, uint32_t* o) {
   for (int w = 0; w < 8; ++w)
     for (uint32_t left = flag[w]; left; left &= left - 1) {
       const int key = lim_first + w * 32 + __ffs(left) - 1;
-      if (key >= lim) continue;
+      if (key >= lim || (half >= 0 && key / kHalf % 2 != half)) continue;
       const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + (key0 + key) * p.v_stride + col;
       for (int e = 0; e < 16; ++e) {
         const float x = __bfloat162float(v[e]);
@@ -881,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 16; ++e) o[e] = 0;
             } else {
-              add_flagged(p, flag, tile_row_limit(p, sg, w.row0), lim, sg.key0, w.h * D + c, o);
+              add_flagged(p, flag, tile_row_limit(p, sg, w.row0), lim, w.pair ? t : -1, sg.key0, w.h * D + c, o);
             }
             tmem_st16(t_o + c, o);
           }
