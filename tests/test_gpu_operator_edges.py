@@ -210,3 +210,20 @@ def test_an_infinite_value_at_the_end_of_a_short_piece_behind_cached_keys(dtype,
     assert (got[row:, :3, 3] == np.inf).all() and (got[row:, 3:, 9] == -np.inf).all() and np.isnan(got[row:, 3:, 10]).all()
     got[row:, :3, 3], got[row:, 3:, 9:11] = want[row:, :3, 3], want[row:, 3:, 9:11]
     assert_within(torch.from_numpy(got), want, bound)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_alpha_of_a_row_whose_prefix_has_nothing_but_nan_keys(dtype):
+    """The row's weights are all NaN, as its output is; the other KV head's are not."""
+    from tiered_kv_cache_split_gb300 import shared_prefix_attention
+    q, pool, table, mask, counts, tb, mk = make_prefix(6, dtype, 8, 2, 64, 33, [40, 2], holes=False)
+    pool[table[0, :33].long(), 0, 0] = float("nan")
+    alpha = torch.zeros(2, 2, table.shape[1] * 16, device=DEV)
+    out = shared_prefix_attention(q, pool, table, mask, counts, 33, alpha_sum=alpha)
+    assert out[:, :4].isnan().all() and not out[:, 4:].isnan().any()
+    for b, n in enumerate(counts):
+        assert alpha[b, 0, 33 * 16:n * 16].isnan().all()
+    pool[table[0, :33].long(), 0, 0] = 0
+    want, bound, aw, ab = prefix_reference(q, pool, tb, mk, counts, 33)
+    assert_within(out[:, 4:], want[:, 4:], bound[:, 4:], "out")
+    assert_within(alpha[:, 1], aw[:, 1], ab[:, 1], "alpha")

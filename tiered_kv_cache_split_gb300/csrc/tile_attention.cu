@@ -322,12 +322,16 @@ __device__ __forceinline__ PartList part_list(const TileParams& p, int n, int h,
   return l;
 }
 
-// M (0 where there is no key) and Z of a row, by one warp in one pass.
+// M (0 where there is no key) and Z of a row, by one warp in one pass. A partial
+// whose logits are all NaN has m = -inf and Z NaN, which stays.
 __device__ __forceinline__ float2 parts_sum(const TileParams& p, const PartList& l, const float* part_z, int lane) {
   float m = -INFINITY, z = 0.f;
   for (int i = lane; i < l.n; i += 32) {
     const float mi = p.part_m[l.at(i)], zi = part_z[l.at(i)], next = fmaxf(m, mi);
-    if (next == -INFINITY) continue;
+    if (next == -INFINITY) {
+      z += zi;
+      continue;
+    }
     z = z * exp2f(m - next) + zi * exp2f(mi - next);
     m = next;
   }
