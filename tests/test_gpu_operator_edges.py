@@ -227,3 +227,19 @@ def test_alpha_of_a_row_whose_prefix_has_nothing_but_nan_keys(dtype):
     want, bound, aw, ab = prefix_reference(q, pool, tb, mk, counts, 33)
     assert_within(out[:, 4:], want[:, 4:], bound[:, 4:], "out")
     assert_within(alpha[:, 1], aw[:, 1], ab[:, 1], "alpha")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_empty_slots_get_no_alpha_from_a_row_of_nan(dtype):
+    """A later token in that slot would start from it."""
+    from tiered_kv_cache_split_gb300 import shared_prefix_attention
+    q, pool, table, mask, counts, tb, mk = make_prefix(7, dtype, 8, 2, 64, 5, [40, 3])
+    page = next(p for p in tb[0, 5:counts[0]] if mk[p])
+    pool[page, 0, 0, int(mk[page]).bit_length() - 1] = float("nan")
+    alpha = torch.full((2, 2, table.shape[1] * 16), 0.5, device=DEV)
+    shared_prefix_attention(q, pool, table, mask, counts, 5, alpha_sum=alpha)
+    ids = tb[0, 5:counts[0]]
+    live = torch.from_numpy(((mk[ids][:, None] >> np.arange(16)) & 1).astype(bool).reshape(-1)).to(DEV)
+    own = alpha[0, 0, 5 * 16:counts[0] * 16]
+    assert own[live].isnan().all() and (own[~live] == 0.5).all()
+    assert not alpha[0, 1].isnan().any() and not alpha[1].isnan().any()

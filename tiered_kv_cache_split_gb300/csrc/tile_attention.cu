@@ -345,6 +345,8 @@ __device__ __forceinline__ float2 parts_sum(const TileParams& p, const PartList&
   return make_float2(M, z);
 }
 __device__ __forceinline__ float parts_inv(float z) { return z > 0.f || z != z ? 1.f / z : 0.f; }
+// Weight of a logit; an empty slot (-inf) has none even where the row is NaN.
+__device__ __forceinline__ float alpha_weight(float x, float m, float inv) { return x == -INFINITY ? 0.f : exp2f(x - m) * inv; }
 
 template <typename T, int D, int kShare>
 __global__ void __launch_bounds__(kMergeThreads) tile_merge_kernel(const __grid_constant__ TileParams p, uint32_t rows, int row_ctas) {
@@ -446,10 +448,10 @@ __global__ void __launch_bounds__(kMergeThreads) tile_merge_kernel(const __grid_
 #pragma unroll 4
   for (int g = 0; g < G; ++g) {
     const float4 x = *reinterpret_cast<const float4*>(l + static_cast<int64_t>(g) * so.nkeys);
-    sum.x += exp2f(x.x - s_m[g]) * s_inv[g];
-    sum.y += exp2f(x.y - s_m[g]) * s_inv[g];
-    sum.z += exp2f(x.z - s_m[g]) * s_inv[g];
-    sum.w += exp2f(x.w - s_m[g]) * s_inv[g];
+    sum.x += alpha_weight(x.x, s_m[g], s_inv[g]);
+    sum.y += alpha_weight(x.y, s_m[g], s_inv[g]);
+    sum.z += alpha_weight(x.z, s_m[g], s_inv[g]);
+    sum.w += alpha_weight(x.w, s_m[g], s_inv[g]);
   }
   *at = sum;
 }
