@@ -243,3 +243,33 @@ def test_empty_slots_get_no_alpha_from_a_row_of_nan(dtype):
     own = alpha[0, 0, 5 * 16:counts[0] * 16]
     assert own[live].isnan().all() and (own[~live] == 0.5).all()
     assert not alpha[0, 1].isnan().any() and not alpha[1].isnan().any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [1e33, 1e36, 1e-33])
+def test_values_of_any_size_behind_logits_that_rise(dtype, scale):
+    """The first keys have logit 0 and later ones up to 13 (19 in base 2): results
+    that fit the type are found whatever the size of V."""
+    from tiered_kv_cache_split_gb300 import prompt_attention, shared_prefix_attention
+    d, n = 64, 700
+    q, k, v = make_prompt(5, dtype, 4, 2, d, [200], [n])
+    level = torch.zeros(n, device=DEV)
+    level[64:], level[300:] = 6.0, 13.0
+    q[:] = 0.01 * q
+    q[..., 0], k[..., 0] = 1.0, level[:, None].to(k.dtype) * d ** 0.5
+    v = (v.float() * scale).to(v.dtype)
+    out = prompt_attention(q, k, v, [200], [n])
+    want, bound = prompt_reference(q, k, v, [200], [n])
+    assert_within(out, want, bound, "prompt")
+    pages = 43
+    pool = torch.zeros(pages, 2, 2, 16, d, dtype=q.dtype, device=DEV)
+    for x, t in enumerate((k, v)):
+        pool[:, :, x] = t[:pages * 16].view(pages, 16, 2, d).transpose(1, 2)
+    table = torch.arange(pages, dtype=torch.int32, device=DEV).repeat(3, 1)
+    mask = torch.full((pages,), 0xFFFF, dtype=torch.int32, device=DEV)
+    alpha = torch.zeros(3, 2, pages * 16, device=DEV)
+    rows = q[:3].contiguous()
+    out = shared_prefix_attention(rows, pool, table, mask, [pages, 20, 35], 20, alpha_sum=alpha)
+    want, bound, aw, ab = prefix_reference(rows, pool, table.cpu().numpy(), mask.cpu().numpy(), [pages, 20, 35], 20)
+    assert_within(out, want, bound, "prefix")
+    assert_within(alpha, aw, ab, "alpha")

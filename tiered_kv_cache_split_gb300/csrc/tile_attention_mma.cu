@@ -37,11 +37,13 @@
 // the end of the one before.
 //
 // Running maximum: O is rescaled only when a row's maximum has risen by more
-// than kRise (base 2) over the one its weights refer to, or at the first key.
-// O and Z always refer to the same maximum, and a weight's relative error does
-// not depend on its size, so nothing is lost; weights stay below 2^20 and sums
-// of 2^18 of them below 2^38, far inside fp32. With a rise of 8 one half in six
-// was rescaled, at about 1500 cycles each (prompt of 8192, normal queries).
+// than kRise (base 2) over the one its weights refer to, or at the first key. A
+// weight is 2^(l - reference - kRise): 2^-kRise for the reference itself and at
+// most 1 for what may follow before a rescaling, so O stays below the sum of |V|
+// whatever the size of V. O and Z always refer to the same maximum, and a
+// weight's relative error does not depend on its size; those 2^-106 of the
+// largest or smaller count as 0. With a rise of 8 one half in six was rescaled,
+// at about 1500 cycles each (prompt of 8192, normal queries).
 //
 // The weights are rounded to bf16 (half a step 2^-8 each) because the MMA takes
 // P and V in one type. Z sums the rounded weights, in fp32: where few keys carry
@@ -77,7 +79,7 @@ constexpr int kProducer = 8, kIssuer = 9, kHelper = 11;  // warps; one issuer pe
 constexpr int kHalf = 64;                  // keys of one S
 constexpr int kBlockPages = kKeyBlock / kPage;
 constexpr int kBox = 128 * 128;            // a box: 128 rows of 64 bf16 columns, 128-byte swizzled
-constexpr float kRise = 20.f;              // of a row's maximum, in base 2, that rescales O
+constexpr float kRise = 20.f;              // of a row's maximum, in base 2, that rescales O: weights are 1 at most with it
 constexpr int kBatch = 4;                  // blocks whose page ids are fetched together
 constexpr int kUnits = 4;                  // units the producer may be ahead of the slowest warp
 constexpr int kBatches = 8;                // batches the id ring holds: the producer is at most kUnits units and a
@@ -824,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ref = next;
           }
-          const float base = ref == -INFINITY ? 0.f : ref * qs;
+          const float base = ref == -INFINITY ? 0.f : fmaf(ref, qs, kRise);
           const float2 qs2 = make_float2(qs, qs), base2 = make_float2(-base, -base);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           auto weights = [&](auto exact) {
@@ -911,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!direct && valid) {
-          p.part_m[part + r] = ref * qs;
+          p.part_m[part + r] = fmaf(ref, qs, kRise);  // what the weights refer to
           p.part_z[part + r] = z;
           if (kPaged && p.alpha) p.part_ze[part + r] = z_exact;
         }
