@@ -421,7 +421,8 @@ TKV_API tkv_status tkv_quantize_rows(const void* x, int32_t kv_dtype, int64_t ro
  * are all -inf counts as one without keys and gives 0.
  *   scratch  device, tkv_prompt_attention_scratch_size bytes (256-aligned;
  *            may be NULL when that is 0): partials of calls with too few rows
- *            to fill the device, whose keys are split
+ *            to fill the device, and of sequences of more than 2^18 keys,
+ *            whose keys are split
  *   status   device int32 or NULL: set to 1 (never cleared) if a bounded
  *            device wait gave up; the rows concerned are not valid then */
 TKV_API tkv_status tkv_prompt_attention_scratch_size(int32_t batch, const int32_t* q_lens, const int32_t* k_lens,

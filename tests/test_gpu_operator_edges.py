@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 import torch
 
-from operator_helpers import assert_within, prefix_reference, prompt_reference
+from operator_helpers import assert_within, attend, f64, prefix_reference, prompt_reference
 from test_gpu_pages import Book
 from test_gpu_prompt_attention import make as make_prompt
 from test_gpu_shared_prefix import make as make_prefix
@@ -273,3 +273,48 @@ def test_values_of_any_size_behind_logits_that_rise(dtype, scale):
     want, bound, aw, ab = prefix_reference(rows, pool, table.cpu().numpy(), mask.cpu().numpy(), [pages, 20, 35], 20)
     assert_within(out, want, bound, "prefix")
     assert_within(alpha, aw, ab, "alpha")
+
+
+@pytest.mark.parametrize("spread", [0.0, 1.0])
+def test_sums_over_two_million_keys(spread):
+    """Enough rows that none needs its keys split for speed. V is constant along
+    the keys, so that the result is V and every sum's error has the same sign."""
+    from tiered_kv_cache_split_gb300 import prompt_attention
+    n, hkv, d, rows = 1 << 21, 8, 64, 76 * 256
+    q = torch.randn(rows, hkv, d, dtype=torch.bfloat16, device=DEV)
+    k = torch.randn(n, hkv, d, dtype=torch.bfloat16, device=DEV) * spread
+    col = torch.linspace(0.5, 2.0, d, device=DEV).to(torch.bfloat16)
+    v = col.expand(n, hkv, d).contiguous()
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = prompt_attention(q, k, v, [rows], [n], status=status)
+    err = (out.float() / col.float() - 1).abs().max().item()
+    assert status.item() == 0
+    # Half a step of the output, 2^-8. At most 2^18 keys meet in one fp32 sum of the tensor core, at least 8
+    # to an addition, each off by a step of the sum so far at most, 2^-23 of it: 2^15 2^-23 = 2^-8.
+    # The sum of weights takes 64 to an addition, rounded to nearest: 2^12 2^-24. Joining eight parts: 2^-20.
+    assert err <= 2.0 ** -8 + 2.0 ** -8 + 2.0 ** -11
+
+
+@pytest.mark.parametrize("dtype,q_lens,k_lens", [("bf16", [300, 5100, 1], [300, (1 << 18) + 5100, 900]),
+                                                 ("f32", [2500, 40], [(1 << 18) + 700, 40])])
+def test_a_long_sequence_that_takes_turns_over_the_scratch(dtype, q_lens, k_lens):
+    """More rows than four waves of tiles over more than 2^18 keys, other
+    sequences beside it; rows at the ends of the turns and a few between them."""
+    from tiered_kv_cache_split_gb300 import prompt_attention
+    hq, d = 64, 64
+    x = make_prompt(9, dtype, hq, 1, d, q_lens, k_lens)
+    s = Guarded(size_of("tkv_prompt_attention", len(q_lens), ints(q_lens), ints(k_lens), hq, 1, d, code(dtype)))
+    out = torch.full_like(x[0], float("nan"))
+    prompt_attention(*x, q_lens, k_lens, scratch=s.mid, out=out)
+    assert s.intact() and not out.isnan().any()
+    turn = 4 * 152 * 256 // hq if dtype == "bf16" else 4 * 304 * 64 // hq
+    q0 = k0 = 0
+    for nq, nk in zip(q_lens, k_lens):
+        rows = sorted({i for i in (0, 1, turn - 1, turn, turn + 1, 2 * turn - 1, 2 * turn, nq // 2, nq - 1) if i < nq})
+        k, v = f64(x[1][k0:k0 + nk, 0]), f64(x[2][k0:k0 + nk, 0])
+        seen = np.arange(nk)[None] <= np.array(rows)[:, None] + nk - nq
+        for h in (0, 41):
+            at = torch.tensor(rows, device=DEV) + q0
+            want, bound, _ = attend(f64(x[0][at, h]), k, v, seen, DT[dtype])
+            assert_within(out[at, h], want, bound, f"{nq} of {nk}, head {h}")
+        q0, k0 = q0 + nq, k0 + nk

@@ -39,6 +39,34 @@ def test_alpha_has_room_for_its_sums_of_weights(lib, hq, hkv, d, counts, shared)
     assert 4 * own <= with_alpha - without < 4 * own + 256
 
 
+def prompt_scratch(lib, dt, q_lens, k_lens, hq, hkv, d):
+    n = ctypes.c_size_t()
+    a, b = ((ctypes.c_int32 * len(x))(*x) for x in (q_lens, k_lens))
+    L.check(lib.tkv_prompt_attention_scratch_size(len(q_lens), a, b, hq, hkv, d, dt, ctypes.byref(n)))
+    return n.value
+
+
+@pytest.mark.parametrize("dt", [L.DTYPE_BF16, L.DTYPE_F32])
+def test_key_ranges_of_a_prompt_end_after_two_to_the_eighteen_keys(lib, dt):
+    """So many rows that nothing is gained by splitting keys: partials appear only
+    where one sum would pass 2^18 of them, of four waves of tiles at a time."""
+    rows = 8 * (19456 if dt == L.DTYPE_BF16 else 9728)
+    for keys in (1 << 16, 1 << 18, (1 << 18) + 1, 1 << 20, 1 << 26):
+        ranges = -(-keys // (1 << 18))
+        got = prompt_scratch(lib, dt, [76 * 256], [keys], 8, 8, 64)
+        assert got == 0 if ranges == 1 else 0 <= got - ranges * rows * 4 * (64 + 2) <= 1024
+
+
+def test_long_prompts_take_turns_over_the_partials(lib):
+    """Whole documents: the scratch is that of four waves of tiles, not of all rows."""
+    for tokens in (1 << 19, 1 << 20, 1 << 22):
+        rows = 4 * 152 * 256 + 8 * 256                       # the waves, and what tiles leave empty
+        assert 0 < prompt_scratch(lib, L.DTYPE_BF16, [tokens], [tokens], 32, 8, 128) <= tokens // (1 << 18) * rows * 4 * (128 + 2) + 4096
+    # beside them, short prompts need nothing, and a chunk behind a long cache what it needs alone
+    alone = prompt_scratch(lib, L.DTYPE_BF16, [1 << 20], [1 << 20], 32, 8, 128)
+    assert prompt_scratch(lib, L.DTYPE_BF16, [9000, 1 << 20, 300], [9000, 1 << 20, 300], 32, 8, 128) == alone
+
+
 class FakeStreams:
     """torch.cuda as far as buffers for a call on another stream need it."""
 

@@ -23,7 +23,14 @@ constexpr int kFmaThreads = 256;
 constexpr int kFmaRows = 64;   // rows of a tile
 constexpr int kMmaRows = 128;  // rows of a bf16 tile, two to a group
 constexpr int kFmaKeys = 64;   // keys staged at once (half a key block)
-constexpr int kMaxPromptKeys = 1 << 26;  // a unit over all of them runs under a second, inside the waits' limit
+constexpr int kMaxPromptKeys = 1 << 26;
+// Longest key range of a unit (what a full page table holds). Its sums are
+// sequential in fp32, and the tensor core's accumulator loses up to a step
+// (2^-23 of it) at every addition of 8 or 16 keys into O: at most 2^-8 of a sum of
+// 2^18 keys that agree in sign, half a step of bf16. Longer rows are joined from
+// partials (one unit over 2^21 keys of a constant V gave results 2 % low; over 2^18
+// they round to V). A unit stays under 10 ms, too.
+constexpr int kMaxUnitKeys = 1 << 18;
 constexpr int kSms = 152;      // SMs of a GB300: what the plan fills (results do not depend on the device)
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
@@ -520,7 +527,8 @@ bool whole_is_direct(const TileParams& p, const TileSeg& s, const TileShape& ts)
 // the time is about the larger of what one place gets on average and of the
 // waves the longest kind of unit makes. Rows alone leave a decode step, or a
 // short piece of a prompt, with a few long units: then keys are split, and the
-// candidate with the shortest time wins. More than four waves are never split.
+// candidate with the shortest time wins. More than four waves are split only where a
+// unit would pass kMaxUnitKeys.
 int64_t blocks_per_unit(const TileParams& p, const SegWork* w, const TileShape& ts) {
   int64_t whole = 0, most = 1, blocks = 0;
   struct Live {
@@ -539,6 +547,8 @@ int64_t blocks_per_unit(const TileParams& p, const SegWork* w, const TileShape& 
     live[nlive++] = {w[i].groups * p.Hkv, unit_cost(ts, rows, false), unit_cost(ts, rows, true), static_cast<uint32_t>(w[i].most), leads(p, i),
                      whole_is_direct(p, p.seg[i], ts)};
   }
+  const int64_t uncut = most;
+  most = std::min<int64_t>(most, kMaxUnitKeys / kKeyBlock);
   if (whole >= 4 * ts.slots) return most;
   // candidates: keys whole, and around what each place gets if all is even
   const int64_t even = std::max<int64_t>(1, ceil_div(blocks, ts.slots));
@@ -550,7 +560,7 @@ int64_t blocks_per_unit(const TileParams& p, const SegWork* w, const TileShape& 
     const int64_t per = c < 0 ? most : std::max<int64_t>(1, even * kSixteenths[c] / 16);
     if (per > most || per == last) continue;
     last = per;
-    const bool split = p.paged || per < most;
+    const bool split = p.paged || per < uncut;
     double work = static_cast<double>(blocks), longest = 0, rest = 0;
     int64_t n_longest = 0, n_rest = 0;
     for (int i = 0; i < nlive; ++i) {
@@ -685,8 +695,13 @@ int check_heads(int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype) {
   return TKV_OK;
 }
 
+// A call runs in rounds, nearly always one. A sequence of more than kMaxUnitKeys
+// keys has its keys split however many rows there are, and partials of all its rows
+// at once could be larger than the cache (34 GB for 2^20 tokens of 32 heads, d 128,
+// and two ranges): each round takes as many of its tokens as make four waves of
+// units, and the rounds share the scratch.
 int plan_prompt(TileParams& p, TilePlan* plan, int32_t batch, const int32_t* q_lens, const int32_t* k_lens, int32_t Hq,
-                int32_t Hkv, int32_t D, int32_t dtype, int64_t* tokens, int64_t* keys) {
+                int32_t Hkv, int32_t D, int32_t dtype, int round, int* rounds, int64_t* tokens, int64_t* keys) {
   if (batch < 1 || batch > kMaxBatch) return report(TKV_ERR_INVALID_ARG, "batch must be 1 to %d", kMaxBatch);
   if (int st = check_heads(Hq, Hkv, D, dtype)) return st;
   if (!q_lens || !k_lens) return report(TKV_ERR_INVALID_ARG, "null pointer");
@@ -694,15 +709,24 @@ int plan_prompt(TileParams& p, TilePlan* plan, int32_t batch, const int32_t* q_l
   p.causal = 1;
   p.nseg = batch;
   p.qscale = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
+  const TileShape ts = tile_shape(dtype);
+  const int64_t round_tokens = ceil_div(int64_t(4) * ts.slots * ts.rows * ts.tpg, Hq);
   int64_t tq = 0, tk = 0;
+  *rounds = 1;
   for (int i = 0; i < batch; ++i) {
     if (q_lens[i] < 0 || k_lens[i] < q_lens[i]) return report(TKV_ERR_INVALID_ARG, "sequence %d: 0 <= q_len <= k_len", i);
     if (k_lens[i] > kMaxPromptKeys) return report(TKV_ERR_INVALID_ARG, "sequence %d: k_len above 2^26", i);
-    p.seg[i].tok0 = static_cast<int32_t>(tq);
-    p.seg[i].ntok = q_lens[i];
+    int64_t first = round > 0 ? q_lens[i] : 0, last = q_lens[i];  // tokens of this round
+    if (k_lens[i] > kMaxUnitKeys) {
+      first = std::min(last, round * round_tokens);
+      last = std::min(last, first + round_tokens);
+      *rounds = std::max(*rounds, static_cast<int>(ceil_div(q_lens[i], round_tokens)));
+    }
+    p.seg[i].tok0 = static_cast<int32_t>(tq + first);
+    p.seg[i].ntok = static_cast<int32_t>(last - first);
     p.seg[i].key0 = tk;
-    p.seg[i].nkeys = k_lens[i];
-    p.seg[i].see0 = k_lens[i] - q_lens[i];
+    p.seg[i].see0 = static_cast<int32_t>(k_lens[i] - q_lens[i] + first);
+    p.seg[i].nkeys = p.seg[i].see0 + p.seg[i].ntok;
     tq += q_lens[i];
     tk += k_lens[i];
     if (tq * p.G > INT32_MAX || tk > INT32_MAX - 2 * kKeyBlock)
@@ -839,9 +863,14 @@ tkv_status tkv_prompt_attention_scratch_size(int32_t batch, const int32_t* q_len
   TileParams p{};
   TilePlan plan;
   int64_t tq, tk;
-  if (int st = plan_prompt(p, &plan, batch, q_lens, k_lens, n_q_heads, n_kv_heads, head_dim, kv_dtype, &tq, &tk))
-    return tkv_status(st);
-  *scratch_bytes = tile_scratch(plan, head_dim).bytes;
+  int rounds = 1;
+  size_t most = 0;
+  for (int round = 0; round < rounds; ++round) {
+    if (int st = plan_prompt(p, &plan, batch, q_lens, k_lens, n_q_heads, n_kv_heads, head_dim, kv_dtype, round, &rounds, &tq, &tk))
+      return tkv_status(st);
+    most = std::max(most, tile_scratch(plan, head_dim).bytes);
+  }
+  *scratch_bytes = most;
   return TKV_OK;
 }
 
@@ -853,8 +882,11 @@ tkv_status tkv_prompt_attention(int32_t batch, const int32_t* q_lens, const int3
   TileParams p{};
   TilePlan plan;
   int64_t tq, tk;
-  if (int st = plan_prompt(p, &plan, batch, q_lens, k_lens, n_q_heads, n_kv_heads, head_dim, kv_dtype, &tq, &tk))
-    return tkv_status(st);
+  int rounds;
+  auto plan_round = [&](int round) {
+    return plan_prompt(p, &plan, batch, q_lens, k_lens, n_q_heads, n_kv_heads, head_dim, kv_dtype, round, &rounds, &tq, &tk);
+  };
+  if (int st = plan_round(0)) return tkv_status(st);
   if (tq == 0) return TKV_OK;
   if (!q || !k || !v || !out) return tkv_status(report(TKV_ERR_INVALID_ARG, "null pointer"));
   const int64_t unit = kv_dtype == TKV_DTYPE_BF16 ? 8 : 4;  // elements of 16 bytes
@@ -864,16 +896,27 @@ tkv_status tkv_prompt_attention(int32_t batch, const int32_t* q_lens, const int3
   if (q_stride < qrow || out_stride < qrow || k_stride < krow || v_stride < krow || q_stride % unit || out_stride % unit ||
       k_stride % unit || v_stride % unit || (q_stride | out_stride | k_stride | v_stride) >> 36)
     return tkv_status(report(TKV_ERR_INVALID_ARG, "token strides must hold a token and be multiples of 16 bytes"));
-  if (int st = bind_scratch(p, plan, head_dim, scratch, scratch_bytes)) return tkv_status(st);
-  p.q = q; p.q_stride = q_stride;
-  p.k = k; p.k_stride = k_stride;
-  p.v = v; p.v_stride = v_stride;
-  p.out = out; p.out_stride = out_stride;
-  p.out_sectors = !misaligned(out, 32) && out_stride % (2 * unit) == 0;
-  p.status = status;
-  set_waits(p, kv_dtype);
-  const cudaError_t e = launch_dtype(p, kv_dtype, head_dim, tk, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return tkv_status(report(TKV_ERR_CUDA, "prompt attention launch failed: %s", cudaGetErrorString(e)));
+  // the last round is planned first: none is launched unless the scratch is enough for all
+  for (int round = rounds - 1; round >= 0; --round) {
+    if (rounds > 1)
+      if (int st = plan_round(round)) return tkv_status(st);
+    if (int st = bind_scratch(p, plan, head_dim, scratch, scratch_bytes)) return tkv_status(st);
+  }
+  for (int round = 0; round < rounds; ++round) {
+    if (round > 0) {
+      if (int st = plan_round(round)) return tkv_status(st);
+      if (int st = bind_scratch(p, plan, head_dim, scratch, scratch_bytes)) return tkv_status(st);
+    }
+    p.q = q; p.q_stride = q_stride;
+    p.k = k; p.k_stride = k_stride;
+    p.v = v; p.v_stride = v_stride;
+    p.out = out; p.out_stride = out_stride;
+    p.out_sectors = !misaligned(out, 32) && out_stride % (2 * unit) == 0;
+    p.status = status;
+    set_waits(p, kv_dtype);
+    const cudaError_t e = launch_dtype(p, kv_dtype, head_dim, tk, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return tkv_status(report(TKV_ERR_CUDA, "prompt attention launch failed: %s", cudaGetErrorString(e)));
+  }
   return TKV_OK;
 }
 
