@@ -399,8 +399,8 @@ TKV_API tkv_status tkv_quantize_rows(const void* x, int32_t kv_dtype, int64_t ro
  * Stateless operators for one prompt that several chains continue: attend the
  * prompt, fork its pages, decode over the shared pages, compact what eviction
  * (Methodology 1, T3) left, free what is done. All are enqueued on `stream`,
- * touch only the buffers they are given and may be captured into a graph;
- * calls that overlap on the GPU need scratch buffers of their own. Pool, page
+ * touch only the buffers they are given (and a word of the library's that says
+ * a device wait gave up) and may be captured into a graph; calls that overlap on the GPU need scratch buffers of their own. Pool, page
  * table and slot masks are those of tkv_paged_attention. */
 
 /* Causal attention over packed prompts: token i of a sequence with k_len keys
@@ -423,8 +423,12 @@ TKV_API tkv_status tkv_quantize_rows(const void* x, int32_t kv_dtype, int64_t ro
  *            may be NULL when that is 0): partials of calls with too few rows
  *            to fill the device, and of sequences of more than 2^18 keys,
  *            whose keys are split
- *   status   device int32 or NULL: set to 1 (never cleared) if a bounded
- *            device wait gave up; the rows concerned are not valid then */
+ *   status   device int32: set to 1 (never cleared) if a bounded device wait
+ *            gave up; the rows concerned are not valid then. NULL: the library
+ *            keeps that word, and the next call of this operator or of
+ *            tkv_shared_prefix_attention on the device that begins after it
+ *            was set returns TKV_ERR_TIMEOUT, once, and enqueues nothing
+ *            (tkv_attention_synchronize asks for it) */
 TKV_API tkv_status tkv_prompt_attention_scratch_size(int32_t batch, const int32_t* q_lens, const int32_t* k_lens,
                                                      int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
                                                      int32_t kv_dtype, size_t* scratch_bytes);
@@ -458,6 +462,11 @@ TKV_API tkv_status tkv_shared_prefix_attention(int32_t batch, int32_t n_q_heads,
                                                const int32_t* page_counts, int32_t max_pages, int32_t shared_pages,
                                                void* out, float* alpha_sum, void* scratch, size_t scratch_bytes,
                                                int32_t* status, tkv_stream stream);
+
+/* Waits for the work enqueued on `stream` so far and returns TKV_ERR_TIMEOUT,
+ * once, if a wait of either operator gave up on the current device in a call
+ * that had no status word of its own. */
+TKV_API tkv_status tkv_attention_synchronize(tkv_stream stream);
 
 /* Test hook for the bounded waits of the two operators above (the paper has no
  * counterpart): in this thread's next BF16 call of either, one CTA withholds

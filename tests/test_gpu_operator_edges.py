@@ -318,3 +318,76 @@ def test_a_long_sequence_that_takes_turns_over_the_scratch(dtype, q_lens, k_lens
             want, bound, _ = attend(f64(x[0][at, h]), k, v, seen, DT[dtype])
             assert_within(out[at, h], want, bound, f"{nq} of {nk}, head {h}")
         q0, k0 = q0 + nq, k0 + nk
+
+
+def stalled(call, *args, **kw):
+    from tiered_kv_cache_split_gb300 import _lib as L
+    L.check(L.load().tkv_test_stall_next_tiles(5_000_000))
+    return call(*args, **kw)
+
+
+def test_a_wait_that_runs_out_is_raised_later_where_the_caller_gave_no_status():
+    from tiered_kv_cache_split_gb300 import TkvError, _lib as L, attention_synchronize, prompt_attention, shared_prefix_attention
+    x = make_prompt(6, "bf16", 8, 2, 128, [400], [400])
+    y = make_prefix(9, "bf16", 8, 2, 64, 40, [3, 9])[:5]
+    good_x, good_y = prompt_attention(*x, [400]), shared_prefix_attention(*y, 40)
+    attention_synchronize()
+    for again, same, args, good in ((prompt_attention, prompt_attention, (*x, [400]), good_x),
+                                    (shared_prefix_attention, prompt_attention, (*x, [400]), good_x),
+                                    (prompt_attention, shared_prefix_attention, (*y, 40), good_y)):
+        stalled(same, *args)
+        torch.cuda.synchronize()
+        with pytest.raises(TkvError, match="gave up") as err:
+            again(*((*x, [400]) if again is prompt_attention else (*y, 40)))
+        assert err.value.status == L.ERR_TIMEOUT
+        assert torch.equal(same(*args), good)   # raised once
+        stalled(same, *args)
+        with pytest.raises(TkvError, match="gave up"):
+            attention_synchronize()
+        attention_synchronize()
+        assert torch.equal(same(*args), good)
+    # a caller's word keeps the library's clean
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    stalled(prompt_attention, *x, [400], status=status)
+    attention_synchronize()
+    assert status.item() == 1
+    # the wait of a captured call
+    stalled_graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(stalled_graph):
+        stalled(prompt_attention, *x, [400])
+    attention_synchronize()
+    stalled_graph.replay()
+    with pytest.raises(TkvError, match="gave up"):
+        attention_synchronize()
+    # a call on another stream
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    stalled(shared_prefix_attention, *y, 40, stream=side)
+    with pytest.raises(TkvError, match="gave up"):
+        attention_synchronize(side)
+    assert torch.equal(prompt_attention(*x, [400]), good_x)
+
+
+FIRST_CALL = """
+import torch, sys
+from tiered_kv_cache_split_gb300 import attention_synchronize, prompt_attention
+gen = torch.Generator().manual_seed(0)
+q, k, v = (torch.randn(300, h, 64, generator=gen).to(torch.bfloat16).cuda() for h in (4, 2, 2))
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = prompt_attention(q, k, v, [300])
+graph.replay()
+attention_synchronize()
+assert torch.equal(out, prompt_attention(q, k, v, [300]))
+print("fine")
+"""
+
+
+def test_the_first_call_of_a_process_may_be_a_captured_one():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stdout + r.stderr

@@ -8,8 +8,9 @@ this package only marshals arguments.
 """
 from ._lib import TkvError, load
 from .cache import TieredKVCache, classify, paged_attention, quantize_rows
-from .operators import (compact_sequences, fork_sequences, free_sequences, prompt_attention,
-                        shared_prefix_attention)
+from .operators import (attention_synchronize, compact_sequences, fork_sequences, free_sequences,
+                        prompt_attention, shared_prefix_attention)
 
 __all__ = ["TieredKVCache", "TkvError", "load", "paged_attention", "classify", "quantize_rows",
-           "prompt_attention", "shared_prefix_attention", "fork_sequences", "free_sequences", "compact_sequences"]
+           "prompt_attention", "shared_prefix_attention", "fork_sequences", "free_sequences", "compact_sequences",
+           "attention_synchronize"]

@@ -93,6 +93,7 @@ _SIGS = {
     "tkv_prompt_attention_scratch_size": [c_i32, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, ctypes.POINTER(c_sz)],
     "tkv_prompt_attention": [c_i32, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64,
                              c_vp, c_i64, c_vp, c_sz, c_vp, c_vp],
+    "tkv_attention_synchronize": [c_vp],
     "tkv_test_stall_next_tiles": [ctypes.c_uint64],
     "tkv_shared_prefix_attention_scratch_size": [c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_i32, c_i32, c_i32,
                                                  ctypes.POINTER(c_sz)],

@@ -12,6 +12,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "tile_attention.h"
 #include "tkv.h"
@@ -832,6 +833,53 @@ void set_waits(TileParams& p, int32_t dtype) {
   }
 }
 
+// Words that waits raise in calls without a status word of their own: one per
+// device, in mapped host memory, so that a later call finds one raised without
+// waiting for the device. Made by the first call, which may be captured.
+constexpr int kWordDevices = 64;
+std::mutex g_words_mu;
+int32_t* g_words = nullptr;
+
+int device_word(int32_t** word) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev >= kWordDevices) return report(TKV_ERR_INVALID_ARG, "device index above %d", kWordDevices - 1);
+  std::lock_guard<std::mutex> lock(g_words_mu);
+  if (e == cudaSuccess && !g_words) {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // of this thread, for the allocation
+    void* made = nullptr;
+    e = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e == cudaSuccess) {
+      e = cudaHostAlloc(&made, kWordDevices * sizeof(int32_t), cudaHostAllocPortable | cudaHostAllocMapped);
+      const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+      if (e == cudaSuccess) e = back;
+    }
+    if (e == cudaSuccess) {
+      g_words = static_cast<int32_t*>(made);
+      std::fill(g_words, g_words + kWordDevices, 0);
+    }
+  }
+  if (e != cudaSuccess) return report(TKV_ERR_CUDA, "status word of the device: %s", cudaGetErrorString(e));
+  *word = g_words + dev;
+  return TKV_OK;
+}
+
+// TKV_ERR_TIMEOUT, once, if an earlier call's wait on the current device raised its word.
+int raised(int32_t* word) {
+  if (__atomic_load_n(word, __ATOMIC_RELAXED) == 0) return TKV_OK;
+  __atomic_store_n(word, 0, __ATOMIC_RELAXED);
+  return report(TKV_ERR_TIMEOUT, "a bounded device wait of an earlier attention call gave up: rows of its output are not valid");
+}
+
+// The word for a call's waits: the caller's, or the device's.
+int bind_status(TileParams& p, int32_t* status) {
+  int32_t* word;
+  if (int st = device_word(&word)) return st;
+  if (int st = raised(word)) return st;
+  p.status = status ? status : word;
+  return TKV_OK;
+}
+
 bool misaligned(const void* ptr, size_t to) { return reinterpret_cast<uintptr_t>(ptr) % to != 0; }
 
 int bind_scratch(TileParams& p, const TilePlan& plan, int D, void* scratch, size_t bytes) {
@@ -902,6 +950,7 @@ tkv_status tkv_prompt_attention(int32_t batch, const int32_t* q_lens, const int3
       if (int st = plan_round(round)) return tkv_status(st);
     if (int st = bind_scratch(p, plan, head_dim, scratch, scratch_bytes)) return tkv_status(st);
   }
+  if (int st = bind_status(p, status)) return tkv_status(st);
   for (int round = 0; round < rounds; ++round) {
     if (round > 0) {
       if (int st = plan_round(round)) return tkv_status(st);
@@ -912,12 +961,19 @@ tkv_status tkv_prompt_attention(int32_t batch, const int32_t* q_lens, const int3
     p.v = v; p.v_stride = v_stride;
     p.out = out; p.out_stride = out_stride;
     p.out_sectors = !misaligned(out, 32) && out_stride % (2 * unit) == 0;
-    p.status = status;
     set_waits(p, kv_dtype);
     const cudaError_t e = launch_dtype(p, kv_dtype, head_dim, tk, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return tkv_status(report(TKV_ERR_CUDA, "prompt attention launch failed: %s", cudaGetErrorString(e)));
   }
   return TKV_OK;
+}
+
+tkv_status tkv_attention_synchronize(tkv_stream stream) {
+  const cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return tkv_status(report(TKV_ERR_CUDA, "cudaStreamSynchronize failed: %s", cudaGetErrorString(e)));
+  int32_t* word;
+  if (int st = device_word(&word)) return tkv_status(st);
+  return tkv_status(raised(word));
 }
 
 tkv_status tkv_test_stall_next_tiles(uint64_t wait_limit_ns) {
@@ -967,7 +1023,7 @@ tkv_status tkv_shared_prefix_attention(int32_t batch, int32_t n_q_heads, int32_t
   p.alpha = alpha_sum;
   p.alpha_stride_h = static_cast<int64_t>(max_pages) * kPage;
   p.alpha_first = static_cast<int64_t>(shared_pages) * kPage;
-  p.status = status;
+  if (int st = bind_status(p, status)) return tkv_status(st);
   set_waits(p, kv_dtype);
   const cudaError_t e = launch_dtype(p, kv_dtype, head_dim, 0, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess)

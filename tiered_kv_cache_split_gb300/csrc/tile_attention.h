@@ -62,7 +62,7 @@ struct TileParams {
   float* alpha;                // [B][Hkv][alpha slots], or null
   int64_t alpha_stride_h;
   int64_t alpha_first;         // slots ahead of a sequence's own pages
-  int32_t* status;             // set to 1 by a wait that gave up, or null
+  int32_t* status;             // set to 1 by a wait that gave up: the caller's word, or the device's in host memory
   unsigned long long wait_limit_ns;
   int32_t stall;               // test hook: the CTA of unit 0 withholds its first copy
   float qscale;                // log2(e) / sqrt(D): logits are kept in base 2

@@ -130,6 +130,9 @@ def prompt_attention(q, k, v, q_lens, k_lens=None, out=None, scratch=None, statu
     per sequence (k_lens defaults to q_lens; the keys ahead of a sequence's
     queries are an already cached part). The tokens of q, k, v and out may be
     strided, as views of a fused projection are.
+    status: int32 [1] that becomes 1 if a bounded device wait gave up (rows of
+    out are not valid then); without one, the next attention call on the device
+    raises TkvError, and so does attention_synchronize.
     """
     lib = L.load()
     tq, hq, d, sq = _tokens(q, "q")
@@ -179,7 +182,7 @@ def shared_prefix_attention(q, pool, page_table, slot_mask, page_counts, shared_
     q [B, Hq, d]; pool [pages, Hkv, 2, 16, d]; page_table int32 [B, max_pages];
     slot_mask int32/uint32 [pages]; page_counts host ints [B], the prefix among
     them; alpha_sum float32 [B, Hkv, max_pages * 16] or None (accumulated into
-    behind the prefix).
+    behind the prefix); status as for prompt_attention.
     """
     lib = L.load()
     dt = _DTYPES.get(q.dtype)
@@ -218,6 +221,16 @@ def shared_prefix_attention(q, pool, page_table, slot_mask, page_counts, shared_
         if st:
             L.check(st)
     return out
+
+
+def attention_synchronize(stream=None):
+    """Waits for a stream (the current one); TkvError if a wait of
+    prompt_attention or shared_prefix_attention gave up on its device in a call
+    without a status of its own (see tkv_attention_synchronize)."""
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    with torch.cuda.device(stream.device_index):
+        L.check(L.load().tkv_attention_synchronize(stream.cuda_stream))
 
 
 def _pool(pool):
