@@ -119,3 +119,28 @@ def test_buffers_of_the_other_stateless_calls_too(monkeypatch):
     assert f.made == ["side"] and f.recorded == ["current"]
     cache._empty(None, 4, "dtype", "device")
     assert f.made == ["side", "current"] and f.recorded == ["current"]
+
+
+def test_tensors_that_ask_for_a_gradient_are_refused():
+    """The operators have no backward pass: an output without history would end
+    a gradient's way without a word."""
+    import torch
+
+    import tiered_kv_cache_split_gb300 as t
+    x = [torch.zeros(6, h, 64) for h in (4, 2, 2)]
+    for i in range(3):
+        y = list(x)
+        y[i] = x[i].clone().requires_grad_()
+        with pytest.raises(ValueError, match="q, k, v: the operator has no backward pass"):
+            t.prompt_attention(*y, [6])
+        for again in (y[i] * 2, y[i].detach()):
+            y[i] = again
+            with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):   # as far as a CPU tensor gets
+                t.prompt_attention(*y, [6])
+    q, pool = torch.zeros(3, 4, 64), torch.zeros(9, 2, 2, 16, 64)
+    table, mask = torch.zeros(3, 4, dtype=torch.int32), torch.zeros(9, dtype=torch.int32)
+    for a, b in ((q.clone().requires_grad_(), pool), (q, pool.clone().requires_grad_())):
+        with pytest.raises(ValueError, match="q, pool: the operator has no backward pass"):
+            t.shared_prefix_attention(a, b, table, mask, [1] * 3, 0)
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+            t.shared_prefix_attention(a, b, table, mask, [1] * 3, 0)

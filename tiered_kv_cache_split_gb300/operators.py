@@ -6,7 +6,8 @@ tensor of a call lies on one CUDA device, which need not be the current one;
 a call on a stream other than the current one takes the buffers it makes from
 that stream's memory (work on the current stream waits for that stream before
 it uses them). ValueError names an argument of the wrong type, shape, layout
-or device; the library's own checks raise TkvError.
+or device, or one that asks for a gradient; the library's own checks raise
+TkvError.
 """
 from __future__ import annotations
 
@@ -69,6 +70,12 @@ def _tokens(t, name, like=None):
     if (s2 != 1 and d != 1) or (s1 != d and h != 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     return n, h, d, (s0 if n > 1 else h * d)
+
+
+def _no_gradient(names, *tensors):
+    for t in tensors:
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{names}: the operator has no backward pass; call it under torch.no_grad() or detach them")
 
 
 class _On:
@@ -138,6 +145,7 @@ def prompt_attention(q, k, v, q_lens, k_lens=None, out=None, scratch=None, statu
     tq, hq, d, sq = _tokens(q, "q")
     tk, hkv, dk, sk = _tokens(k, "k", q)
     tv, hv, dv, sv = _tokens(v, "v", q)
+    _no_gradient("q, k, v", q, k, v)
     dt = _DTYPES.get(q.dtype)
     if dt is None:
         raise ValueError("q: float32 or bfloat16")
@@ -190,6 +198,7 @@ def shared_prefix_attention(q, pool, page_table, slot_mask, page_counts, shared_
         raise ValueError("q: float32 or bfloat16 [B, Hq, d]")
     if pool.dim() != 5:
         raise ValueError("pool: must be [pages, Hkv, 2, 16, d]")
+    _no_gradient("q, pool", q, pool)
     if page_table.dim() != 2 or page_table.shape[0] != q.shape[0]:
         raise ValueError("page_table: must be [B, max_pages]")
     dev, dtypes = q.get_device(), (q.dtype,)
