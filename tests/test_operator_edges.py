@@ -144,3 +144,48 @@ def test_tensors_that_ask_for_a_gradient_are_refused():
             t.shared_prefix_attention(a, b, table, mask, [1] * 3, 0)
         with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
             t.shared_prefix_attention(a, b, table, mask, [1] * 3, 0)
+
+
+def test_arguments_of_another_type_are_named():
+    import numpy as np
+    import torch
+
+    import tiered_kv_cache_split_gb300 as t
+    q, pool = torch.zeros(3, 4, 64), torch.zeros(9, 2, 2, 16, 64)
+    table, mask, refs = torch.zeros(3, 4, dtype=torch.int32), torch.zeros(9, dtype=torch.int32), torch.zeros(9, dtype=torch.int32)
+    good = dict(q=q, pool=pool, page_table=table, slot_mask=mask, page_counts=[1] * 3, shared_pages=0)
+    for name, bad in (("q", None), ("q", q.numpy()), ("pool", None), ("pool", [1]), ("page_table", table.numpy()), ("page_table", None),
+                      ("slot_mask", None), ("page_counts", None), ("page_counts", [1.0] * 3), ("page_counts", torch.ones(3)),
+                      ("page_counts", [2 ** 31] * 3), ("shared_pages", 1.5), ("shared_pages", None), ("shared_pages", "1")):
+        with pytest.raises(ValueError, match=name):
+            t.shared_prefix_attention(**{**good, name: bad})
+    for counts in (np.array([1, 1, 1]), torch.ones(3, dtype=torch.int64), (1, 1, 1)):      # these are host ints: the device is next
+        with pytest.raises(ValueError, match="CUDA"):
+            t.shared_prefix_attention(**{**good, "page_counts": counts, "shared_pages": np.int64(0)})
+    k = torch.zeros(6, 2, 64)
+    for name, bad in (("q", None), ("k", k.numpy()), ("v", None), ("q_lens", None), ("q_lens", 6), ("q_lens", [6.0]), ("k_lens", "6")):
+        with pytest.raises(ValueError, match=name):
+            t.prompt_attention(**{**dict(q=torch.zeros(6, 4, 64), k=k, v=k, q_lens=[6], k_lens=[6]), name: bad})
+    book = dict(page_table=table, page_counts=[1] * 3, page_refs=refs, slot_mask=mask)
+    for name, bad in (("page_table", None), ("page_table", table.numpy()), ("page_refs", None), ("slot_mask", mask.numpy()), ("seqs", None),
+                      ("seqs", [0.5])):
+        with pytest.raises(ValueError, match=name):
+            t.free_sequences(**{**book, "seqs": [0], name: bad})
+        if name != "seqs":
+            for call, more in ((t.fork_sequences, dict(parents=[0], children=[1])), (t.compact_sequences, {})):
+                if name != "page_refs":
+                    with pytest.raises(ValueError, match=name):
+                        call(**{**book, "pool": pool, **more, name: bad})
+    for call, more in ((t.fork_sequences, dict(parents=[0], children=[1])), (t.compact_sequences, {})):
+        for bad in (None, pool.numpy(), pool[0], pool[..., ::2]):
+            with pytest.raises(ValueError, match="pool"):
+                call(**{**book, "pool": bad, **more})
+
+
+def test_a_stream_of_another_type_is_named(monkeypatch):
+    from tiered_kv_cache_split_gb300 import operators
+    monkeypatch.setattr(operators, "_current_device", lambda: 0)
+    monkeypatch.setattr(operators, "_raw_stream", lambda i: 0)
+    for bad in (0, "side", object()):
+        with pytest.raises(ValueError, match="stream"):
+            operators._On(0, bad)

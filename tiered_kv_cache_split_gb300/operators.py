@@ -92,6 +92,8 @@ class _On:
         self.given = None
         self.raw = _raw_stream(device)
         if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                raise ValueError("stream: a torch.cuda.Stream")
             if stream.device_index != device:
                 raise ValueError("stream: of another device")
             if stream.cuda_stream != self.raw:
@@ -193,13 +195,13 @@ def shared_prefix_attention(q, pool, page_table, slot_mask, page_counts, shared_
     behind the prefix); status as for prompt_attention.
     """
     lib = L.load()
-    dt = _DTYPES.get(q.dtype)
+    dt = _DTYPES.get(q.dtype) if isinstance(q, torch.Tensor) else None
     if dt is None or q.dim() != 3:
         raise ValueError("q: float32 or bfloat16 [B, Hq, d]")
-    if pool.dim() != 5:
+    if not isinstance(pool, torch.Tensor) or pool.dim() != 5:
         raise ValueError("pool: must be [pages, Hkv, 2, 16, d]")
     _no_gradient("q, pool", q, pool)
-    if page_table.dim() != 2 or page_table.shape[0] != q.shape[0]:
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.shape[0] != q.shape[0]:
         raise ValueError("page_table: must be [B, max_pages]")
     dev, dtypes = q.get_device(), (q.dtype,)
     batch, hq, d = q.shape
@@ -211,7 +213,7 @@ def shared_prefix_attention(q, pool, page_table, slot_mask, page_counts, shared_
     pm = _dense(slot_mask, "slot_mask", _MASK, dev, (pages,))
     pa = None if alpha_sum is None else _dense(alpha_sum, "alpha_sum", (torch.float32,), dev, (batch, hkv, max_pages * 16))
     counts = _ints(page_counts, batch, "page_counts")
-    shared_pages = int(shared_pages)
+    shared_pages = _ints([shared_pages], 1, "shared_pages")[0]
     with _On(dev, stream) as on:
         if out is None:
             out = on.empty((batch, hq, d), q.dtype)
@@ -305,6 +307,8 @@ def free_sequences(page_table, page_counts, page_refs, slot_mask, seqs, stream=N
     -1 if a row listed a page that was not held.
     """
     lib = L.load()
+    if not isinstance(page_table, torch.Tensor):
+        raise ValueError("page_table: must be [rows, max_pages]")
     dev = page_table.get_device()
     if not isinstance(page_refs, torch.Tensor) or page_refs.dim() != 1:
         raise ValueError("page_refs: must be [pages]")
