@@ -517,7 +517,10 @@ TKV_API tkv_status tkv_free_sequences(int32_t* page_table, int32_t rows, int32_t
  * freed (mask 0, positions -1, count 0) and leave the row, whose freed entries
  * become -1. Pages listed by other rows too stay as they are. page_refs NULL:
  * no page is shared. new_counts device int32 [rows]: entries left, or -1 for a
- * row that lists a page that is not held (that row is not changed). */
+ * row that lists a page that is not held (that row is not changed).
+ * alpha_sum of the attention calls goes by table slot and does not move with the
+ * tokens: add a row's sums to its tokens' scores, by positions, before slots are
+ * emptied and the row is compacted, and let the next call start from zeros. */
 TKV_API tkv_status tkv_compact_sequences_scratch_size(int32_t rows, int32_t max_pages, const int32_t* page_counts,
                                                       size_t* scratch_bytes);
 TKV_API tkv_status tkv_compact_sequences(void* pool, int32_t n_layers, int64_t pool_pages, int32_t n_kv_heads,

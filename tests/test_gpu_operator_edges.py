@@ -391,3 +391,44 @@ def test_the_first_call_of_a_process_may_be_a_captured_one():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "fine" in r.stdout, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_scores_by_token_over_a_compaction(dtype):
+    """alpha goes by slot and stays behind when tokens move: added to the tokens'
+    scores by positions ahead of the eviction, and started again from zeros, the
+    sums are those of the tokens."""
+    from tiered_kv_cache_split_gb300 import compact_sequences, shared_prefix_attention
+    hq, hkv, d, tokens = 8, 2, 64, 16 * 30
+    b = Book(11, 1, 120, hkv, d, dtype, 3, 32)
+    for r, n in enumerate((30, 3, 17)):
+        b.fill(r, n, drop=0.1, last=5)
+    b.upload()
+    gen = torch.Generator().manual_seed(2)
+    scores = torch.zeros(3, tokens, device=DEV)
+    want, tolerance = np.zeros((3, tokens)), np.zeros((3, tokens))
+    for step in range(3):
+        q = torch.randn(3, hq, d, generator=gen).to(DT[dtype]).to(DEV)
+        alpha = torch.zeros(3, hkv, 32 * 16, device=DEV)
+        shared_prefix_attention(q, b.dpool[0], b.dtable, b.dmask, b.counts, 0, alpha_sum=alpha)
+        at = b.dpos[b.dtable.clamp(min=0).long()].clamp(min=0).flatten(1).long()
+        scores.scatter_add_(1, at, alpha.sum(1))
+        _, _, aw, ab = prefix_reference(q, b.dpool[0], b.table, b.mask, b.counts)
+        for r, n in enumerate(b.counts):
+            for j in range(n):
+                for s in range(16):
+                    if (b.mask[b.table[r, j]] >> s) & 1:
+                        t = b.pos[b.table[r, j], s]
+                        want[r, t] += aw[r, :, 16 * j + s].sum()
+                        tolerance[r, t] += ab[r, :, 16 * j + s].sum()
+        for p in range(120):                                 # half of the tokens leave, the rest moves up
+            for s in range(16):
+                if (b.mask[p] >> s) & 1 and b.rng.random() < 0.5:
+                    b.mask[p] &= ~(1 << s)
+                    b.pos[p, s] = -1
+        b.upload()
+        new = compact_sequences(b.dpool, b.dtable, list(b.counts), b.drefs, b.dmask, positions=b.dpos)
+        assert new.tolist() == b.compact()
+        b.same()
+    # the sum over heads and steps is rounded a few times more, in fp32
+    assert_within(scores, want, tolerance + 8 * 2.0 ** -24 * want + 1e-30, "scores")

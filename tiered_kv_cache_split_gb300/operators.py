@@ -330,7 +330,9 @@ def compact_sequences(pool, page_table, page_counts, page_refs, slot_mask, posit
     """Moves the tokens of every row of the page table into its first pages and
     frees the emptied ones (see tkv_compact_sequences). page_refs None: no page
     is shared. Returns the new page counts, device int32 [rows] (-1: that row
-    lists a page that is not held and was not changed).
+    lists a page that is not held and was not changed). alpha_sum of earlier
+    attention calls does not move with the tokens: add it to their scores, by
+    positions, before slots are emptied, and start the next one from zeros.
     """
     lib = L.load()
     pp, layers, pages, hkv, d, dt = _pool(pool)
