@@ -481,8 +481,12 @@ TKV_API tkv_status tkv_test_stall_next_tiles(uint64_t wait_limit_ns);
  *   page_counts HOST int32 [rows]: entries in use per row
  *   page_refs   device int32 [pool_pages]: rows that list a page, 0 = free
  *   slot_mask   device uint32 [pool_pages], positions device int32
- *               [pool_pages][16] or NULL (the position each slot holds)
- * and up to 64 sequences per call. The paper fixes no allocator; a new page is
+ *               [pool_pages][16] or NULL: the position a slot holds where its
+ *               mask bit is set; elsewhere the entry means nothing (a fork
+ *               copies it, compaction writes -1 where it empties a slot, and
+ *               freeing a page leaves its entries)
+ * and up to 64 sequences per call. A row that lists a page that is not held, or
+ * a lack of pages, shows in a device word only: read it before the rows are used. The paper fixes no allocator; a new page is
  * the lowest free id, as in the handle's slot rule. */
 
 /* Forks row parents[i] into the empty row children[i] (HOST int32 [n_forks];
@@ -492,7 +496,8 @@ TKV_API tkv_status tkv_test_stall_next_tiles(uint64_t wait_limit_ns);
  * page is copied. Copies take K/V of all layers, mask and positions. The
  * child's count is the parent's. *status (device) becomes 0; or the number of
  * pages lacking; or -1 if a parent's row lists a page that is not held. If it
- * is not 0 nothing else has changed. */
+ * is not 0 nothing else has changed: the children's rows hold what they held, and
+ * attention over them with the parent's counts would read that. */
 TKV_API tkv_status tkv_fork_sequences_scratch_size(int32_t rows, int32_t max_pages, const int32_t* page_counts,
                                                    int32_t n_forks, const int32_t* parents, const int32_t* children,
                                                    int32_t share, size_t* scratch_bytes);
@@ -506,7 +511,7 @@ TKV_API tkv_status tkv_fork_sequences(void* pool, int32_t n_layers, int64_t pool
 /* Frees rows seqs[i] (HOST int32 [n_seqs], distinct): every page they list is
  * counted once less, a page at 0 is free and its mask 0, and the rows' entries
  * become -1. *status (device) becomes 0, or -1 if a row listed a page that was
- * not held (that entry is dropped). */
+ * not held (that entry is dropped, the others are freed all the same). */
 TKV_API tkv_status tkv_free_sequences(int32_t* page_table, int32_t rows, int32_t max_pages, const int32_t* page_counts,
                                       int64_t pool_pages, int32_t* page_refs, uint32_t* slot_mask, int32_t n_seqs,
                                       const int32_t* seqs, int32_t* status, tkv_stream stream);

@@ -273,8 +273,9 @@ def fork_sequences(pool, page_table, page_counts, page_refs, slot_mask, parents,
     (see tkv_fork_sequences): full pages are shared by count and an unfilled
     last page copied (share), or every page copied. Returns the device status
     int32 [1]: 0, the pages lacking (nothing changed), or -1 (a parent lists a
-    page that is not held; nothing changed). The children's counts are their
-    parents'; page_counts (host ints [rows]) stays the caller's to update.
+    page that is not held; nothing changed). If it is 0 the children's counts are
+    their parents'; page_counts (host ints [rows]) stays the caller's to update.
+    Read it before the children are used: their rows are not forked otherwise.
     """
     lib = L.load()
     pp, layers, pages, hkv, d, dt = _pool(pool)
@@ -304,7 +305,7 @@ def fork_sequences(pool, page_table, page_counts, page_refs, slot_mask, parents,
 def free_sequences(page_table, page_counts, page_refs, slot_mask, seqs, stream=None):
     """Frees rows `seqs` of the page table (see tkv_free_sequences): pages no
     row lists any more become free. Returns the device status int32 [1]: 0, or
-    -1 if a row listed a page that was not held.
+    -1 if a row listed a page that was not held (its other pages are freed).
     """
     lib = L.load()
     if not isinstance(page_table, torch.Tensor):
