@@ -432,3 +432,20 @@ def test_scores_by_token_over_a_compaction(dtype):
         b.same()
     # the sum over heads and steps is rounded a few times more, in fp32
     assert_within(scores, want, tolerance + 8 * 2.0 ** -24 * want + 1e-30, "scores")
+
+
+def test_a_stalled_round_is_one_round():
+    """The hook stalls the first launch of a call that takes several; the others
+    wait for nothing."""
+    import time
+
+    from tiered_kv_cache_split_gb300 import prompt_attention
+    x = make_prompt(9, "bf16", 64, 1, 64, [5100], [(1 << 18) + 5100])
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    good = prompt_attention(*x, [5100], [(1 << 18) + 5100])
+    torch.cuda.synchronize()
+    t = time.monotonic()
+    stalled(prompt_attention, *x, [5100], [(1 << 18) + 5100], status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 1 and time.monotonic() - t < 1.5       # a wait of the default length takes 2 s
+    assert torch.equal(prompt_attention(*x, [5100], [(1 << 18) + 5100]), good)

@@ -826,6 +826,7 @@ thread_local uint64_t g_stall_limit_ns = 0;  // tkv_test_stall_next_tiles
 
 void set_waits(TileParams& p, int32_t dtype) {
   p.wait_limit_ns = 2000000000ull;
+  p.stall = 0;
   if (g_stall_limit_ns && dtype == TKV_DTYPE_BF16) {
     p.wait_limit_ns = g_stall_limit_ns;
     p.stall = 1;
