@@ -296,6 +296,7 @@ def test_sums_over_two_million_keys(spread):
 
 
 @pytest.mark.parametrize("dtype,q_lens,k_lens", [("bf16", [300, 5100, 1], [300, (1 << 18) + 5100, 900]),
+                                                 ("bf16", [2500, 6, 4000], [(1 << 18) + 3000, 6, (1 << 18) + 4001]),
                                                  ("f32", [2500, 40], [(1 << 18) + 700, 40])])
 def test_a_long_sequence_that_takes_turns_over_the_scratch(dtype, q_lens, k_lens):
     """More rows than four waves of tiles over more than 2^18 keys, other
@@ -307,7 +308,7 @@ def test_a_long_sequence_that_takes_turns_over_the_scratch(dtype, q_lens, k_lens
     out = torch.full_like(x[0], float("nan"))
     prompt_attention(*x, q_lens, k_lens, scratch=s.mid, out=out)
     assert s.intact() and not out.isnan().any()
-    turn = 4 * 152 * 256 // hq if dtype == "bf16" else 4 * 304 * 64 // hq
+    turn = (4 * 152 * 256 if dtype == "bf16" else 4 * 304 * 64) // hq // sum(n > 1 << 18 for n in k_lens)
     q0 = k0 = 0
     for nq, nk in zip(q_lens, k_lens):
         rows = sorted({i for i in (0, 1, turn - 1, turn, turn + 1, 2 * turn - 1, 2 * turn, nq // 2, nq - 1) if i < nq})
@@ -449,3 +450,39 @@ def test_a_stalled_round_is_one_round():
     torch.cuda.synchronize()
     assert status.item() == 1 and time.monotonic() - t < 1.5       # a wait of the default length takes 2 s
     assert torch.equal(prompt_attention(*x, [5100], [(1 << 18) + 5100]), good)
+
+
+@pytest.mark.parametrize("dtype,layers,hkv,d", [("bf16", 2, 4, 128), ("f32", 1, 2, 64)])
+@pytest.mark.parametrize("chains", [5, 31, 63])
+def test_compaction_of_many_chains_behind_a_shared_prefix(dtype, layers, hkv, d, chains):
+    """Rows that share their first pages and lost tokens everywhere: the shared
+    pages stay, with their holes; the end of a chain makes pages of the last row
+    that lists them its own."""
+    from tiered_kv_cache_split_gb300 import compact_sequences, fork_sequences, free_sequences
+    b = Book(chains, layers, 8 + chains * 9, hkv, d, dtype, chains + 1, 24)
+    b.fill(0, 8, drop=0.2, last=7)
+    b.upload()
+    forks = [0] * chains, list(range(1, chains + 1))
+    st = fork_sequences(b.dpool, b.dtable, b.counts, b.drefs, b.dmask, *forks, positions=b.dpos)
+    assert b.fork(*forks, True) == st.item() == 0
+    b.same()
+    for r in range(1, chains + 1):                       # each goes on by up to seven pages of its own
+        b.free = [p for p in range(len(b.refs)) if b.refs[p] == 0]
+        n, more = b.counts[r], r % 8
+        before = b.table[r, :n].copy()
+        b.fill(r, more, drop=0.1 * (r % 10), last=1 + r % 16)
+        b.table[r, n:n + more] = b.table[r, :more].copy()
+        b.table[r, :n] = before
+        b.counts[r] = n + more
+    b.upload()
+    for round in range(2):
+        counts = list(b.counts)
+        got = compact_sequences(b.dpool, b.dtable, counts, b.drefs, b.dmask, positions=b.dpos)
+        assert got.tolist() == b.compact()
+        b.same()
+        gone = list(range(0, chains)) if round == 0 else [chains]     # all but one end
+        st = free_sequences(b.dtable, b.counts, b.drefs, b.dmask, gone)
+        b.free_rows(gone)
+        b.same()
+        assert st.item() == 0
+    assert not b.refs.any()

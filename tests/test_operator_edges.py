@@ -62,6 +62,9 @@ def test_long_prompts_take_turns_over_the_partials(lib):
     for tokens in (1 << 19, 1 << 20, 1 << 22):
         rows = 4 * 152 * 256 + 8 * 256                       # the waves, and what tiles leave empty
         assert 0 < prompt_scratch(lib, L.DTYPE_BF16, [tokens], [tokens], 32, 8, 128) <= tokens // (1 << 18) * rows * 4 * (128 + 2) + 4096
+        # two of them take turns of half the length
+        both = prompt_scratch(lib, L.DTYPE_BF16, [tokens, tokens], [tokens, tokens], 32, 8, 128)
+        assert both <= tokens // (1 << 18) * (rows + 8 * 256) * 4 * (128 + 2) + 4096
     # beside them, short prompts need nothing, and a chunk behind a long cache what it needs alone
     alone = prompt_scratch(lib, L.DTYPE_BF16, [1 << 20], [1 << 20], 32, 8, 128)
     assert prompt_scratch(lib, L.DTYPE_BF16, [9000, 1 << 20, 300], [9000, 1 << 20, 300], 32, 8, 128) == alone

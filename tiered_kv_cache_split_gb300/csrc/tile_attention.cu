@@ -48,10 +48,11 @@ __device__ __forceinline__ bool finite1(float x) { return (__float_as_uint(x) & 
 
 // fp32 FMA kernel: 64 rows x 64 keys at a time, 256 threads as 16 x 16, each
 // with a 4 x 4 patch of S and 4 rows x D / 16 columns of O. The weights take the
-// place of K in shared memory, so that two CTAs fit on an SM at d = 128 (four at
-// 64) and one loads while another computes. Bound by the FMA pipe and about as
+// place of K in shared memory, so that two CTAs fit on an SM at d = 128 and one
+// loads while the other computes; at 64 more would fit, but 128 registers a thread
+// allow two. Bound by the FMA pipe and about as
 // much by shared-memory reads: tensor cores would round fp32 operands. Two
-// 1024-token prompts with 28 / 4 heads, d 128: 424 us, 35.5 TFLOP/s (half of the
+// 1024-token prompts with 28 / 4 heads, d 128: 422 us, 35.7 TFLOP/s (half of the
 // FMA pipe's 75).
 template <int D>
 __global__ void __launch_bounds__(kFmaThreads, 2) tile_fma_kernel(const __grid_constant__ TileParams p) {
@@ -698,9 +699,9 @@ int check_heads(int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype) {
 
 // A call runs in rounds, nearly always one. A sequence of more than kMaxUnitKeys
 // keys has its keys split however many rows there are, and partials of all its rows
-// at once could be larger than the cache (34 GB for 2^20 tokens of 32 heads, d 128,
-// and two ranges): each round takes as many of its tokens as make four waves of
-// units, and the rounds share the scratch.
+// at once could be larger than the cache (70 GB for 2^20 tokens of 32 heads, d 128):
+// each round takes as many tokens of such sequences as make four waves of tiles,
+// and the rounds share the scratch.
 int plan_prompt(TileParams& p, TilePlan* plan, int32_t batch, const int32_t* q_lens, const int32_t* k_lens, int32_t Hq,
                 int32_t Hkv, int32_t D, int32_t dtype, int round, int* rounds, int64_t* tokens, int64_t* keys) {
   if (batch < 1 || batch > kMaxBatch) return report(TKV_ERR_INVALID_ARG, "batch must be 1 to %d", kMaxBatch);
@@ -711,7 +712,9 @@ int plan_prompt(TileParams& p, TilePlan* plan, int32_t batch, const int32_t* q_l
   p.nseg = batch;
   p.qscale = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
   const TileShape ts = tile_shape(dtype);
-  const int64_t round_tokens = ceil_div(int64_t(4) * ts.slots * ts.rows * ts.tpg, Hq);
+  int64_t taking_turns = 0;
+  for (int i = 0; i < batch; ++i) taking_turns += k_lens[i] > kMaxUnitKeys;
+  const int64_t round_tokens = ceil_div(int64_t(4) * ts.slots * ts.rows * ts.tpg, Hq * std::max<int64_t>(1, taking_turns));  // of each
   int64_t tq = 0, tk = 0;
   *rounds = 1;
   for (int i = 0; i < batch; ++i) {
