@@ -399,9 +399,11 @@ TKV_API tkv_status tkv_quantize_rows(const void* x, int32_t kv_dtype, int64_t ro
  * Stateless operators for one prompt that several chains continue: attend the
  * prompt, fork its pages, decode over the shared pages, compact what eviction
  * (Methodology 1, T3) left, free what is done. All are enqueued on `stream`,
- * touch only the buffers they are given (and a word of the library's that says
- * a device wait gave up) and may be captured into a graph; calls that overlap on the GPU need scratch buffers of their own. Pool, page
- * table and slot masks are those of tkv_paged_attention. */
+ * touch only the buffers they are given (and a word of the library's, in 256
+ * bytes of pinned host memory that the first call makes, which says that a device
+ * wait gave up) and may be captured into a graph; calls that overlap on the GPU
+ * need scratch buffers of their own. Pool, page table and slot masks are those of
+ * tkv_paged_attention. */
 
 /* Causal attention over packed prompts: token i of a sequence with k_len keys
  * and q_len queries sees keys 0 .. i + k_len - q_len (its own keys end at the

@@ -147,9 +147,10 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const __grid_co
 }
 
 // Copies the 16-byte chunks of one page of one layer; the parent's page is read
-// by the CTAs of all its children at about the same time, so HBM sees it once
-// (three copies of 2000 tokens, 28 layers of 4 heads at d 128: 115 MB read and
-// 344 written in 72 us, 6.4 TB/s of 6.8).
+// by the CTAs of all its children at about the same time, so HBM sees it once.
+// Three copies of 2000 tokens, 28 layers of 4 heads at d 128: 115 MB to read and 344
+// to write in 72 us, 6.4 TB/s; a copy with torch reaches 6.8. Of the 344 MB, 287
+// are in HBM when the launch ends and the rest still in the L2.
 __device__ __forceinline__ void copy_page(const PoolDesc& d, int layer, int64_t src, int64_t dst) {
   const int4* from = reinterpret_cast<const int4*>(d.base + layer * d.layer_bytes + src * d.page_bytes);
   int4* to = reinterpret_cast<int4*>(d.base + layer * d.layer_bytes + dst * d.page_bytes);
@@ -362,7 +363,8 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid
 
 // One warp per moved token of the CTA's layer (blockIdx.y): its 2 * Hkv rows, 16
 // bytes per lane, four in flight. Index arithmetic is 32-bit and by shifts: with
-// divisions the issue slots, not HBM, were the bound. 264 MB: 41 us, 6.4 TB/s of 6.8.
+// divisions the issue slots, not HBM, were the bound. 264 MB to read and write: 41
+// us, 6.4 TB/s (a copy with torch: 6.8); 217 MB of it pass HBM within the launch.
 __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const __grid_constant__ CompactParams p) {
   __shared__ int s_first[kMaxBatch + 1];
   cudaGridDependencySynchronize();

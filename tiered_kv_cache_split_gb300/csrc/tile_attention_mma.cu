@@ -24,12 +24,13 @@
 // 8192: 18.8 us, against 20.6 with one tile idle; long splits, bound by HBM,
 // take the same time either way).
 //
-// Measured (d 128; GB300, 6.8 TB/s and 1.89 PFLOP/s bf16 as peaks): a causal
-// prompt of 8192 tokens with 32 / 8 heads 360 us, 1.53 PFLOP/s, the tensor pipe
-// active 66 % of the time and the softmax the rest; 64 decode rows over a shared
-// 131072-token prefix 118 us, 4.9 TB/s with the tensor pipe at 54 %; 8 decode rows
-// over 15360 tokens with 32 KV heads 60 us, 5.2 TB/s, bound by HBM and the last
-// wave of units.
+// Measured (d 128; GB300, where a copy reaches 6.8 TB/s and a library product
+// 1.89 PFLOP/s): a causal prompt of 8192 tokens with 32 / 8 heads 358 us, 1.54
+// PFLOP/s, 81 % of that product's rate; the tensor pipe is busy in 66 % of an SM's
+// active cycles (all of them would be 2.37 PFLOP/s at the 1.90 GHz it ran at) and
+// waits for the softmax in the rest; 64 decode rows over a shared 131072-token prefix
+// 119 us, 4.8 TB/s with the pipe busy in 54 %; 8 decode rows over 15360 tokens with
+// 32 KV heads 60 us, 5.2 TB/s, bound by HBM and the last wave of units.
 //
 // The grid has a CTA per unit; a running CTA takes the units of CTAs that have
 // not started (cluster launch control), so units are handed out in grid order,
@@ -49,8 +50,9 @@
 // P and V in one type. Z sums the rounded weights, in fp32: where few keys carry
 // a row, their errors then leave the quotient (0.0018 off the 64-bit result in
 // the 2-norm, against 0.0023 with Z of the unrounded ones; output rounding alone
-// is 0.0016). alpha is made of unrounded weights: calls that ask for it keep
-// their sum too.
+// is 0.0016), for 2 % of the time of a prompt of 8192 (351 us with the unrounded
+// ones). alpha is made of unrounded weights: calls that ask for it keep their sum
+// too.
 //
 // 0 * NaN must not reach O: the V rows of holes are zeroed in shared memory, and
 // keys past a sequence's end or that only some rows see have their non-finite V
