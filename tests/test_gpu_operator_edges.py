@@ -486,3 +486,15 @@ def test_compaction_of_many_chains_behind_a_shared_prefix(dtype, layers, hkv, d,
         b.same()
         assert st.item() == 0
     assert not b.refs.any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hkv,d", [(64, 1, 64), (28, 4, 128), (3, 3, 64)])
+def test_sums_that_are_large_already_are_rounded_once(dtype, hq, hkv, d):
+    """However many heads share a KV head."""
+    from tiered_kv_cache_split_gb300 import shared_prefix_attention
+    q, pool, table, mask, counts, tb, mk = make_prefix(8, dtype, hq, hkv, d, 20, [38, 0, 9, 55])
+    alpha = torch.full((4, hkv, table.shape[1] * 16), 4096.0, device=DEV)
+    shared_prefix_attention(q, pool, table, mask, counts, 20, alpha_sum=alpha)
+    _, _, aw, ab = prefix_reference(q, pool, tb, mk, counts, 20)
+    assert_within(alpha, 4096 + aw, ab + (4096 + aw) * 2.0 ** -24, "alpha")

@@ -453,7 +453,8 @@ __global__ void __launch_bounds__(kMergeThreads) tile_merge_kernel(const __grid_
   if (i >= so.nkeys) return;
   const float* l = p.spill + so.spill0 + static_cast<int64_t>(h) * G * so.nkeys + i;
   float4* at = reinterpret_cast<float4*>(p.alpha + (static_cast<int64_t>(tok) * p.Hkv + h) * p.alpha_stride_h + p.alpha_first + i);
-  float4 sum = *at;
+  const float4 before = *at;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);  // of the heads first: what was there may be much larger, and is rounded once
 #pragma unroll 4
   for (int g = 0; g < G; ++g) {
     const float4 x = *reinterpret_cast<const float4*>(l + static_cast<int64_t>(g) * so.nkeys);
@@ -462,7 +463,7 @@ __global__ void __launch_bounds__(kMergeThreads) tile_merge_kernel(const __grid_
     sum.z += alpha_weight(x.z, s_m[g], s_inv[g]);
     sum.w += alpha_weight(x.w, s_m[g], s_inv[g]);
   }
-  *at = sum;
+  *at = make_float4(before.x + sum.x, before.y + sum.y, before.z + sum.z, before.w + sum.w);
 }
 
 // ---- planning (host)
