@@ -4,8 +4,8 @@ Argument marshalling only, as in cache.py: torch owns the buffers, the CUDA
 kernels of libtkv.so do the work (include/tkv.h states each operator). Every
 tensor of a call lies on one CUDA device, which need not be the current one;
 a call on a stream other than the current one takes the buffers it makes from
-that stream's memory (work on the current stream waits for that stream before
-it uses them). ValueError names an argument of the wrong type, shape, layout
+that stream's memory; the caller has other streams wait for it before they use
+the result. ValueError names an argument of the wrong type, shape, layout
 or device, or one that asks for a gradient; the library's own checks raise
 TkvError.
 """
