@@ -721,7 +721,7 @@ int plan_prompt(TileParams& p, TilePlan* plan, int32_t batch, const int32_t* q_l
   for (int i = 0; i < batch; ++i) {
     if (q_lens[i] < 0 || k_lens[i] < q_lens[i]) return report(TKV_ERR_INVALID_ARG, "sequence %d: 0 <= q_len <= k_len", i);
     if (k_lens[i] > kMaxPromptKeys) return report(TKV_ERR_INVALID_ARG, "sequence %d: k_len above 2^26", i);
-    int64_t first = round > 0 ? q_lens[i] : 0, last = q_lens[i];  // tokens of this round
+    int64_t first = round > 0 ? q_lens[i] : 0, last = q_lens[i];  // the tokens taken now
     if (k_lens[i] > kMaxUnitKeys) {
       first = std::min(last, round * round_tokens);
       last = std::min(last, first + round_tokens);
@@ -949,7 +949,7 @@ tkv_status tkv_prompt_attention(int32_t batch, const int32_t* q_lens, const int3
   if (q_stride < qrow || out_stride < qrow || k_stride < krow || v_stride < krow || q_stride % unit || out_stride % unit ||
       k_stride % unit || v_stride % unit || (q_stride | out_stride | k_stride | v_stride) >> 36)
     return tkv_status(report(TKV_ERR_INVALID_ARG, "token strides must hold a token and be multiples of 16 bytes"));
-  // the last round is planned first: none is launched unless the scratch is enough for all
+  // planned from the end: nothing is launched unless the scratch is enough for all of it
   for (int round = rounds - 1; round >= 0; --round) {
     if (rounds > 1)
       if (int st = plan_round(round)) return tkv_status(st);
