@@ -536,6 +536,99 @@ TKV_API tkv_status tkv_compact_sequences(void* pool, int32_t n_layers, int64_t p
                                          uint32_t* slot_mask, int32_t* positions, int32_t* new_counts, void* scratch,
                                          size_t scratch_bytes, tkv_stream stream);
 
+/* ---- rotary positions and a cache held in 8 bits --------------------------
+ * Stateless operators for what lies between a model's projections and its
+ * attention: q and k are rotated by their positions, K and V quantised as they
+ * are written into pages, read back for a further prompt chunk, and attended by
+ * one token per sequence. The paper keeps full-precision pages and an 8-bit tier
+ * of the handle's own (T2, Methodology 1); here a whole pool is 8-bit. All are enqueued on
+ * `stream`, touch only the buffers they are given and may be captured into a
+ * graph; calls that overlap on the GPU need scratch buffers of their own. The
+ * 8-bit pool:
+ *   pool    device int8 [pool_pages][Hkv][2][16][d], 16-byte aligned: codes, K rows then V rows
+ *   scales  device float [pool_pages][Hkv][2], 8-byte aligned: one per BLOCK (page, head, K or V)
+ * A row's value is code * scale; pool_pages x Hkv <= 2^29, d 64 or 128. Page
+ * table and slot masks are those of tkv_paged_attention. A listed page id
+ * outside the pool is never accessed. */
+
+/* Rotary positions. Pair i of a head, elements (i, i + r/2) of its first
+ * r = rotary_dim, or (2 i, 2 i + 1) if interleaved, turns by pos * f_i:
+ *   a' = scale (a cos - b sin), b' = scale (b cos + a sin); inverse: by -pos * f_i.
+ * Elements behind r pass unscaled. Angles are formed in 64-bit fixed point: off by
+ * at most |pos| 2^-64 turns, so below fp32's own error up to |pos| = 2^33 and
+ * consistent beyond; products and sums are fp32, rounded once.
+ *   steps      device uint64 [r / 2] of tkv_rotary_steps
+ *   positions  device int32 or int64 (position_bits) [n_tokens], any sign
+ *   q, k       device [n_tokens][heads][head_dim] in dtype, tokens *_stride
+ *              elements apart; either may have 0 heads
+ *   q_out, k_out  the same, or the inputs themselves (in place, equal strides);
+ *              no other overlap
+ * head_dim 2 .. 512, even rotary_dim 2 .. head_dim. Rows that are 16-byte
+ * aligned and whose r / 2 (interleaved: r) is a multiple of 16 bytes are read 16 bytes at a time. */
+TKV_API tkv_status tkv_rotate(int64_t n_tokens, int32_t n_q_heads, int32_t n_k_heads, int32_t head_dim,
+                              int32_t rotary_dim, int32_t dtype, int32_t interleaved, int32_t inverse, float scale,
+                              const uint64_t* steps, const void* positions, int32_t position_bits, const void* q,
+                              int64_t q_stride, const void* k, int64_t k_stride, void* q_out, int64_t q_out_stride,
+                              void* k_out, int64_t k_out_stride, tkv_stream stream);
+/* Host only: turns per position in 2^-64 turns, inv_freq (radians per
+ * position, HOST double [n], finite, at most 2^32 in size) / 2 pi modulo 1. */
+TKV_API tkv_status tkv_rotary_steps(int32_t n, const double* inv_freq, uint64_t* steps);
+
+/* Writes new_lens[b] tokens behind the lens[b] of each row: slots lens[b] ..
+ * lens[b] + new_lens[b] - 1 of the pages it lists, quantised per block:
+ *   scale = max(absmax of the block's new tokens / 127, the block's scale if it
+ *           holds earlier tokens (its slot 0 is not written by this call))
+ *   code  = clamp(rint(x / scale), -127, 127); scale 0 gives codes 0
+ * and where the scale of a block with earlier tokens grew, their codes become
+ * rint(code * (old / new)): each growth costs them at most half a step more.
+ * A block that gets a NaN or an infinity has a NaN scale and reads as NaN until
+ * its slot 0 is written again. All arithmetic is fp32.
+ *   lens, new_lens  HOST int32 [rows], rows 1 .. 64
+ *   k, v       device [sum new_lens][Hkv][d] in dtype, packed in row order,
+ *              strides in elements, multiples of 16 bytes; 16-byte aligned
+ *   slot_mask  device or NULL: a written slot's bit is set (a page whose slot 0
+ *              is written has the written bits only)
+ *   page_refs  device int32 [pool_pages] or NULL: rows that list a page; a page
+ *              whose count is not 1 is not written
+ *   status     device int32 or NULL: set to -1 (never cleared) if a listed page
+ *              is outside the pool or not the row's alone; its tokens are not written
+ * A page written by a call is listed by one of its rows only, once. */
+TKV_API tkv_status tkv_append_quantized(int32_t rows, const int32_t* lens, const int32_t* new_lens, int32_t n_kv_heads,
+                                        int32_t head_dim, int32_t dtype, const void* k, int64_t k_stride, const void* v,
+                                        int64_t v_stride, int8_t* pool, float* scales, int64_t pool_pages,
+                                        const int32_t* page_table, int32_t max_pages, uint32_t* slot_mask,
+                                        const int32_t* page_refs, int32_t* status, tkv_stream stream);
+
+/* Reads slots first[b] .. lens[b] - 1 of each row back as packed K and V
+ * [sum (lens - first)][Hkv][d] in dtype (code * scale in fp32, rounded once),
+ * as tkv_prompt_attention takes them. Slots whose mask bit is 0 (slot_mask may
+ * be NULL: none) and pages outside the pool read as zeros. first, lens: HOST
+ * int32 [rows], 0 <= first <= len. */
+TKV_API tkv_status tkv_read_quantized(int32_t rows, const int32_t* first, const int32_t* lens, int32_t n_kv_heads,
+                                      int32_t head_dim, int32_t dtype, const int8_t* pool, const float* scales,
+                                      int64_t pool_pages, const int32_t* page_table, int32_t max_pages,
+                                      const uint32_t* slot_mask, void* k, int64_t k_stride, void* v, int64_t v_stride,
+                                      tkv_stream stream);
+
+/* tkv_paged_attention over an 8-bit pool: one query token per sequence, and the
+ * score increments of Methodology 2 if alpha_sum is given. Arguments are those
+ * of tkv_paged_attention with `scales` beside the pool, except:
+ *   pool_pages  pages of the pool; a listed id outside reads as an empty page
+ *   n_q_heads   1 .. 64 times n_kv_heads
+ *   dtype       of q and out (F32 or BF16)
+ *   scratch     tkv_quantized_attention_scratch_size bytes (256-aligned; may be NULL when that is 0)
+ * A sequence without a valid slot, or whose logits are all -inf, gives 0. Empty
+ * slots may hold any codes; a scale that is not finite counts as NaN and reaches exactly the sequences with a
+ * valid slot in its block. */
+TKV_API tkv_status tkv_quantized_attention_scratch_size(int32_t batch, int32_t n_q_heads, int32_t n_kv_heads,
+                                                        int32_t head_dim, int32_t dtype, const int32_t* page_counts,
+                                                        int32_t max_pages, int32_t want_alpha, size_t* scratch_bytes);
+TKV_API tkv_status tkv_quantized_attention(int32_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                           int32_t dtype, const void* q, const int8_t* pool, const float* scales,
+                                           int64_t pool_pages, const int32_t* page_table, const uint32_t* slot_mask,
+                                           const int32_t* page_counts, int32_t max_pages, void* out, float* alpha_sum,
+                                           void* scratch, size_t scratch_bytes, tkv_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

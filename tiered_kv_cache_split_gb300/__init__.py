@@ -10,7 +10,10 @@ from ._lib import TkvError, load
 from .cache import TieredKVCache, classify, paged_attention, quantize_rows
 from .operators import (attention_synchronize, compact_sequences, fork_sequences, free_sequences,
                         prompt_attention, shared_prefix_attention)
+from .quantized import (RotaryTable, append_quantized, quantized_attention, read_quantized, rotary_table,
+                        rotate)
 
 __all__ = ["TieredKVCache", "TkvError", "load", "paged_attention", "classify", "quantize_rows",
            "prompt_attention", "shared_prefix_attention", "fork_sequences", "free_sequences", "compact_sequences",
-           "attention_synchronize"]
+           "attention_synchronize", "RotaryTable", "rotary_table", "rotate", "append_quantized", "read_quantized",
+           "quantized_attention"]

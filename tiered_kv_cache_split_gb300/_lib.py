@@ -106,6 +106,16 @@ _SIGS = {
     "tkv_compact_sequences_scratch_size": [c_i32, c_i32, c_vp, ctypes.POINTER(c_sz)],
     "tkv_compact_sequences": [c_vp, c_i32, c_i64, c_i32, c_i32, c_i32, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp,
                               c_vp, c_vp, c_sz, c_vp],
+    "tkv_rotary_steps": [c_i32, c_vp, c_vp],
+    "tkv_rotate": [c_i64, c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, ctypes.c_float, c_vp, c_vp, c_i32, c_vp, c_i64,
+                   c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp],
+    "tkv_append_quantized": [c_i32, c_vp, c_vp, c_i32, c_i32, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_i64, c_vp,
+                             c_i32, c_vp, c_vp, c_vp, c_vp],
+    "tkv_read_quantized": [c_i32, c_vp, c_vp, c_i32, c_i32, c_i32, c_vp, c_vp, c_i64, c_vp, c_i32, c_vp, c_vp, c_i64,
+                           c_vp, c_i64, c_vp],
+    "tkv_quantized_attention_scratch_size": [c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_i32, c_i32, ctypes.POINTER(c_sz)],
+    "tkv_quantized_attention": [c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_i64, c_vp, c_vp, c_vp, c_i32, c_vp,
+                                c_vp, c_vp, c_sz, c_vp],
 }
 
 _lib = None

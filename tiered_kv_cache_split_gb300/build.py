@@ -20,8 +20,8 @@ BUILD = os.path.join(HERE, "_build")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libtkv.so")
 LIB_DEBUG = os.path.join(HERE, "libtkv_debug.so")
-SOURCES = ["attention.cu", "classify.cu", "movement.cu", "pages.cu", "runtime.cu", "tile_attention.cu",
-           "tile_attention_mma.cu"]
+SOURCES = ["attention.cu", "classify.cu", "movement.cu", "pages.cu", "quantized.cu", "rotary.cu", "runtime.cu",
+           "tile_attention.cu", "tile_attention_mma.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I" + INCLUDE, "-I" + CSRC]
