@@ -20,8 +20,8 @@ BUILD = os.path.join(HERE, "_build")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libtkv.so")
 LIB_DEBUG = os.path.join(HERE, "libtkv_debug.so")
-SOURCES = ["attention.cu", "classify.cu", "movement.cu", "pages.cu", "quantized.cu", "rotary.cu", "runtime.cu",
-           "tile_attention.cu", "tile_attention_mma.cu"]
+SOURCES = ["attention.cu", "classify.cu", "movement.cu", "pages.cu", "quantized.cu", "quantized_attention.cu",
+           "rotary.cu", "runtime.cu", "tile_attention.cu", "tile_attention_mma.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I" + INCLUDE, "-I" + CSRC]
@@ -48,7 +48,7 @@ def build(verbose: bool = False, force: bool = False, debug: bool = False) -> st
     flags = FLAGS + (["-DTKV_DEBUG"] if debug else [])
     os.makedirs(out_dir, exist_ok=True)
     headers = [os.path.join(CSRC, "tkv_internal.h"), os.path.join(CSRC, "tile_attention.h"),
-               os.path.join(INCLUDE, "tkv.h")]
+               os.path.join(CSRC, "quantized.h"), os.path.join(INCLUDE, "tkv.h")]
     jobs = []
     for s in SOURCES:
         src = os.path.join(CSRC, s)

@@ -1,9 +1,5 @@
-// A paged cache held in 8 bits: tokens quantised as they are written, read back,
-// and attended by one token per sequence.
-//
-// A BLOCK is the 16 slots of a page, one KV head, K or V: 16 rows of int8 codes
-// and one fp32 scale; a row's value is code * scale. The pool is
-// [pages][Hkv][2][16][D] codes, the scales [pages][Hkv][2].
+// A paged cache held in 8 bits: tokens quantised as they are written, and read
+// back (quantized.h has the layout).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -11,51 +7,18 @@
 #include <cmath>
 #include <cstdint>
 
-#include "tkv.h"
-#include "tkv_internal.h"
+#include "quantized.h"
 
 namespace tkv {
 namespace {
 
 constexpr int kCopyThreads = 256;
 constexpr int kCopyWarps = kCopyThreads / 32;
-constexpr uint32_t kFullMask = 0xffffu;
-constexpr float kNegInf = -INFINITY;
 
-// Elements as they lie in a 16-byte vector.
-template <typename T> struct Vec;
-template <> struct Vec<float> {
-  static constexpr int n = 4;
-  using Codes = uint32_t;
-  static __device__ __forceinline__ void unpack(const int4& v, float* x) {
-    x[0] = __int_as_float(v.x); x[1] = __int_as_float(v.y); x[2] = __int_as_float(v.z); x[3] = __int_as_float(v.w);
-  }
-  static __device__ __forceinline__ int4 pack(const float* x) {
-    return make_int4(__float_as_int(x[0]), __float_as_int(x[1]), __float_as_int(x[2]), __float_as_int(x[3]));
-  }
-};
-template <> struct Vec<__nv_bfloat16> {
-  static constexpr int n = 8;
-  using Codes = uint2;
-  static __device__ __forceinline__ void unpack(const int4& v, float* x) {
-    const int w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __int_as_float(w[i] << 16);
-      x[2 * i + 1] = __int_as_float(w[i] & 0xffff0000);
-    }
-  }
-  static __device__ __forceinline__ int4 pack(const float* x) {
-    int w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const int*>(&h);
-    }
-    return make_int4(w[0], w[1], w[2], w[3]);
-  }
-};
-
+// int8 codes of the elements of a 16-byte vector
+template <typename T> struct CodesOf;
+template <> struct CodesOf<float> { using type = uint32_t; };
+template <> struct CodesOf<__nv_bfloat16> { using type = uint2; };
 union CodeBytes {
   uint32_t w[2];
   int8_t c[8];
@@ -71,16 +34,6 @@ struct RowRange {
   int32_t first[kMaxBatch], last[kMaxBatch];
   int64_t page0[kMaxBatch + 1];  // prefix sums of the pages touched
   int64_t token0[kMaxBatch];     // packed index of slot `first`
-};
-
-struct PoolRef {
-  int8_t* codes;
-  float* scales;
-  int64_t pages;
-  const int32_t* table;
-  int64_t table_stride;
-  uint32_t* mask;         // may be null
-  int32_t hkv;
 };
 
 struct Item {
@@ -139,7 +92,7 @@ __device__ __forceinline__ int8_t to_code(float x, float scale) {
 template <typename T, int D>
 __global__ void __launch_bounds__(kCopyThreads) append_quantized_kernel(const __grid_constant__ AppendQParams p) {
   using V = Vec<T>;
-  using Codes = typename V::Codes;
+  using Codes = typename CodesOf<T>::type;
   constexpr int kLanes = D / V::n;                       // lanes of a row
   constexpr int kRows = 32 / kLanes, kPasses = kPage / kRows;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * kCopyWarps + (threadIdx.x >> 5);
@@ -221,7 +174,7 @@ struct ReadQParams {
 template <typename T, int D>
 __global__ void __launch_bounds__(kCopyThreads) read_quantized_kernel(const __grid_constant__ ReadQParams p) {
   using V = Vec<T>;
-  using Codes = typename V::Codes;
+  using Codes = typename CodesOf<T>::type;
   constexpr int kLanes = D / V::n;
   constexpr int kRows = 32 / kLanes, kPasses = kPage / kRows;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * kCopyWarps + (threadIdx.x >> 5);
@@ -252,120 +205,7 @@ __global__ void __launch_bounds__(kCopyThreads) read_quantized_kernel(const __gr
   }
 }
 
-// ---- attention
-
-struct AttendQParams {
-  PoolRef p;
-  const void* q;
-  void* out;
-  float* alpha;          // may be null
-  float2* stats;         // [B][Hq] running maximum (base 2) and sum
-  int32_t B, Hq, G, max_pages;
-  float qscale;          // log2(e) / sqrt(D)
-  int32_t count[kMaxBatch];
-};
-
-__device__ __forceinline__ float to_float(float x) { return x; }
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void put(float* at, float x) { *at = x; }
-__device__ __forceinline__ void put(__nv_bfloat16* at, float x) { *at = __float2bfloat16_rn(x); }
-
-__device__ __forceinline__ float finite_or_nan(float x) { return fabsf(x) < INFINITY ? x : NAN; }
-
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int m = 16; m; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
-  return x;
-}
-
-// A warp per (sequence, query head): keys one after another, D / 32 elements per lane.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) attend_quantized_kernel(const __grid_constant__ AttendQParams p) {
-  constexpr int E = D / 32;
-  const int w = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (w >= p.B * p.Hq) return;
-  const int b = w / p.Hq, hq = w % p.Hq, h = hq / p.G;
-  float q[E], o[E] = {};
-#pragma unroll
-  for (int j = 0; j < E; ++j) q[j] = to_float(static_cast<const T*>(p.q)[static_cast<int64_t>(w) * D + lane * E + j]);
-  float m = kNegInf, z = 0.f;
-  for (int i = 0; i < p.count[b]; ++i) {
-    const int32_t id = p.p.table[b * p.p.table_stride + i];
-    if (id < 0 || id >= p.p.pages) continue;
-    const uint32_t live = p.p.mask[id];
-    const int64_t block = (static_cast<int64_t>(id) * p.p.hkv + h) * 2;
-    const float sk = finite_or_nan(p.p.scales[block]), sv = finite_or_nan(p.p.scales[block + 1]);
-    for (int s = 0; s < kPage; ++s) {
-      if (!(live >> s & 1)) continue;
-      const int8_t* k = p.p.codes + (block * kPage + s) * D + lane * E;
-      float dot = 0.f;
-#pragma unroll
-      for (int j = 0; j < E; ++j) dot += q[j] * k[j];
-      const float l = warp_sum(dot) * sk * p.qscale;
-      if (l == kNegInf) continue;
-      const float top = fmaxf(m, l), keep = exp2f(m - top), x = exp2f(l - top);
-      const float before = z * keep;
-      z = before + x;
-      const float wo = before / z, wx = x / z;  // a mean at every key: sums of V could pass the type's largest value
-#pragma unroll
-      for (int j = 0; j < E; ++j) o[j] = o[j] * wo + wx * (k[kPage * D + j] * sv);
-      m = top;
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < E; ++j) put(static_cast<T*>(p.out) + static_cast<int64_t>(w) * D + lane * E + j, o[j]);
-  if (p.stats && lane == 0) p.stats[w] = make_float2(m, z);
-}
-
-// A warp per (sequence, KV head, page): the weights of its slots, summed over the heads.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) alpha_quantized_kernel(const __grid_constant__ AttendQParams p) {
-  constexpr int E = D / 32;
-  const int w = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int i = w % p.max_pages, h = w / p.max_pages % p.p.hkv, b = w / p.max_pages / p.p.hkv;
-  if (b >= p.B || i >= p.count[b]) return;
-  const int32_t id = p.p.table[b * p.p.table_stride + i];
-  if (id < 0 || id >= p.p.pages) return;
-  const uint32_t live = p.p.mask[id];
-  const int64_t block = (static_cast<int64_t>(id) * p.p.hkv + h) * 2;
-  const float sk = finite_or_nan(p.p.scales[block]);
-  float* to = p.alpha + (static_cast<int64_t>(b) * p.p.hkv + h) * p.max_pages * kPage + i * kPage;
-  for (int s = 0; s < kPage; ++s) {
-    if (!(live >> s & 1)) continue;
-    const int8_t* k = p.p.codes + (block * kPage + s) * D + lane * E;
-    float sum = 0.f;
-    for (int g = 0; g < p.G; ++g) {
-      const T* q = static_cast<const T*>(p.q) + (static_cast<int64_t>(b) * p.Hq + h * p.G + g) * D + lane * E;
-      float dot = 0.f;
-#pragma unroll
-      for (int j = 0; j < E; ++j) dot += to_float(q[j]) * k[j];
-      const float l = warp_sum(dot) * sk * p.qscale;
-      const float2 st = p.stats[b * p.Hq + h * p.G + g];
-      sum += l == kNegInf ? 0.f : exp2f(l - st.x) / st.y;
-    }
-    if (lane == 0) to[s] += sum;
-  }
-}
-
 // ---- host side
-
-bool misaligned(const void* ptr, size_t to) { return reinterpret_cast<uintptr_t>(ptr) % to != 0; }
-
-int launched(const char* what, cudaError_t e) {
-  return e == cudaSuccess ? TKV_OK : report(TKV_ERR_CUDA, "%s launch failed: %s", what, cudaGetErrorString(e));
-}
-
-int check_pool(PoolRef* p, int8_t* pool, float* scales, int64_t pool_pages, int32_t n_kv_heads, int32_t head_dim,
-               const int32_t* page_table, int32_t max_pages, uint32_t* slot_mask) {
-  if (n_kv_heads < 1 || n_kv_heads > 65535 || pool_pages < 1 || pool_pages > (int64_t(1) << 29) / n_kv_heads)
-    return report(TKV_ERR_INVALID_ARG, "pool_pages x n_kv_heads must be 1 to 2^29");
-  if (head_dim != 64 && head_dim != 128) return report(TKV_ERR_INVALID_ARG, "head_dim must be 64 or 128");
-  if (max_pages < 1 || max_pages > kMaxSeqPages) return report(TKV_ERR_INVALID_ARG, "max_pages must be 1 to %d", kMaxSeqPages);
-  if (!pool || !scales || !page_table) return report(TKV_ERR_INVALID_ARG, "null pointer");
-  if (misaligned(pool, 16) || misaligned(scales, 8)) return report(TKV_ERR_INVALID_ARG, "pool must be 16-byte, scales 8-byte aligned");
-  *p = {pool, scales, pool_pages, page_table, max_pages, slot_mask, n_kv_heads};
-  return TKV_OK;
-}
 
 // Fills the ranges [first, last) of each row; *tokens, *pages their sums.
 int check_rows(RowRange* r, int32_t rows, const int32_t* first, const int32_t* last, int32_t max_pages, int64_t* tokens) {
@@ -390,41 +230,6 @@ int check_tokens(int32_t dtype, int32_t n_kv_heads, int32_t head_dim, const void
   if (k_stride < row || v_stride < row || k_stride % unit || v_stride % unit || (k_stride | v_stride) >> 36)
     return report(TKV_ERR_INVALID_ARG, "token strides must hold a token and be multiples of 16 bytes");
   return TKV_OK;
-}
-
-int check_dtype(int32_t dtype) {
-  return dtype == TKV_DTYPE_F32 || dtype == TKV_DTYPE_BF16 ? TKV_OK : report(TKV_ERR_INVALID_ARG, "dtype");
-}
-
-int check_heads(int32_t Hq, int32_t Hkv, int32_t D) {
-  if (Hkv < 1 || Hq < 1 || Hkv > 65535 || Hq % Hkv || Hq / Hkv > 64)
-    return report(TKV_ERR_INVALID_ARG, "n_q_heads must be 1 to 64 times n_kv_heads");
-  if (D != 64 && D != 128) return report(TKV_ERR_INVALID_ARG, "head_dim must be 64 or 128");
-  return TKV_OK;
-}
-
-int plan_attend(AttendQParams* p, int32_t batch, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype, const int32_t* page_counts,
-                int32_t max_pages, int want_alpha, size_t* bytes) {
-  if (batch < 1 || batch > kMaxBatch) return report(TKV_ERR_INVALID_ARG, "batch must be 1 to %d", kMaxBatch);
-  if (int st = check_heads(Hq, Hkv, D)) return st;
-  if (int st = check_dtype(dtype)) return st;
-  if (max_pages < 1 || max_pages > kMaxSeqPages) return report(TKV_ERR_INVALID_ARG, "max_pages must be 1 to %d", kMaxSeqPages);
-  if (!page_counts) return report(TKV_ERR_INVALID_ARG, "null pointer");
-  for (int b = 0; b < batch; ++b) {
-    if (page_counts[b] < 0 || page_counts[b] > max_pages) return report(TKV_ERR_INVALID_ARG, "page_counts[%d] out of 0..max_pages", b);
-    p->count[b] = page_counts[b];
-  }
-  p->B = batch; p->Hq = Hq; p->G = Hq / Hkv; p->max_pages = max_pages;
-  p->qscale = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
-  *bytes = want_alpha ? (static_cast<size_t>(batch) * Hq * sizeof(float2) + 255) / 256 * 256 : 0;
-  return TKV_OK;
-}
-
-template <typename T, int D>
-cudaError_t launch_attend(const AttendQParams& p, cudaStream_t s) {
-  attend_quantized_kernel<T, D><<<(p.B * p.Hq + 3) / 4, 128, 0, s>>>(p);
-  if (p.alpha) alpha_quantized_kernel<T, D><<<static_cast<unsigned>((static_cast<int64_t>(p.B) * p.p.hkv * p.max_pages + 3) / 4), 128, 0, s>>>(p);
-  return cudaGetLastError();
 }
 
 }  // namespace
@@ -479,8 +284,7 @@ tkv_status tkv_read_quantized(int32_t rows, const int32_t* first, const int32_t*
   if (rows < 1 || rows > kMaxBatch) return tkv_status(report(TKV_ERR_INVALID_ARG, "rows must be 1 to %d", kMaxBatch));
   ReadQParams p{};
   if (int st = check_dtype(dtype)) return tkv_status(st);
-  if (int st = check_pool(&p.p, const_cast<int8_t*>(pool), const_cast<float*>(scales), pool_pages, n_kv_heads, head_dim, page_table,
-                          max_pages, const_cast<uint32_t*>(slot_mask)))
+  if (int st = check_pool(&p.p, pool, scales, pool_pages, n_kv_heads, head_dim, page_table, max_pages, slot_mask))
     return tkv_status(st);
   if (!first || !lens) return tkv_status(report(TKV_ERR_INVALID_ARG, "null pointer"));
   for (int i = 0; i < rows; ++i)
@@ -503,43 +307,6 @@ tkv_status tkv_read_quantized(int32_t rows, const int32_t* first, const int32_t*
     else read_quantized_kernel<float, 128><<<n, kCopyThreads, 0, s>>>(p);
   }
   return tkv_status(launched("quantised read", cudaGetLastError()));
-}
-
-tkv_status tkv_quantized_attention_scratch_size(int32_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
-                                                int32_t dtype, const int32_t* page_counts, int32_t max_pages,
-                                                int32_t want_alpha, size_t* scratch_bytes) {
-  if (!scratch_bytes) return tkv_status(report(TKV_ERR_INVALID_ARG, "null pointer"));
-  AttendQParams p{};
-  return tkv_status(plan_attend(&p, batch, n_q_heads, n_kv_heads, head_dim, dtype, page_counts, max_pages, want_alpha, scratch_bytes));
-}
-
-tkv_status tkv_quantized_attention(int32_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t dtype,
-                                   const void* q, const int8_t* pool, const float* scales, int64_t pool_pages,
-                                   const int32_t* page_table, const uint32_t* slot_mask, const int32_t* page_counts,
-                                   int32_t max_pages, void* out, float* alpha_sum, void* scratch, size_t scratch_bytes,
-                                   tkv_stream stream) {
-  AttendQParams p{};
-  size_t need;
-  if (int st = plan_attend(&p, batch, n_q_heads, n_kv_heads, head_dim, dtype, page_counts, max_pages, alpha_sum != nullptr, &need))
-    return tkv_status(st);
-  if (int st = check_pool(&p.p, const_cast<int8_t*>(pool), const_cast<float*>(scales), pool_pages, n_kv_heads, head_dim, page_table,
-                          max_pages, const_cast<uint32_t*>(slot_mask)))
-    return tkv_status(st);
-  if (!q || !out || !slot_mask) return tkv_status(report(TKV_ERR_INVALID_ARG, "null pointer"));
-  if (misaligned(q, 16) || misaligned(out, 16) || misaligned(alpha_sum, 16))
-    return tkv_status(report(TKV_ERR_INVALID_ARG, "q, out and alpha_sum must be 16-byte aligned"));
-  if (need) {
-    if (!scratch) return tkv_status(report(TKV_ERR_INVALID_ARG, "null scratch: need %zu bytes", need));
-    if (scratch_bytes < need) return tkv_status(report(TKV_ERR_CAPACITY, "scratch too small: need %zu bytes", need));
-    if (misaligned(scratch, 256)) return tkv_status(report(TKV_ERR_INVALID_ARG, "scratch not 256-byte aligned"));
-  }
-  p.q = q; p.out = out; p.alpha = alpha_sum;
-  p.stats = need ? static_cast<float2*>(scratch) : nullptr;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (dtype == TKV_DTYPE_BF16) e = head_dim == 64 ? launch_attend<__nv_bfloat16, 64>(p, s) : launch_attend<__nv_bfloat16, 128>(p, s);
-  else e = head_dim == 64 ? launch_attend<float, 64>(p, s) : launch_attend<float, 128>(p, s);
-  return tkv_status(launched("quantised attention", e));
 }
 
 }  // extern "C"
