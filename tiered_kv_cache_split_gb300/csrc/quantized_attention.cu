@@ -108,9 +108,6 @@ constexpr int kLow = 0x4140, kHigh = 0x4342;
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
-__device__ __forceinline__ void copy8(uint32_t to, const void* from) {
-  asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
-}
 __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;"); }
 template <int N> __device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
@@ -151,27 +148,30 @@ struct Smem {
   static constexpr int bytes = o_stat + kWarps * heads * 16;
 };
 
-// The copies of one page by one warp. Each thread copies what it alone will read,
-// so its own wait is all the synchronisation there is.
+// Where the 16-byte chunk c of row r of a slot lies (rows 0 .. 15 are K's, 16 .. 31
+// V's): rows are whole 128-byte lines on the way in, and the fragments' reads
+// (below) touch every bank group once.
 template <int D>
-__device__ __forceinline__ void copy_page(uint32_t to, const int8_t* block, int g, int t, int lane) {
-  const int8_t* v = block + kPage * D;
-  if (D == 128) {
+__device__ __forceinline__ int chunk_at(int r, int c) {
+  if (D == 128) return r * 128 + (r < kPage ? c ^ (r & 1) << 2 : c ^ (r & 6)) * 16;
+  const int u = (r & 1) * 4 + c;                                      // chunk of a pair of rows
+  return (r >> 1) * 128 + (r < kPage ? u : u ^ (r & 6)) * 16;
+}
+
+// The copies of one page by one warp: 512 bytes in a row each.
+template <int D>
+__device__ __forceinline__ void copy_page(uint32_t to, const int8_t* block, int lane) {
+  constexpr int kRowChunks = D / 16;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) copy16(to + c * 512 + lane * 16, block + (g + (c >> 1) * 8) * D + (c & 1) * 64 + t * 16);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) copy16(to + (4 + c) * 512 + lane * 16, v + (2 * t + (c & 1) + (c >> 1) * 8) * D + g * 16);
-  } else {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) copy16(to + c * 512 + lane * 16, block + (g + c * 8) * D + t * 16);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) copy8(to + 1024 + c * 256 + lane * 8, v + (2 * t + (c & 1) + (c >> 1) * 8) * D + g * 8);
+  for (int i = 0; i < 2 * kPage * D / 512; ++i) {
+    const int at = i * 32 + lane;
+    copy16(to + chunk_at<D>(at / kRowChunks, at % kRowChunks), block + at * 16);
   }
 }
 
 // A CTA per unit: pages j0 .. j1 of a sequence, a KV head and a group of its
-// query heads. Page j goes to warp j % 4, which keeps 3 (D 64: 6) pages on their
-// way in thread-private slots of shared memory.
+// query heads. Page j goes to warp j % 4, which keeps 2 (D 64: 5) pages on their
+// way besides the one it reads; no warp waits for another before the end.
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_kernel(const __grid_constant__ AttendParams p) {
   using S = Smem<T, D, NT>;
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
     if (i < mine) {
       const int id = s_info[warp + i * kWarps].x;
       if (id >= 0)
-        copy_page<D>(ring + (i % R::stages) * R::page_bytes, p.p.codes + (static_cast<int64_t>(id) * p.p.hkv + h) * R::page_bytes, g, t, lane);
+        copy_page<D>(ring + (i % R::stages) * R::page_bytes, p.p.codes + (static_cast<int64_t>(id) * p.p.hkv + h) * R::page_bytes, lane);
     }
     commit();
   };
@@ -258,8 +258,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
 #pragma unroll
   for (int i = 0; i < R::stages - 1; ++i) start(i);
   for (int i = 0; i < mine; ++i) {
+    wait_copies<R::stages - 2>();
+    __syncwarp();                                  // page i is here for all lanes, and page i - 1 is read
     start(i + R::stages - 1);
-    wait_copies<R::stages - 1>();
     const int page = warp + i * kWarps;
     const int4 info = s_info[page];
     const uint32_t live = info.y & kFullMask;
@@ -275,8 +276,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
     float s[NT][4] = {};
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-      const uint4 a = *reinterpret_cast<const uint4*>(slot + c * 512 + lane * 16);
-      const uint4 d = *reinterpret_cast<const uint4*>(slot + (kChunks + c) * 512 + lane * 16);
+      const uint4 a = *reinterpret_cast<const uint4*>(slot + chunk_at<D>(g, c * 4 + t));
+      const uint4 d = *reinterpret_cast<const uint4*>(slot + chunk_at<D>(g + 8, c * 4 + t));
       const uint32_t av[4] = {a.x, a.y, a.z, a.w}, dv[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
@@ -361,11 +362,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
     uint32_t v[4][D / 32];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
+      const int row = kPage + 2 * t + (c & 1) + (c >> 1) * 8;
       if (D == 128) {
-        const uint4 x = *reinterpret_cast<const uint4*>(slot + (4 + c) * 512 + lane * 16);
+        const uint4 x = *reinterpret_cast<const uint4*>(slot + chunk_at<D>(row, g));
         v[c][0] = x.x, v[c][1] = x.y, v[c][D / 32 - 2] = x.z, v[c][D / 32 - 1] = x.w;
       } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(slot + 1024 + c * 256 + lane * 8);
+        const uint2 x = *reinterpret_cast<const uint2*>(slot + chunk_at<D>(row, g >> 1) + (g & 1) * 8);
         v[c][0] = x.x, v[c][1] = x.y;
       }
     }
