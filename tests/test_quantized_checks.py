@@ -129,6 +129,7 @@ def attend(lib, batch=2, hq=8, hkv=2, d=64, dt=L.DTYPE_BF16, q=I, pool=I, scales
     (dict(q=None), ("null",)), (dict(pool=None), ("null",)), (dict(scales=None), ("null",)), (dict(table=None), ("null",)),
     (dict(mask=None), ("null",)), (dict(out=None), ("null",)), (dict(q=I + 8), ("aligned",)), (dict(out=I + 8), ("aligned",)),
     (dict(pool=I + 8), ("aligned",)), (dict(scales=I + 4), ("aligned",)), (dict(alpha=I + 4), ("aligned",)),
+    (dict(batch=64, hq=4096, hkv=4096, counts=(16384,) * 64, width=16384), ("2^30",)),
 ])
 def test_attention_refusals(lib, bad, words):
     refused(lib, attend(lib, **bad), L.ERR_INVALID_ARG, *words)

@@ -35,9 +35,12 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kUnitPages = 384;     // most pages of a unit: what its shared memory describes
+constexpr int kWindow = 384;        // pages that shared memory describes at a time
+constexpr int kSegmentCost = 8;     // pages' time of a piece's start and end
+constexpr int kLeastPages = 16;     // pages of a CTA's stretch, at least
+constexpr int kWholePages = 24;     // pages of a sequence up to which its segments are not cut
 constexpr int kMergeThreads = 128;
-constexpr int kAlphaSlots = 1024;   // slots of an alpha CTA
+constexpr int kAlphaSlots = 256;    // slots of an alpha CTA
 constexpr int kSms = 152;
 constexpr float kNegInf = -INFINITY;
 constexpr float kWeightBits = 13.f; // weights are at most 2^15: reference lag and f below 2 each
@@ -46,23 +49,34 @@ template <typename T> struct Columns;  // heads of an 8-column tile, and columns
 template <> struct Columns<__nv_bfloat16> { static constexpr int heads = 8, parts = 1; };
 template <> struct Columns<float> { static constexpr int heads = 4, parts = 2; };
 
+// How a call is cut. A SEGMENT is the pages of a sequence for one KV head and one
+// group of its query heads. Either every CTA takes a segment (`whole`), or the
+// segments lie one behind the other on a line, each with kSegmentCost pages' room
+// ahead of its pages for its start and end, and CTA k takes the stretch
+// [k, k + 1) * share of that line: all CTAs run at once and read the same number
+// of pages, and a segment is cut only where a stretch ends. (Units of 72 pages in
+// several waves took 191 us where this takes 168, 4 x 131072 tokens of 8 heads:
+// every start waits out the queue that the running CTAs fill.) A PIECE is what a CTA has
+// of a segment; one that is not all of it leaves a partial, of which a CTA has two at
+// most: one that goes on from the CTA before (2 k), and one that starts here (2 k + 1).
 struct AttendParams {
   PoolRef p;
   const void* q;
   void* out;
   float* alpha;             // [B][Hkv][max_pages * 16], or null
-  float* part_o;            // [chunk][Hq][D]
-  float4* part_m;           // [chunk][Hq]: maximum, V's reference, sum
-  float* spill;             // [page of the call][Hkv][16][columns of heads], logits in base 2
-  int32_t B, Hq, G, groups; // groups: head groups of a KV head, each a unit of its own
+  float* part_o;            // [2 * CTAs][heads of a unit][D]
+  float4* part_m;           // [2 * CTAs][heads of a unit]: maximum, V's reference, sum
+  float2* stats;            // [B][Hq] maximum and sum of rows written whole, for alpha
+  float* spill;             // [page of the call][Hkv][16][groups * heads of a unit], logits in base 2
+  int32_t B, Hq, G, groups; // groups: head groups of a KV head
   int32_t max_pages;
-  int32_t units;
+  int32_t ctas, share, total, whole;
+  int32_t alpha_parts;      // alpha CTAs of a sequence and KV head
   float qscale;             // log2(e) / sqrt(D)
-  int32_t count[kMaxBatch];            // pages
-  int32_t order[kMaxBatch];            // sequences by decreasing pages per unit
-  int32_t order_first[kMaxBatch + 1];  // prefix sums of their chunks in that order
-  int32_t chunk0[kMaxBatch + 1];       // prefix sums of the chunks by sequence
-  int32_t page0[kMaxBatch + 1];        // prefix sums of the pages
+  int32_t count[kMaxBatch];     // pages
+  int32_t order[kMaxBatch];     // whole: sequences, longest first
+  int32_t base[kMaxBatch + 1];  // where the segments of a sequence start on the line
+  int32_t page0[kMaxBatch + 1]; // prefix sums of the pages
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -113,8 +127,7 @@ template <int N> __device__ __forceinline__ void wait_copies() { asm volatile("c
 
 // What a unit keeps of a page: id (-1: none of its slots counts), valid slots and
 // the power k of V's scale, K's scale in the logits' units, and V's scale as f in f 2^k.
-__device__ __forceinline__ int4 page_info(const AttendParams& p, int b, int page, int h) {
-  const int32_t id = p.p.table[b * p.p.table_stride + page];
+__device__ __forceinline__ int4 page_info(const AttendParams& p, int32_t id, int h) {
   if (id < 0 || id >= p.p.pages) return make_int4(-1, 0, 0, 0);
   const uint32_t live = p.p.mask[id] & kFullMask;
   if (!live) return make_int4(-1, 0, 0, 0);
@@ -134,7 +147,9 @@ __device__ __forceinline__ int4 page_info(const AttendParams& p, int b, int page
 template <int D>
 struct Ring {
   static constexpr int page_bytes = 2 * kPage * D;                    // a head's K and V codes
-  static constexpr int stages = D == 128 ? 3 : 6;                     // 12 KB per warp
+  // 8 KB per warp. More in flight only lengthens the queues, and with them each
+  // start and the spread of the ends: with 12 KB the same call took 179 us, not 168.
+  static constexpr int stages = D == 128 ? 2 : 4;
   static constexpr int bytes = kWarps * stages * page_bytes;
 };
 
@@ -144,7 +159,7 @@ struct Smem {
   static constexpr int out_row = D + 4;                               // floats; rows start in different banks
   static constexpr int merge_bytes = kWarps * heads * out_row * 4;
   static constexpr int o_info = Ring<D>::bytes > merge_bytes ? Ring<D>::bytes : merge_bytes;
-  static constexpr int o_stat = o_info + kUnitPages * 16;
+  static constexpr int o_stat = o_info + kWindow * 16;
   static constexpr int bytes = o_stat + kWarps * heads * 16;
 };
 
@@ -169,9 +184,10 @@ __device__ __forceinline__ void copy_page(uint32_t to, const int8_t* block, int 
   }
 }
 
-// A CTA per unit: pages j0 .. j1 of a sequence, a KV head and a group of its
-// query heads. Page j goes to warp j % 4, which keeps 2 (D 64: 5) pages on their
-// way besides the one it reads; no warp waits for another before the end.
+// Page j of a piece goes to warp j % 4, which keeps one (D 64: 3) on its way
+// besides the one it reads; no warp waits for another before the end of a piece.
+// The first copies need the page ids only, so they leave before the masks, scales
+// and queries are here.
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_kernel(const __grid_constant__ AttendParams p) {
   using S = Smem<T, D, NT>;
@@ -184,372 +200,463 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
   int4* s_info = reinterpret_cast<int4*>(smem + S::o_info);
   float4* s_stat = reinterpret_cast<float4*>(smem + S::o_stat);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  // the unit
-  const int per_chunk = p.p.hkv * p.groups;
-  const int rank = blockIdx.x / per_chunk, rest = blockIdx.x % per_chunk;
-  const int h = rest / p.groups, group = rest % p.groups;
-  int lo = 0, hi = p.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.order_first[mid] <= rank) lo = mid; else hi = mid - 1;
-  }
-  const int b = p.order[lo], chunk = rank - p.order_first[lo], chunks = p.order_first[lo + 1] - p.order_first[lo];
-  const int each = p.count[b] / chunks, longer = p.count[b] % chunks;
-  const int j0 = chunk * each + min(chunk, longer), n = each + (chunk < longer);
-  for (int i = tid; i < n; i += kThreads) s_info[i] = page_info(p, b, j0 + i, h);
-
-  // queries: fragments of Q^T, and the power of two taken out of each head
-  const int head0 = h * p.G + group * S::heads;    // first head of the group
-  const int nheads = min(S::heads, p.G - group * S::heads);
-  uint32_t qf[NT][kChunks * 4][2];
-  float qpow[NT][kOwn];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int head = nt * kHeads + g / kParts, part = g % kParts;
-    float x[kChunks * 16], top = 0.f;
-    const T* q = static_cast<const T*>(p.q) + (static_cast<int64_t>(b) * p.Hq + head0 + head) * D + t * 16;
-#pragma unroll
-    for (int i = 0; i < kChunks * 16; i += Vec<T>::n)
-      Vec<T>::unpack(head < nheads ? *reinterpret_cast<const int4*>(q + (i >> 4) * 64 + (i & 15)) : make_int4(0, 0, 0, 0), x + i);
-#pragma unroll
-    for (int i = 0; i < kChunks * 16; ++i) top = fmaxf(top, fabsf(x[i]));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -126);
-    const float down0 = __uint_as_float(static_cast<uint32_t>(127 - e / 2) << 23), down1 = __uint_as_float(static_cast<uint32_t>(127 - (e - e / 2)) << 23);
-#pragma unroll
-    for (int i = 0; i < kChunks * 16; i += 2) {
-      float y[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        y[j] = x[i + j] * down0 * down1;
-        if (kParts == 2 && part == 1) y[j] = (y[j] - __half2float(__float2half_rn(y[j]))) * 2048.f;
-      }
-      qf[nt][i >> 2][(i >> 1) & 1] = half2_bits(y[0], y[1]);
-    }
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) {
-      const int of = __shfl_sync(0xffffffffu, e, (2 * t + i) * 4);
-      qpow[nt][i] = __uint_as_float(static_cast<uint32_t>(of + 127) << 23);  // infinity for a row that holds one
+  const int segments = p.p.hkv * p.groups;         // of a sequence
+  int b = 0, pos = 0, end = 1;                     // the CTA's stretch
+  if (p.whole) {
+    b = p.order[blockIdx.x / segments];
+  } else {
+    pos = blockIdx.x * p.share;
+    end = min(pos + p.share, p.total);
+    int hi = p.B - 1;
+    while (b < hi) {
+      const int mid = (b + hi + 1) >> 1;
+      if (p.base[mid] <= pos) b = mid; else hi = mid - 1;
     }
   }
-
-  float o[NT][kTiles][4] = {};
-  float m[NT][kOwn], r[NT][kOwn], z[NT][kOwn];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) m[nt][i] = r[nt][i] = kNegInf, z[nt][i] = 0.f;
-  __syncthreads();
-
-  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * R::stages * R::page_bytes;
-  const int mine = n > warp ? (n - warp + kWarps - 1) / kWarps : 0;
-  auto start = [&](int i) {                        // the copies of this warp's page i, if there is one
-    if (i < mine) {
-      const int id = s_info[warp + i * kWarps].x;
-      if (id >= 0)
-        copy_page<D>(ring + (i % R::stages) * R::page_bytes, p.p.codes + (static_cast<int64_t>(id) * p.p.hkv + h) * R::page_bytes, lane);
-    }
-    commit();
-  };
-  float* spill = p.spill ? p.spill + ((static_cast<int64_t>(p.page0[b] + j0) * p.p.hkv + h) * kPage * p.groups) * S::heads + group * S::heads : nullptr;
-  const int64_t spill_page = static_cast<int64_t>(p.p.hkv) * kPage * p.groups * S::heads;
-  const int spill_slot = p.groups * S::heads;
-#pragma unroll
-  for (int i = 0; i < R::stages - 1; ++i) start(i);
-  for (int i = 0; i < mine; ++i) {
-    wait_copies<R::stages - 2>();
-    __syncwarp();                                  // page i is here for all lanes, and page i - 1 is read
-    start(i + R::stages - 1);
-    const int page = warp + i * kWarps;
-    const int4 info = s_info[page];
-    const uint32_t live = info.y & kFullMask;
-    if (info.x < 0) {                              // an empty page: nothing was copied
-      if (spill) {
-        float* at = spill + page * spill_page;
-        for (int w = lane; w < kPage * S::heads; w += 32) at[(w / S::heads) * spill_slot + w % S::heads] = kNegInf;
-      }
-      continue;
-    }
-    const char* slot = smem + (warp * R::stages + i % R::stages) * R::page_bytes;
-    // S^T = K Q^T
-    float s[NT][4] = {};
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const uint4 a = *reinterpret_cast<const uint4*>(slot + chunk_at<D>(g, c * 4 + t));
-      const uint4 d = *reinterpret_cast<const uint4*>(slot + chunk_at<D>(g + 8, c * 4 + t));
-      const uint32_t av[4] = {a.x, a.y, a.z, a.w}, dv[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const uint32_t x = av[w] ^ 0x80808080u, y = dv[w] ^ 0x80808080u;
-        const uint32_t a0 = codes2<kLow>(x), a1 = codes2<kLow>(y), a2 = codes2<kHigh>(x), a3 = codes2<kHigh>(y);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma(s[nt], a0, a1, a2, a3, qf[nt][c * 4 + w][0], qf[nt][c * 4 + w][1]);
-      }
-    }
-    // logits (base 2) of keys g and g + 8
-    const float sk = __int_as_float(info.z), f = __int_as_float(info.w);
-    const float k = static_cast<float>((info.y >> 16) - 256);
-    const bool live0 = live >> g & 1, live1 = live >> (g + 8) & 1;
-    float l[NT][kOwn][2];
-    bool rise = false;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if (kParts == 2) {
-        s[nt][0] += s[nt][1] * 0x1p-11f;
-        s[nt][2] += s[nt][3] * 0x1p-11f;
-      }
-#pragma unroll
-      for (int j = 0; j < kOwn; ++j) {
-        l[nt][j][0] = live0 ? s[nt][j] * sk * qpow[nt][j] : kNegInf;
-        l[nt][j][1] = live1 ? s[nt][2 + j] * sk * qpow[nt][j] : kNegInf;
-        const float top = fmaxf(l[nt][j][0], l[nt][j][1]);
-        rise |= top > m[nt][j] + 1.f || top + k > r[nt][j] + 1.f;
-      }
-      if (spill) {
-        float* at = spill + page * spill_page + g * spill_slot + nt * kHeads + t * kOwn;
-        if (kOwn == 2) {
-          *reinterpret_cast<float2*>(at) = make_float2(l[nt][0][0], l[nt][kOwn - 1][0]);
-          *reinterpret_cast<float2*>(at + 8 * spill_slot) = make_float2(l[nt][0][1], l[nt][kOwn - 1][1]);
-        } else {
-          at[0] = l[nt][0][0];
-          at[8 * spill_slot] = l[nt][0][1];
-        }
-      }
-    }
-    if (__any_sync(0xffffffffu, rise)) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float keep[2];
-#pragma unroll
-        for (int j = 0; j < kOwn; ++j) {
-          float top = fmaxf(l[nt][j][0], l[nt][j][1]);
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-          const float m1 = fmaxf(m[nt][j], top), r1 = fmaxf(r[nt][j], top + k);
-          z[nt][j] *= m1 == kNegInf ? 1.f : ex2(m[nt][j] - m1);
-          keep[j] = r1 == kNegInf ? 1.f : ex2(r[nt][j] - r1);
-          if (kOwn == 1) keep[1] = keep[0];
-          m[nt][j] = m1;
-          r[nt][j] = r1;
-        }
-#pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-          o[nt][i][0] *= keep[0], o[nt][i][2] *= keep[0];
-          o[nt][i][1] *= keep[1], o[nt][i][3] *= keep[1];
-        }
-      }
-    }
-    // weights, and P^T as the second product takes it
-    uint32_t pf[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float w[2][2];
-#pragma unroll
-      for (int j = 0; j < kOwn; ++j) {
-        const float mz = m[nt][j] == kNegInf ? 0.f : m[nt][j], ro = r[nt][j] == kNegInf ? 0.f : k + kWeightBits - r[nt][j];
-        z[nt][j] += ex2(l[nt][j][0] - mz) + ex2(l[nt][j][1] - mz);
-        w[0][j] = live0 ? ex2(l[nt][j][0] + ro) * f : 0.f;
-        w[1][j] = live1 ? ex2(l[nt][j][1] + ro) * f : 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (kParts == 2) w[i][1] = (w[i][0] - __half2float(__float2half_rn(w[i][0]))) * 2048.f;
-        pf[nt][i] = transposed(half2_bits(w[i][0], w[i][1]));
-      }
-    }
-    // O^T += V^T P^T: V's rows of four tokens, 16 (D 64: 8) of their codes
-    uint32_t v[4][D / 32];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int row = kPage + 2 * t + (c & 1) + (c >> 1) * 8;
-      if (D == 128) {
-        const uint4 x = *reinterpret_cast<const uint4*>(slot + chunk_at<D>(row, g));
-        v[c][0] = x.x, v[c][1] = x.y, v[c][D / 32 - 2] = x.z, v[c][D / 32 - 1] = x.w;
-      } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(slot + chunk_at<D>(row, g >> 1) + (g & 1) * 8);
-        v[c][0] = x.x, v[c][1] = x.y;
-      }
-    }
-#pragma unroll
-    for (int w = 0; w < D / 32; ++w) {
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int pick = half ? 0x7362 : 0x5140;   // codes 2, 3 or 0, 1 of both tokens
-        const uint32_t x = __byte_perm(v[0][w], v[1][w], pick) ^ 0x80808080u, y = __byte_perm(v[2][w], v[3][w], pick) ^ 0x80808080u;
-        const uint32_t a0 = codes2<kLow>(x), a1 = codes2<kHigh>(x), a2 = codes2<kLow>(y), a3 = codes2<kHigh>(y);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma(o[nt][w * 2 + half], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-      }
-    }
-  }
-  wait_copies<0>();
-  __syncthreads();                                 // the ring becomes the merge's
-
-  // join the four warps
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int j = 0; j < kOwn; ++j) {
-#pragma unroll
-      for (int d = 4; d < 32; d <<= 1) z[nt][j] += __shfl_xor_sync(0xffffffffu, z[nt][j], d);
-      if (g == 0) s_stat[warp * S::heads + nt * kHeads + t * kOwn + j] = make_float4(m[nt][j], r[nt][j], z[nt][j], 0.f);
-    }
-  __syncthreads();
-  float* s_out = reinterpret_cast<float*>(smem);
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int j = 0; j < kOwn; ++j) {
-      const int head = nt * kHeads + t * kOwn + j;
-      float top = kNegInf;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_stat[w * S::heads + head].y);
-      const float keep = r[nt][j] == kNegInf ? (z[nt][j] == z[nt][j] ? 0.f : NAN) : ex2(r[nt][j] - top);
-      float* row = s_out + (warp * S::heads + head) * S::out_row + g * (D / 8);
-#pragma unroll
-      for (int i = 0; i < kTiles; i += 2) {
-        float4 x;
-        if (kParts == 2) {
-          x = make_float4(o[nt][i][0] + o[nt][i][1] * 0x1p-11f, o[nt][i][2] + o[nt][i][3] * 0x1p-11f,
-                          o[nt][i + 1][0] + o[nt][i + 1][1] * 0x1p-11f, o[nt][i + 1][2] + o[nt][i + 1][3] * 0x1p-11f);
-        } else {
-          x = make_float4(o[nt][i][j], o[nt][i][2 + j], o[nt][i + 1][j], o[nt][i + 1][2 + j]);
-        }
-        *reinterpret_cast<float4*>(row + i * 2) = make_float4(x.x * keep, x.y * keep, x.z * keep, x.w * keep);
-      }
-    }
-  __syncthreads();
-  const int64_t part = static_cast<int64_t>(p.chunk0[b] + chunk) * p.Hq + head0;
-  for (int i = tid; i < nheads * (D / 4); i += kThreads) {
-    const int head = i / (D / 4), d = i % (D / 4) * 4;
-    float top = kNegInf, ref = kNegInf, sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float4 st = s_stat[w * S::heads + head];
-      top = fmaxf(top, st.x);
-      ref = fmaxf(ref, st.y);
-    }
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float4 st = s_stat[w * S::heads + head];
-      sum += st.x == kNegInf ? st.z : st.z * ex2(st.x - top);
-      const float4 y = *reinterpret_cast<const float4*>(s_out + (w * S::heads + head) * S::out_row + d);
-      x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-    }
-    if (p.part_m && d == 0) p.part_m[part + head] = make_float4(top, ref, sum, 0.f);
-    if (chunks == 1) {
-      const float by = sum == 0.f ? 0.f : 1.f / sum, e = sum == 0.f ? 0.f : ref - top - kWeightBits;
-      put4(static_cast<T*>(p.out) + (static_cast<int64_t>(b) * p.Hq + head0 + head) * D + d,
-           make_float4(times_ex2(x.x * by, e), times_ex2(x.y * by, e), times_ex2(x.z * by, e), times_ex2(x.w * by, e)));
+  bool later = false;                              // not the first window: shared memory may be in use
+  while (pos < end) {
+    int segment, lo = 0, hi = p.count[b], stop = end;  // pages lo .. hi - 1 of it
+    const int n = hi;
+    bool last = false;                             // the stretch goes on with the next sequence
+    if (p.whole) {
+      segment = blockIdx.x % segments;
     } else {
-      *reinterpret_cast<float4*>(p.part_o + (part + head) * D + d) = x;
+      const int span = n + kSegmentCost;
+      segment = (pos - p.base[b]) / span;
+      const int from = p.base[b] + segment * span;
+      stop = min(end, from + span);
+      last = stop == p.base[b + 1];
+      lo = max(pos - from - kSegmentCost, 0);
+      hi = max(stop - from - kSegmentCost, 0);
+      if (hi <= lo && !(n == 0 && pos == from)) {  // room ahead of the pages only
+        pos = stop;
+        b += last;
+        continue;
+      }
     }
+    const int h = segment / p.groups, group = segment % p.groups;
+    const int head0 = h * p.G + group * S::heads;  // first head of the group
+    const int nheads = min(S::heads, p.G - group * S::heads);
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * R::stages * R::page_bytes;
+    const int32_t* row = p.p.table + b * p.p.table_stride;
+
+    uint32_t qf[NT][kChunks * 4][2];
+    float qpow[NT][kOwn];
+    float o[NT][kTiles][4];
+    float m[NT][kOwn], r[NT][kOwn], z[NT][kOwn];
+    for (int w0 = lo;; w0 += kWindow) {
+      const int count = min(kWindow, hi - w0), mine = count > warp ? (count - warp + kWarps - 1) / kWarps : 0;
+      auto copy = [&](int i, int id) {
+        if (id >= 0 && id < p.p.pages)
+          copy_page<D>(ring + (i % R::stages) * R::page_bytes, p.p.codes + (static_cast<int64_t>(id) * p.p.hkv + h) * R::page_bytes, lane);
+        commit();
+      };
+      auto start = [&](int i) { copy(i, i < mine ? s_info[warp + i * kWarps].x : -1); };
+      int32_t first[R::stages - 1], ids[kWindow / kThreads];
+#pragma unroll
+      for (int i = 0; i < R::stages - 1; ++i) first[i] = i < mine ? row[w0 + warp + i * kWarps] : -1;
+#pragma unroll
+      for (int i = 0; i < kWindow / kThreads; ++i) ids[i] = tid + i * kThreads < count ? row[w0 + tid + i * kThreads] : -1;
+      if (later) __syncthreads();                  // what the last window or piece left is read
+      later = true;
+#pragma unroll
+      for (int i = 0; i < R::stages - 1; ++i) copy(i, first[i]);
+#pragma unroll
+      for (int i = 0; i < kWindow / kThreads; ++i)
+        if (tid + i * kThreads < count) s_info[tid + i * kThreads] = page_info(p, ids[i], h);
+      if (w0 == lo) {
+        // queries: fragments of Q^T, and the power of two taken out of each head
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int head = nt * kHeads + g / kParts, part = g % kParts;
+          float x[kChunks * 16], top = 0.f;
+          const T* q = static_cast<const T*>(p.q) + (static_cast<int64_t>(b) * p.Hq + head0 + head) * D + t * 16;
+#pragma unroll
+          for (int i = 0; i < kChunks * 16; i += Vec<T>::n)
+            Vec<T>::unpack(head < nheads ? *reinterpret_cast<const int4*>(q + (i >> 4) * 64 + (i & 15)) : make_int4(0, 0, 0, 0), x + i);
+#pragma unroll
+          for (int i = 0; i < kChunks * 16; ++i) top = fmaxf(top, fabsf(x[i]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -126);
+          const float down0 = __uint_as_float(static_cast<uint32_t>(127 - e / 2) << 23), down1 = __uint_as_float(static_cast<uint32_t>(127 - (e - e / 2)) << 23);
+#pragma unroll
+          for (int i = 0; i < kChunks * 16; i += 2) {
+            float y[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              y[j] = x[i + j] * down0 * down1;
+              if (kParts == 2 && part == 1) y[j] = (y[j] - __half2float(__float2half_rn(y[j]))) * 2048.f;
+            }
+            qf[nt][i >> 2][(i >> 1) & 1] = half2_bits(y[0], y[1]);
+          }
+#pragma unroll
+          for (int i = 0; i < kOwn; ++i) {
+            const int of = __shfl_sync(0xffffffffu, e, (2 * t + i) * 4);
+            qpow[nt][i] = __uint_as_float(static_cast<uint32_t>(of + 127) << 23);  // infinity for a row that holds one
+            m[nt][i] = r[nt][i] = kNegInf;
+            z[nt][i] = 0.f;
+          }
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+        }
+      }
+      __syncthreads();
+      float* spill = p.spill ? p.spill + ((static_cast<int64_t>(p.page0[b] + w0) * p.p.hkv + h) * kPage * p.groups) * S::heads + group * S::heads : nullptr;
+      const int64_t spill_page = static_cast<int64_t>(p.p.hkv) * kPage * p.groups * S::heads;
+      const int spill_slot = p.groups * S::heads;
+      for (int i = 0; i < mine; ++i) {
+        wait_copies<R::stages - 2>();
+        __syncwarp();                                  // page i is here for all lanes, and page i - 1 is read
+        start(i + R::stages - 1);
+        const int page = warp + i * kWarps;
+        const int4 info = s_info[page];
+        const uint32_t live = info.y & kFullMask;
+        if (info.x < 0) {                              // an empty page: nothing was copied
+          if (spill) {
+            float* at = spill + page * spill_page;
+            for (int w = lane; w < kPage * S::heads; w += 32) at[(w / S::heads) * spill_slot + w % S::heads] = kNegInf;
+          }
+          continue;
+        }
+        const char* slot = smem + (warp * R::stages + i % R::stages) * R::page_bytes;
+        // S^T = K Q^T
+        float s[NT][4] = {};
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          const uint4 a = *reinterpret_cast<const uint4*>(slot + chunk_at<D>(g, c * 4 + t));
+          const uint4 d = *reinterpret_cast<const uint4*>(slot + chunk_at<D>(g + 8, c * 4 + t));
+          const uint32_t av[4] = {a.x, a.y, a.z, a.w}, dv[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t x = av[w] ^ 0x80808080u, y = dv[w] ^ 0x80808080u;
+            const uint32_t a0 = codes2<kLow>(x), a1 = codes2<kLow>(y), a2 = codes2<kHigh>(x), a3 = codes2<kHigh>(y);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma(s[nt], a0, a1, a2, a3, qf[nt][c * 4 + w][0], qf[nt][c * 4 + w][1]);
+          }
+        }
+        // logits (base 2) of keys g and g + 8
+        const float sk = __int_as_float(info.z), f = __int_as_float(info.w);
+        const float k = static_cast<float>((info.y >> 16) - 256);
+        const bool live0 = live >> g & 1, live1 = live >> (g + 8) & 1;
+        float l[NT][kOwn][2];
+        bool rise = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if (kParts == 2) {
+            s[nt][0] += s[nt][1] * 0x1p-11f;
+            s[nt][2] += s[nt][3] * 0x1p-11f;
+          }
+#pragma unroll
+          for (int j = 0; j < kOwn; ++j) {
+            l[nt][j][0] = live0 ? s[nt][j] * sk * qpow[nt][j] : kNegInf;
+            l[nt][j][1] = live1 ? s[nt][2 + j] * sk * qpow[nt][j] : kNegInf;
+            const float top = fmaxf(l[nt][j][0], l[nt][j][1]);
+            rise |= top > m[nt][j] + 1.f || top + k > r[nt][j] + 1.f;
+          }
+          if (spill) {
+            float* at = spill + page * spill_page + g * spill_slot + nt * kHeads + t * kOwn;
+            if (kOwn == 2) {
+              *reinterpret_cast<float2*>(at) = make_float2(l[nt][0][0], l[nt][kOwn - 1][0]);
+              *reinterpret_cast<float2*>(at + 8 * spill_slot) = make_float2(l[nt][0][1], l[nt][kOwn - 1][1]);
+            } else {
+              at[0] = l[nt][0][0];
+              at[8 * spill_slot] = l[nt][0][1];
+            }
+          }
+        }
+        if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float keep[2];
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j) {
+              float top = fmaxf(l[nt][j][0], l[nt][j][1]);
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+              const float m1 = fmaxf(m[nt][j], top), r1 = fmaxf(r[nt][j], top + k);
+              z[nt][j] *= m1 == kNegInf ? 1.f : ex2(m[nt][j] - m1);
+              keep[j] = r1 == kNegInf ? 1.f : ex2(r[nt][j] - r1);
+              if (kOwn == 1) keep[1] = keep[0];
+              m[nt][j] = m1;
+              r[nt][j] = r1;
+            }
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+              o[nt][i][0] *= keep[0], o[nt][i][2] *= keep[0];
+              o[nt][i][1] *= keep[1], o[nt][i][3] *= keep[1];
+            }
+          }
+        }
+        // weights, and P^T as the second product takes it
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[2][2];
+#pragma unroll
+          for (int j = 0; j < kOwn; ++j) {
+            const float mz = m[nt][j] == kNegInf ? 0.f : m[nt][j], ro = r[nt][j] == kNegInf ? 0.f : k + kWeightBits - r[nt][j];
+            z[nt][j] += ex2(l[nt][j][0] - mz) + ex2(l[nt][j][1] - mz);
+            w[0][j] = live0 ? ex2(l[nt][j][0] + ro) * f : 0.f;
+            w[1][j] = live1 ? ex2(l[nt][j][1] + ro) * f : 0.f;
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (kParts == 2) w[i][1] = (w[i][0] - __half2float(__float2half_rn(w[i][0]))) * 2048.f;
+            pf[nt][i] = transposed(half2_bits(w[i][0], w[i][1]));
+          }
+        }
+        // O^T += V^T P^T: V's rows of four tokens, 16 (D 64: 8) of their codes
+        uint32_t v[4][D / 32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int row = kPage + 2 * t + (c & 1) + (c >> 1) * 8;
+          if (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(slot + chunk_at<D>(row, g));
+            v[c][0] = x.x, v[c][1] = x.y, v[c][D / 32 - 2] = x.z, v[c][D / 32 - 1] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(slot + chunk_at<D>(row, g >> 1) + (g & 1) * 8);
+            v[c][0] = x.x, v[c][1] = x.y;
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int pick = half ? 0x7362 : 0x5140;   // codes 2, 3 or 0, 1 of both tokens
+            const uint32_t x = __byte_perm(v[0][w], v[1][w], pick) ^ 0x80808080u, y = __byte_perm(v[2][w], v[3][w], pick) ^ 0x80808080u;
+            const uint32_t a0 = codes2<kLow>(x), a1 = codes2<kHigh>(x), a2 = codes2<kLow>(y), a3 = codes2<kHigh>(y);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma(o[nt][w * 2 + half], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+          }
+        }
+      }
+      if (w0 + kWindow >= hi) break;
+    }
+    wait_copies<0>();
+    __syncthreads();                                 // the ring becomes the merge's
+
+    // join the four warps
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < kOwn; ++j) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) z[nt][j] += __shfl_xor_sync(0xffffffffu, z[nt][j], d);
+        if (g == 0) s_stat[warp * S::heads + nt * kHeads + t * kOwn + j] = make_float4(m[nt][j], r[nt][j], z[nt][j], 0.f);
+      }
+    __syncthreads();
+    float* s_out = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < kOwn; ++j) {
+        const int head = nt * kHeads + t * kOwn + j;
+        float top = kNegInf;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_stat[w * S::heads + head].y);
+        const float keep = r[nt][j] == kNegInf ? (z[nt][j] == z[nt][j] ? 0.f : NAN) : ex2(r[nt][j] - top);
+        float* row = s_out + (warp * S::heads + head) * S::out_row + g * (D / 8);
+#pragma unroll
+        for (int i = 0; i < kTiles; i += 2) {
+          float4 x;
+          if (kParts == 2) {
+            x = make_float4(o[nt][i][0] + o[nt][i][1] * 0x1p-11f, o[nt][i][2] + o[nt][i][3] * 0x1p-11f,
+                            o[nt][i + 1][0] + o[nt][i + 1][1] * 0x1p-11f, o[nt][i + 1][2] + o[nt][i + 1][3] * 0x1p-11f);
+          } else {
+            x = make_float4(o[nt][i][j], o[nt][i][2 + j], o[nt][i + 1][j], o[nt][i + 1][2 + j]);
+          }
+          *reinterpret_cast<float4*>(row + i * 2) = make_float4(x.x * keep, x.y * keep, x.z * keep, x.w * keep);
+        }
+      }
+    __syncthreads();
+    const bool all = lo == 0 && hi == n;
+    const int64_t part = (2 * static_cast<int64_t>(blockIdx.x) + (lo == 0)) * S::heads;
+    for (int i = tid; i < nheads * (D / 4); i += kThreads) {
+      const int head = i / (D / 4), d = i % (D / 4) * 4;
+      float top = kNegInf, ref = kNegInf, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 st = s_stat[w * S::heads + head];
+        top = fmaxf(top, st.x);
+        ref = fmaxf(ref, st.y);
+      }
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 st = s_stat[w * S::heads + head];
+        sum += st.x == kNegInf ? st.z : st.z * ex2(st.x - top);
+        const float4 y = *reinterpret_cast<const float4*>(s_out + (w * S::heads + head) * S::out_row + d);
+        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+      }
+      const int64_t at = static_cast<int64_t>(b) * p.Hq + head0 + head;
+      if (all) {
+        const float by = sum == 0.f ? 0.f : 1.f / sum, e = sum == 0.f ? 0.f : ref - top - kWeightBits;
+        put4(static_cast<T*>(p.out) + at * D + d,
+             make_float4(times_ex2(x.x * by, e), times_ex2(x.y * by, e), times_ex2(x.z * by, e), times_ex2(x.w * by, e)));
+        if (p.stats && d == 0) p.stats[at] = make_float2(top, sum);
+      } else {
+        if (d == 0) p.part_m[part + head] = make_float4(top, ref, sum, 0.f);
+        *reinterpret_cast<float4*>(p.part_o + (part + head) * D + d) = x;
+      }
+    }
+    pos = stop;
+    b += last;
   }
 }
 
-// Joins the chunks of a row: the first B * Hq CTAs a query head each, four
-// warps taking every fourth chunk. The others (alpha) take 1024 slots of a
-// sequence and KV head: the maximum and sum of each query head from its chunks,
-// then the weights of the slots from their logits.
+// The partials of a segment: CTAs first .. last have a piece of it, and all of it
+// if they are the same.
+struct Pieces {
+  int first, last;
+  __device__ int64_t row(int cta, int heads) const { return (2 * static_cast<int64_t>(cta) + (cta == first)) * heads; }
+};
+__device__ __forceinline__ Pieces pieces_of(const AttendParams& p, int b, int segment) {
+  if (p.whole || p.count[b] == 0) return {0, 0};
+  const int from = p.base[b] + segment * (p.count[b] + kSegmentCost) + kSegmentCost;
+  return {from / p.share, (from + p.count[b] - 1) / p.share};
+}
+
+// (m, z) and (m1, z1) joined
+__device__ __forceinline__ void join(float& m, float& z, float m1, float z1) {
+  const float top = fmaxf(m, m1);
+  z = (m == kNegInf ? z : z * ex2(m - top)) + (m1 == kNegInf ? z1 : z1 * ex2(m1 - top));
+  m = top;
+}
+
+// The first B * Hq CTAs join the pieces of a query head each, a warp every fourth
+// piece. The others (alpha) take kAlphaSlots slots of a sequence and KV head: the
+// maximum and sum of each query head, then the slots' weights from their logits,
+// which are on their way meanwhile.
 template <typename T, int D>
-__global__ void __launch_bounds__(kMergeThreads) merge_quantized_kernel(const __grid_constant__ AttendParams p, int rows, int columns) {
+__global__ void __launch_bounds__(kMergeThreads) merge_quantized_kernel(const __grid_constant__ AttendParams p, int rows, int heads) {
   constexpr int E = D / 32;
   __shared__ float s_x[4][D];
+  __shared__ float4 s_st[4];
   __shared__ float2 s_head[64];
   cudaGridDependencySynchronize();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (static_cast<int>(blockIdx.x) < rows) {
-    const int b = blockIdx.x / p.Hq, hq = blockIdx.x % p.Hq;
-    const int c0 = p.chunk0[b], chunks = p.chunk0[b + 1] - c0;
-    T* out = static_cast<T*>(p.out) + static_cast<int64_t>(blockIdx.x) * D;
-    if (chunks == 1) return;                       // written by its unit
-    float m = kNegInf, r = kNegInf, z = 0.f;
-    for (int c = lane; c < chunks; c += 32) {
-      const float4 st = p.part_m[static_cast<int64_t>(c0 + c) * p.Hq + hq];
-      m = fmaxf(m, st.x);
-      r = fmaxf(r, st.y);
+    const int b = blockIdx.x / p.Hq, hq = blockIdx.x % p.Hq, h = hq / p.G, head = hq % p.G;
+    const Pieces pc = pieces_of(p, b, h * p.groups + head / heads);
+    if (pc.first == pc.last) return;               // written by its CTA
+    float m = kNegInf, r = kNegInf, z = 0.f, x[E] = {};
+#pragma unroll 4
+    for (int c = pc.first + warp; c <= pc.last; c += 4) {
+      const int64_t row = pc.row(c, heads) + head % heads;
+      const float4 st = p.part_m[row];
+      float y[E];
+#pragma unroll
+      for (int i = 0; i < E; ++i) y[i] = p.part_o[row * D + lane * E + i];
+      join(m, z, st.x, st.z);
+      const float top = fmaxf(r, st.y), keep = r == kNegInf ? 1.f : ex2(r - top), take = st.y == kNegInf ? 1.f : ex2(st.y - top);
+#pragma unroll
+      for (int i = 0; i < E; ++i) x[i] = x[i] * keep + y[i] * take;
+      r = top;
     }
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-      r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, d));
-    }
-    for (int c = lane; c < chunks; c += 32) {
-      const float4 st = p.part_m[static_cast<int64_t>(c0 + c) * p.Hq + hq];
-      z += st.x == kNegInf ? st.z : st.z * ex2(st.x - m);
-    }
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-    float x[E] = {};
-    for (int c = warp; c < chunks; c += 4) {
-      const int64_t row = static_cast<int64_t>(c0 + c) * p.Hq + hq;
-      const float ref = p.part_m[row].y, keep = ref == kNegInf ? 1.f : ex2(ref - r);
-#pragma unroll
-      for (int i = 0; i < E; ++i) x[i] += p.part_o[row * D + i * 32 + lane] * keep;
-    }
-#pragma unroll
-    for (int i = 0; i < E; ++i) s_x[warp][i * 32 + lane] = x[i];
+    for (int i = 0; i < E; ++i) s_x[warp][lane * E + i] = x[i];
+    if (lane == 0) s_st[warp] = make_float4(m, r, z, 0.f);
     __syncthreads();
-    const float by = z == 0.f ? 0.f : 1.f / z, e = z == 0.f ? 0.f : r - m - kWeightBits;
     if (tid < D / 4) {
+      m = r = kNegInf;
+      z = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        join(m, z, s_st[w].x, s_st[w].z);
+        r = fmaxf(r, s_st[w].y);
+      }
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         const float4 a = *reinterpret_cast<const float4*>(&s_x[w][tid * 4]);
-        y.x += a.x, y.y += a.y, y.z += a.z, y.w += a.w;
+        const float take = s_st[w].y == kNegInf ? 1.f : ex2(s_st[w].y - r);
+        y.x += a.x * take, y.y += a.y * take, y.z += a.z * take, y.w += a.w * take;
       }
-      put4(out + tid * 4, make_float4(times_ex2(y.x * by, e), times_ex2(y.y * by, e), times_ex2(y.z * by, e), times_ex2(y.w * by, e)));
+      const float by = z == 0.f ? 0.f : 1.f / z, e = z == 0.f ? 0.f : r - m - kWeightBits;
+      put4(static_cast<T*>(p.out) + static_cast<int64_t>(blockIdx.x) * D + tid * 4,
+           make_float4(times_ex2(y.x * by, e), times_ex2(y.y * by, e), times_ex2(y.z * by, e), times_ex2(y.w * by, e)));
     }
     return;
   }
   // alpha
-  const int most = (p.max_pages * kPage + kAlphaSlots - 1) / kAlphaSlots;
+  constexpr int kSlots = kAlphaSlots / kMergeThreads;  // of a thread
   int at = blockIdx.x - rows;
-  const int piece = at % most;
-  at /= most;
+  const int part = at % p.alpha_parts;
+  at /= p.alpha_parts;
   const int h = at % p.p.hkv, b = at / p.p.hkv;
-  const int slots = p.count[b] * kPage, first = piece * kAlphaSlots;
-  if (first >= slots) return;
-  const int c0 = p.chunk0[b], chunks = p.chunk0[b + 1] - c0;
-  for (int i = warp; i < p.G; i += 4) {
-    const int hq = h * p.G + i;
+  const int slots = p.count[b] * kPage, first = part * kAlphaSlots + tid;
+  if (part * kAlphaSlots >= slots) return;
+  const int columns = p.groups * heads;
+  float4 l[kSlots][2];
+  const float* spill[kSlots];
+  float* alpha = p.alpha + (static_cast<int64_t>(b) * p.p.hkv + h) * p.max_pages * kPage;
+  float before[kSlots], sum[kSlots];
+  bool any[kSlots];
+  auto load = [&](int j) {                         // logits of heads j .. j + 7
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        l[k][v] = make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
+        if (first + k * kMergeThreads < slots && j + 4 * v < columns) l[k][v] = *reinterpret_cast<const float4*>(spill[k] + j + 4 * v);
+      }
+  };
+#pragma unroll
+  for (int k = 0; k < kSlots; ++k) {
+    const int i = first + k * kMergeThreads;
+    spill[k] = p.spill + ((static_cast<int64_t>(p.page0[b] + i / kPage) * p.p.hkv + h) * kPage + i % kPage) * columns;
+    before[k] = i < slots ? alpha[i] : 0.f;
+    sum[k] = 0.f;
+    any[k] = false;
+  }
+  load(0);
+  for (int i = tid / 8; i < p.G; i += kMergeThreads / 8) {  // eight lanes per head
+    const uint32_t lanes = 0xffu << (lane & 24);
+    const Pieces pc = pieces_of(p, b, h * p.groups + i / heads);
     float m = kNegInf, z = 0.f;
-    for (int c = lane; c < chunks; c += 32) m = fmaxf(m, p.part_m[static_cast<int64_t>(c0 + c) * p.Hq + hq].x);
+    if (pc.first == pc.last) {
+      const float2 st = p.stats[static_cast<int64_t>(b) * p.Hq + h * p.G + i];
+      m = st.x, z = st.y;
+    } else {
+#pragma unroll 4
+      for (int c = pc.first + lane % 8; c <= pc.last; c += 8) {
+        const float4 st = p.part_m[pc.row(c, heads) + i % heads];
+        join(m, z, st.x, st.z);
+      }
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    for (int c = lane; c < chunks; c += 32) {
-      const float4 st = p.part_m[static_cast<int64_t>(c0 + c) * p.Hq + hq];
-      z += st.x == kNegInf ? st.z : st.z * ex2(st.x - m);
+      for (int d = 1; d < 8; d <<= 1) join(m, z, __shfl_xor_sync(lanes, m, d), __shfl_xor_sync(lanes, z, d));
     }
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-    if (lane == 0) s_head[i] = make_float2(m, z == 0.f ? 0.f : 1.f / z);
+    if (lane % 8 == 0) s_head[i] = make_float2(m, z == 0.f ? 0.f : 1.f / z);
   }
   __syncthreads();
-  float* alpha = p.alpha + (static_cast<int64_t>(b) * p.p.hkv + h) * p.max_pages * kPage;
-  for (int i = first + tid; i < min(slots, first + kAlphaSlots); i += kMergeThreads) {
-    const float* l = p.spill + ((static_cast<int64_t>(p.page0[b] + i / kPage) * p.p.hkv + h) * kPage + i % kPage) * columns;
-    float sum = 0.f;
-    bool any = false;
-    for (int j = 0; j < p.G; ++j) {
-      const float x = l[j];
-      if (x == kNegInf) continue;
-      any = true;
-      sum += ex2(x - s_head[j].x) * s_head[j].y;
-    }
-    if (any) alpha[i] += sum;
+  for (int j = 0; j < p.G; j += 8) {
+    if (j) load(j);
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const float x[4] = {l[k][v].x, l[k][v].y, l[k][v].z, l[k][v].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int head = j + 4 * v + i;
+          if (head >= p.G || x[i] == kNegInf) continue;
+          any[k] = true;
+          sum[k] += ex2(x[i] - s_head[head].x) * s_head[head].y;
+        }
+      }
   }
+#pragma unroll
+  for (int k = 0; k < kSlots; ++k)
+    if (any[k]) alpha[first + k * kMergeThreads] = before[k] + sum[k];
 }
 
 // ---- host side
 
 struct Plan {
-  int nt;                     // column tiles of a unit
-  int heads;                  // of a unit
-  bool merge;                 // some sequence has several chunks
-  size_t o_m, o_spill, bytes; // scratch
+  int nt;      // column tiles of a unit
+  int heads;   // of a unit
+  size_t o_m, o_stats, o_spill, bytes;  // scratch
 };
 
 int plan_attend(AttendParams* p, Plan* plan, int32_t batch, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype,
@@ -576,50 +683,30 @@ int plan_attend(AttendParams* p, Plan* plan, int32_t batch, int32_t Hq, int32_t 
     p->page0[b + 1] = p->page0[b] + n;
     most = std::max(most, n);
   }
-  // Pages per unit: the shortest estimated time, in pages' time of one of the CTAs
-  // that run at once; a unit's start and end cost about as much as kUnitCost pages,
-  // the launch that joins chunks kMergeCost.
-  constexpr double kUnitCost = 7, kMergeCost = 7;
-  const int64_t per_chunk = static_cast<int64_t>(Hkv) * p->groups, slots = kSms * (plan->nt == 1 ? 4 : 3);
-  int best = std::min(std::max(most, 1), kUnitPages);
-  double best_time = 1e300;
-  for (int parts = 1; parts <= kMaxSeqPages; parts = parts < 8 ? parts + 1 : parts + parts / 8) {
-    const int per = (most + parts - 1) / parts;
-    if (per > kUnitPages) continue;
-    if (per < 4) break;
-    int64_t units = 0;
-    for (int b = 0; b < batch; ++b) units += (p->count[b] + per - 1) / per;
-    units *= per_chunk;
-    const double work = static_cast<double>(p->page0[batch]) * per_chunk + kUnitCost * units;
-    const double longest = per + kUnitCost;
-    double time = units <= slots ? longest : std::max(longest, work / slots + 0.5 * longest);
-    if (parts > 1) time += kMergeCost;
-    if (time < best_time) best_time = time, best = per;
+  p->alpha_parts = (most * kPage + kAlphaSlots - 1) / kAlphaSlots;
+  const int64_t segments = static_cast<int64_t>(Hkv) * p->groups, slots = kSms * (plan->nt == 1 ? 4 : 3);
+  const int64_t total = segments * (p->page0[batch] + static_cast<int64_t>(batch) * kSegmentCost);
+  if (total > (int64_t(1) << 30)) return report(TKV_ERR_INVALID_ARG, "more than 2^30 pages and heads in one call");
+  p->total = static_cast<int32_t>(total);
+  p->share = static_cast<int32_t>(std::max<int64_t>((total + slots - 1) / slots, kSegmentCost + kLeastPages));
+  // Short segments stay whole: a CTA reads kWholePages in the time that the launch
+  // which joins partials would take.
+  p->whole = most <= kWholePages;
+  if (p->whole) {
+    p->ctas = static_cast<int32_t>(segments * batch);
+    for (int b = 0; b < batch; ++b) p->order[b] = b;
+    std::sort(p->order, p->order + batch, [&](int a, int b) { return p->count[a] != p->count[b] ? p->count[a] > p->count[b] : a < b; });
+  } else {
+    p->ctas = static_cast<int32_t>((total + p->share - 1) / p->share);
+    p->base[0] = 0;
+    for (int b = 0; b < batch; ++b) p->base[b + 1] = p->base[b] + static_cast<int32_t>(segments) * (p->count[b] + kSegmentCost);
   }
-  int chunks[kMaxBatch];
-  int64_t total = 0;
-  plan->merge = false;
-  p->chunk0[0] = 0;
-  for (int b = 0; b < batch; ++b) {
-    chunks[b] = std::max(1, (p->count[b] + best - 1) / best);
-    plan->merge |= chunks[b] > 1;
-    total += chunks[b];
-    p->chunk0[b + 1] = static_cast<int32_t>(total);
-    p->order[b] = b;
-  }
-  std::sort(p->order, p->order + batch, [&](int a, int b) {
-    const int64_t x = static_cast<int64_t>(p->count[a]) * chunks[b], y = static_cast<int64_t>(p->count[b]) * chunks[a];
-    return x != y ? x > y : a < b;
-  });
-  p->order_first[0] = 0;
-  for (int i = 0; i < batch; ++i) p->order_first[i + 1] = p->order_first[i] + chunks[p->order[i]];
-  if (total * per_chunk > INT32_MAX) return report(TKV_ERR_INVALID_ARG, "more than 2^31 units of work in one call");
-  p->units = static_cast<int32_t>(total * per_chunk);
   auto align = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t rows = static_cast<size_t>(total) * Hq;
-  plan->o_m = plan->merge ? align(rows * D * 4) : 0;
-  plan->o_spill = plan->o_m + (plan->merge || want_alpha ? align(rows * 16) : 0);
-  plan->bytes = plan->o_spill + (want_alpha ? align(static_cast<size_t>(p->page0[batch]) * Hkv * kPage * p->groups * plan->heads * 4) : 0);
+  const size_t rows = p->whole ? 0 : 2 * static_cast<size_t>(p->ctas) * plan->heads;
+  plan->o_m = align(rows * D * 4);
+  plan->o_stats = plan->o_m + align(rows * 16);
+  plan->o_spill = plan->o_stats + (want_alpha ? align(static_cast<size_t>(batch) * Hq * 8) : 0);
+  plan->bytes = plan->o_spill + (want_alpha ? align(static_cast<size_t>(p->page0[batch]) * segments * kPage * plan->heads * 4) : 0);
   return TKV_OK;
 }
 
@@ -629,17 +716,17 @@ cudaError_t launch_units(const AttendParams& p, cudaStream_t s) {
   static SharedMemoryOptIn opt_in;
   const cudaError_t e = opt_in.once(reinterpret_cast<const void*>(attend_quantized_kernel<T, D, NT>), bytes);
   if (e != cudaSuccess) return e;
-  attend_quantized_kernel<T, D, NT><<<static_cast<unsigned>(p.units), kThreads, bytes, s>>>(p);
+  attend_quantized_kernel<T, D, NT><<<static_cast<unsigned>(p.ctas), kThreads, bytes, s>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T, int D>
 cudaError_t launch_attend(const AttendParams& p, const Plan& plan, cudaStream_t s) {
   cudaError_t e = plan.nt == 1 ? launch_units<T, D, 1>(p, s) : launch_units<T, D, 2>(p, s);
-  if (e != cudaSuccess || !(plan.merge || p.alpha)) return e;
-  const int64_t rows = plan.merge ? static_cast<int64_t>(p.B) * p.Hq : 0;
-  const int64_t pieces = p.alpha ? static_cast<int64_t>(p.B) * p.p.hkv * ((p.max_pages * kPage + kAlphaSlots - 1) / kAlphaSlots) : 0;
-  if (rows + pieces > INT32_MAX) return cudaErrorInvalidConfiguration;
+  if (e != cudaSuccess || (p.whole && !p.alpha)) return e;
+  const int64_t rows = p.whole ? 0 : static_cast<int64_t>(p.B) * p.Hq;
+  const int64_t pieces = p.alpha ? static_cast<int64_t>(p.B) * p.p.hkv * p.alpha_parts : 0;
+  if (rows + pieces == 0) return e;                // no sequence has a page
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows + pieces));
   cfg.blockDim = dim3(kMergeThreads);
@@ -649,7 +736,7 @@ cudaError_t launch_attend(const AttendParams& p, const Plan& plan, cudaStream_t 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_quantized_kernel<T, D>, p, static_cast<int>(rows), p.groups * plan.heads);
+  return cudaLaunchKernelEx(&cfg, merge_quantized_kernel<T, D>, p, static_cast<int>(rows), plan.heads);
 }
 
 }  // namespace
@@ -691,8 +778,9 @@ tkv_status tkv_quantized_attention(int32_t batch, int32_t n_q_heads, int32_t n_k
   }
   char* at = static_cast<char*>(scratch);
   p.q = q; p.out = out; p.alpha = alpha_sum;
-  p.part_o = plan.merge ? reinterpret_cast<float*>(at) : nullptr;
-  p.part_m = plan.merge || alpha_sum ? reinterpret_cast<float4*>(at + plan.o_m) : nullptr;
+  p.part_o = reinterpret_cast<float*>(at);
+  p.part_m = reinterpret_cast<float4*>(at + plan.o_m);
+  p.stats = alpha_sum ? reinterpret_cast<float2*>(at + plan.o_stats) : nullptr;
   p.spill = alpha_sum ? reinterpret_cast<float*>(at + plan.o_spill) : nullptr;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
