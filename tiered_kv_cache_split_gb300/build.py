@@ -48,7 +48,8 @@ def build(verbose: bool = False, force: bool = False, debug: bool = False) -> st
     flags = FLAGS + (["-DTKV_DEBUG"] if debug else [])
     os.makedirs(out_dir, exist_ok=True)
     headers = [os.path.join(CSRC, "tkv_internal.h"), os.path.join(CSRC, "tile_attention.h"),
-               os.path.join(CSRC, "quantized.h"), os.path.join(INCLUDE, "tkv.h")]
+               os.path.join(CSRC, "quantized.h"), os.path.join(CSRC, "elements.h"),
+               os.path.join(INCLUDE, "tkv.h")]
     jobs = []
     for s in SOURCES:
         src = os.path.join(CSRC, s)

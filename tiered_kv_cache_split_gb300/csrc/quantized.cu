@@ -32,7 +32,7 @@ __device__ __forceinline__ void store_codes(uint2* at, const CodeBytes& b) { *at
 struct RowRange {
   int32_t rows;
   int32_t first[kMaxBatch], last[kMaxBatch];
-  int64_t page0[kMaxBatch + 1];  // prefix sums of the pages touched
+  int32_t page0[kMaxBatch + 1];  // prefix sums of the pages touched
   int64_t token0[kMaxBatch];     // packed index of slot `first`
 };
 
@@ -46,19 +46,20 @@ struct Item {
 
 // Item w of a call: K or V fastest, then the head, then the page, so that
 // neighbouring warps take neighbouring pieces of the packed tokens and of a page.
-__device__ __forceinline__ Item item_of(const RowRange& r, const PoolRef& p, int64_t w) {
+__device__ __forceinline__ Item item_of(const RowRange& r, const PoolRef& p, uint32_t w) {
   Item t;
   t.kv = static_cast<int>(w & 1);
   w >>= 1;
-  t.h = static_cast<int>(w % p.hkv);
-  w /= p.hkv;
+  const uint32_t heads = p.hkv;
+  t.h = static_cast<int>(w % heads);
+  w /= heads;
   int lo = 0, hi = r.rows - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (r.page0[mid] <= w) lo = mid; else hi = mid - 1;
+    if (r.page0[mid] <= static_cast<int32_t>(w)) lo = mid; else hi = mid - 1;
   }
   t.row = lo;
-  const int page = r.first[lo] / kPage + static_cast<int>(w - r.page0[lo]);
+  const int page = r.first[lo] / kPage + static_cast<int>(w) - r.page0[lo];
   t.slot0 = page * kPage;
   t.lo = max(r.first[lo] - t.slot0, 0);
   t.hi = min(r.last[lo] - t.slot0, kPage);
@@ -77,12 +78,44 @@ struct AppendQParams {
   int64_t k_stride, v_stride;
   const int32_t* refs;  // may be null
   int32_t* status;      // may be null
-  int64_t items;
+  uint32_t items;
 };
 
-__device__ __forceinline__ int8_t to_code(float x, float scale) {
-  const float c = rintf(x / scale);
-  return static_cast<int8_t>(fminf(fmaxf(c, -127.f), 127.f));
+// Absolute bits of the largest element of a vector; a NaN is above infinity.
+__device__ __forceinline__ uint32_t top_bits(const int4& v, float) {
+  const uint32_t m = 0x7fffffffu;
+  return max(max(v.x & m, v.y & m), max(v.z & m, v.w & m));
+}
+__device__ __forceinline__ uint32_t top_bits(const int4& v, __nv_bfloat16) {
+  const uint32_t m = 0x7fff7fffu;
+  const uint32_t w = __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+  return max(w << 16, w & 0xffff0000u);
+}
+
+// Codes rint(x / scale) of a vector. With the reciprocal r, x * r is off the rounded
+// quotient by at most 127 * 2^-23 < 2^-15 (half a step each), so wherever it is further than that
+// from the middle of two codes both give the same one; false where it is not, and
+// the division has to decide. Adding 1.5 * 2^23 rounds to a whole number and
+// leaves it in the low byte.
+template <int N>
+__device__ __forceinline__ bool to_codes(const float (&x)[N], float inverse, CodeBytes* b) {
+  constexpr float kRound = 0x1.8p23f;
+  b->w[0] = b->w[1] = 0;
+  float off = 0.f;
+  uint32_t t[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float y = fmaf(x[j], inverse, kRound);
+    off = fmaxf(off, fabsf(fmaf(x[j], inverse, kRound - y)));
+    t[j] = __float_as_uint(y);
+  }
+#pragma unroll
+  for (int j = 0; j < N; j += 4)
+    b->w[j / 4] = __byte_perm(__byte_perm(t[j], t[j + 1], 0x0040), __byte_perm(t[j + 2], t[j + 3], 0x0040), 0x5410);
+  return off <= 0.5f - 0x1p-15f;
+}
+__device__ __forceinline__ int8_t divided(float x, float scale) {
+  return scale > 0.f ? static_cast<int8_t>(fminf(fmaxf(rintf(x / scale), -127.f), 127.f)) : 0;
 }
 
 // A warp per block: the rows of the block that are written stay in registers
@@ -95,7 +128,7 @@ __global__ void __launch_bounds__(kCopyThreads) append_quantized_kernel(const __
   using Codes = typename CodesOf<T>::type;
   constexpr int kLanes = D / V::n;                       // lanes of a row
   constexpr int kRows = 32 / kLanes, kPasses = kPage / kRows;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * kCopyWarps + (threadIdx.x >> 5);
+  const uint32_t w = blockIdx.x * kCopyWarps + (threadIdx.x >> 5);
   if (w >= p.items) return;
   const int lane = threadIdx.x & 31, r0 = lane / kLanes, c0 = (lane % kLanes) * V::n;
   const Item t = item_of(p.r, p.p, w);
@@ -114,12 +147,7 @@ __global__ void __launch_bounds__(kCopyThreads) append_quantized_kernel(const __
     if (s >= t.lo && s < t.hi) x[i] = *reinterpret_cast<const int4*>(from + (t.token + s - t.lo) * stride);
   }
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    float f[V::n];
-    V::unpack(x[i], f);
-#pragma unroll
-    for (int j = 0; j < V::n; ++j) top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);  // a NaN is above infinity
-  }
+  for (int i = 0; i < kPasses; ++i) top = max(top, top_bits(x[i], T()));
   top = __reduce_max_sync(0xffffffffu, top);
   const int64_t block = (t.id * p.p.hkv + t.h) * 2 + t.kv;
   const float old = t.lo > 0 ? p.p.scales[block] : 0.f;
@@ -128,17 +156,35 @@ __global__ void __launch_bounds__(kCopyThreads) append_quantized_kernel(const __
   const bool finite = grown < INFINITY;
   const float scale = finite ? grown : NAN;                     // every value of the block reads as NaN
   int8_t* codes = p.p.codes + block * kPage * D + c0;
+  // scales below 2^-100, whose reciprocals may overflow and whose own rounding can
+  // make codes above 127, leave every row to the division
+  const float inverse = scale >= 0x1p-100f ? 1.f / scale : 0.f;
+  uint32_t divide = 0;
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const int s = i * kRows + r0;
+    float f[V::n];
+    V::unpack(x[i], f);
+    CodeBytes b;
+    const bool ok = to_codes(f, inverse, &b) && inverse > 0.f;
+    if (!finite) b.w[0] = b.w[1] = 0;
     if (s >= t.lo && s < t.hi) {
-      float f[V::n];
-      V::unpack(x[i], f);
-      CodeBytes b;
-#pragma unroll
-      for (int j = 0; j < V::n; ++j) b.c[j] = finite && scale > 0.f ? to_code(f[j], scale) : 0;
       store_codes(reinterpret_cast<Codes*>(codes + s * D), b);
+      if (!ok) divide |= 1u << s;
     }
+  }
+  // in a loop of its own: unrolled into the passes it made the code too long for
+  // the instruction cache (a fifth of the stalls)
+#pragma unroll 1
+  for (divide = finite ? divide : 0; divide; divide &= divide - 1) {
+    const int s = __ffs(divide) - 1;
+    float f[V::n];
+    V::unpack(*reinterpret_cast<const int4*>(from + (t.token + s - t.lo) * stride), f);
+    CodeBytes b;
+    b.w[0] = b.w[1] = 0;
+#pragma unroll
+    for (int j = 0; j < V::n; ++j) b.c[j] = divided(f[j], scale);
+    store_codes(reinterpret_cast<Codes*>(codes + s * D), b);
   }
   if (t.lo > 0 && scale > old && finite) {
     const float ratio = old / scale;
@@ -167,7 +213,7 @@ struct ReadQParams {
   PoolRef p;
   void *k, *v;
   int64_t k_stride, v_stride;
-  int64_t items;
+  uint32_t items;
 };
 
 // A warp per block, as the append's.
@@ -177,7 +223,7 @@ __global__ void __launch_bounds__(kCopyThreads) read_quantized_kernel(const __gr
   using Codes = typename CodesOf<T>::type;
   constexpr int kLanes = D / V::n;
   constexpr int kRows = 32 / kLanes, kPasses = kPage / kRows;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * kCopyWarps + (threadIdx.x >> 5);
+  const uint32_t w = blockIdx.x * kCopyWarps + (threadIdx.x >> 5);
   if (w >= p.items) return;
   const int lane = threadIdx.x & 31, r0 = lane / kLanes, c0 = (lane % kLanes) * V::n;
   const Item t = item_of(p.r, p.p, w);
@@ -187,20 +233,22 @@ __global__ void __launch_bounds__(kCopyThreads) read_quantized_kernel(const __gr
   const int8_t* codes = p.p.codes + block * kPage * D + c0;
   T* to = static_cast<T*>(t.kv ? p.v : p.k) + t.h * D + c0;
   const int64_t stride = t.kv ? p.v_stride : p.k_stride;
-  CodeBytes b[kPasses];
+  Codes c[kPasses];
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const int s = i * kRows + r0;
-    b[i].w[0] = b[i].w[1] = 0;
-    if (s >= t.lo && s < t.hi && (live >> s & 1)) b[i] = load_codes(reinterpret_cast<const Codes*>(codes + s * D));
+    c[i] = Codes{};
+    if (s >= t.lo && s < t.hi && (live >> s & 1)) c[i] = *reinterpret_cast<const Codes*>(codes + s * D);
   }
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const int s = i * kRows + r0;
     if (s < t.lo || s >= t.hi) continue;
+    const float by = live >> s & 1 ? scale : 0.f;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&c[i]);
     float f[V::n];
 #pragma unroll
-    for (int j = 0; j < V::n; ++j) f[j] = live >> s & 1 ? b[i].c[j] * scale : 0.f;
+    for (int j = 0; j < V::n; ++j) f[j] = static_cast<float>(static_cast<int8_t>(w[j / 4] >> (8 * (j % 4)))) * by;
     *reinterpret_cast<int4*>(to + (t.token + s - t.lo) * stride) = V::pack(f);
   }
 }
@@ -261,10 +309,10 @@ tkv_status tkv_append_quantized(int32_t rows, const int32_t* lens, const int32_t
   if (int st = check_tokens(dtype, n_kv_heads, head_dim, k, k_stride, v, v_stride)) return tkv_status(st);
   p.k = k; p.v = v; p.k_stride = k_stride; p.v_stride = v_stride;
   p.refs = page_refs; p.status = status;
-  p.items = p.r.page0[rows] * n_kv_heads * 2;
-  const int64_t ctas = (p.items + kCopyWarps - 1) / kCopyWarps;
-  if (ctas > INT32_MAX) return tkv_status(report(TKV_ERR_INVALID_ARG, "too many blocks in one call"));
-  const unsigned n = static_cast<unsigned>(ctas);
+  const int64_t items = static_cast<int64_t>(p.r.page0[rows]) * n_kv_heads * 2;
+  if (items > INT32_MAX) return tkv_status(report(TKV_ERR_INVALID_ARG, "more than 2^31 blocks in one call"));
+  p.items = static_cast<uint32_t>(items);
+  const unsigned n = (p.items + kCopyWarps - 1) / kCopyWarps;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == TKV_DTYPE_BF16) {
     if (head_dim == 64) append_quantized_kernel<__nv_bfloat16, 64><<<n, kCopyThreads, 0, s>>>(p);
@@ -294,10 +342,10 @@ tkv_status tkv_read_quantized(int32_t rows, const int32_t* first, const int32_t*
   if (tokens == 0) return TKV_OK;
   if (int st = check_tokens(dtype, n_kv_heads, head_dim, k, k_stride, v, v_stride)) return tkv_status(st);
   p.k = k; p.v = v; p.k_stride = k_stride; p.v_stride = v_stride;
-  p.items = p.r.page0[rows] * n_kv_heads * 2;
-  const int64_t ctas = (p.items + kCopyWarps - 1) / kCopyWarps;
-  if (ctas > INT32_MAX) return tkv_status(report(TKV_ERR_INVALID_ARG, "too many blocks in one call"));
-  const unsigned n = static_cast<unsigned>(ctas);
+  const int64_t items = static_cast<int64_t>(p.r.page0[rows]) * n_kv_heads * 2;
+  if (items > INT32_MAX) return tkv_status(report(TKV_ERR_INVALID_ARG, "more than 2^31 blocks in one call"));
+  p.items = static_cast<uint32_t>(items);
+  const unsigned n = (p.items + kCopyWarps - 1) / kCopyWarps;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == TKV_DTYPE_BF16) {
     if (head_dim == 64) read_quantized_kernel<__nv_bfloat16, 64><<<n, kCopyThreads, 0, s>>>(p);
