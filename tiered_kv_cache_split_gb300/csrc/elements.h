@@ -49,6 +49,24 @@ inline int launched(const char* what, cudaError_t e) {
   return e == cudaSuccess ? TKV_OK : report(TKV_ERR_CUDA, "%s launch failed: %s", what, cudaGetErrorString(e));
 }
 
+// Launches a kernel whose CTAs may be set up while the kernel ahead of it on the
+// stream ends. Every thread of it waits for that one (cudaGridDependencySynchronize)
+// before it touches memory, so that its own end is the end of all before it.
+template <typename P, typename... A>
+cudaError_t launch_early(void (*kernel)(P, A...), dim3 ctas, int threads, int bytes, cudaStream_t s, const P& p, A... more) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = ctas;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, more...);
+}
+
 inline int check_dtype(int32_t dtype) {
   return dtype == TKV_DTYPE_F32 || dtype == TKV_DTYPE_BF16 ? TKV_OK : report(TKV_ERR_INVALID_ARG, "dtype");
 }

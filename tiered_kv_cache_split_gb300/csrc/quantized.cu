@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(kCopyThreads) append_quantized_kernel(const __
   using Codes = typename CodesOf<T>::type;
   constexpr int kLanes = D / V::n;                       // lanes of a row
   constexpr int kRows = 32 / kLanes, kPasses = kPage / kRows;
+  cudaGridDependencySynchronize();
   const uint32_t w = blockIdx.x * kCopyWarps + (threadIdx.x >> 5);
   if (w >= p.items) return;
   const int lane = threadIdx.x & 31, r0 = lane / kLanes, c0 = (lane % kLanes) * V::n;
@@ -223,6 +224,7 @@ __global__ void __launch_bounds__(kCopyThreads) read_quantized_kernel(const __gr
   using Codes = typename CodesOf<T>::type;
   constexpr int kLanes = D / V::n;
   constexpr int kRows = 32 / kLanes, kPasses = kPage / kRows;
+  cudaGridDependencySynchronize();
   const uint32_t w = blockIdx.x * kCopyWarps + (threadIdx.x >> 5);
   if (w >= p.items) return;
   const int lane = threadIdx.x & 31, r0 = lane / kLanes, c0 = (lane % kLanes) * V::n;
@@ -314,14 +316,9 @@ tkv_status tkv_append_quantized(int32_t rows, const int32_t* lens, const int32_t
   p.items = static_cast<uint32_t>(items);
   const unsigned n = (p.items + kCopyWarps - 1) / kCopyWarps;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == TKV_DTYPE_BF16) {
-    if (head_dim == 64) append_quantized_kernel<__nv_bfloat16, 64><<<n, kCopyThreads, 0, s>>>(p);
-    else append_quantized_kernel<__nv_bfloat16, 128><<<n, kCopyThreads, 0, s>>>(p);
-  } else {
-    if (head_dim == 64) append_quantized_kernel<float, 64><<<n, kCopyThreads, 0, s>>>(p);
-    else append_quantized_kernel<float, 128><<<n, kCopyThreads, 0, s>>>(p);
-  }
-  return tkv_status(launched("quantised append", cudaGetLastError()));
+  void (*const kernel)(AppendQParams) = dtype == TKV_DTYPE_BF16 ? (head_dim == 64 ? append_quantized_kernel<__nv_bfloat16, 64> : append_quantized_kernel<__nv_bfloat16, 128>)
+                                                         : (head_dim == 64 ? append_quantized_kernel<float, 64> : append_quantized_kernel<float, 128>);
+  return tkv_status(launched("quantised append", launch_early(kernel, dim3(n), kCopyThreads, 0, s, p)));
 }
 
 tkv_status tkv_read_quantized(int32_t rows, const int32_t* first, const int32_t* lens, int32_t n_kv_heads,
@@ -347,14 +344,9 @@ tkv_status tkv_read_quantized(int32_t rows, const int32_t* first, const int32_t*
   p.items = static_cast<uint32_t>(items);
   const unsigned n = (p.items + kCopyWarps - 1) / kCopyWarps;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == TKV_DTYPE_BF16) {
-    if (head_dim == 64) read_quantized_kernel<__nv_bfloat16, 64><<<n, kCopyThreads, 0, s>>>(p);
-    else read_quantized_kernel<__nv_bfloat16, 128><<<n, kCopyThreads, 0, s>>>(p);
-  } else {
-    if (head_dim == 64) read_quantized_kernel<float, 64><<<n, kCopyThreads, 0, s>>>(p);
-    else read_quantized_kernel<float, 128><<<n, kCopyThreads, 0, s>>>(p);
-  }
-  return tkv_status(launched("quantised read", cudaGetLastError()));
+  void (*const kernel)(ReadQParams) = dtype == TKV_DTYPE_BF16 ? (head_dim == 64 ? read_quantized_kernel<__nv_bfloat16, 64> : read_quantized_kernel<__nv_bfloat16, 128>)
+                                                         : (head_dim == 64 ? read_quantized_kernel<float, 64> : read_quantized_kernel<float, 128>);
+  return tkv_status(launched("quantised read", launch_early(kernel, dim3(n), kCopyThreads, 0, s, p)));
 }
 
 }  // extern "C"

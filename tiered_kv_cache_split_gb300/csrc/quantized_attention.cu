@@ -38,9 +38,11 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kWindow = 384;        // pages that shared memory describes at a time
 constexpr int kSegmentCost = 8;     // pages' time of a piece's start and end
 constexpr int kLeastPages = 16;     // pages of a CTA's stretch, at least
-constexpr int kWholePages = 24;     // pages of a sequence up to which its segments are not cut
+constexpr int kWholePages = 40;     // pages of a sequence up to which its segments are not cut
+constexpr int kAlphaPages = 64;     // pages of a segment up to which its one CTA forms alpha itself
+static_assert(kWholePages <= kAlphaPages, "the CTAs of a call without partials form alpha");
 constexpr int kMergeThreads = 128;
-constexpr int kAlphaSlots = 256;    // slots of an alpha CTA
+constexpr int kAlphaSlots = 256;    // slots of an alpha CTA (with 1024 the launch took 16 us, not 9.5)
 constexpr int kSms = 152;
 constexpr float kNegInf = -INFINITY;
 constexpr float kWeightBits = 13.f; // weights are at most 2^15: reference lag and f below 2 each
@@ -125,6 +127,21 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
 __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;"); }
 template <int N> __device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// A slot's weights, summed over the heads, from their logits.
+struct AlphaSum {
+  float value = 0.f;
+  bool any = false;
+  __device__ __forceinline__ void add(const float4& l, const float2* head, int j, int G) {  // heads j .. j + 3: (maximum, 1 / sum)
+    const float x[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (j + i >= G || x[i] == kNegInf) continue;
+      any = true;
+      value += ex2(x[i] - head[j + i].x) * head[j + i].y;
+    }
+  }
+};
+
 // What a unit keeps of a page: id (-1: none of its slots counts), valid slots and
 // the power k of V's scale, K's scale in the logits' units, and V's scale as f in f 2^k.
 __device__ __forceinline__ int4 page_info(const AttendParams& p, int32_t id, int h) {
@@ -160,7 +177,8 @@ struct Smem {
   static constexpr int merge_bytes = kWarps * heads * out_row * 4;
   static constexpr int o_info = Ring<D>::bytes > merge_bytes ? Ring<D>::bytes : merge_bytes;
   static constexpr int o_stat = o_info + kWindow * 16;
-  static constexpr int bytes = o_stat + kWarps * heads * 16;
+  static constexpr int o_head = o_stat + kWarps * heads * 16;
+  static constexpr int bytes = o_head + heads * 8;
 };
 
 // Where the 16-byte chunk c of row r of a slot lies (rows 0 .. 15 are K's, 16 .. 31
@@ -199,7 +217,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
   extern __shared__ __align__(128) char smem[];
   int4* s_info = reinterpret_cast<int4*>(smem + S::o_info);
   float4* s_stat = reinterpret_cast<float4*>(smem + S::o_stat);
+  float2* s_head = reinterpret_cast<float2*>(smem + S::o_head);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  cudaGridDependencySynchronize();
   const int segments = p.p.hkv * p.groups;         // of a sequence
   int b = 0, pos = 0, end = 1;                     // the CTA's stretch
   if (p.whole) {
@@ -494,10 +514,26 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
         const float by = sum == 0.f ? 0.f : 1.f / sum, e = sum == 0.f ? 0.f : ref - top - kWeightBits;
         put4(static_cast<T*>(p.out) + at * D + d,
              make_float4(times_ex2(x.x * by, e), times_ex2(x.y * by, e), times_ex2(x.z * by, e), times_ex2(x.w * by, e)));
-        if (p.stats && d == 0) p.stats[at] = make_float2(top, sum);
+        if (p.stats && d == 0) {
+        p.stats[at] = make_float2(top, sum);
+        s_head[head] = make_float2(top, sum == 0.f ? 0.f : 1.f / sum);
+      }
       } else {
         if (d == 0) p.part_m[part + head] = make_float4(top, ref, sum, 0.f);
         *reinterpret_cast<float4*>(p.part_o + (part + head) * D + d) = x;
+      }
+    }
+    if (p.alpha && all && p.groups == 1 && n <= kAlphaPages) {
+      __syncthreads();
+      const float* l = p.spill + (static_cast<int64_t>(p.page0[b]) * p.p.hkv + h) * kPage * S::heads;
+      float* alpha = p.alpha + (static_cast<int64_t>(b) * p.p.hkv + h) * p.max_pages * kPage;
+#pragma unroll 4
+      for (int i = tid; i < n * kPage; i += kThreads) {
+        const float* at = l + ((i / kPage) * static_cast<int64_t>(p.p.hkv) * kPage + i % kPage) * S::heads;
+        AlphaSum sum;
+#pragma unroll
+        for (int j = 0; j < S::heads; j += 4) sum.add(*reinterpret_cast<const float4*>(at + j), s_head, j, p.G);
+        if (sum.any) alpha[i] += sum.value;
       }
     }
     pos = stop;
@@ -587,12 +623,16 @@ __global__ void __launch_bounds__(kMergeThreads) merge_quantized_kernel(const __
   const int h = at % p.p.hkv, b = at / p.p.hkv;
   const int slots = p.count[b] * kPage, first = part * kAlphaSlots + tid;
   if (part * kAlphaSlots >= slots) return;
+  if (p.groups == 1 && p.count[b] <= kAlphaPages) {
+    const Pieces pc = pieces_of(p, b, h);
+    if (pc.first == pc.last) return;               // formed by its CTA
+  }
   const int columns = p.groups * heads;
   float4 l[kSlots][2];
   const float* spill[kSlots];
   float* alpha = p.alpha + (static_cast<int64_t>(b) * p.p.hkv + h) * p.max_pages * kPage;
-  float before[kSlots], sum[kSlots];
-  bool any[kSlots];
+  float before[kSlots];
+  AlphaSum sum[kSlots];
   auto load = [&](int j) {                         // logits of heads j .. j + 7
 #pragma unroll
     for (int k = 0; k < kSlots; ++k)
@@ -607,8 +647,6 @@ __global__ void __launch_bounds__(kMergeThreads) merge_quantized_kernel(const __
     const int i = first + k * kMergeThreads;
     spill[k] = p.spill + ((static_cast<int64_t>(p.page0[b] + i / kPage) * p.p.hkv + h) * kPage + i % kPage) * columns;
     before[k] = i < slots ? alpha[i] : 0.f;
-    sum[k] = 0.f;
-    any[k] = false;
   }
   load(0);
   for (int i = tid / 8; i < p.G; i += kMergeThreads / 8) {  // eight lanes per head
@@ -635,20 +673,11 @@ __global__ void __launch_bounds__(kMergeThreads) merge_quantized_kernel(const __
 #pragma unroll
     for (int k = 0; k < kSlots; ++k)
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const float x[4] = {l[k][v].x, l[k][v].y, l[k][v].z, l[k][v].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int head = j + 4 * v + i;
-          if (head >= p.G || x[i] == kNegInf) continue;
-          any[k] = true;
-          sum[k] += ex2(x[i] - s_head[head].x) * s_head[head].y;
-        }
-      }
+      for (int v = 0; v < 2; ++v) sum[k].add(l[k][v], s_head, j + 4 * v, p.G);
   }
 #pragma unroll
   for (int k = 0; k < kSlots; ++k)
-    if (any[k]) alpha[first + k * kMergeThreads] = before[k] + sum[k];
+    if (sum[k].any) alpha[first + k * kMergeThreads] = before[k] + sum[k].value;
 }
 
 // ---- host side
@@ -683,7 +712,6 @@ int plan_attend(AttendParams* p, Plan* plan, int32_t batch, int32_t Hq, int32_t 
     p->page0[b + 1] = p->page0[b] + n;
     most = std::max(most, n);
   }
-  p->alpha_parts = (most * kPage + kAlphaSlots - 1) / kAlphaSlots;
   const int64_t segments = static_cast<int64_t>(Hkv) * p->groups, slots = kSms * (plan->nt == 1 ? 4 : 3);
   const int64_t total = segments * (p->page0[batch] + static_cast<int64_t>(batch) * kSegmentCost);
   if (total > (int64_t(1) << 30)) return report(TKV_ERR_INVALID_ARG, "more than 2^30 pages and heads in one call");
@@ -692,6 +720,7 @@ int plan_attend(AttendParams* p, Plan* plan, int32_t batch, int32_t Hq, int32_t 
   // Short segments stay whole: a CTA reads kWholePages in the time that the launch
   // which joins partials would take.
   p->whole = most <= kWholePages;
+  p->alpha_parts = p->whole && p->groups == 1 ? 0 : (most * kPage + kAlphaSlots - 1) / kAlphaSlots;
   if (p->whole) {
     p->ctas = static_cast<int32_t>(segments * batch);
     for (int b = 0; b < batch; ++b) p->order[b] = b;
@@ -716,27 +745,16 @@ cudaError_t launch_units(const AttendParams& p, cudaStream_t s) {
   static SharedMemoryOptIn opt_in;
   const cudaError_t e = opt_in.once(reinterpret_cast<const void*>(attend_quantized_kernel<T, D, NT>), bytes);
   if (e != cudaSuccess) return e;
-  attend_quantized_kernel<T, D, NT><<<static_cast<unsigned>(p.ctas), kThreads, bytes, s>>>(p);
-  return cudaGetLastError();
+  return launch_early(attend_quantized_kernel<T, D, NT>, dim3(p.ctas), kThreads, bytes, s, p);
 }
 
 template <typename T, int D>
 cudaError_t launch_attend(const AttendParams& p, const Plan& plan, cudaStream_t s) {
   cudaError_t e = plan.nt == 1 ? launch_units<T, D, 1>(p, s) : launch_units<T, D, 2>(p, s);
-  if (e != cudaSuccess || (p.whole && !p.alpha)) return e;
   const int64_t rows = p.whole ? 0 : static_cast<int64_t>(p.B) * p.Hq;
-  const int64_t pieces = p.alpha ? static_cast<int64_t>(p.B) * p.p.hkv * p.alpha_parts : 0;
-  if (rows + pieces == 0) return e;                // no sequence has a page
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows + pieces));
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_quantized_kernel<T, D>, p, static_cast<int>(rows), plan.heads);
+  const int64_t parts = p.alpha ? static_cast<int64_t>(p.B) * p.p.hkv * p.alpha_parts : 0;
+  if (e != cudaSuccess || rows + parts == 0) return e;
+  return launch_early(merge_quantized_kernel<T, D>, dim3(static_cast<unsigned>(rows + parts)), kMergeThreads, 0, s, p, static_cast<int>(rows), plan.heads);
 }
 
 }  // namespace

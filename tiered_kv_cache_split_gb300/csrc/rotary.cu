@@ -75,6 +75,7 @@ __device__ __forceinline__ void form_turns(const RotateParams& p, int64_t token0
 template <typename T>
 __global__ void __launch_bounds__(kRotaryThreads) rotate_kernel(const __grid_constant__ RotateParams p) {
   __shared__ float2 s_turn[kTurns];
+  cudaGridDependencySynchronize();
   const int64_t token0 = static_cast<int64_t>(blockIdx.x) * p.per_cta;
   const int tokens = static_cast<int>(min(p.tokens - token0, static_cast<int64_t>(p.per_cta)));
   form_turns<1>(p, token0, tokens, s_turn);
@@ -111,6 +112,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotate_vectors_kernel(const __
   constexpr int kAhead = kInterleaved ? 4 : 2;            // vectors (half layout: pairs of them) on their way
   constexpr int kGroup = kInterleaved ? V::n / 2 : V::n;  // pairs of a thread
   __shared__ float2 s_turn[kTurns];
+  cudaGridDependencySynchronize();
   const int64_t token0 = static_cast<int64_t>(blockIdx.x) * p.per_cta;
   const int tokens = static_cast<int>(min(p.tokens - token0, static_cast<int64_t>(p.per_cta)));
   const int turning = (kInterleaved ? 2 * p.pairs : p.pairs) / V::n, items = turning + (p.d - 2 * p.pairs) / V::n;
@@ -179,10 +181,8 @@ __global__ void __launch_bounds__(kRotaryThreads) rotate_vectors_kernel(const __
 
 template <typename T>
 cudaError_t launch_rotate(const RotateParams& p, bool vectors, dim3 ctas, cudaStream_t s) {
-  if (!vectors) rotate_kernel<T><<<ctas, kRotaryThreads, 0, s>>>(p);
-  else if (p.interleaved) rotate_vectors_kernel<T, true><<<ctas, kRotaryThreads, 0, s>>>(p);
-  else rotate_vectors_kernel<T, false><<<ctas, kRotaryThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  void (*const kernel)(RotateParams) = !vectors ? rotate_kernel<T> : p.interleaved ? rotate_vectors_kernel<T, true> : rotate_vectors_kernel<T, false>;
+  return launch_early(kernel, ctas, kRotaryThreads, 0, s, p);
 }
 
 }  // namespace
