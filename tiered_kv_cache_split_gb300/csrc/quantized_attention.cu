@@ -41,8 +41,9 @@ constexpr int kLeastPages = 16;     // pages of a CTA's stretch, at least
 constexpr int kWholePages = 40;     // pages of a sequence up to which its segments are not cut
 constexpr int kAlphaPages = 64;     // pages of a segment up to which its one CTA forms alpha itself
 static_assert(kWholePages <= kAlphaPages, "the CTAs of a call without partials form alpha");
-constexpr int kMergeThreads = 128;
-constexpr int kAlphaSlots = 256;    // slots of an alpha CTA (with 1024 the launch took 16 us, not 9.5)
+constexpr int kMergeWarps = 4;
+constexpr int kMergeThreads = kMergeWarps * 32;
+constexpr int kAlphaSlots = 512;    // slots of an alpha CTA
 constexpr int kSms = 152;
 constexpr float kNegInf = -INFINITY;
 constexpr float kWeightBits = 13.f; // weights are at most 2^15: reference lag and f below 2 each
@@ -73,12 +74,12 @@ struct AttendParams {
   int32_t B, Hq, G, groups; // groups: head groups of a KV head
   int32_t max_pages;
   int32_t ctas, share, total, whole;
-  int32_t alpha_parts;      // alpha CTAs of a sequence and KV head
   float qscale;             // log2(e) / sqrt(D)
   int32_t count[kMaxBatch];     // pages
   int32_t order[kMaxBatch];     // whole: sequences, longest first
   int32_t base[kMaxBatch + 1];  // where the segments of a sequence start on the line
   int32_t page0[kMaxBatch + 1]; // prefix sums of the pages
+  int32_t alpha0[kMaxBatch + 1];  // prefix sums of the alpha CTAs of a KV head
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -121,8 +122,8 @@ __device__ __forceinline__ uint32_t codes2(uint32_t x) {
 }
 constexpr int kLow = 0x4140, kHigh = 0x4342;
 
-__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "l"(policy) : "memory");
 }
 __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;"); }
 template <int N> __device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -193,12 +194,12 @@ __device__ __forceinline__ int chunk_at(int r, int c) {
 
 // The copies of one page by one warp: 512 bytes in a row each.
 template <int D>
-__device__ __forceinline__ void copy_page(uint32_t to, const int8_t* block, int lane) {
+__device__ __forceinline__ void copy_page(uint32_t to, const int8_t* block, int lane, uint64_t policy) {
   constexpr int kRowChunks = D / 16;
 #pragma unroll
   for (int i = 0; i < 2 * kPage * D / 512; ++i) {
     const int at = i * 32 + lane;
-    copy16(to + chunk_at<D>(at / kRowChunks, at % kRowChunks), block + at * 16);
+    copy16(to + chunk_at<D>(at / kRowChunks, at % kRowChunks), block + at * 16, policy);
   }
 }
 
@@ -233,6 +234,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
       if (p.base[mid] <= pos) b = mid; else hi = mid - 1;
     }
   }
+  // codes are read once: their lines leave the L2 before the logits and partials (41 us for the
+  // benchmark's batch with alpha, 45 without this)
+  uint64_t policy;
+  if (p.groups == 1) asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  else asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));  // the other groups read them too
   bool later = false;                              // not the first window: shared memory may be in use
   while (pos < end) {
     int segment, lo = 0, hi = p.count[b], stop = end;  // pages lo .. hi - 1 of it
@@ -268,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
       const int count = min(kWindow, hi - w0), mine = count > warp ? (count - warp + kWarps - 1) / kWarps : 0;
       auto copy = [&](int i, int id) {
         if (id >= 0 && id < p.p.pages)
-          copy_page<D>(ring + (i % R::stages) * R::page_bytes, p.p.codes + (static_cast<int64_t>(id) * p.p.hkv + h) * R::page_bytes, lane);
+          copy_page<D>(ring + (i % R::stages) * R::page_bytes, p.p.codes + (static_cast<int64_t>(id) * p.p.hkv + h) * R::page_bytes, lane, policy);
         commit();
       };
       auto start = [&](int i) { copy(i, i < mine ? s_info[warp + i * kWarps].x : -1); };
@@ -560,25 +566,26 @@ __device__ __forceinline__ void join(float& m, float& z, float m1, float z1) {
   m = top;
 }
 
-// The first B * Hq CTAs join the pieces of a query head each, a warp every fourth
+// The last B * Hq CTAs join the pieces of a query head each, a warp every fourth
 // piece. The others (alpha) take kAlphaSlots slots of a sequence and KV head: the
 // maximum and sum of each query head, then the slots' weights from their logits,
 // which are on their way meanwhile.
 template <typename T, int D>
-__global__ void __launch_bounds__(kMergeThreads) merge_quantized_kernel(const __grid_constant__ AttendParams p, int rows, int heads) {
+__global__ void __launch_bounds__(kMergeThreads) merge_quantized_kernel(const __grid_constant__ AttendParams p, int heads) {
   constexpr int E = D / 32;
-  __shared__ float s_x[4][D];
-  __shared__ float4 s_st[4];
+  __shared__ float s_x[kMergeWarps][D];
+  __shared__ float4 s_st[kMergeWarps];
   __shared__ float2 s_head[64];
   cudaGridDependencySynchronize();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (static_cast<int>(blockIdx.x) < rows) {
-    const int b = blockIdx.x / p.Hq, hq = blockIdx.x % p.Hq, h = hq / p.G, head = hq % p.G;
+  const int parts = p.alpha ? p.alpha0[p.B] * p.p.hkv : 0;
+  if (static_cast<int>(blockIdx.x) >= parts) {
+    const int row_out = blockIdx.x - parts, b = row_out / p.Hq, hq = row_out % p.Hq, h = hq / p.G, head = hq % p.G;
     const Pieces pc = pieces_of(p, b, h * p.groups + head / heads);
     if (pc.first == pc.last) return;               // written by its CTA
     float m = kNegInf, r = kNegInf, z = 0.f, x[E] = {};
 #pragma unroll 4
-    for (int c = pc.first + warp; c <= pc.last; c += 4) {
+    for (int c = pc.first + warp; c <= pc.last; c += kMergeWarps) {
       const int64_t row = pc.row(c, heads) + head % heads;
       const float4 st = p.part_m[row];
       float y[E];
@@ -598,31 +605,32 @@ __global__ void __launch_bounds__(kMergeThreads) merge_quantized_kernel(const __
       m = r = kNegInf;
       z = 0.f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
+      for (int w = 0; w < kMergeWarps; ++w) {
         join(m, z, s_st[w].x, s_st[w].z);
         r = fmaxf(r, s_st[w].y);
       }
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
+      for (int w = 0; w < kMergeWarps; ++w) {
         const float4 a = *reinterpret_cast<const float4*>(&s_x[w][tid * 4]);
         const float take = s_st[w].y == kNegInf ? 1.f : ex2(s_st[w].y - r);
         y.x += a.x * take, y.y += a.y * take, y.z += a.z * take, y.w += a.w * take;
       }
       const float by = z == 0.f ? 0.f : 1.f / z, e = z == 0.f ? 0.f : r - m - kWeightBits;
-      put4(static_cast<T*>(p.out) + static_cast<int64_t>(blockIdx.x) * D + tid * 4,
+      put4(static_cast<T*>(p.out) + static_cast<int64_t>(row_out) * D + tid * 4,
            make_float4(times_ex2(y.x * by, e), times_ex2(y.y * by, e), times_ex2(y.z * by, e), times_ex2(y.w * by, e)));
     }
     return;
   }
   // alpha
   constexpr int kSlots = kAlphaSlots / kMergeThreads;  // of a thread
-  int at = blockIdx.x - rows;
-  const int part = at % p.alpha_parts;
-  at /= p.alpha_parts;
-  const int h = at % p.p.hkv, b = at / p.p.hkv;
-  const int slots = p.count[b] * kPage, first = part * kAlphaSlots + tid;
-  if (part * kAlphaSlots >= slots) return;
+  const int h = blockIdx.x % p.p.hkv, at = blockIdx.x / p.p.hkv;
+  int b = 0, last = p.B - 1;
+  while (b < last) {
+    const int mid = (b + last + 1) >> 1;
+    if (p.alpha0[mid] <= at) b = mid; else last = mid - 1;
+  }
+  const int slots = p.count[b] * kPage, first = (at - p.alpha0[b]) * kAlphaSlots + tid;
   if (p.groups == 1 && p.count[b] <= kAlphaPages) {
     const Pieces pc = pieces_of(p, b, h);
     if (pc.first == pc.last) return;               // formed by its CTA
@@ -720,7 +728,9 @@ int plan_attend(AttendParams* p, Plan* plan, int32_t batch, int32_t Hq, int32_t 
   // Short segments stay whole: a CTA reads kWholePages in the time that the launch
   // which joins partials would take.
   p->whole = most <= kWholePages;
-  p->alpha_parts = p->whole && p->groups == 1 ? 0 : (most * kPage + kAlphaSlots - 1) / kAlphaSlots;
+  p->alpha0[0] = 0;
+  for (int b = 0; b < batch; ++b)
+    p->alpha0[b + 1] = p->alpha0[b] + (p->whole && p->groups == 1 ? 0 : (p->count[b] * kPage + kAlphaSlots - 1) / kAlphaSlots);
   if (p->whole) {
     p->ctas = static_cast<int32_t>(segments * batch);
     for (int b = 0; b < batch; ++b) p->order[b] = b;
@@ -752,9 +762,9 @@ template <typename T, int D>
 cudaError_t launch_attend(const AttendParams& p, const Plan& plan, cudaStream_t s) {
   cudaError_t e = plan.nt == 1 ? launch_units<T, D, 1>(p, s) : launch_units<T, D, 2>(p, s);
   const int64_t rows = p.whole ? 0 : static_cast<int64_t>(p.B) * p.Hq;
-  const int64_t parts = p.alpha ? static_cast<int64_t>(p.B) * p.p.hkv * p.alpha_parts : 0;
+  const int64_t parts = p.alpha ? static_cast<int64_t>(p.alpha0[p.B]) * p.p.hkv : 0;
   if (e != cudaSuccess || rows + parts == 0) return e;
-  return launch_early(merge_quantized_kernel<T, D>, dim3(static_cast<unsigned>(rows + parts)), kMergeThreads, 0, s, p, static_cast<int>(rows), plan.heads);
+  return launch_early(merge_quantized_kernel<T, D>, dim3(static_cast<unsigned>(rows + parts)), kMergeThreads, 0, s, p, plan.heads);
 }
 
 }  // namespace
