@@ -118,6 +118,26 @@ def test_scale_edges():
     assert torch.equal(got[:16], torch.zeros_like(got[:16])) and torch.isfinite(got).all()
 
 
+def test_quotients_next_to_borders():
+    """Values a few steps from the middle of two codes, over scales of every size:
+    the code is that of the rounded quotient."""
+    rng = np.random.default_rng(5)
+    pages, hkv, d = 64, 4, 128
+    p = Pool(pages, hkv, d)
+    table = rows(pages, [pages])
+    x = np.empty((2, pages, hkv, PAGE * d), np.float32)
+    for block in np.ndindex(x.shape[:3]):
+        top = np.float32(rng.uniform(1, 2) * 2.0 ** rng.integers(-70, 100))
+        scale = np.float32(top / np.float32(127))
+        mid = ((rng.integers(0, 127, PAGE * d) + 0.5) * np.float64(scale)).astype(np.float32)
+        near = (mid.view(np.int32) + rng.integers(-3, 4, PAGE * d)).astype(np.int32).view(np.float32)
+        x[block] = np.minimum(near, top) * rng.choice([-1, 1], PAGE * d)
+        x[block][rng.integers(PAGE * d)] = top
+    k, v = (torch.from_numpy(a.reshape(pages, hkv, PAGE, d).transpose(0, 2, 1, 3).reshape(pages * PAGE, hkv, d).copy()).cuda() for a in x)
+    p.append(k, v, table, [0], [pages * PAGE])
+    p.check()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_nan_and_infinity(dtype):
     """They make their block, and no other, read as NaN until it starts anew."""

@@ -11,6 +11,11 @@
 
 namespace tkv {
 
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void put(float* at, float x) { *at = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* at, float x) { *at = __float2bfloat16_rn(x); }
+
 // Elements as they lie in a 16-byte vector.
 template <typename T> struct Vec;
 template <> struct Vec<float> {

@@ -12,7 +12,7 @@
 namespace tkv {
 namespace {
 
-constexpr int kCopyThreads = 256;
+constexpr int kCopyThreads = 128;
 constexpr int kCopyWarps = kCopyThreads / 32;
 
 // int8 codes of the elements of a 16-byte vector
@@ -92,30 +92,55 @@ __device__ __forceinline__ uint32_t top_bits(const int4& v, __nv_bfloat16) {
   return max(w << 16, w & 0xffff0000u);
 }
 
-// Codes rint(x / scale) of a vector. With the reciprocal r, x * r is off the rounded
-// quotient by at most 127 * 2^-23 < 2^-15 (half a step each), so wherever it is further than that
-// from the middle of two codes both give the same one; false where it is not, and
-// the division has to decide. Adding 1.5 * 2^23 rounds to a whole number and
-// leaves it in the low byte.
+// Two fp32 operations at a time.
+struct Two {
+  float x, y;
+};
+__device__ __forceinline__ unsigned long long bits(Two v) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+  return r;
+}
+__device__ __forceinline__ Two two(unsigned long long v) {
+  Two r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+  return two(r);
+}
+
+// Codes rint(x / scale) of a vector, the quotient correctly rounded without a division
+// (Markstein 1990): a quotient by the correctly rounded reciprocal, once corrected by
+// its residual, is next to x / scale, and once more is x / scale rounded. That holds
+// while nothing underflows: kLeastScale keeps residuals of quotients from 1/4 up in
+// range, and smaller ones give code 0 whatever their error. Adding 1.5 * 2^23 rounds to a whole number
+// and leaves it in the low byte. Divisions were half of the time; a reciprocal
+// alone would need them wherever a quotient is near a border, which in bf16 the
+// elements of half the largest one always are.
+constexpr float kLeastScale = 0x1p-60f;
 template <int N>
-__device__ __forceinline__ bool to_codes(const float (&x)[N], float inverse, CodeBytes* b) {
-  constexpr float kRound = 0x1.8p23f;
-  b->w[0] = b->w[1] = 0;
-  float off = 0.f;
+__device__ __forceinline__ CodeBytes to_codes(const float (&x)[N], float scale, float inverse) {
+  const Two inv = {inverse, inverse}, minus = {-scale, -scale}, zero = {-0.f, -0.f}, one = {1.f, 1.f}, round = {0x1.8p23f, 0x1.8p23f};
+  CodeBytes b;
+  b.w[0] = b.w[1] = 0;
   uint32_t t[N];
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const float y = fmaf(x[j], inverse, kRound);
-    off = fmaxf(off, fabsf(fmaf(x[j], inverse, kRound - y)));
-    t[j] = __float_as_uint(y);
+  for (int j = 0; j < N; j += 2) {
+    const Two a = {x[j], x[j + 1]};
+    Two q = fma2(a, inv, zero);
+    q = fma2(fma2(q, minus, a), inv, q);
+    q = fma2(fma2(q, minus, a), inv, q);
+    q = fma2(q, one, round);
+    t[j] = __float_as_uint(q.x);
+    t[j + 1] = __float_as_uint(q.y);
   }
 #pragma unroll
   for (int j = 0; j < N; j += 4)
-    b->w[j / 4] = __byte_perm(__byte_perm(t[j], t[j + 1], 0x0040), __byte_perm(t[j + 2], t[j + 3], 0x0040), 0x5410);
-  return off <= 0.5f - 0x1p-15f;
-}
-__device__ __forceinline__ int8_t divided(float x, float scale) {
-  return scale > 0.f ? static_cast<int8_t>(fminf(fmaxf(rintf(x / scale), -127.f), 127.f)) : 0;
+    b.w[j / 4] = __byte_perm(__byte_perm(t[j], t[j + 1], 0x0040), __byte_perm(t[j + 2], t[j + 3], 0x0040), 0x5410);
+  return b;
 }
 
 // A warp per block: the rows of the block that are written stay in registers
@@ -133,59 +158,59 @@ __global__ void __launch_bounds__(kCopyThreads) append_quantized_kernel(const __
   if (w >= p.items) return;
   const int lane = threadIdx.x & 31, r0 = lane / kLanes, c0 = (lane % kLanes) * V::n;
   const Item t = item_of(p.r, p.p, w);
+  const T* from = static_cast<const T*>(t.kv ? p.v : p.k) + (t.token + r0 - t.lo) * (t.kv ? p.v_stride : p.k_stride) + t.h * D + c0;
+  const int64_t stride = (t.kv ? p.v_stride : p.k_stride) * kRows;  // of a pass
+  const bool whole = t.lo == 0 && t.hi == kPage;
+  auto written = [&](int i) { return i * kRows + r0 >= t.lo && i * kRows + r0 < t.hi; };
+  int4 x[kPasses];
+  uint32_t top = 0;
+  if (whole) {
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) x[i] = *reinterpret_cast<const int4*>(from + i * stride);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      x[i] = make_int4(0, 0, 0, 0);
+      if (written(i)) x[i] = *reinterpret_cast<const int4*>(from + i * stride);
+    }
+  }
   if (t.id < 0 || (p.refs && p.refs[t.id] != 1)) {
     if (lane == 0 && p.status) *p.status = -1;
     return;
   }
-  const T* from = static_cast<const T*>(t.kv ? p.v : p.k) + t.h * D + c0;
-  const int64_t stride = t.kv ? p.v_stride : p.k_stride;
-  int4 x[kPasses];
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int s = i * kRows + r0;
-    x[i] = make_int4(0, 0, 0, 0);
-    if (s >= t.lo && s < t.hi) x[i] = *reinterpret_cast<const int4*>(from + (t.token + s - t.lo) * stride);
-  }
+  const int64_t block = (t.id * p.p.hkv + t.h) * 2 + t.kv;
+  const float old = t.lo > 0 ? p.p.scales[block] : 0.f;
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) top = max(top, top_bits(x[i], T()));
   top = __reduce_max_sync(0xffffffffu, top);
-  const int64_t block = (t.id * p.p.hkv + t.h) * 2 + t.kv;
-  const float old = t.lo > 0 ? p.p.scales[block] : 0.f;
   const float mine = __uint_as_float(top) / 127.f;
   const float grown = mine > old || mine != mine ? mine : old;  // a NaN stays
   const bool finite = grown < INFINITY;
   const float scale = finite ? grown : NAN;                     // every value of the block reads as NaN
   int8_t* codes = p.p.codes + block * kPage * D + c0;
-  // scales below 2^-100, whose reciprocals may overflow and whose own rounding can
-  // make codes above 127, leave every row to the division
-  const float inverse = scale >= 0x1p-100f ? 1.f / scale : 0.f;
-  uint32_t divide = 0;
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int s = i * kRows + r0;
+  const float inverse = 1.f / scale;
+  auto store = [&](int i) {
     float f[V::n];
     V::unpack(x[i], f);
-    CodeBytes b;
-    const bool ok = to_codes(f, inverse, &b) && inverse > 0.f;
+    CodeBytes b = to_codes(f, scale, inverse);
     if (!finite) b.w[0] = b.w[1] = 0;
-    if (s >= t.lo && s < t.hi) {
-      store_codes(reinterpret_cast<Codes*>(codes + s * D), b);
-      if (!ok) divide |= 1u << s;
-    }
-  }
-  // in a loop of its own: unrolled into the passes it made the code too long for
-  // the instruction cache (a fifth of the stalls)
+    store_codes(reinterpret_cast<Codes*>(codes + (i * kRows + r0) * D), b);
+  };
+  if (scale < kLeastScale) {
+    // by division, whose quotients pass 127 where the scale itself was rounded down
 #pragma unroll 1
-  for (divide = finite ? divide : 0; divide; divide &= divide - 1) {
-    const int s = __ffs(divide) - 1;
-    float f[V::n];
-    V::unpack(*reinterpret_cast<const int4*>(from + (t.token + s - t.lo) * stride), f);
-    CodeBytes b;
-    b.w[0] = b.w[1] = 0;
+    for (int i = 0; i < kPasses; ++i)
+#pragma unroll 1
+      for (int j = 0; j < V::n && written(i); ++j)
+        codes[(i * kRows + r0) * D + j] = scale > 0.f ? static_cast<int8_t>(fminf(fmaxf(rintf(to_float(from[i * stride + j]) / scale), -127.f), 127.f)) : 0;
+  } else if (whole) {
 #pragma unroll
-    for (int j = 0; j < V::n; ++j) b.c[j] = divided(f[j], scale);
-    store_codes(reinterpret_cast<Codes*>(codes + s * D), b);
+    for (int i = 0; i < kPasses; ++i) store(i);
+  } else {
+    // a token or two of a decode step: most passes have none (a branch of the warp)
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i)
+      if ((i + 1) * kRows > t.lo && i * kRows < t.hi && written(i)) store(i);
   }
   if (t.lo > 0 && scale > old && finite) {
     const float ratio = old / scale;

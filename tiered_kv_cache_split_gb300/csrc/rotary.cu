@@ -55,11 +55,6 @@ __device__ __forceinline__ int64_t position(const RotateParams& p, int64_t token
   return p.wide ? static_cast<const int64_t*>(p.positions)[token] : static_cast<const int32_t*>(p.positions)[token];
 }
 
-__device__ __forceinline__ float to_float(float x) { return x; }
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void put(float* at, float x) { *at = x; }
-__device__ __forceinline__ void put(__nv_bfloat16* at, float x) { *at = __float2bfloat16_rn(x); }
-
 // The sines and cosines of a CTA's tokens, formed once for all their heads. Of a
 // vector's kGroup pairs the first ones of all vectors lie together, then the second
 // ones: neighbouring threads then read neighbouring banks.
