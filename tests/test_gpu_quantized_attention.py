@@ -66,6 +66,50 @@ def test_heads_per_kv_head(dtype, d, g):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d,g", [(64, 1), (128, 3), (64, 4), (128, 5), (128, 7), (64, 9), (128, 16), (128, 17), (64, 33), (128, 64)])
+def test_heads_of_sequences_that_are_cut(dtype, d, g):
+    Case([1500, 641, 20, 900], 2 * g, 2, d, dtype, seed=100 + g).check()
+
+
+@pytest.mark.parametrize("dtype,hkv,g,d", [("bf16", 32, 1, 128), ("f32", 32, 2, 64), ("bf16", 32, 9, 64)])
+def test_pieces_longer_than_a_window(dtype, hkv, g, d):
+    """A CTA's pages come in windows of 384: 16384 pages (listed again and again) of 32 heads
+    give each more than that. Against the values in 64 bits, on some of the heads."""
+    gen = torch.Generator().manual_seed(1)
+    pages, n, hq = 300, 16384, hkv * g
+    pool = torch.randint(-127, 128, (pages, hkv, 2, PAGE, d), generator=gen, dtype=torch.int8).cuda()
+    scales = (torch.rand(pages, hkv, 2, generator=gen) / 32).cuda()
+    mask = torch.randint(0, 1 << 16, (pages,), generator=gen, dtype=torch.int32).cuda()
+    table = torch.randint(0, pages, (2, n), generator=gen, dtype=torch.int32).cuda()
+    counts = [n, n - 1001]
+    q = torch.randn(2, hq, d, generator=gen).to(DT[dtype]).cuda()
+    alpha = torch.zeros(2, hkv, n * PAGE, device="cuda")
+    out = t.quantized_attention(q, pool, scales, table, mask, counts, alpha_sum=alpha)
+    slots = torch.arange(PAGE, device="cuda")
+    for b, c in enumerate(counts):
+        ids = table[b, :c].long()
+        live = ((mask[ids][:, None] >> slots) & 1).flatten() != 0
+        for h in (0, 13, hkv - 1):
+            kv = pool[ids, h].double() * scales[ids, h].double()[..., None, None]
+            k, v = kv[:, 0].reshape(-1, d)[live], kv[:, 1].reshape(-1, d)[live]
+            rows = q[b, h * g:(h + 1) * g].double()
+            p = torch.softmax(rows @ k.T / math.sqrt(d), 1)
+            o, a = p @ v, p @ v.abs()
+            m, e = k.shape[0], 2.0 ** -23
+            # the bound of attend_reference; scales are below 2^-5 and above 2^-40, logits below 60
+            mag = (rows.abs() @ k.abs().T).amax(1, keepdim=True) / math.sqrt(d)
+            dq = 2.0 ** -24 if dtype == "bf16" else 2.0 ** -22
+            qerr = dq * rows.abs().amax(1, keepdim=True) * k.abs().sum(1).max() / math.sqrt(d)
+            delta = (d + 4) * e * mag + qerr + e * (1.45 * mag + 40 + 32)
+            u, w = (2.0 ** -8, 2.0 ** -11) if dtype == "bf16" else (2.0 ** -24, 2.0 ** -21)
+            bound = (u * o.abs() + (w + 2 * delta + 2 * m * e) * a + m * 2.0 ** -36 * v.abs().max()) * 1.02
+            assert ((out[b, h * g:(h + 1) * g].double() - o).abs() <= bound).all()
+            got = alpha[b, h, :c * PAGE].double()
+            assert ((got[live] - p.sum(0)).abs() <= (p * (2 * delta + (m + 16) * e)).sum(0) + 1e-30).all()
+            assert (got[~live] == 0).all() and (alpha[b, h, c * PAGE:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_rows_that_keep_nothing(dtype):
     """No page, no valid slot, pages outside the pool: output 0, alpha untouched; other rows as they were."""
     c = Case([100, 50, 0, 64, 40], 8, 2, 64, dtype)

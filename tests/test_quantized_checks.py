@@ -34,7 +34,7 @@ def refused(lib, status, want, *words):
 
 
 def rotate(lib, n=5, hq=8, hk=2, d=64, r=64, dt=L.DTYPE_BF16, il=0, inv=0, scale=1.0, steps=I, pos=I, bits=64, q=I, sq=640, k=I, sk=640,
-           qo=2 * I, so=512, ko=2 * I, to=128):
+           qo=2 * I, so=512, ko=3 * I, to=128):
     return lib.tkv_rotate(n, hq, hk, d, r, dt, il, inv, scale, steps, pos, bits, q, sq, k, sk, qo, so, ko, to, None)
 
 
@@ -47,6 +47,7 @@ def rotate(lib, n=5, hq=8, hk=2, d=64, r=64, dt=L.DTYPE_BF16, il=0, inv=0, scale
     (dict(steps=I + 4), ("aligned",)), (dict(pos=I + 4), ("aligned",)), (dict(q=I + 1), ("aligned",)), (dict(dt=0, ko=I + 2), ("aligned",)),
     (dict(sq=511), ("strides",)), (dict(sk=127), ("strides",)), (dict(so=500), ("strides",)), (dict(to=-128), ("strides",)),
     (dict(sq=1 << 36), ("strides",)), (dict(qo=I), ("in place",)), (dict(ko=I), ("in place",)),
+    (dict(ko=2 * I), ("the same",)), (dict(so=640, qo=I, to=640, ko=I), ("the same",)),
 ])
 def test_rotate_refusals(lib, bad, words):
     refused(lib, rotate(lib, **bad), L.ERR_INVALID_ARG, *words)

@@ -87,8 +87,9 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// 2^x in two halves, for x where one would leave fp32's normal range
+// v 2^x, in two halves where 2^x alone would leave fp32's normal range
 __device__ __forceinline__ float times_ex2(float v, float x) {
+  if (fabsf(x) <= 120.f) return v * exp2f(x);
   const float h = exp2f(0.5f * x);
   return v * h * h;
 }

@@ -231,6 +231,7 @@ tkv_status tkv_rotate(int64_t n_tokens, int32_t n_q_heads, int32_t n_k_heads, in
     return tkv_status(report(TKV_ERR_INVALID_ARG, "token strides must hold a token"));
   if ((n_q_heads && q == q_out && q_stride != q_out_stride) || (n_k_heads && k == k_out && k_stride != k_out_stride))
     return tkv_status(report(TKV_ERR_INVALID_ARG, "in place, the output's stride must be the input's"));
+  if (n_q_heads && n_k_heads && q_out == k_out) return tkv_status(report(TKV_ERR_INVALID_ARG, "q_out and k_out are the same"));
   RotateParams p{};
   p.q = q; p.k = k; p.q_out = q_out; p.k_out = k_out;
   p.q_stride = q_stride; p.k_stride = k_stride; p.q_out_stride = q_out_stride; p.k_out_stride = k_out_stride;

@@ -1,7 +1,9 @@
 """Rotary positions and a paged cache held in 8 bits.
 
 Argument marshalling only, with the checks, streams and errors of operators.py;
-include/tkv.h states each operator.
+include/tkv.h states each operator. Small calls are bound by this file: a call
+first asks whether all its arguments are as they should be, and only where they
+are not goes through the checks that name the one that is not.
 """
 from __future__ import annotations
 
@@ -124,15 +126,50 @@ def rotate(q, k, positions, table, inverse=False, out=None, stream=None):
 
 def _blocks(pool, scales, page_table, slot_mask, rows):
     """(device, pages, Hkv, d, and the addresses) of an 8-bit pool and its rows."""
+    try:
+        pages, hkv, two, page, d = pool.shape
+        n, max_pages = page_table.shape
+        dev = pool.get_device()
+        if (two == 2 and page == 16 and n == rows and pool.dtype is torch.int8 and scales.dtype is torch.float32
+                and page_table.dtype is torch.int32 and scales.shape == (pages, hkv, 2) and pool.is_contiguous()
+                and scales.is_contiguous() and page_table.is_contiguous() and scales.get_device() == dev
+                and page_table.get_device() == dev):
+            if slot_mask is None:
+                return dev, pages, hkv, d, pool.data_ptr(), scales.data_ptr(), page_table.data_ptr(), None, max_pages
+            if (slot_mask.dtype in _MASK and slot_mask.shape == (pages,) and slot_mask.is_contiguous()
+                    and slot_mask.get_device() == dev):
+                return (dev, pages, hkv, d, pool.data_ptr(), scales.data_ptr(), page_table.data_ptr(), slot_mask.data_ptr(),
+                        max_pages)
+    except (AttributeError, ValueError):
+        pass
     if not isinstance(pool, torch.Tensor) or pool.dim() != 5:
         raise ValueError("pool: must be int8 [pages, Hkv, 2, 16, d]")
     dev = pool.get_device()
     pages, hkv, _, _, d = pool.shape
-    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or (rows is not None and page_table.shape[0] != rows):
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.shape[0] != rows:
         raise ValueError("page_table: must be [rows, max_pages]")
     return (dev, pages, hkv, d, _dense(pool, "pool", _I8, dev, (pages, hkv, 2, 16, d)),
             _dense(scales, "scales", _F32, dev, (pages, hkv, 2)), _dense(page_table, "page_table", _I32, dev),
-            None if slot_mask is None else _dense(slot_mask, "slot_mask", _MASK, dev, (pages,)))
+            None if slot_mask is None else _dense(slot_mask, "slot_mask", _MASK, dev, (pages,)), page_table.shape[1])
+
+
+def _pair(k, v):
+    """(tokens, heads, d, token strides, dtype) of keys and values of one shape and kind."""
+    try:
+        n, h, d = k.shape
+        if k.dtype is v.dtype and v.shape == k.shape and k.get_device() == v.get_device():
+            (sk, a, b), (sv, e, f) = k.stride(), v.stride()
+            if n > 1 and b == f == 1 and a == e == d and k.dtype in _DTYPES:
+                return n, h, d, sk, sv, _DTYPES[k.dtype]
+    except (AttributeError, ValueError):
+        pass
+    n, h, d, sk = _tokens(k, "k")
+    tv, hv, dv, sv = _tokens(v, "v", k)
+    if k.dtype not in _DTYPES:
+        raise ValueError("k: float32 or bfloat16")
+    if tv != n or hv != h or dv != d:
+        raise ValueError("v: shape must be that of k")
+    return n, h, d, sk, sv, _DTYPES[k.dtype]
 
 
 def append_quantized(k, v, pool, scales, page_table, slot_mask, lens, new_lens, page_refs=None, status=None, stream=None):
@@ -148,28 +185,22 @@ def append_quantized(k, v, pool, scales, page_table, slot_mask, lens, new_lens, 
     page was outside the pool or not the row's alone; its tokens are not written.
     """
     lib = L.load()
-    tk, hk, dk, sk = _tokens(k, "k")
-    tv, hv, dv, sv = _tokens(v, "v", k)
-    dt = _DTYPES.get(k.dtype)
-    if dt is None:
-        raise ValueError("k: float32 or bfloat16")
+    tk, hk, dk, sk, sv, dt = _pair(k, v)
     _no_gradient("k, v", k, v)
     a = _ints(lens, None, "lens")
     rows = len(a)
     b = _ints(new_lens, rows, "new_lens")
-    dev, pages, hkv, d, pp, ps, pt, pm = _blocks(pool, scales, page_table, slot_mask, rows)
+    dev, pages, hkv, d, pp, ps, pt, pm, max_pages = _blocks(pool, scales, page_table, slot_mask, rows)
     if k.get_device() != dev:
         raise ValueError("k: on another device")
     if hk != hkv or dk != d:
         raise ValueError("k: heads and d must be those of pool")
-    if tv != tk or hv != hk or dv != dk:
-        raise ValueError("v: shape must be that of k")
     if sum(b) != tk:
         raise ValueError("new_lens: must add up to the tokens of k")
     pr = None if page_refs is None else _dense(page_refs, "page_refs", _I32, dev, (pages,))
     with _On(dev, stream) as on:
         st = lib.tkv_append_quantized(rows, _at(a), _at(b), hkv, d, dt, k.data_ptr(), sk, v.data_ptr(), sv, pp, ps, pages, pt,
-                                      page_table.shape[1], pm, pr,
+                                      max_pages, pm, pr,
                                       None if status is None else _dense(status, "status", _I32, dev, (1,)), on.raw)
         if st:
             L.check(st)
@@ -186,7 +217,7 @@ def read_quantized(pool, scales, page_table, slot_mask, lens, first=None, dtype=
     b = _ints(lens, None, "lens")
     rows = len(b)
     a = _ints([0] * rows if first is None else first, rows, "first")
-    dev, pages, hkv, d, pp, ps, pt, pm = _blocks(pool, scales, page_table, slot_mask, rows)
+    dev, pages, hkv, d, pp, ps, pt, pm, max_pages = _blocks(pool, scales, page_table, slot_mask, rows)
     n = sum(b) - sum(a)
     with _On(dev, stream) as on:
         if out is None:
@@ -209,7 +240,7 @@ def read_quantized(pool, scales, page_table, slot_mask, lens, first=None, dtype=
             dtype = k.dtype
             if dtype not in _DTYPES:
                 raise ValueError("out: float32 or bfloat16")
-        st = lib.tkv_read_quantized(rows, _at(a), _at(b), hkv, d, _DTYPES[dtype], pp, ps, pages, pt, page_table.shape[1], pm,
+        st = lib.tkv_read_quantized(rows, _at(a), _at(b), hkv, d, _DTYPES[dtype], pp, ps, pages, pt, max_pages, pm,
                                     k.data_ptr(), sk, v.data_ptr(), sv, on.raw)
         if st:
             L.check(st)
@@ -232,13 +263,12 @@ def quantized_attention(q, pool, scales, page_table, slot_mask, page_counts, out
         raise ValueError("q: float32 or bfloat16 [B, Hq, d]")
     _no_gradient("q", q)
     batch, hq, d = q.shape
-    dev, pages, hkv, dp, pp, ps, pt, pm = _blocks(pool, scales, page_table, slot_mask, batch)
+    dev, pages, hkv, dp, pp, ps, pt, pm, max_pages = _blocks(pool, scales, page_table, slot_mask, batch)
     pq = _dense(q, "q", (q.dtype,), dev)
     if dp != d:
         raise ValueError("q: d must be that of pool")
     if pm is None:
         raise ValueError("slot_mask: int32 or uint32 [pages]")
-    max_pages = page_table.shape[1]
     pa = None if alpha_sum is None else _dense(alpha_sum, "alpha_sum", _F32, dev, (batch, hkv, max_pages * 16))
     counts = _ints(page_counts, batch, "page_counts")
     with _On(dev, stream) as on:
