@@ -617,6 +617,9 @@ TKV_API tkv_status tkv_read_quantized(int32_t rows, const int32_t* first, const 
  *   n_q_heads   1 .. 64 times n_kv_heads
  *   dtype       of q and out (F32 or BF16)
  *   scratch     tkv_quantized_attention_scratch_size bytes (256-aligned; may be NULL when that is 0)
+ * At most 2^30 pages x KV heads (each counted for every 16 query heads of a KV
+ * head, F32: 8, and with 8 more per sequence) in one call. Products have codes exact and queries
+ * and weights in fp16 (F32: in two fp16 parts); logits, statistics and sums are fp32.
  * A sequence without a valid slot, or whose logits are all -inf, gives 0. Empty
  * slots may hold any codes; a scale that is not finite counts as NaN and reaches exactly the sequences with a
  * valid slot in its block. */

@@ -144,9 +144,11 @@ __device__ __forceinline__ CodeBytes to_codes(const float (&x)[N], float scale, 
 }
 
 // A warp per block: the rows of the block that are written stay in registers
-// between the maximum and the codes, so K and V are read once. Of a block that
-// holds earlier tokens the scale only grows; where it does, their codes are
-// scaled to it.
+// between the maximum and the codes, so K and V are read once; they are on their
+// way before the page id is here. Of a block that holds earlier tokens the scale only
+// grows; where it does, their codes are scaled to it. HBM bounds the large calls: 40959
+// tokens of 8 heads at d 128 in bf16 (168 MB in, 84 out) take 44 us, 5.8 TB/s, the
+// issue slots being 51 % busy; the least call 4 us.
 template <typename T, int D>
 __global__ void __launch_bounds__(kCopyThreads) append_quantized_kernel(const __grid_constant__ AppendQParams p) {
   using V = Vec<T>;
@@ -242,7 +244,8 @@ struct ReadQParams {
   uint32_t items;
 };
 
-// A warp per block, as the append's.
+// A warp per block, as the append's. 28296 tokens of 8 heads at d 128 to bf16 (58 MB in,
+// 116 out) take 28 us, 6.1 TB/s.
 template <typename T, int D>
 __global__ void __launch_bounds__(kCopyThreads) read_quantized_kernel(const __grid_constant__ ReadQParams p) {
   using V = Vec<T>;

@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotate_kernel(const __grid_con
 // of pairs, or the two that hold them, or one that passes) and goes through the heads
 // of the CTA's tokens, 64 bytes on their way at a time; the first ones leave before
 // the sines are formed. HBM bounds it: 8192 tokens of 40 heads at d 128 in bf16,
-// 168 MB, take 31 us in a graph (5.4 TB/s; 25 at the rate of a copy). CTAs of
+// 168 MB, take 27 us in a row of calls (6.3 TB/s; 25 at the rate of a copy). CTAs of
 // 1024 vectors: with 2048 the second wave is short of CTAs (32 us, and 25 for 22 at
 // 1501 tokens of 64 heads in fp32), with 512 the sines weigh more (34 us).
 template <typename T, bool kInterleaved>
