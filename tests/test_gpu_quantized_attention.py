@@ -67,8 +67,17 @@ def test_heads_per_kv_head(dtype, d, g):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("d,g", [(64, 1), (128, 3), (64, 4), (128, 5), (128, 7), (64, 9), (128, 16), (128, 17), (64, 33), (128, 64)])
-def test_heads_of_sequences_that_are_cut(dtype, d, g):
-    Case([1500, 641, 20, 900], 2 * g, 2, d, dtype, seed=100 + g).check()
+@pytest.mark.parametrize("lens", [[1500, 641, 20, 900], [9000, 33, 0, 4100]])
+def test_heads_of_sequences_that_are_cut(dtype, d, g, lens):
+    """In clusters (up to 16 heads), and on the line."""
+    Case(lens, 2 * g, 2, d, dtype, seed=100 + g).check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("batch,longest", [(1, 200), (1, 1700), (40, 310), (60, 250), (64, 70), (3, 127), (3, 129), (9, 1025)])
+def test_clusters_of_every_size(dtype, batch, longest):
+    """1 to 8 CTAs a sequence and KV head, some of them without a page."""
+    Case([longest * (i + 1) // batch for i in range(batch)], 12, 4, 64, dtype, seed=batch).check()
 
 
 @pytest.mark.parametrize("dtype,hkv,g,d", [("bf16", 32, 1, 128), ("f32", 32, 2, 64), ("bf16", 32, 9, 64)])

@@ -56,19 +56,23 @@ inline int launched(const char* what, cudaError_t e) {
 
 // Launches a kernel whose CTAs may be set up while the kernel ahead of it on the
 // stream ends. Every thread of it waits for that one (cudaGridDependencySynchronize)
-// before it touches memory, so that its own end is the end of all before it.
+// before it touches memory, so that its own end is the end of all before it. cluster:
+// CTAs of a cluster.
 template <typename P, typename... A>
-cudaError_t launch_early(void (*kernel)(P, A...), dim3 ctas, int threads, int bytes, cudaStream_t s, const P& p, A... more) {
+cudaError_t launch_early(void (*kernel)(P, A...), dim3 ctas, int threads, int bytes, cudaStream_t s, int cluster, const P& p, A... more) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = ctas;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, p, more...);
 }
 

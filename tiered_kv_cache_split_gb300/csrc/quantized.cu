@@ -346,7 +346,7 @@ tkv_status tkv_append_quantized(int32_t rows, const int32_t* lens, const int32_t
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   void (*const kernel)(AppendQParams) = dtype == TKV_DTYPE_BF16 ? (head_dim == 64 ? append_quantized_kernel<__nv_bfloat16, 64> : append_quantized_kernel<__nv_bfloat16, 128>)
                                                          : (head_dim == 64 ? append_quantized_kernel<float, 64> : append_quantized_kernel<float, 128>);
-  return tkv_status(launched("quantised append", launch_early(kernel, dim3(n), kCopyThreads, 0, s, p)));
+  return tkv_status(launched("quantised append", launch_early(kernel, dim3(n), kCopyThreads, 0, s, 1, p)));
 }
 
 tkv_status tkv_read_quantized(int32_t rows, const int32_t* first, const int32_t* lens, int32_t n_kv_heads,
@@ -374,7 +374,7 @@ tkv_status tkv_read_quantized(int32_t rows, const int32_t* first, const int32_t*
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   void (*const kernel)(ReadQParams) = dtype == TKV_DTYPE_BF16 ? (head_dim == 64 ? read_quantized_kernel<__nv_bfloat16, 64> : read_quantized_kernel<__nv_bfloat16, 128>)
                                                          : (head_dim == 64 ? read_quantized_kernel<float, 64> : read_quantized_kernel<float, 128>);
-  return tkv_status(launched("quantised read", launch_early(kernel, dim3(n), kCopyThreads, 0, s, p)));
+  return tkv_status(launched("quantised read", launch_early(kernel, dim3(n), kCopyThreads, 0, s, 1, p)));
 }
 
 }  // extern "C"

@@ -43,12 +43,11 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kWindow = 384;        // pages that shared memory describes at a time
 constexpr int kSegmentCost = 8;     // pages' time of a piece's start and end
 constexpr int kLeastPages = 16;     // pages of a CTA's stretch, at least
-// Pages of the longest sequence up to which no segment is cut: a warp takes 0.36 us per
-// page, so 40 pages take 3.6 us, and cutting them costs a second launch (2 us on the
-// device, 4 on the host).
-constexpr int kWholePages = 40;
-constexpr int kAlphaPages = 64;     // pages of a segment up to which its one CTA forms alpha itself
-static_assert(kWholePages <= kAlphaPages, "the CTAs of a call without partials form alpha");
+constexpr int kMaxCluster = 8;      // CTAs of a cluster
+constexpr int kClusterPages = 8;    // pages of each, at least
+constexpr int kJoinPages = 24;      // pages' time of the launch that joins partials: 3 us
+constexpr int kWholePages = 40;     // pages of segments that are not cut however many there are
+constexpr int kAlphaPages = 64;     // line: pages of a segment up to which its one CTA forms alpha itself
 constexpr int kMergeWarps = 4;
 constexpr int kMergeThreads = kMergeWarps * 32;
 constexpr int kAlphaSlots = 512;    // slots of an alpha CTA
@@ -61,15 +60,17 @@ template <> struct Columns<__nv_bfloat16> { static constexpr int heads = 8, part
 template <> struct Columns<float> { static constexpr int heads = 4, parts = 2; };
 
 // How a call is cut. A SEGMENT is the pages of a sequence for one KV head and one
-// group of its query heads. Either every CTA takes a segment (`whole`), or the
-// segments lie one behind the other on a line, each with kSegmentCost pages' room
-// ahead of its pages for its start and end, and CTA k takes the stretch
-// [k, k + 1) * share of that line: all CTAs run at once and read the same number
-// of pages, and a segment is cut only where a stretch ends. (Units of 72 pages in
-// several waves took 191 us where this takes 168, 4 x 131072 tokens of 8 heads:
-// every start waits out the queue that the running CTAs fill.) A PIECE is what a CTA has
-// of a segment; one that is not all of it leaves a partial, of which a CTA has two at
-// most: one that goes on from the CTA before (2 k), and one that starts here (2 k + 1).
+// group of its query heads.
+//   Clusters: each segment is a cluster of 1 to 8 CTAs, whose results meet in shared
+//   memory: one launch and no partials, for segments short enough for it.
+//   The line: the segments lie one behind the other, each with kSegmentCost pages' room
+//   ahead of its pages for its start and end, and CTA k takes the stretch
+//   [k, k + 1) * share: all CTAs run at once and read the same number of pages. (Units of
+//   72 pages in several waves took 191 us where this takes 168, 4 x 131072 tokens of 8
+//   heads: every start waits out the queue that the running CTAs fill.)
+// A PIECE is what a CTA has of a segment. On the line a piece that is not all of it
+// leaves a partial, of which a CTA has two at most: one that goes on from the CTA before
+// (2 k), and one that starts here (2 k + 1); a second launch joins them.
 struct AttendParams {
   PoolRef p;
   const void* q;
@@ -78,13 +79,15 @@ struct AttendParams {
   float* part_o;            // [2 * CTAs][heads of a unit][D]
   float4* part_m;           // [2 * CTAs][heads of a unit]: maximum, V's reference, sum
   float2* stats;            // [B][Hq] maximum and sum of rows written whole, for alpha
-  float* spill;             // [page of the call][Hkv][16][groups * heads of a unit], logits in base 2
+  float* spill;             // [page of the call][Hkv][16][columns], logits in base 2
+  int32_t columns;          // query heads of a KV head, filled up to 4 (several groups: to whole ones)
   int32_t B, Hq, G, groups; // groups: head groups of a KV head
   int32_t max_pages;
-  int32_t ctas, share, total, whole;
+  int32_t ctas, cluster;    // cluster: CTAs of a segment, 0: stretches of the line
+  int32_t share, total;
   float qscale;             // log2(e) / sqrt(D)
   int32_t count[kMaxBatch];     // pages
-  int32_t order[kMaxBatch];     // whole: sequences, longest first
+  int32_t order[kMaxBatch];     // clusters: sequences, longest first
   int32_t base[kMaxBatch + 1];  // where the segments of a sequence start on the line
   int32_t page0[kMaxBatch + 1]; // prefix sums of the pages
   int32_t alpha0[kMaxBatch + 1];  // prefix sums of the alpha CTAs of a KV head
@@ -164,6 +167,24 @@ struct AlphaSum {
   }
 };
 
+// A quarter of a row's output from its sum of weighted V, in the units of its references.
+template <typename T>
+__device__ __forceinline__ void put_row(T* at, const float4& x, float top, float ref, float sum) {
+  const float by = sum == 0.f ? 0.f : 1.f / sum, e = sum == 0.f ? 0.f : ref - top - kWeightBits;
+  put4(at, make_float4(times_ex2(x.x * by, e), times_ex2(x.y * by, e), times_ex2(x.z * by, e), times_ex2(x.w * by, e)));
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+// 16 bytes of another CTA's shared memory, at this CTA's address of them
+__device__ __forceinline__ float4 load_cluster(uint32_t at, int cta) {
+  uint32_t there;
+  float4 x;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(cta));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(there) : "memory");
+  return x;
+}
+
 // What a unit keeps of a page: id (-1: none of its slots counts), valid slots and
 // the power k of V's scale, K's scale in the logits' units, and V's scale as f in f 2^k.
 __device__ __forceinline__ int4 page_info(const AttendParams& p, int32_t id, int h) {
@@ -200,7 +221,8 @@ struct Smem {
   static constexpr int o_info = Ring<D>::bytes > merge_bytes ? Ring<D>::bytes : merge_bytes;
   static constexpr int o_stat = o_info + kWindow * 16;
   static constexpr int o_head = o_stat + kWarps * heads * 16;
-  static constexpr int bytes = o_head + heads * 8;
+  static constexpr int o_piece = o_head + heads * 8;
+  static constexpr int bytes = o_piece + heads * 16;
 };
 
 // Where the 16-byte chunk c of row r of a slot lies (rows 0 .. 15 are K's, 16 .. 31
@@ -240,12 +262,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
   int4* s_info = reinterpret_cast<int4*>(smem + S::o_info);
   float4* s_stat = reinterpret_cast<float4*>(smem + S::o_stat);
   float2* s_head = reinterpret_cast<float2*>(smem + S::o_head);
+  float4* s_piece = reinterpret_cast<float4*>(smem + S::o_piece);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   cudaGridDependencySynchronize();
   const int segments = p.p.hkv * p.groups;         // of a sequence
   int b = 0, pos = 0, end = 1;                     // the CTA's stretch
-  if (p.whole) {
-    b = p.order[blockIdx.x / segments];
+  const int rank = p.cluster ? blockIdx.x % p.cluster : 0;
+  if (p.cluster) {
+    b = p.order[blockIdx.x / p.cluster / segments];
   } else {
     pos = blockIdx.x * p.share;
     end = min(pos + p.share, p.total);
@@ -265,8 +289,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
     int segment, lo = 0, hi = p.count[b], stop = end;  // pages lo .. hi - 1 of it
     const int n = hi;
     bool last = false;                             // the stretch goes on with the next sequence
-    if (p.whole) {
-      segment = blockIdx.x % segments;
+    if (p.cluster) {
+      segment = blockIdx.x / p.cluster % segments;
+      lo = n * rank / p.cluster;
+      hi = n * (rank + 1) / p.cluster;
     } else {
       const int span = n + kSegmentCost;
       segment = (pos - p.base[b]) / span;
@@ -349,9 +375,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
         }
       }
       __syncthreads();
-      float* spill = p.spill ? p.spill + ((static_cast<int64_t>(p.page0[b] + w0) * p.p.hkv + h) * kPage * p.groups) * S::heads + group * S::heads : nullptr;
-      const int64_t spill_page = static_cast<int64_t>(p.p.hkv) * kPage * p.groups * S::heads;
-      const int spill_slot = p.groups * S::heads;
+      float* spill = p.spill ? p.spill + (static_cast<int64_t>(p.page0[b] + w0) * p.p.hkv + h) * kPage * p.columns + group * S::heads : nullptr;
+      const int64_t spill_page = static_cast<int64_t>(p.p.hkv) * kPage * p.columns;
+      const int own = min(S::heads, p.columns - group * S::heads);  // columns of the group
       for (int i = 0; i < mine; ++i) {
         wait_copies<R::stages - 2>();
         __syncwarp();                                  // page i is here for all lanes, and page i - 1 is read
@@ -362,7 +388,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
         if (info.x < 0) {                              // an empty page: nothing was copied
           if (spill) {
             float* at = spill + page * spill_page;
-            for (int w = lane; w < kPage * S::heads; w += 32) at[(w / S::heads) * spill_slot + w % S::heads] = kNegInf;
+            for (int w = lane; w < kPage * S::heads; w += 32)
+              if (w % S::heads < own) at[(w / S::heads) * p.columns + w % S::heads] = kNegInf;
           }
           continue;
         }
@@ -401,14 +428,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
             const float top = fmaxf(l[nt][j][0], l[nt][j][1]);
             rise |= top > m[nt][j] + 1.f || top + k > r[nt][j] + 1.f;
           }
-          if (spill) {
-            float* at = spill + page * spill_page + g * spill_slot + nt * kHeads + t * kOwn;
+          if (spill && nt * kHeads + t * kOwn < own) {
+            float* at = spill + page * spill_page + g * p.columns + nt * kHeads + t * kOwn;
             if (kOwn == 2) {
               *reinterpret_cast<float2*>(at) = make_float2(l[nt][0][0], l[nt][kOwn - 1][0]);
-              *reinterpret_cast<float2*>(at + 8 * spill_slot) = make_float2(l[nt][0][1], l[nt][kOwn - 1][1]);
+              *reinterpret_cast<float2*>(at + 8 * p.columns) = make_float2(l[nt][0][1], l[nt][kOwn - 1][1]);
             } else {
               at[0] = l[nt][0][0];
-              at[8 * spill_slot] = l[nt][0][1];
+              at[8 * p.columns] = l[nt][0][1];
             }
           }
         }
@@ -521,8 +548,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
         }
       }
     __syncthreads();
-    const bool all = lo == 0 && hi == n;
+    const bool all = p.cluster || (lo == 0 && hi == n), alone = p.cluster <= 1;
     const int64_t part = (2 * static_cast<int64_t>(blockIdx.x) + (lo == 0)) * S::heads;
+    const int64_t row0 = static_cast<int64_t>(b) * p.Hq + head0;
     for (int i = tid; i < nheads * (D / 4); i += kThreads) {
       const int head = i / (D / 4), d = i % (D / 4) * 4;
       float top = kNegInf, ref = kNegInf, sum = 0.f;
@@ -540,33 +568,76 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
         const float4 y = *reinterpret_cast<const float4*>(s_out + (w * S::heads + head) * S::out_row + d);
         x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
       }
-      const int64_t at = static_cast<int64_t>(b) * p.Hq + head0 + head;
-      if (all) {
-        const float by = sum == 0.f ? 0.f : 1.f / sum, e = sum == 0.f ? 0.f : ref - top - kWeightBits;
-        put4(static_cast<T*>(p.out) + at * D + d,
-             make_float4(times_ex2(x.x * by, e), times_ex2(x.y * by, e), times_ex2(x.z * by, e), times_ex2(x.w * by, e)));
+      if (!alone) {                                // for the cluster, in the first warp's place
+        *reinterpret_cast<float4*>(s_out + head * S::out_row + d) = x;
+        if (d == 0) s_piece[head] = make_float4(top, ref, sum, 0.f);
+      } else if (all) {
+        put_row(static_cast<T*>(p.out) + (row0 + head) * D + d, x, top, ref, sum);
         if (p.stats && d == 0) {
-        p.stats[at] = make_float2(top, sum);
-        s_head[head] = make_float2(top, sum == 0.f ? 0.f : 1.f / sum);
-      }
+          p.stats[row0 + head] = make_float2(top, sum);
+          s_head[head] = make_float2(top, sum == 0.f ? 0.f : 1.f / sum);
+        }
       } else {
         if (d == 0) p.part_m[part + head] = make_float4(top, ref, sum, 0.f);
         *reinterpret_cast<float4*>(p.part_o + (part + head) * D + d) = x;
       }
     }
-    if (p.alpha && all && p.groups == 1 && n <= kAlphaPages) {
+    if (!alone) {
+      // each CTA joins its share of the rows, and for alpha the sums of all heads
+      cluster_arrive();
+      cluster_wait();
+      const uint32_t pieces = static_cast<uint32_t>(__cvta_generic_to_shared(s_piece)), outs = static_cast<uint32_t>(__cvta_generic_to_shared(s_out));
+      float4 st[kMaxCluster];
+      float take[kMaxCluster];
+      float top, ref, sum;
+      auto join_head = [&](int head) {
+        top = ref = kNegInf;
+        sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+          st[c] = c < p.cluster ? load_cluster(pieces + head * 16, c) : make_float4(kNegInf, kNegInf, 0.f, 0.f);
+          top = fmaxf(top, st[c].x);
+          ref = fmaxf(ref, st[c].y);
+        }
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+          sum += st[c].x == kNegInf ? st[c].z : st[c].z * ex2(st[c].x - top);
+          take[c] = st[c].y == kNegInf ? 1.f : ex2(st[c].y - ref);
+        }
+      };
+      for (int i = rank * kThreads + tid; i < nheads * (D / 4); i += p.cluster * kThreads) {
+        const int head = i / (D / 4), d = i % (D / 4) * 4;
+        join_head(head);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+          if (c >= p.cluster) break;
+          const float4 y = load_cluster(outs + (head * S::out_row + d) * 4, c);
+          x.x += y.x * take[c], x.y += y.y * take[c], x.z += y.z * take[c], x.w += y.w * take[c];
+        }
+        put_row(static_cast<T*>(p.out) + (row0 + head) * D + d, x, top, ref, sum);
+      }
+      if (p.alpha && tid < nheads) {
+        join_head(tid);
+        s_head[tid] = make_float2(top, sum == 0.f ? 0.f : 1.f / sum);
+      }
+      cluster_arrive();                            // the others' shared memory is read
+    }
+    if (p.alpha && all && p.groups == 1 && (p.cluster || n <= kAlphaPages)) {
       __syncthreads();
-      const float* l = p.spill + (static_cast<int64_t>(p.page0[b]) * p.p.hkv + h) * kPage * S::heads;
+      const float* l = p.spill + (static_cast<int64_t>(p.page0[b]) * p.p.hkv + h) * kPage * p.columns;
       float* alpha = p.alpha + (static_cast<int64_t>(b) * p.p.hkv + h) * p.max_pages * kPage;
 #pragma unroll 4
-      for (int i = tid; i < n * kPage; i += kThreads) {
-        const float* at = l + ((i / kPage) * static_cast<int64_t>(p.p.hkv) * kPage + i % kPage) * S::heads;
+      for (int i = lo * kPage + tid; i < hi * kPage; i += kThreads) {
+        const float* at = l + ((i / kPage) * static_cast<int64_t>(p.p.hkv) * kPage + i % kPage) * p.columns;
         AlphaSum sum;
 #pragma unroll
-        for (int j = 0; j < S::heads; j += 4) sum.add(*reinterpret_cast<const float4*>(at + j), s_head, j, p.G);
+        for (int j = 0; j < S::heads; j += 4)
+          if (j < p.columns) sum.add(*reinterpret_cast<const float4*>(at + j), s_head, j, p.G);
         if (sum.any) alpha[i] += sum.value;
       }
     }
+    if (!alone) cluster_wait();
     pos = stop;
     b += last;
   }
@@ -579,7 +650,7 @@ struct Pieces {
   __device__ int64_t row(int cta, int heads) const { return (2 * static_cast<int64_t>(cta) + (cta == first)) * heads; }
 };
 __device__ __forceinline__ Pieces pieces_of(const AttendParams& p, int b, int segment) {
-  if (p.whole || p.count[b] == 0) return {0, 0};
+  if (p.count[b] == 0) return {0, 0};
   const int from = p.base[b] + segment * (p.count[b] + kSegmentCost) + kSegmentCost;
   return {from / p.share, (from + p.count[b] - 1) / p.share};
 }
@@ -641,9 +712,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_quantized_kernel(const __
         const float take = s_st[w].y == kNegInf ? 1.f : ex2(s_st[w].y - r);
         y.x += a.x * take, y.y += a.y * take, y.z += a.z * take, y.w += a.w * take;
       }
-      const float by = z == 0.f ? 0.f : 1.f / z, e = z == 0.f ? 0.f : r - m - kWeightBits;
-      put4(static_cast<T*>(p.out) + static_cast<int64_t>(row_out) * D + tid * 4,
-           make_float4(times_ex2(y.x * by, e), times_ex2(y.y * by, e), times_ex2(y.z * by, e), times_ex2(y.w * by, e)));
+      put_row(static_cast<T*>(p.out) + static_cast<int64_t>(row_out) * D + tid * 4, y, m, r, z);
     }
     return;
   }
@@ -660,7 +729,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_quantized_kernel(const __
     const Pieces pc = pieces_of(p, b, h);
     if (pc.first == pc.last) return;               // formed by its CTA
   }
-  const int columns = p.groups * heads;
+  const int columns = p.columns;
   float4 l[kSlots][2];
   const float* spill[kSlots];
   float* alpha = p.alpha + (static_cast<int64_t>(b) * p.p.hkv + h) * p.max_pages * kPage;
@@ -736,6 +805,7 @@ int plan_attend(AttendParams* p, Plan* plan, int32_t batch, int32_t Hq, int32_t 
   plan->nt = p->G > tile ? 2 : 1;
   plan->heads = tile * plan->nt;
   p->groups = (p->G + plan->heads - 1) / plan->heads;
+  p->columns = p->groups == 1 ? (p->G + 3) / 4 * 4 : p->groups * plan->heads;
   int most = 0;
   p->page0[0] = 0;
   for (int b = 0; b < batch; ++b) {
@@ -750,14 +820,20 @@ int plan_attend(AttendParams* p, Plan* plan, int32_t batch, int32_t Hq, int32_t 
   if (total > (int64_t(1) << 30)) return report(TKV_ERR_INVALID_ARG, "more than 2^30 pages and heads in one call");
   p->total = static_cast<int32_t>(total);
   p->share = static_cast<int32_t>(std::max<int64_t>((total + slots - 1) / slots, kSegmentCost + kLeastPages));
-  // Short segments stay whole: a CTA reads kWholePages in the time that the launch
-  // which joins partials would take.
-  p->whole = most <= kWholePages;
+  // Clusters save the partials and the launch that joins them, worth kJoinPages pages of a
+  // CTA's time, and lose where their CTAs get more pages than the line's (us with alpha, line
+  // and clusters): 8 rows of 2000 tokens, 4 KV heads, 16.4 and 14.4; 64 of 1000, 8, 37 and 31; one of 8192,
+  // 8, 15 and 24; the benchmark's batch 43 and 46. More segments than CTAs run at once would leave the last
+  // wave short: then only if they are short too.
+  int c = 1;
+  while (c < kMaxCluster && segments * batch * c * 2 <= slots && most >= 2 * c * kClusterPages) c *= 2;
+  const bool clusters = segments * batch <= slots ? (most + c - 1) / c <= p->share + kJoinPages : most <= kWholePages;
+  p->cluster = p->groups == 1 && clusters ? c : 0;  // alpha takes the sums of all heads: one group
   p->alpha0[0] = 0;
   for (int b = 0; b < batch; ++b)
-    p->alpha0[b + 1] = p->alpha0[b] + (p->whole && p->groups == 1 ? 0 : (p->count[b] * kPage + kAlphaSlots - 1) / kAlphaSlots);
-  if (p->whole) {
-    p->ctas = static_cast<int32_t>(segments * batch);
+    p->alpha0[b + 1] = p->alpha0[b] + (p->cluster ? 0 : (p->count[b] * kPage + kAlphaSlots - 1) / kAlphaSlots);
+  if (p->cluster) {
+    p->ctas = static_cast<int32_t>(segments * batch * p->cluster);
     for (int b = 0; b < batch; ++b) p->order[b] = b;
     std::sort(p->order, p->order + batch, [&](int a, int b) { return p->count[a] != p->count[b] ? p->count[a] > p->count[b] : a < b; });
   } else {
@@ -766,11 +842,11 @@ int plan_attend(AttendParams* p, Plan* plan, int32_t batch, int32_t Hq, int32_t 
     for (int b = 0; b < batch; ++b) p->base[b + 1] = p->base[b] + static_cast<int32_t>(segments) * (p->count[b] + kSegmentCost);
   }
   auto align = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t rows = p->whole ? 0 : 2 * static_cast<size_t>(p->ctas) * plan->heads;
+  const size_t rows = p->cluster ? 0 : 2 * static_cast<size_t>(p->ctas) * plan->heads;
   plan->o_m = align(rows * D * 4);
   plan->o_stats = plan->o_m + align(rows * 16);
   plan->o_spill = plan->o_stats + (want_alpha ? align(static_cast<size_t>(batch) * Hq * 8) : 0);
-  plan->bytes = plan->o_spill + (want_alpha ? align(static_cast<size_t>(p->page0[batch]) * segments * kPage * plan->heads * 4) : 0);
+  plan->bytes = plan->o_spill + (want_alpha ? align(static_cast<size_t>(p->page0[batch]) * Hkv * kPage * p->columns * 4) : 0);
   return TKV_OK;
 }
 
@@ -780,16 +856,16 @@ cudaError_t launch_units(const AttendParams& p, cudaStream_t s) {
   static SharedMemoryOptIn opt_in;
   const cudaError_t e = opt_in.once(reinterpret_cast<const void*>(attend_quantized_kernel<T, D, NT>), bytes);
   if (e != cudaSuccess) return e;
-  return launch_early(attend_quantized_kernel<T, D, NT>, dim3(p.ctas), kThreads, bytes, s, p);
+  return launch_early(attend_quantized_kernel<T, D, NT>, dim3(p.ctas), kThreads, bytes, s, std::max(p.cluster, 1), p);
 }
 
 template <typename T, int D>
 cudaError_t launch_attend(const AttendParams& p, const Plan& plan, cudaStream_t s) {
   cudaError_t e = plan.nt == 1 ? launch_units<T, D, 1>(p, s) : launch_units<T, D, 2>(p, s);
-  const int64_t rows = p.whole ? 0 : static_cast<int64_t>(p.B) * p.Hq;
+  const int64_t rows = p.cluster ? 0 : static_cast<int64_t>(p.B) * p.Hq;
   const int64_t parts = p.alpha ? static_cast<int64_t>(p.alpha0[p.B]) * p.p.hkv : 0;
   if (e != cudaSuccess || rows + parts == 0) return e;
-  return launch_early(merge_quantized_kernel<T, D>, dim3(static_cast<unsigned>(rows + parts)), kMergeThreads, 0, s, p, plan.heads);
+  return launch_early(merge_quantized_kernel<T, D>, dim3(static_cast<unsigned>(rows + parts)), kMergeThreads, 0, s, 1, p, plan.heads);
 }
 
 }  // namespace

@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotate_vectors_kernel(const __
 template <typename T>
 cudaError_t launch_rotate(const RotateParams& p, bool vectors, dim3 ctas, cudaStream_t s) {
   void (*const kernel)(RotateParams) = !vectors ? rotate_kernel<T> : p.interleaved ? rotate_vectors_kernel<T, true> : rotate_vectors_kernel<T, false>;
-  return launch_early(kernel, ctas, kRotaryThreads, 0, s, p);
+  return launch_early(kernel, ctas, kRotaryThreads, 0, s, 1, p);
 }
 
 }  // namespace
