@@ -52,6 +52,8 @@ constexpr int kMergeWarps = 4;
 constexpr int kMergeThreads = kMergeWarps * 32;
 constexpr int kAlphaSlots = 512;    // slots of an alpha CTA
 constexpr int kSms = 152;
+constexpr int kMaxShared = 232448;    // bytes of a CTA, and of an SM (of which each CTA takes 1 KB more)
+constexpr int kSmShared = 233472;
 constexpr float kNegInf = -INFINITY;
 constexpr float kWeightBits = 13.f; // weights are at most 2^15: reference lag and f below 2 each
 
@@ -79,7 +81,8 @@ struct AttendParams {
   float* part_o;            // [2 * CTAs][heads of a unit][D]
   float4* part_m;           // [2 * CTAs][heads of a unit]: maximum, V's reference, sum
   float2* stats;            // [B][Hq] maximum and sum of rows written whole, for alpha
-  float* spill;             // [page of the call][Hkv][16][columns], logits in base 2
+  float* spill;             // [page of the call][Hkv][16][columns], logits in base 2; null: in shared memory
+  int32_t keep;             // logits are kept, for alpha
   int32_t columns;          // query heads of a KV head, filled up to 4 (several groups: to whole ones)
   int32_t B, Hq, G, groups; // groups: head groups of a KV head
   int32_t max_pages;
@@ -263,6 +266,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
   float4* s_stat = reinterpret_cast<float4*>(smem + S::o_stat);
   float2* s_head = reinterpret_cast<float2*>(smem + S::o_head);
   float4* s_piece = reinterpret_cast<float4*>(smem + S::o_piece);
+  float* s_spill = reinterpret_cast<float*>(smem + S::bytes);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   cudaGridDependencySynchronize();
   const int segments = p.p.hkv * p.groups;         // of a sequence
@@ -375,8 +379,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
         }
       }
       __syncthreads();
-      float* spill = p.spill ? p.spill + (static_cast<int64_t>(p.page0[b] + w0) * p.p.hkv + h) * kPage * p.columns + group * S::heads : nullptr;
-      const int64_t spill_page = static_cast<int64_t>(p.p.hkv) * kPage * p.columns;
+      float* spill = p.spill ? p.spill + (static_cast<int64_t>(p.page0[b] + w0) * p.p.hkv + h) * kPage * p.columns + group * S::heads
+                             : s_spill + (w0 - lo) * kPage * p.columns;
+      const int64_t spill_page = static_cast<int64_t>(p.spill ? p.p.hkv : 1) * kPage * p.columns;
       const int own = min(S::heads, p.columns - group * S::heads);  // columns of the group
       for (int i = 0; i < mine; ++i) {
         wait_copies<R::stages - 2>();
@@ -386,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
         const int4 info = s_info[page];
         const uint32_t live = info.y & kFullMask;
         if (info.x < 0) {                              // an empty page: nothing was copied
-          if (spill) {
+          if (p.keep) {
             float* at = spill + page * spill_page;
             for (int w = lane; w < kPage * S::heads; w += 32)
               if (w % S::heads < own) at[(w / S::heads) * p.columns + w % S::heads] = kNegInf;
@@ -428,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
             const float top = fmaxf(l[nt][j][0], l[nt][j][1]);
             rise |= top > m[nt][j] + 1.f || top + k > r[nt][j] + 1.f;
           }
-          if (spill && nt * kHeads + t * kOwn < own) {
+          if (p.keep && nt * kHeads + t * kOwn < own) {
             float* at = spill + page * spill_page + g * p.columns + nt * kHeads + t * kOwn;
             if (kOwn == 2) {
               *reinterpret_cast<float2*>(at) = make_float2(l[nt][0][0], l[nt][kOwn - 1][0]);
@@ -573,8 +578,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
         if (d == 0) s_piece[head] = make_float4(top, ref, sum, 0.f);
       } else if (all) {
         put_row(static_cast<T*>(p.out) + (row0 + head) * D + d, x, top, ref, sum);
-        if (p.stats && d == 0) {
-          p.stats[row0 + head] = make_float2(top, sum);
+        if (p.keep && d == 0) {
+          if (p.stats) p.stats[row0 + head] = make_float2(top, sum);
           s_head[head] = make_float2(top, sum == 0.f ? 0.f : 1.f / sum);
         }
       } else {
@@ -625,11 +630,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
     }
     if (p.alpha && all && p.groups == 1 && (p.cluster || n <= kAlphaPages)) {
       __syncthreads();
-      const float* l = p.spill + (static_cast<int64_t>(p.page0[b]) * p.p.hkv + h) * kPage * p.columns;
+      const float* l = p.spill ? p.spill + (static_cast<int64_t>(p.page0[b]) * p.p.hkv + h) * kPage * p.columns : s_spill - lo * kPage * p.columns;
+      const int64_t page = static_cast<int64_t>(p.spill ? p.p.hkv : 1) * kPage;
       float* alpha = p.alpha + (static_cast<int64_t>(b) * p.p.hkv + h) * p.max_pages * kPage;
 #pragma unroll 4
       for (int i = lo * kPage + tid; i < hi * kPage; i += kThreads) {
-        const float* at = l + ((i / kPage) * static_cast<int64_t>(p.p.hkv) * kPage + i % kPage) * p.columns;
+        const float* at = l + ((i / kPage) * page + i % kPage) * p.columns;
         AlphaSum sum;
 #pragma unroll
         for (int j = 0; j < S::heads; j += 4)
@@ -787,8 +793,15 @@ __global__ void __launch_bounds__(kMergeThreads) merge_quantized_kernel(const __
 struct Plan {
   int nt;      // column tiles of a unit
   int heads;   // of a unit
+  int shared;  // bytes of shared memory for logits
   size_t o_m, o_stats, o_spill, bytes;  // scratch
 };
+
+template <int D>
+int smem_bytes(int dtype, int nt) {
+  if (dtype == TKV_DTYPE_BF16) return nt == 1 ? Smem<__nv_bfloat16, D, 1>::bytes : Smem<__nv_bfloat16, D, 2>::bytes;
+  return nt == 1 ? Smem<float, D, 1>::bytes : Smem<float, D, 2>::bytes;
+}
 
 int plan_attend(AttendParams* p, Plan* plan, int32_t batch, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype,
                 const int32_t* page_counts, int32_t max_pages, bool want_alpha) {
@@ -845,23 +858,31 @@ int plan_attend(AttendParams* p, Plan* plan, int32_t batch, int32_t Hq, int32_t 
   const size_t rows = p->cluster ? 0 : 2 * static_cast<size_t>(p->ctas) * plan->heads;
   plan->o_m = align(rows * D * 4);
   plan->o_stats = plan->o_m + align(rows * 16);
-  plan->o_spill = plan->o_stats + (want_alpha ? align(static_cast<size_t>(batch) * Hq * 8) : 0);
-  plan->bytes = plan->o_spill + (want_alpha ? align(static_cast<size_t>(p->page0[batch]) * Hkv * kPage * p->columns * 4) : 0);
+  plan->o_spill = plan->o_stats + (want_alpha && !p->cluster ? align(static_cast<size_t>(batch) * Hq * 8) : 0);
+  plan->bytes = plan->o_spill;
+  plan->shared = 0;
+  if (want_alpha) {
+    // logits stay in the clusters' shared memory where all CTAs still run at once with it
+    const int64_t need = static_cast<int64_t>((most + c - 1) / c) * kPage * p->columns * 4;
+    const int64_t cta = need + (D == 64 ? smem_bytes<64>(dtype, plan->nt) : smem_bytes<128>(dtype, plan->nt));
+    if (p->cluster && cta <= kMaxShared && p->ctas <= kSms * (kSmShared / (cta + 1024))) plan->shared = static_cast<int>(need);
+    else plan->bytes += align(static_cast<size_t>(p->page0[batch]) * Hkv * kPage * p->columns * 4);
+  }
   return TKV_OK;
 }
 
 template <typename T, int D, int NT>
-cudaError_t launch_units(const AttendParams& p, cudaStream_t s) {
-  constexpr int bytes = Smem<T, D, NT>::bytes;
+cudaError_t launch_units(const AttendParams& p, int shared, cudaStream_t s) {
+  const int bytes = Smem<T, D, NT>::bytes + shared;
   static SharedMemoryOptIn opt_in;
-  const cudaError_t e = opt_in.once(reinterpret_cast<const void*>(attend_quantized_kernel<T, D, NT>), bytes);
+  const cudaError_t e = opt_in.once(reinterpret_cast<const void*>(attend_quantized_kernel<T, D, NT>), kMaxShared);
   if (e != cudaSuccess) return e;
   return launch_early(attend_quantized_kernel<T, D, NT>, dim3(p.ctas), kThreads, bytes, s, std::max(p.cluster, 1), p);
 }
 
 template <typename T, int D>
 cudaError_t launch_attend(const AttendParams& p, const Plan& plan, cudaStream_t s) {
-  cudaError_t e = plan.nt == 1 ? launch_units<T, D, 1>(p, s) : launch_units<T, D, 2>(p, s);
+  cudaError_t e = plan.nt == 1 ? launch_units<T, D, 1>(p, plan.shared, s) : launch_units<T, D, 2>(p, plan.shared, s);
   const int64_t rows = p.cluster ? 0 : static_cast<int64_t>(p.B) * p.Hq;
   const int64_t parts = p.alpha ? static_cast<int64_t>(p.alpha0[p.B]) * p.p.hkv : 0;
   if (e != cudaSuccess || rows + parts == 0) return e;
@@ -909,8 +930,9 @@ tkv_status tkv_quantized_attention(int32_t batch, int32_t n_q_heads, int32_t n_k
   p.q = q; p.out = out; p.alpha = alpha_sum;
   p.part_o = reinterpret_cast<float*>(at);
   p.part_m = reinterpret_cast<float4*>(at + plan.o_m);
-  p.stats = alpha_sum ? reinterpret_cast<float2*>(at + plan.o_stats) : nullptr;
-  p.spill = alpha_sum ? reinterpret_cast<float*>(at + plan.o_spill) : nullptr;
+  p.keep = alpha_sum != nullptr;
+  p.stats = alpha_sum && !p.cluster ? reinterpret_cast<float2*>(at + plan.o_stats) : nullptr;
+  p.spill = alpha_sum && !plan.shared ? reinterpret_cast<float*>(at + plan.o_spill) : nullptr;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (dtype == TKV_DTYPE_BF16) e = head_dim == 64 ? launch_attend<__nv_bfloat16, 64>(p, plan, s) : launch_attend<__nv_bfloat16, 128>(p, plan, s);
