@@ -51,6 +51,7 @@ constexpr int kAlphaPages = 64;     // line: pages of a segment up to which its 
 constexpr int kMergeWarps = 4;
 constexpr int kMergeThreads = kMergeWarps * 32;
 constexpr int kAlphaSlots = 512;    // slots of an alpha CTA
+constexpr int kMaxColumns = 72;     // 64 heads per KV head in groups of 8 or 16, and what a load of 8 reads past them
 constexpr int kSms = 152;
 constexpr int kMaxShared = 232448;    // bytes of a CTA, and of an SM (of which each CTA takes 1 KB more)
 constexpr int kSmShared = 233472;
@@ -155,20 +156,23 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from, uint64_t p
 __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;"); }
 template <int N> __device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// A slot's weights, summed over the heads, from their logits.
+// A slot's weights, summed over the heads, from their logits and each head's (maximum,
+// 1 / sum), which are (0, 0) for columns without a head and for rows without a weight.
 struct AlphaSum {
   float value = 0.f;
-  bool any = false;
-  __device__ __forceinline__ void add(const float4& l, const float2* head, int j, int G) {  // heads j .. j + 3: (maximum, 1 / sum)
+  bool any = false;  // a valid slot
+  __device__ __forceinline__ void add(const float4& l, const float2* head) {
     const float x[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (j + i >= G || x[i] == kNegInf) continue;
-      any = true;
-      value += ex2(x[i] - head[j + i].x) * head[j + i].y;
+      const float w = ex2(x[i] - head[i].x) * head[i].y;
+      const bool valid = x[i] != kNegInf;
+      value += valid ? w : 0.f;  // a NaN of the row stays out of its empty slots
+      any |= valid;
     }
   }
 };
+__device__ __forceinline__ float2 alpha_head(float top, float sum) { return sum == 0.f ? make_float2(0.f, 0.f) : make_float2(top, 1.f / sum); }
 
 // A quarter of a row's output from its sum of weighted V, in the units of its references.
 template <typename T>
@@ -399,8 +403,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
           continue;
         }
         const char* slot = smem + (warp * R::stages + i % R::stages) * R::page_bytes;
-        // S^T = K Q^T
-        float s[NT][4] = {};
+        // S^T = K Q^T, as two sums: shorter chains, and half as many cut additions in each
+        float s[NT][4] = {}, s1[NT][4] = {};
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
           const uint4 a = *reinterpret_cast<const uint4*>(slot + chunk_at<D>(g, c * 4 + t));
@@ -411,9 +415,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
             const uint32_t x = av[w] ^ 0x80808080u, y = dv[w] ^ 0x80808080u;
             const uint32_t a0 = codes2<kLow>(x), a1 = codes2<kLow>(y), a2 = codes2<kHigh>(x), a3 = codes2<kHigh>(y);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma(s[nt], a0, a1, a2, a3, qf[nt][c * 4 + w][0], qf[nt][c * 4 + w][1]);
+            for (int nt = 0; nt < NT; ++nt) mma(w & 1 ? s1[nt] : s[nt], a0, a1, a2, a3, qf[nt][c * 4 + w][0], qf[nt][c * 4 + w][1]);
           }
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) add4(s[nt], s1[nt]);
         // logits (base 2) of keys g and g + 8
         const float sk = __int_as_float(info.z), f = __int_as_float(info.w);
         const float k = static_cast<float>((info.y >> 16) - 256);
@@ -580,13 +586,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
         put_row(static_cast<T*>(p.out) + (row0 + head) * D + d, x, top, ref, sum);
         if (p.keep && d == 0) {
           if (p.stats) p.stats[row0 + head] = make_float2(top, sum);
-          s_head[head] = make_float2(top, sum == 0.f ? 0.f : 1.f / sum);
+          s_head[head] = alpha_head(top, sum);
         }
       } else {
         if (d == 0) p.part_m[part + head] = make_float4(top, ref, sum, 0.f);
         *reinterpret_cast<float4*>(p.part_o + (part + head) * D + d) = x;
       }
     }
+    if (p.keep && tid >= nheads && tid < S::heads) s_head[tid] = make_float2(0.f, 0.f);
     if (!alone) {
       // each CTA joins its share of the rows, and for alpha the sums of all heads
       cluster_arrive();
@@ -624,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
       }
       if (p.alpha && tid < nheads) {
         join_head(tid);
-        s_head[tid] = make_float2(top, sum == 0.f ? 0.f : 1.f / sum);
+        s_head[tid] = alpha_head(top, sum);
       }
       cluster_arrive();                            // the others' shared memory is read
     }
@@ -639,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
         AlphaSum sum;
 #pragma unroll
         for (int j = 0; j < S::heads; j += 4)
-          if (j < p.columns) sum.add(*reinterpret_cast<const float4*>(at + j), s_head, j, p.G);
+          if (j < p.columns) sum.add(*reinterpret_cast<const float4*>(at + j), s_head + j);
         if (sum.any) alpha[i] += sum.value;
       }
     }
@@ -677,7 +684,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_quantized_kernel(const __
   constexpr int E = D / 32;
   __shared__ float s_x[kMergeWarps][D];
   __shared__ float4 s_st[kMergeWarps];
-  __shared__ float2 s_head[64];
+  __shared__ float2 s_head[kMaxColumns];
   cudaGridDependencySynchronize();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int parts = p.alpha ? p.alpha0[p.B] * p.p.hkv : 0;
@@ -757,6 +764,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_quantized_kernel(const __
     before[k] = i < slots ? alpha[i] : 0.f;
   }
   load(0);
+  if (tid >= p.G && tid < kMaxColumns) s_head[tid] = make_float2(0.f, 0.f);
   for (int i = tid / 8; i < p.G; i += kMergeThreads / 8) {  // eight lanes per head
     const uint32_t lanes = 0xffu << (lane & 24);
     const Pieces pc = pieces_of(p, b, h * p.groups + i / heads);
@@ -773,7 +781,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_quantized_kernel(const __
 #pragma unroll
       for (int d = 1; d < 8; d <<= 1) join(m, z, __shfl_xor_sync(lanes, m, d), __shfl_xor_sync(lanes, z, d));
     }
-    if (lane % 8 == 0) s_head[i] = make_float2(m, z == 0.f ? 0.f : 1.f / z);
+    if (lane % 8 == 0) s_head[i] = alpha_head(m, z);
   }
   __syncthreads();
   for (int j = 0; j < p.G; j += 8) {
@@ -781,7 +789,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_quantized_kernel(const __
 #pragma unroll
     for (int k = 0; k < kSlots; ++k)
 #pragma unroll
-      for (int v = 0; v < 2; ++v) sum[k].add(l[k][v], s_head, j + 4 * v, p.G);
+      for (int v = 0; v < 2; ++v) sum[k].add(l[k][v], s_head + j + 4 * v);
   }
 #pragma unroll
   for (int k = 0; k < kSlots; ++k)
