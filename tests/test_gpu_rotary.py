@@ -169,3 +169,14 @@ def test_many_tokens():
     for i in range(0, 5001, 97):
         one, _ = t.rotate(q[i:i + 1], None, pos[i:i + 1], table)
         assert torch.equal(one[0], qo[i])
+
+
+def test_outputs_are_packed():
+    """Whatever the inputs' strides."""
+    table = t.rotary_table(64)
+    qkv = rand(17, 9, 12, 64).cuda()
+    for q, k in ((qkv[:, :8], qkv[:, 8:10]), (qkv[::2, :1], qkv[::2, 8:9]), (qkv[:1, :8], qkv[:1, 9:]), (qkv[:, 3:4], qkv[:, 4:8])):
+        qo, ko = t.rotate(q, k, torch.arange(len(q)).cuda(), table)
+        assert qo.is_contiguous() and ko.is_contiguous() and qo.shape == q.shape and ko.shape == k.shape
+        wq, wk = t.rotate(q.contiguous(), k.contiguous(), torch.arange(len(q)).cuda(), table)
+        assert torch.equal(qo, wq) and torch.equal(ko, wk)

@@ -16,6 +16,12 @@ from . import _lib as L
 from .operators import _DTYPES, _I32, _MASK, _On, _at, _dense, _ints, _no_gradient, _tokens
 
 _I8, _F32 = (torch.int8,), (torch.float32,)
+_SHORT_PAGES = 192     # 8 CTAs of a cluster with 24 pages each
+
+
+def _like(on, x):
+    """A dense tensor like x, from the memory of the call's stream."""
+    return torch.empty_like(x) if on.given is None else on.empty(x.shape, x.dtype)
 
 
 class RotaryTable:
@@ -102,8 +108,8 @@ def rotate(q, k, positions, table, inverse=False, out=None, stream=None):
     ps = _dense(table.steps, "table", (torch.int64,), dev)
     with _On(dev, stream) as on:
         if out is None:
-            qo, so = on.empty((n, hq, d), q.dtype), hq * d
-            ko, to = (None, 0) if k is None else (on.empty((n, hk, d), q.dtype), hk * d)
+            qo, so = _like(on, q), hq * d
+            ko, to = (None, 0) if k is None else (_like(on, k), hk * d)
         else:
             if not isinstance(out, (tuple, list)) or len(out) != 2 or (out[1] is None) != (k is None):
                 raise ValueError("out: (q_out, k_out)")
@@ -225,7 +231,8 @@ def read_quantized(pool, scales, page_table, slot_mask, lens, first=None, dtype=
                 raise ValueError("first: must not pass lens")
             if dtype not in _DTYPES:
                 raise ValueError("dtype: float32 or bfloat16")
-            k, v = on.empty((n, hkv, d), dtype), on.empty((n, hkv, d), dtype)
+            k = on.empty((n, hkv, d), dtype)
+            v = _like(on, k)
             sk = sv = hkv * d
         else:
             if not isinstance(out, (tuple, list)) or len(out) != 2:
@@ -273,11 +280,19 @@ def quantized_attention(q, pool, scales, page_table, slot_mask, page_counts, out
     counts = _ints(page_counts, batch, "page_counts")
     with _On(dev, stream) as on:
         if out is None:
-            out = on.empty((batch, hq, d), q.dtype)
+            out = _like(on, q)
             po = out.data_ptr()
         else:
             po = _dense(out, "out", (q.dtype,), dev, (batch, hq, d))
-        c, need = _at(counts), ctypes.c_size_t()
+        c = _at(counts)
+        # short sequences mostly need no scratch: asking for its size first would take a quarter of the call
+        if scratch is None and max(counts, default=0) <= _SHORT_PAGES:
+            st = lib.tkv_quantized_attention(batch, hq, hkv, d, dt, pq, pp, ps, pages, pt, pm, c, max_pages, po, pa, None, 0, on.raw)
+            if st == L.OK:
+                return out
+            if st != L.ERR_INVALID_ARG:
+                L.check(st)
+        need = ctypes.c_size_t()
         st = lib.tkv_quantized_attention_scratch_size(batch, hq, hkv, d, dt, c, max_pages, pa is not None, ctypes.byref(need))
         if st:
             L.check(st)
