@@ -105,7 +105,7 @@ def read(lib, rows=2, first=(0, 3), lens=(5, 16), hkv=2, d=64, dt=L.DTYPE_BF16, 
 
 
 @pytest.mark.parametrize("bad,words", POOL_REFUSALS + [
-    (dict(first=None), ("null",)), (dict(first=(-1, 3)), ("row 0",)), (dict(first=(0, 17)), ("row 1",)), (dict(lens=(129, 16)), ("row 0", "max_pages")),
+    (dict(first=None), ("null",)), (dict(first=(-1, 3)), ("row 0",)), (dict(first=(0, 17)), ("row 1",)), (dict(lens=(129, 16)), ("row 0", "max_pages")), (dict(lens=(5, 2 ** 31 - 1)), ("row 1", "max_pages")),
 ])
 def test_read_refusals(lib, bad, words):
     refused(lib, read(lib, **bad), L.ERR_INVALID_ARG, *words)

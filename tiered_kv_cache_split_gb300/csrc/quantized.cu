@@ -285,18 +285,18 @@ __global__ void __launch_bounds__(kCopyThreads) read_quantized_kernel(const __gr
 
 // ---- host side
 
-// Fills the ranges [first, last) of each row; *tokens, *pages their sums.
+// Fills the ranges [first, last) of each row; *tokens is their sum.
 int check_rows(RowRange* r, int32_t rows, const int32_t* first, const int32_t* last, int32_t max_pages, int64_t* tokens) {
   *tokens = 0;
   r->rows = rows;
   r->page0[0] = 0;
   for (int i = 0; i < rows; ++i) {
+    if (last[i] > max_pages * kPage) return report(TKV_ERR_INVALID_ARG, "row %d: more tokens than its max_pages hold", i);
     r->first[i] = first[i];
     r->last[i] = last[i];
     r->token0[i] = *tokens;
     *tokens += last[i] - first[i];
     r->page0[i + 1] = r->page0[i] + (last[i] > first[i] ? (last[i] + kPage - 1) / kPage - first[i] / kPage : 0);
-    if (last[i] > max_pages * kPage) return report(TKV_ERR_INVALID_ARG, "row %d: more tokens than its max_pages hold", i);
   }
   return TKV_OK;
 }
