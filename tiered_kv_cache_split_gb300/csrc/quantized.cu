@@ -37,7 +37,7 @@ struct RowRange {
 };
 
 struct Item {
-  int row, h, kv;
+  int h, kv;
   int slot0;        // first slot of the page in its row
   int lo, hi;       // slots of the page that the call covers
   int64_t id;       // page id, -1: outside the pool
@@ -58,7 +58,6 @@ __device__ __forceinline__ Item item_of(const RowRange& r, const PoolRef& p, uin
     const int mid = (lo + hi + 1) >> 1;
     if (r.page0[mid] <= static_cast<int32_t>(w)) lo = mid; else hi = mid - 1;
   }
-  t.row = lo;
   const int page = r.first[lo] / kPage + static_cast<int>(w) - r.page0[lo];
   t.slot0 = page * kPage;
   t.lo = max(r.first[lo] - t.slot0, 0);
