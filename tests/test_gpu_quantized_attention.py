@@ -80,25 +80,27 @@ def test_clusters_of_every_size(dtype, batch, longest):
     Case([longest * (i + 1) // batch for i in range(batch)], 12, 4, 64, dtype, seed=batch).check()
 
 
-@pytest.mark.parametrize("dtype,hkv,g,d", [("bf16", 32, 1, 128), ("f32", 32, 2, 64), ("bf16", 32, 9, 64)])
-def test_pieces_longer_than_a_window(dtype, hkv, g, d):
-    """A CTA's pages come in windows of 384: 16384 pages (listed again and again) of 32 heads
-    give each more than that. Against the values in 64 bits, on some of the heads."""
+@pytest.mark.parametrize("dtype,hkv,g,d,batch,n", [("bf16", 32, 1, 128, 2, 16384), ("f32", 32, 2, 64, 2, 16384), ("bf16", 32, 9, 64, 2, 16384),
+                                                   ("bf16", 32, 4, 64, 19, 450), ("f32", 4, 7, 128, 19, 4000)])
+def test_pieces_longer_than_a_window(dtype, hkv, g, d, batch, n):
+    """A CTA's pages come in windows of 384: many pages (listed again and again) of many
+    heads give each more than that, on the line and in clusters of 1 and 8. Against the values in
+    64 bits, on some of the heads."""
     gen = torch.Generator().manual_seed(1)
-    pages, n, hq = 300, 16384, hkv * g
+    pages, hq = 300, hkv * g
     pool = torch.randint(-127, 128, (pages, hkv, 2, PAGE, d), generator=gen, dtype=torch.int8).cuda()
     scales = (torch.rand(pages, hkv, 2, generator=gen) / 32).cuda()
     mask = torch.randint(0, 1 << 16, (pages,), generator=gen, dtype=torch.int32).cuda()
-    table = torch.randint(0, pages, (2, n), generator=gen, dtype=torch.int32).cuda()
-    counts = [n, n - 1001]
-    q = torch.randn(2, hq, d, generator=gen).to(DT[dtype]).cuda()
-    alpha = torch.zeros(2, hkv, n * PAGE, device="cuda")
+    table = torch.randint(0, pages, (batch, n), generator=gen, dtype=torch.int32).cuda()
+    counts = [n - b * (n // 16 if batch == 2 else 1) for b in range(batch)]
+    q = torch.randn(batch, hq, d, generator=gen).to(DT[dtype]).cuda()
+    alpha = torch.zeros(batch, hkv, n * PAGE, device="cuda")
     out = t.quantized_attention(q, pool, scales, table, mask, counts, alpha_sum=alpha)
     slots = torch.arange(PAGE, device="cuda")
-    for b, c in enumerate(counts):
+    for b, c in list(enumerate(counts))[::max(1, batch - 1)]:
         ids = table[b, :c].long()
         live = ((mask[ids][:, None] >> slots) & 1).flatten() != 0
-        for h in (0, 13, hkv - 1):
+        for h in (0, hkv // 2, hkv - 1):
             kv = pool[ids, h].double() * scales[ids, h].double()[..., None, None]
             k, v = kv[:, 0].reshape(-1, d)[live], kv[:, 1].reshape(-1, d)[live]
             rows = q[b, h * g:(h + 1) * g].double()

@@ -180,7 +180,7 @@ def test_python_checks_name_the_argument():
     x = torch.zeros(6, 2, 64)
     ok = (x, x, pool, scales, table, mask, [0, 1, 2], [3, 3, 0])
     for i, bad, word in ((0, x.half(), "v:"), (0, x[:5], "v:"), (1, x[..., :32], "k|v:"), (2, pool.float(), "pool"), (2, pool[:, :, :1], "pool"),
-                         (3, scales[:8], "scales"), (3, scales.double(), "scales"), (4, table.long(), "page_table"), (4, table[:2], "page_table"),
+                         (3, scales[:8], "scales"), (3, scales.double(), "scales"), (3, scales.clone().requires_grad_(), "scales.*backward"), (3, None, "scales"), (4, table.long(), "page_table"), (4, table[:2], "page_table"),
                          (5, mask[:8], "slot_mask"), (6, [0, 1], "new_lens"), (7, [3, 3, 1], "new_lens"), (7, [3, 3], "new_lens"), (0, x[:, :1], "k:|v:")):
         args = list(ok)
         args[i] = bad

@@ -139,7 +139,7 @@ def _blocks(pool, scales, page_table, slot_mask, rows):
         if (two == 2 and page == 16 and n == rows and pool.dtype is torch.int8 and scales.dtype is torch.float32
                 and page_table.dtype is torch.int32 and scales.shape == (pages, hkv, 2) and pool.is_contiguous()
                 and scales.is_contiguous() and page_table.is_contiguous() and scales.get_device() == dev
-                and page_table.get_device() == dev):
+                and page_table.get_device() == dev and not scales.requires_grad):
             if slot_mask is None:
                 return dev, pages, hkv, d, pool.data_ptr(), scales.data_ptr(), page_table.data_ptr(), None, max_pages
             if (slot_mask.dtype in _MASK and slot_mask.shape == (pages,) and slot_mask.is_contiguous()
@@ -154,6 +154,8 @@ def _blocks(pool, scales, page_table, slot_mask, rows):
     pages, hkv, _, _, d = pool.shape
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.shape[0] != rows:
         raise ValueError("page_table: must be [rows, max_pages]")
+    if isinstance(scales, torch.Tensor):
+        _no_gradient("scales", scales)
     return (dev, pages, hkv, d, _dense(pool, "pool", _I8, dev, (pages, hkv, 2, 16, d)),
             _dense(scales, "scales", _F32, dev, (pages, hkv, 2)), _dense(page_table, "page_table", _I32, dev),
             None if slot_mask is None else _dense(slot_mask, "slot_mask", _MASK, dev, (pages,)), page_table.shape[1])
