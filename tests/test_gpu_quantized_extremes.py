@@ -1,0 +1,82 @@
+"""The 8-bit operators where logits, scales and queries are far from one, with
+bounds that a wrong weight cannot hide in."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import tiered_kv_cache_split_gb300 as t
+from operator_helpers import HALF, assert_within
+from quantized_helpers import PAGE
+
+pytestmark = pytest.mark.gpu
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+WEIGHT = {"f32": 2.0 ** -21, "bf16": 2.0 ** -11}     # a weight in two fp16 parts, and in one
+
+
+class Rows:
+    """Sequences of pages of one pool, all in NumPy: codes, scales, masks (10 % of the slots empty, slot 0 never)."""
+
+    def __init__(self, lens, hkv, d, seed):
+        rng = np.random.default_rng(seed)
+        self.counts = [-(-n // PAGE) for n in lens]
+        self.pages = sum(self.counts) + 2
+        ids, at = rng.permutation(self.pages), 0
+        self.table = np.full((len(lens), max(self.counts)), -1, np.int32)
+        self.live = np.zeros((len(lens), self.table.shape[1] * PAGE), bool)
+        self.masks = np.zeros(self.pages, np.int32)
+        for b, n in enumerate(self.counts):
+            self.table[b, :n] = ids[at:at + n]
+            at += n
+            self.live[b, :lens[b]] = rng.random(lens[b]) >= 0.1
+            self.live[b, 0] = lens[b] > 0
+            self.masks[self.table[b, :n]] = (self.live[b, :n * PAGE].reshape(n, PAGE) << np.arange(PAGE)).sum(1)
+        self.codes = rng.integers(-127, 128, (self.pages, hkv, 2, PAGE, d)).astype(np.int8)
+        self.scales = np.ones((self.pages, hkv, 2), np.float32)
+        self.rng = rng
+
+    def attend(self, q, alpha=True):
+        a = torch.zeros(len(self.counts), self.codes.shape[1], self.table.shape[1] * PAGE).cuda() if alpha else None
+        out = t.quantized_attention(q, torch.from_numpy(self.codes).cuda(), torch.from_numpy(self.scales).cuda(),
+                                    torch.from_numpy(self.table).cuda(), torch.from_numpy(self.masks).cuda(), self.counts, alpha_sum=a)
+        return out, a
+
+
+SHAPES = [([1], 1, 64), ([40, 7], 2, 128), ([700, 1, 2600], 4, 64), ([1500, 641, 20, 900], 9, 128), ([9000, 33, 4100], 3, 64),
+          ([9000, 33, 4100], 9, 128), ([333, 40], 17, 64)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("lens,g,d", SHAPES)
+def test_one_key_above_all_at_large_logits(dtype, sign, lens, g, d):
+    """Logits of 2^20 to 2^30 of either sign, one key far above the rest: its V is the
+    output and its weight one, however coarse the logits are. In clusters, on the line and
+    joined by the second launch.
+
+    The gap between the largest logit and the next is a quarter of it, far above its error of some
+    2^-20, so the weights are one and zero. The bound: the output's rounding, the
+    weight's, and 2^-20 for the exponential, the sum of one and the powers of two."""
+    hkv, hq = 2, 2 * g
+    c = Rows(lens, hkv, d, seed=g + d)
+    c.codes[:, :, 0] = 0
+    top = 127 if sign > 0 else -40
+    c.codes[:, :, 0, :, 0] = c.rng.integers(-127, -79, c.codes[:, :, 0, :, 0].shape) if sign < 0 else c.rng.integers(-127, 80, c.codes[:, :, 0, :, 0].shape)
+    c.scales[:, :, 1] = np.exp2(c.rng.uniform(-9, 9, c.scales[:, :, 1].shape))
+    want, wa = np.zeros((len(lens), hq, d)), np.zeros((len(lens), hkv, c.table.shape[1] * PAGE))
+    for b in range(len(lens)):
+        at = c.rng.choice(np.flatnonzero(c.live[b]))
+        page, slot = c.table[b, at // PAGE], at % PAGE
+        c.codes[page, :, 0, slot, 0] = top
+        v = c.codes[page, :, 1, slot].astype(np.float64) * c.scales[page, :, 1, None]
+        want[b], wa[b, :, at] = np.repeat(v, g, 0), g
+    size = np.exp2(c.rng.uniform(20, 30, (len(lens), hq))) * math.sqrt(d) / abs(top)
+    q = np.zeros((len(lens), hq, d), np.float32)
+    q[..., 0] = size
+    q = torch.from_numpy(q).to(DT[dtype]).cuda()
+    bound = (HALF[DT[dtype]] + WEIGHT[dtype] + 2.0 ** -20) * np.abs(want)
+    out, a = c.attend(q)
+    assert_within(out, want, bound)
+    assert_within(a, wa, wa * 2.0 ** -20, "alpha")
+    assert torch.equal(c.attend(q, alpha=False)[0], out)

@@ -17,11 +17,13 @@
 // accumulators are fp32.
 //
 // The scale of K multiplies a page's logits. That of V multiplies its weights: a
-// weight is 2^(l + k + 13 - r) f with V's scale f 2^k, and r a running maximum
-// of l + k of its own, so that pages whose scales are far apart lose nothing in
-// fp16 (weights down to 2^-38 of the largest count). Z sums 2^(l - m) as always.
-// Both references rise only when a logit passes them by more than 1 (a vote per
-// page), so the shuffles and the rescaling are rare.
+// weight is 2^((l - m) + (k + 13 - r)) f with V's scale f 2^k, m the running
+// maximum of the logits and r one of (l - m) + k, so that pages whose scales are
+// far apart lose nothing in fp16 (weights down to 2^-38 of the largest count). Z
+// sums 2^(l - m) as always. r is relative to m: a reference of l + k itself would lose k
+// to rounding from |l| = 2^24 on, and the output its scale. Both references rise only when
+// a logit passes them by more than 1 (a vote per page), so the shuffles and the
+// rescaling are rare.
 //
 // 4 x 131072 tokens of 8 KV heads at d 128 (1.07 GB) take 160 us, 6.7 TB/s, the rate of a
 // copy; the tensor pipe is 17 % busy and the issue slots 53 %. The benchmark's batch (152 MB, 32
@@ -81,7 +83,7 @@ struct AttendParams {
   void* out;
   float* alpha;             // [B][Hkv][max_pages * 16], or null
   float* part_o;            // [2 * CTAs][heads of a unit][D]
-  float4* part_m;           // [2 * CTAs][heads of a unit]: maximum, V's reference, sum
+  float4* part_m;           // [2 * CTAs][heads of a unit]: maximum, V's reference above it, sum
   float2* stats;            // [B][Hq] maximum and sum of rows written whole, for alpha
   float* spill;             // [page of the call][Hkv][16][columns], logits in base 2; null: in shared memory
   int32_t keep;             // logits are kept, for alpha
@@ -174,12 +176,25 @@ struct AlphaSum {
     }
   }
 };
+// The joint maximum of n statistics (maximum, V's reference above it, sum), and V's reference above that.
+struct Peak {
+  float top, ref;
+};
+template <int n, typename Stat>
+__device__ __forceinline__ Peak peak_of(Stat stat) {
+  Peak p = {kNegInf, kNegInf};
+#pragma unroll
+  for (int i = 0; i < n; ++i) p.top = fmaxf(p.top, stat(i).x);
+#pragma unroll
+  for (int i = 0; i < n; ++i) p.ref = fmaxf(p.ref, (stat(i).x - p.top) + stat(i).y);  // -inf or NaN of one without a maximum
+  return p;
+}
 __device__ __forceinline__ float2 alpha_head(float top, float sum) { return sum == 0.f ? make_float2(0.f, 0.f) : make_float2(top, 1.f / sum); }
 
-// A quarter of a row's output from its sum of weighted V, in the units of its references.
+// Four elements of a row's output from its sum of weighted V, in the units of its reference.
 template <typename T>
-__device__ __forceinline__ void put_row(T* at, const float4& x, float top, float ref, float sum) {
-  const float by = sum == 0.f ? 0.f : 1.f / sum, e = sum == 0.f ? 0.f : ref - top - kWeightBits;
+__device__ __forceinline__ void put_row(T* at, const float4& x, float ref, float sum) {
+  const float by = sum == 0.f ? 0.f : 1.f / sum, e = sum == 0.f ? 0.f : ref - kWeightBits;
   put4(at, make_float4(times_ex2(x.x * by, e), times_ex2(x.y * by, e), times_ex2(x.z * by, e), times_ex2(x.w * by, e)));
 }
 
@@ -377,8 +392,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
           for (int i = 0; i < kOwn; ++i) {
             const int of = __shfl_sync(0xffffffffu, e, (2 * t + i) * 4);
             qpow[nt][i] = __uint_as_float(static_cast<uint32_t>(of + 127) << 23);  // infinity for a row that holds one
-            m[nt][i] = r[nt][i] = kNegInf;
-            z[nt][i] = 0.f;
+            m[nt][i] = kNegInf;
+            r[nt][i] = z[nt][i] = 0.f;
           }
 #pragma unroll
           for (int i = 0; i < kTiles; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
@@ -438,8 +453,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
           for (int j = 0; j < kOwn; ++j) {
             l[nt][j][0] = live0 ? s[nt][j] * sk * qpow[nt][j] : kNegInf;
             l[nt][j][1] = live1 ? s[nt][2 + j] * sk * qpow[nt][j] : kNegInf;
-            const float top = fmaxf(l[nt][j][0], l[nt][j][1]);
-            rise |= top > m[nt][j] + 1.f || top + k > r[nt][j] + 1.f;
+            const float over = fmaxf(l[nt][j][0], l[nt][j][1]) - m[nt][j];
+            rise |= over > 1.f || over + k > r[nt][j] + 1.f;
           }
           if (p.keep && nt * kHeads + t * kOwn < own) {
             float* at = spill + page * spill_page + g * p.columns + nt * kHeads + t * kOwn;
@@ -461,12 +476,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
               float top = fmaxf(l[nt][j][0], l[nt][j][1]);
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-              const float m1 = fmaxf(m[nt][j], top), r1 = fmaxf(r[nt][j], top + k);
-              z[nt][j] *= m1 == kNegInf ? 1.f : ex2(m[nt][j] - m1);
-              keep[j] = r1 == kNegInf ? 1.f : ex2(r[nt][j] - r1);
+              const float m1 = fmaxf(m[nt][j], top);
+              keep[j] = 1.f;
+              if (m1 != kNegInf) {
+                const float fall = m[nt][j] - m1, r1 = fmaxf(r[nt][j] + fall, (top - m1) + k);
+                z[nt][j] *= ex2(fall);
+                keep[j] = ex2(fall + (r[nt][j] - r1));
+                m[nt][j] = m1;
+                r[nt][j] = r1;
+              }
               if (kOwn == 1) keep[1] = keep[0];
-              m[nt][j] = m1;
-              r[nt][j] = r1;
             }
 #pragma unroll
             for (int i = 0; i < kTiles; ++i) {
@@ -482,10 +501,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
           float w[2][2];
 #pragma unroll
           for (int j = 0; j < kOwn; ++j) {
-            const float mz = m[nt][j] == kNegInf ? 0.f : m[nt][j], ro = r[nt][j] == kNegInf ? 0.f : k + kWeightBits - r[nt][j];
-            z[nt][j] += ex2(l[nt][j][0] - mz) + ex2(l[nt][j][1] - mz);
-            w[0][j] = live0 ? ex2(l[nt][j][0] + ro) * f : 0.f;
-            w[1][j] = live1 ? ex2(l[nt][j][1] + ro) * f : 0.f;
+            const float mz = m[nt][j] == kNegInf ? 0.f : m[nt][j], ro = k + kWeightBits - r[nt][j];
+            const float x0 = l[nt][j][0] - mz, x1 = l[nt][j][1] - mz;
+            z[nt][j] += ex2(x0) + ex2(x1);
+            w[0][j] = live0 ? ex2(x0 + ro) * f : 0.f;
+            w[1][j] = live1 ? ex2(x1 + ro) * f : 0.f;
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -543,10 +563,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
 #pragma unroll
       for (int j = 0; j < kOwn; ++j) {
         const int head = nt * kHeads + t * kOwn + j;
-        float top = kNegInf;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_stat[w * S::heads + head].y);
-        const float keep = r[nt][j] == kNegInf ? (z[nt][j] == z[nt][j] ? 0.f : NAN) : ex2(r[nt][j] - top);
+        const Peak at = peak_of<kWarps>([&](int w) { return s_stat[w * S::heads + head]; });
+        const float keep = m[nt][j] == kNegInf ? (z[nt][j] == z[nt][j] ? 0.f : NAN) : ex2((m[nt][j] - at.top) + (r[nt][j] - at.ref));
         float* row = s_out + (warp * S::heads + head) * S::out_row + g * (D / 8);
 #pragma unroll
         for (int i = 0; i < kTiles; i += 2) {
@@ -566,32 +584,27 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
     const int64_t row0 = static_cast<int64_t>(b) * p.Hq + head0;
     for (int i = tid; i < nheads * (D / 4); i += kThreads) {
       const int head = i / (D / 4), d = i % (D / 4) * 4;
-      float top = kNegInf, ref = kNegInf, sum = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float4 st = s_stat[w * S::heads + head];
-        top = fmaxf(top, st.x);
-        ref = fmaxf(ref, st.y);
-      }
+      const Peak of = peak_of<kWarps>([&](int w) { return s_stat[w * S::heads + head]; });
+      float sum = 0.f;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float4 st = s_stat[w * S::heads + head];
-        sum += st.x == kNegInf ? st.z : st.z * ex2(st.x - top);
+        sum += st.x == kNegInf ? st.z : st.z * ex2(st.x - of.top);
         const float4 y = *reinterpret_cast<const float4*>(s_out + (w * S::heads + head) * S::out_row + d);
         x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
       }
       if (!alone) {                                // for the cluster, in the first warp's place
         *reinterpret_cast<float4*>(s_out + head * S::out_row + d) = x;
-        if (d == 0) s_piece[head] = make_float4(top, ref, sum, 0.f);
+        if (d == 0) s_piece[head] = make_float4(of.top, of.ref, sum, 0.f);
       } else if (all) {
-        put_row(static_cast<T*>(p.out) + (row0 + head) * D + d, x, top, ref, sum);
+        put_row(static_cast<T*>(p.out) + (row0 + head) * D + d, x, of.ref, sum);
         if (p.keep && d == 0) {
-          if (p.stats) p.stats[row0 + head] = make_float2(top, sum);
-          s_head[head] = alpha_head(top, sum);
+          if (p.stats) p.stats[row0 + head] = make_float2(of.top, sum);
+          s_head[head] = alpha_head(of.top, sum);
         }
       } else {
-        if (d == 0) p.part_m[part + head] = make_float4(top, ref, sum, 0.f);
+        if (d == 0) p.part_m[part + head] = make_float4(of.top, of.ref, sum, 0.f);
         *reinterpret_cast<float4*>(p.part_o + (part + head) * D + d) = x;
       }
     }
@@ -603,20 +616,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
       const uint32_t pieces = static_cast<uint32_t>(__cvta_generic_to_shared(s_piece)), outs = static_cast<uint32_t>(__cvta_generic_to_shared(s_out));
       float4 st[kMaxCluster];
       float take[kMaxCluster];
-      float top, ref, sum;
+      Peak of;
+      float sum;
       auto join_head = [&](int head) {
-        top = ref = kNegInf;
         sum = 0.f;
 #pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c) {
-          st[c] = c < p.cluster ? load_cluster(pieces + head * 16, c) : make_float4(kNegInf, kNegInf, 0.f, 0.f);
-          top = fmaxf(top, st[c].x);
-          ref = fmaxf(ref, st[c].y);
-        }
+        for (int c = 0; c < kMaxCluster; ++c) st[c] = c < p.cluster ? load_cluster(pieces + head * 16, c) : make_float4(kNegInf, 0.f, 0.f, 0.f);
+        of = peak_of<kMaxCluster>([&](int c) { return st[c]; });
 #pragma unroll
         for (int c = 0; c < kMaxCluster; ++c) {
-          sum += st[c].x == kNegInf ? st[c].z : st[c].z * ex2(st[c].x - top);
-          take[c] = st[c].y == kNegInf ? 1.f : ex2(st[c].y - ref);
+          sum += st[c].x == kNegInf ? st[c].z : st[c].z * ex2(st[c].x - of.top);
+          take[c] = st[c].x == kNegInf ? 1.f : ex2((st[c].x - of.top) + (st[c].y - of.ref));
         }
       };
       for (int i = rank * kThreads + tid; i < nheads * (D / 4); i += p.cluster * kThreads) {
@@ -629,11 +639,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
           const float4 y = load_cluster(outs + (head * S::out_row + d) * 4, c);
           x.x += y.x * take[c], x.y += y.y * take[c], x.z += y.z * take[c], x.w += y.w * take[c];
         }
-        put_row(static_cast<T*>(p.out) + (row0 + head) * D + d, x, top, ref, sum);
+        put_row(static_cast<T*>(p.out) + (row0 + head) * D + d, x, of.ref, sum);
       }
       if (p.alpha && tid < nheads) {
         join_head(tid);
-        s_head[tid] = alpha_head(top, sum);
+        s_head[tid] = alpha_head(of.top, sum);
       }
       cluster_arrive();                            // the others' shared memory is read
     }
@@ -694,7 +704,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_quantized_kernel(const __
     const int row_out = blockIdx.x - parts, b = row_out / p.Hq, hq = row_out % p.Hq, h = hq / p.G, head = hq % p.G;
     const Pieces pc = pieces_of(p, b, h * p.groups + head / heads);
     if (pc.first == pc.last) return;               // written by its CTA
-    float m = kNegInf, r = kNegInf, z = 0.f, x[E] = {};
+    float m = kNegInf, r = 0.f, z = 0.f, x[E] = {};
 #pragma unroll 4
     for (int c = pc.first + warp; c <= pc.last; c += kMergeWarps) {
       const int64_t row = pc.row(c, heads) + head % heads;
@@ -702,32 +712,32 @@ __global__ void __launch_bounds__(kMergeThreads) merge_quantized_kernel(const __
       float y[E];
 #pragma unroll
       for (int i = 0; i < E; ++i) y[i] = p.part_o[row * D + lane * E + i];
+      const float m0 = m;
       join(m, z, st.x, st.z);
-      const float top = fmaxf(r, st.y), keep = r == kNegInf ? 1.f : ex2(r - top), take = st.y == kNegInf ? 1.f : ex2(st.y - top);
+      const float ref = fmaxf((m0 - m) + r, (st.x - m) + st.y);
+      const float keep = m0 == kNegInf ? 1.f : ex2((m0 - m) + (r - ref)), take = st.x == kNegInf ? 1.f : ex2((st.x - m) + (st.y - ref));
 #pragma unroll
       for (int i = 0; i < E; ++i) x[i] = x[i] * keep + y[i] * take;
-      r = top;
+      r = m == kNegInf ? 0.f : ref;
     }
 #pragma unroll
     for (int i = 0; i < E; ++i) s_x[warp][lane * E + i] = x[i];
     if (lane == 0) s_st[warp] = make_float4(m, r, z, 0.f);
     __syncthreads();
     if (tid < D / 4) {
-      m = r = kNegInf;
+      m = kNegInf;
       z = 0.f;
 #pragma unroll
-      for (int w = 0; w < kMergeWarps; ++w) {
-        join(m, z, s_st[w].x, s_st[w].z);
-        r = fmaxf(r, s_st[w].y);
-      }
+      for (int w = 0; w < kMergeWarps; ++w) join(m, z, s_st[w].x, s_st[w].z);
+      const Peak of = peak_of<kMergeWarps>([&](int w) { return s_st[w]; });
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kMergeWarps; ++w) {
         const float4 a = *reinterpret_cast<const float4*>(&s_x[w][tid * 4]);
-        const float take = s_st[w].y == kNegInf ? 1.f : ex2(s_st[w].y - r);
+        const float take = s_st[w].x == kNegInf ? 1.f : ex2((s_st[w].x - of.top) + (s_st[w].y - of.ref));
         y.x += a.x * take, y.y += a.y * take, y.z += a.z * take, y.w += a.w * take;
       }
-      put_row(static_cast<T*>(p.out) + static_cast<int64_t>(row_out) * D + tid * 4, y, m, r, z);
+      put_row(static_cast<T*>(p.out) + static_cast<int64_t>(row_out) * D + tid * 4, y, of.ref, z);
     }
     return;
   }
