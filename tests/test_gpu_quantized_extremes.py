@@ -8,7 +8,7 @@ import torch
 
 import tiered_kv_cache_split_gb300 as t
 from operator_helpers import HALF, assert_within
-from quantized_helpers import PAGE
+from quantized_helpers import PAGE, attend_reference
 
 pytestmark = pytest.mark.gpu
 DT = {"f32": torch.float32, "bf16": torch.bfloat16}
@@ -80,3 +80,28 @@ def test_one_key_above_all_at_large_logits(dtype, sign, lens, g, d):
     assert_within(out, want, bound)
     assert_within(a, wa, wa * 2.0 ** -20, "alpha")
     assert torch.equal(c.attend(q, alpha=False)[0], out)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["both", "negative", "apart"])
+@pytest.mark.parametrize("lens,g,d", SHAPES)
+def test_scales_of_either_sign(dtype, kind, lens, g, d):
+    """A row's value is code * scale, whatever the scale's sign, and as read_quantized has it. The reference gets
+    the same values from scales above 0 and codes of the other sign."""
+    c = Rows(lens, 2, d, seed=7 + g + d)
+    size = np.exp(0.5 * c.rng.standard_normal(c.scales.shape)) / 64
+    if kind == "apart":                              # V's blocks up to 2^30 from each other
+        size[..., 1] = np.exp2(c.rng.uniform(-15, 15, size[..., 1].shape))
+    sign = c.rng.choice([-1, 1], c.scales.shape) if kind != "negative" else np.full(c.scales.shape, -1)
+    c.scales = (size * sign).astype(np.float32)
+    q = torch.from_numpy(c.rng.standard_normal((len(lens), 2 * g, d)).astype(np.float32)).to(DT[dtype]).cuda()
+    want, bound, wa, ab = attend_reference(q, c.codes * sign[..., None, None].astype(np.int8), np.abs(c.scales), c.table, c.masks, c.counts)
+    out, a = c.attend(q)
+    assert_within(out, want, bound)
+    assert_within(a, wa, ab, "alpha")
+    for b, n in enumerate(lens):
+        k, v = t.read_quantized(torch.from_numpy(c.codes).cuda(), torch.from_numpy(c.scales).cuda(), torch.from_numpy(c.table[b:b + 1]).cuda(), None, [n],
+                                dtype=torch.float32)
+        rows = c.codes[c.table[b, :c.counts[b]]].astype(np.float32) * c.scales[c.table[b, :c.counts[b]], :, :, None, None]
+        for x, j in ((k, 0), (v, 1)):
+            assert np.array_equal(x.cpu().numpy(), rows[:, :, j].transpose(0, 2, 1, 3).reshape(-1, 2, d)[:n])

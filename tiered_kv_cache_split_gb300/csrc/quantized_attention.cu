@@ -210,7 +210,8 @@ __device__ __forceinline__ float4 load_cluster(uint32_t at, int cta) {
 }
 
 // What a unit keeps of a page: id (-1: none of its slots counts), valid slots and
-// the power k of V's scale, K's scale in the logits' units, and V's scale as f in f 2^k.
+// the power k of V's scale, K's scale in the logits' units, and V's scale as f in f 2^k
+// (1 <= |f| < 2, of the scale's sign).
 __device__ __forceinline__ int4 page_info(const AttendParams& p, int32_t id, int h) {
   if (id < 0 || id >= p.p.pages) return make_int4(-1, 0, 0, 0);
   const uint32_t live = p.p.mask[id] & kFullMask;
@@ -218,11 +219,11 @@ __device__ __forceinline__ int4 page_info(const AttendParams& p, int32_t id, int
   const float2 s = *reinterpret_cast<const float2*>(p.p.scales + (static_cast<int64_t>(id) * p.p.hkv + h) * 2);
   float f = finite_or_nan(s.y);
   int k = -126;                                  // of 0 and NaN: no reference rises for them
-  if (f > 0.f) {
-    const bool small = f < 0x1p-100f;
+  if (fabsf(f) > 0.f) {
+    const bool small = fabsf(f) < 0x1p-100f;
     const uint32_t bits = __float_as_uint(small ? f * 0x1p40f : f);
-    k = static_cast<int>(bits >> 23) - 127 - (small ? 40 : 0);
-    f = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+    k = static_cast<int>(bits >> 23 & 0xffu) - 127 - (small ? 40 : 0);
+    f = __uint_as_float((bits & 0x807fffffu) | 0x3f800000u);
   }
   return make_int4(id, static_cast<int>(live | static_cast<uint32_t>(k + 256) << 16), __float_as_int(finite_or_nan(s.x) * p.qscale),
                    __float_as_int(f));
