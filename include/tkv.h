@@ -576,8 +576,9 @@ TKV_API tkv_status tkv_rotary_steps(int32_t n, const double* inv_freq, uint64_t*
 
 /* Writes new_lens[b] tokens behind the lens[b] of each row: slots lens[b] ..
  * lens[b] + new_lens[b] - 1 of the pages it lists, quantised per block:
- *   scale = max(absmax of the block's new tokens / 127, the block's scale if it
- *           holds earlier tokens (its slot 0 is not written by this call))
+ *   scale = absmax of the block's new tokens / 127, or the block's scale if it holds
+ *           earlier tokens (its slot 0 is not written by this call) and its scale
+ *           is at least as large in size
  *   code  = clamp(rint(x / scale), -127, 127); scale 0 gives codes 0
  * and where the scale of a block with earlier tokens grew, their codes become
  * rint(code * (old / new)): each growth costs them at most half a step more.

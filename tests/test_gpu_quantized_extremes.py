@@ -8,7 +8,7 @@ import torch
 
 import tiered_kv_cache_split_gb300 as t
 from operator_helpers import HALF, assert_within
-from quantized_helpers import PAGE, attend_reference
+from quantized_helpers import PAGE, Cache, attend_reference
 
 pytestmark = pytest.mark.gpu
 DT = {"f32": torch.float32, "bf16": torch.bfloat16}
@@ -105,3 +105,30 @@ def test_scales_of_either_sign(dtype, kind, lens, g, d):
         rows = c.codes[c.table[b, :c.counts[b]]].astype(np.float32) * c.scales[c.table[b, :c.counts[b]], :, :, None, None]
         for x, j in ((k, 0), (v, 1)):
             assert np.array_equal(x.cpu().numpy(), rows[:, :, j].transpose(0, 2, 1, 3).reshape(-1, 2, d)[:n])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -70])
+def test_append_behind_scales_below_zero(dtype, d, size):
+    """A block whose scale a caller made negative keeps its earlier tokens, whether the scale grows or not. The
+    twin holds the same values with scales above 0; rounding to even is the same on both sides of 0."""
+    hkv, pages, rng = 2, 24, np.random.default_rng(d)
+    codes = rng.integers(-127, 128, (pages, hkv, 2, PAGE, d)).astype(np.int8)
+    scales = (np.exp(rng.uniform(-3, 3, (pages, hkv, 2))) * size / 64).astype(np.float32)
+    sign = rng.choice([-1, 1], scales.shape)
+    twin = Cache(pages, hkv, d, codes * sign[..., None, None].astype(np.int8), scales, np.zeros(pages))
+    pool, s = torch.from_numpy(codes).cuda(), torch.from_numpy(scales * sign.astype(np.float32)).cuda()
+    mask, table = torch.zeros(pages, dtype=torch.int32).cuda(), torch.from_numpy(rng.permutation(pages).reshape(12, 2).astype(np.int32)).cuda()
+    lens, new = list(range(1, 13)), [1, 20, 3, 5, 1, 12, 9, 1, 2, 21, 1, 4]
+    k, v = (torch.from_numpy((rng.standard_normal((sum(new), hkv, d)) * size / 2).astype(np.float32)).to(DT[dtype]).cuda() for _ in range(2))
+    t.append_quantized(k, v, pool, s, table, mask, lens, new)
+    twin.append(k.float().cpu().numpy(), v.float().cpu().numpy(), table.tolist(), lens, new)
+    s = s.cpu().numpy()
+    assert np.array_equal(np.abs(s), twin.scales) and (s < 0).any() and (np.abs(s) > scales).any()
+    held = np.zeros((pages, PAGE), bool)              # the bytes of other slots stay, whatever becomes of their block's scale
+    for b in range(12):
+        held[table[b].cpu().numpy()] = (np.arange(2 * PAGE) < lens[b] + new[b]).reshape(2, PAGE)
+    got = pool.cpu().numpy() * np.sign(s)[..., None, None].astype(np.int8)
+    assert np.array_equal(got.transpose(0, 3, 1, 2, 4)[held], twin.codes.transpose(0, 3, 1, 2, 4)[held])
+    assert np.array_equal(mask.cpu().numpy(), twin.mask)

@@ -145,7 +145,7 @@ __device__ __forceinline__ CodeBytes to_codes(const float (&x)[N], float scale, 
 // A warp per block: the rows of the block that are written stay in registers
 // between the maximum and the codes, so K and V are read once; they are on their
 // way before the page id is here. Of a block that holds earlier tokens the scale only
-// grows; where it does, their codes are scaled to it. HBM bounds the large calls: 40959
+// grows in size; where it does, their codes are scaled to it. HBM bounds the large calls: 40959
 // tokens of 8 heads at d 128 in bf16 (168 MB in, 84 out) take 44 us, 5.8 TB/s, the
 // issue slots being 51 % busy; the least call 4 us.
 template <typename T, int D>
@@ -185,8 +185,9 @@ __global__ void __launch_bounds__(kCopyThreads) append_quantized_kernel(const __
   for (int i = 0; i < kPasses; ++i) top = max(top, top_bits(x[i], T()));
   top = __reduce_max_sync(0xffffffffu, top);
   const float mine = __uint_as_float(top) / 127.f;
-  const float grown = mine > old || mine != mine ? mine : old;  // a NaN stays
-  const bool finite = grown < INFINITY;
+  const bool grows = mine > fabsf(old);                         // a caller's pool may hold scales below 0
+  const float grown = grows || mine != mine ? mine : old;       // a NaN stays
+  const bool finite = fabsf(grown) < INFINITY;
   const float scale = finite ? grown : NAN;                     // every value of the block reads as NaN
   int8_t* codes = p.p.codes + block * kPage * D + c0;
   const float inverse = 1.f / scale;
@@ -197,13 +198,13 @@ __global__ void __launch_bounds__(kCopyThreads) append_quantized_kernel(const __
     if (!finite) b.w[0] = b.w[1] = 0;
     store_codes(reinterpret_cast<Codes*>(codes + (i * kRows + r0) * D), b);
   };
-  if (scale < kLeastScale) {
+  if (fabsf(scale) < kLeastScale) {
     // by division, whose quotients pass 127 where the scale itself was rounded down
 #pragma unroll 1
     for (int i = 0; i < kPasses; ++i)
 #pragma unroll 1
       for (int j = 0; j < V::n && written(i); ++j)
-        codes[(i * kRows + r0) * D + j] = scale > 0.f ? static_cast<int8_t>(fminf(fmaxf(rintf(to_float(from[i * stride + j]) / scale), -127.f), 127.f)) : 0;
+        codes[(i * kRows + r0) * D + j] = scale != 0.f ? static_cast<int8_t>(fminf(fmaxf(rintf(to_float(from[i * stride + j]) / scale), -127.f), 127.f)) : 0;
   } else if (whole) {
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) store(i);
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(kCopyThreads) append_quantized_kernel(const __
     for (int i = 0; i < kPasses; ++i)
       if ((i + 1) * kRows > t.lo && i * kRows < t.hi && written(i)) store(i);
   }
-  if (t.lo > 0 && scale > old && finite) {
+  if (t.lo > 0 && grows && finite) {
     const float ratio = old / scale;
     for (int s = r0; s < t.lo; s += kRows) {
       Codes* at = reinterpret_cast<Codes*>(codes + s * D);
