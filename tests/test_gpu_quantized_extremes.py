@@ -132,3 +132,35 @@ def test_append_behind_scales_below_zero(dtype, d, size):
     got = pool.cpu().numpy() * np.sign(s)[..., None, None].astype(np.int8)
     assert np.array_equal(got.transpose(0, 3, 1, 2, 4)[held], twin.codes.transpose(0, 3, 1, 2, 4)[held])
     assert np.array_equal(mask.cpu().numpy(), twin.mask)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("power", [-125, -123, -64, 64, 118, 126])
+@pytest.mark.parametrize("lens,g,d", SHAPES[1:4])
+def test_queries_and_scales_of_opposite_size(dtype, power, lens, g, d):
+    """Queries of 2^power and scales of 2^-power: the logits are ordinary ones."""
+    c = Rows(lens, 2, d, seed=11 + g + d)
+    c.scales[..., 0] = c.rng.integers(4, 8, c.scales[..., 0].shape) * np.exp2(-8.0 - power)
+    c.scales[..., 1] = np.exp(0.5 * c.rng.standard_normal(c.scales[..., 1].shape)) / 64
+    q = np.clip(c.rng.standard_normal((len(lens), 2 * g, d)), -1.9, 1.9) * 2.0 ** power
+    check(c, torch.from_numpy(q.astype(np.float32)).to(DT[dtype]).cuda())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,g,d", SHAPES[1:4])
+def test_the_largest_queries_and_subnormal_scales(dtype, lens, g, d):
+    """Scales of 3 to 7 times 2^-137, queries of up to 2^128: logits of up to some 12, all of whose products have one sign."""
+    c = Rows(lens, 2, d, seed=13 + g + d)
+    c.scales[..., 0] = c.rng.integers(3, 8, c.scales[..., 0].shape) * 2.0 ** -137
+    c.scales[..., 1] = 1 / 64
+    sign = c.rng.choice([-1, 1], d)
+    c.codes[:, :, 0] = c.rng.integers(40, 128, c.codes[:, :, 0].shape) * sign
+    q = c.rng.uniform(1.5, 1.99, (len(lens), 2 * g, d)) * 2.0 ** 127 * sign
+    check(c, torch.from_numpy(q.astype(np.float32)).to(DT[dtype]).cuda())
+
+
+def check(c, q):
+    want, bound, wa, ab = attend_reference(q, c.codes, c.scales, c.table, c.masks, c.counts)
+    out, a = c.attend(q)
+    assert_within(out, want, bound)
+    assert_within(a, wa, ab, "alpha")

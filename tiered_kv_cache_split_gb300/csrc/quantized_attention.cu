@@ -210,7 +210,7 @@ __device__ __forceinline__ float4 load_cluster(uint32_t at, int cta) {
 }
 
 // What a unit keeps of a page: id (-1: none of its slots counts), valid slots and
-// the power k of V's scale, K's scale in the logits' units, and V's scale as f in f 2^k
+// the power k of V's scale, K's scale, and V's scale as f in f 2^k
 // (1 <= |f| < 2, of the scale's sign).
 __device__ __forceinline__ int4 page_info(const AttendParams& p, int32_t id, int h) {
   if (id < 0 || id >= p.p.pages) return make_int4(-1, 0, 0, 0);
@@ -225,7 +225,7 @@ __device__ __forceinline__ int4 page_info(const AttendParams& p, int32_t id, int
     k = static_cast<int>(bits >> 23 & 0xffu) - 127 - (small ? 40 : 0);
     f = __uint_as_float((bits & 0x807fffffu) | 0x3f800000u);
   }
-  return make_int4(id, static_cast<int>(live | static_cast<uint32_t>(k + 256) << 16), __float_as_int(finite_or_nan(s.x) * p.qscale),
+  return make_int4(id, static_cast<int>(live | static_cast<uint32_t>(k + 256) << 16), __float_as_int(finite_or_nan(s.x)),
                    __float_as_int(f));
 }
 
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
 #pragma unroll
           for (int i = 0; i < kOwn; ++i) {
             const int of = __shfl_sync(0xffffffffu, e, (2 * t + i) * 4);
-            qpow[nt][i] = __uint_as_float(static_cast<uint32_t>(of + 127) << 23);  // infinity for a row that holds one
+            qpow[nt][i] = __uint_as_float(static_cast<uint32_t>(of + 127) << 23) * p.qscale;  // infinity for a row that holds one
             m[nt][i] = kNegInf;
             r[nt][i] = z[nt][i] = 0.f;
           }
@@ -452,8 +452,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
           }
 #pragma unroll
           for (int j = 0; j < kOwn; ++j) {
-            l[nt][j][0] = live0 ? s[nt][j] * sk * qpow[nt][j] : kNegInf;
-            l[nt][j][1] = live1 ? s[nt][2 + j] * sk * qpow[nt][j] : kNegInf;
+            // the factor below 1 first: no product leaves fp32's range but where the logit does, or is off by 2^-22
+            const bool up = qpow[nt][j] > 1.f;
+            const float first = up ? sk : qpow[nt][j], second = up ? qpow[nt][j] : sk;
+            l[nt][j][0] = live0 ? s[nt][j] * first * second : kNegInf;
+            l[nt][j][1] = live1 ? s[nt][2 + j] * first * second : kNegInf;
             const float over = fmaxf(l[nt][j][0], l[nt][j][1]) - m[nt][j];
             rise |= over > 1.f || over + k > r[nt][j] + 1.f;
           }
