@@ -159,6 +159,29 @@ def test_the_largest_queries_and_subnormal_scales(dtype, lens, g, d):
     check(c, torch.from_numpy(q.astype(np.float32)).to(DT[dtype]).cuda())
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,g,d", SHAPES[1:4])
+def test_an_infinite_query_element(dtype, lens, g, d):
+    """Logits that are all -inf give 0, one of +inf or of inf * 0 gives NaN; other heads get what
+    is theirs (not bit for bit what they were: the references of a page's heads are moved together, when one of them
+    passes its own, and their powers of two need not be whole)."""
+    c = Rows(lens, 2, d, seed=17 + g + d)
+    c.scales = (np.exp(0.5 * c.rng.standard_normal(c.scales.shape)) / 64).astype(np.float32)
+    c.codes[..., 0] = -np.abs(c.codes[..., 0]) - (c.codes[..., 0] == 0)     # element 0: codes below 0
+    c.codes[..., 1] = 0
+    q = torch.from_numpy(c.rng.standard_normal((len(lens), 2 * g, d)).astype(np.float32)).to(DT[dtype]).cuda()
+    exact, bound, _, _ = attend_reference(q, c.codes, c.scales, c.table, c.masks, c.counts)
+    keep = [h for h in range(2 * g) if h != 1]
+    for element, value, want in ((0, math.inf, 0.0), (0, -math.inf, math.nan), (1, math.inf, math.nan)):
+        p = q.clone()
+        p[:, 1, element] = value
+        out, a = c.attend(p)
+        assert torch.equal(out[:, 1], torch.full_like(out[:, 1], want)) if want == want else torch.isnan(out[:, 1]).all()
+        assert_within(out[:, keep], exact[:, keep], bound[:, keep])
+        if want == want:
+            assert (a[:, 0][torch.from_numpy(c.live).cuda()] >= 0).all() and torch.isfinite(a).all()
+
+
 def check(c, q):
     want, bound, wa, ab = attend_reference(q, c.codes, c.scales, c.table, c.masks, c.counts)
     out, a = c.attend(q)

@@ -385,7 +385,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attend_quantized_ke
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               y[j] = x[i + j] * down0 * down1;
-              if (kParts == 2 && part == 1) y[j] = (y[j] - __half2float(__float2half_rn(y[j]))) * 2048.f;
+              if (kParts == 2 && part == 1) {
+                const float rest = y[j] - __half2float(__float2half_rn(y[j]));
+                y[j] = rest == rest ? rest * 2048.f : 0.f;  // of an infinity or NaN the first part says it all
+              }
             }
             qf[nt][i >> 2][(i >> 1) & 1] = half2_bits(y[0], y[1]);
           }
