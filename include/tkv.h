@@ -603,8 +603,9 @@ TKV_API tkv_status tkv_append_quantized(int32_t rows, const int32_t* lens, const
 /* Reads slots first[b] .. lens[b] - 1 of each row back as packed K and V
  * [sum (lens - first)][Hkv][d] in dtype (code * scale in fp32, rounded once),
  * as tkv_prompt_attention takes them. Slots whose mask bit is 0 (slot_mask may
- * be NULL: none) and pages outside the pool read as zeros. first, lens: HOST
- * int32 [rows], 0 <= first <= len. */
+ * be NULL: none) and pages outside the pool read as zeros. k and v do not
+ * overlap, their rows are 16-byte aligned. first, lens: HOST int32 [rows],
+ * 0 <= first <= len. */
 TKV_API tkv_status tkv_read_quantized(int32_t rows, const int32_t* first, const int32_t* lens, int32_t n_kv_heads,
                                       int32_t head_dim, int32_t dtype, const int8_t* pool, const float* scales,
                                       int64_t pool_pages, const int32_t* page_table, int32_t max_pages,

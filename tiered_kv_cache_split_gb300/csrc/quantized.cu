@@ -366,6 +366,7 @@ tkv_status tkv_read_quantized(int32_t rows, const int32_t* first, const int32_t*
   if (int st = check_rows(&p.r, rows, first, lens, max_pages, &tokens)) return tkv_status(st);
   if (tokens == 0) return TKV_OK;
   if (int st = check_tokens(dtype, n_kv_heads, head_dim, k, k_stride, v, v_stride)) return tkv_status(st);
+  if (k == v) return tkv_status(report(TKV_ERR_INVALID_ARG, "k and v are the same"));
   p.k = k; p.v = v; p.k_stride = k_stride; p.v_stride = v_stride;
   const int64_t items = static_cast<int64_t>(p.r.page0[rows]) * n_kv_heads * 2;
   if (items > INT32_MAX) return tkv_status(report(TKV_ERR_INVALID_ARG, "more than 2^31 blocks in one call"));
