@@ -553,7 +553,8 @@ TKV_API tkv_status tkv_compact_sequences(void* pool, int32_t n_layers, int64_t p
 
 /* Rotary positions. Pair i of a head, elements (i, i + r/2) of its first
  * r = rotary_dim, or (2 i, 2 i + 1) if interleaved, turns by pos * f_i:
- *   a' = scale (a cos - b sin), b' = scale (b cos + a sin); inverse: by -pos * f_i.
+ *   a' = scale (a cos - b sin), b' = scale (b cos + a sin); inverse: by -pos * f_i
+ *   (and times scale all the same: there and back is scale^2).
  * Elements behind r pass unscaled. Angles are formed in 64-bit fixed point: off by
  * at most |pos| 2^-64 turns, so below fp32's own error up to |pos| = 2^33 and
  * consistent beyond; products and sums are fp32, rounded once.

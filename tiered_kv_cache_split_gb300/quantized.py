@@ -85,8 +85,10 @@ def rotate(q, k, positions, table, inverse=False, out=None, stream=None):
     q [tokens, Hq, d], k [tokens, Hkv, d] or None, in float32 or bfloat16, their
     tokens possibly strided, as views of a fused projection are; positions int32
     or int64 [tokens] on their device; table of rotary_table on it. inverse turns
-    back. out: (q_out, k_out) or None; a tensor of it may be the input itself (in
-    place) and overlaps no other way. Returns (q_out, k_out).
+    by the opposite angles; the table's scale multiplies then too, so that there
+    and back gives the input times scale^2. out: (q_out, k_out) or None; a tensor of
+    it may be the input itself (in place) and overlaps no other way. Returns
+    (q_out, k_out).
     """
     lib = L.load()
     n, hq, d, sq = _tokens(q, "q")
