@@ -547,7 +547,7 @@ TKV_API tkv_status tkv_compact_sequences(void* pool, int32_t n_layers, int64_t p
  * 8-bit pool:
  *   pool    device int8 [pool_pages][Hkv][2][16][d], 16-byte aligned: codes, K rows then V rows
  *   scales  device float [pool_pages][Hkv][2], 8-byte aligned: one per BLOCK (page, head, K or V)
- * A row's value is code * scale; pool_pages x Hkv <= 2^29, d 64 or 128. Page
+ * A row's value is code * scale, of either sign; pool_pages x Hkv <= 2^29, d 64 or 128. Page
  * table and slot masks are those of tkv_paged_attention. A listed page id
  * outside the pool is never accessed. */
 
@@ -602,9 +602,12 @@ TKV_API tkv_status tkv_append_quantized(int32_t rows, const int32_t* lens, const
                                         const int32_t* page_refs, int32_t* status, tkv_stream stream);
 
 /* Reads slots first[b] .. lens[b] - 1 of each row back as packed K and V
- * [sum (lens - first)][Hkv][d] in dtype (code * scale in fp32, rounded once),
- * as tkv_prompt_attention takes them. Slots whose mask bit is 0 (slot_mask may
- * be NULL: none) and pages outside the pool read as zeros. k and v do not
+ * [sum (lens - first)][Hkv][d] in dtype (code * scale in fp32, rounded once), row
+ * behind row. Slots whose mask bit is 0 (slot_mask may
+ * be NULL: none) and pages outside the pool read as zeros. For a prompt chunk behind
+ * cached tokens tkv_prompt_attention wants a row's cached keys directly ahead of its new
+ * ones: with one row, the new ones are written behind the rows read; with several, each row is
+ * read by a call of its own into its place. k and v do not
  * overlap, their rows are 16-byte aligned. first, lens: HOST int32 [rows],
  * 0 <= first <= len. */
 TKV_API tkv_status tkv_read_quantized(int32_t rows, const int32_t* first, const int32_t* lens, int32_t n_kv_heads,
@@ -623,6 +626,7 @@ TKV_API tkv_status tkv_read_quantized(int32_t rows, const int32_t* first, const 
  * At most 2^30 pages x KV heads (each counted for every 16 query heads of a KV
  * head, F32: 8, and with 8 more per sequence) in one call. Products have codes exact and queries
  * and weights in fp16 (F32: in two fp16 parts); logits, statistics and sums are fp32.
+ * A weight times V's scale below 2^-38 of a row's largest (F32: 2^-49) counts as 0.
  * A sequence without a valid slot, or whose logits are all -inf, gives 0. Empty
  * slots may hold any codes; a scale that is not finite counts as NaN and reaches exactly the sequences with a
  * valid slot in its block. */

@@ -146,8 +146,9 @@ __device__ __forceinline__ CodeBytes to_codes(const float (&x)[N], float scale, 
 // between the maximum and the codes, so K and V are read once; they are on their
 // way before the page id is here. Of a block that holds earlier tokens the scale only
 // grows in size; where it does, their codes are scaled to it. HBM bounds the large calls: 40959
-// tokens of 8 heads at d 128 in bf16 (168 MB in, 84 out) take 44 us, 5.8 TB/s, the
-// issue slots being 51 % busy; the least call 4 us.
+// tokens of 8 heads at d 128 in bf16 (168 MB in, 84 out) take 44 us, 5.7 TB/s, the
+// issue slots being 51 % busy; 20479 tokens in fp32 36 us, 5.8 TB/s; the least call 4 us, and
+// 4 more for a token in each of 64 rows whose blocks' scales all grow.
 template <typename T, int D>
 __global__ void __launch_bounds__(kCopyThreads) append_quantized_kernel(const __grid_constant__ AppendQParams p) {
   using V = Vec<T>;
@@ -245,7 +246,8 @@ struct ReadQParams {
 };
 
 // A warp per block, as the append's. 28296 tokens of 8 heads at d 128 to bf16 (58 MB in,
-// 116 out) take 28 us, 6.1 TB/s.
+// 116 out) take 31 us with inputs past the L2, 5.6 TB/s, and 28 in a row of calls on the same
+// ones; to fp32 50 us, 5.8 TB/s.
 template <typename T, int D>
 __global__ void __launch_bounds__(kCopyThreads) read_quantized_kernel(const __grid_constant__ ReadQParams p) {
   using V = Vec<T>;

@@ -19,16 +19,20 @@
 // The scale of K multiplies a page's logits. That of V multiplies its weights: a
 // weight is 2^((l - m) + (k + 13 - r)) f with V's scale f 2^k, m the running
 // maximum of the logits and r one of (l - m) + k, so that pages whose scales are
-// far apart lose nothing in fp16 (weights down to 2^-38 of the largest count). Z
+// far apart neither overflow fp16 nor crowd at its lower end: a row's weights, V's
+// scale among them, count down to 2^-38 of its largest (fp32: 2^-49, in two parts), with
+// all their bits from 2^-27 on, and are 0 below in every element. Z
 // sums 2^(l - m) as always. r is relative to m: a reference of l + k itself would lose k
 // to rounding from |l| = 2^24 on, and the output its scale. Both references rise only when
 // a logit passes them by more than 1 (a vote per page), so the shuffles and the
 // rescaling are rare.
 //
-// 4 x 131072 tokens of 8 KV heads at d 128 (1.07 GB) take 160 us, 6.7 TB/s, the rate of a
-// copy; the tensor pipe is 17 % busy and the issue slots 53 %. The benchmark's batch (152 MB, 32
-// sequences) takes 33 us without alpha and 41 with it, of which 5 are the start, when every CTA's
-// table, page and scale reads queue up, 2 the uneven end and 3 the joining launch.
+// 4 x 131072 tokens of 8 KV heads at d 128 (1.07 GB) take 166 us, 6.5 TB/s (a copy: 6.8);
+// the tensor pipe is 17 % busy and the issue slots 61 %. The benchmark's batch (152 MB, 32
+// sequences) takes 35 us without alpha and 42 with it, of which 5 are the start, when every CTA's
+// table, page and scale reads queue up, 2 the uneven end and 3 the joining launch. In fp32: 165, 42
+// and 48. Two column tiles (9 to 16 heads per KV head, fp32 5 to 8) at d 128 fill their 168
+// registers and spill 8 bytes (fp32 40) outside the loop over pages: 222 us (fp32 198) for 1.07 GB.
 #include <cuda_fp16.h>
 
 #include <algorithm>

@@ -66,8 +66,9 @@ __device__ __forceinline__ void form_turns(const RotateParams& p, int64_t token0
   }
 }
 
-// Rows of any alignment and pairs of any number: an element or a pair per thread (96 us where
-// vectors take 27, 8192 tokens of 40 heads in bf16).
+// Rows of any alignment and pairs of any number: an element or a pair per thread. 8192 tokens
+// of 40 heads at d 128 in bf16 take 123 us with rows off 16 bytes (vectors: 30) and 201 with 25
+// pairs, whose heads are 103 items of work instead of 64.
 template <typename T>
 __global__ void __launch_bounds__(kRotaryThreads) rotate_kernel(const __grid_constant__ RotateParams p) {
   __shared__ float2 s_turn[kTurns];
@@ -99,7 +100,8 @@ __global__ void __launch_bounds__(kRotaryThreads) rotate_kernel(const __grid_con
 // of pairs, or the two that hold them, or one that passes) and goes through the heads
 // of the CTA's tokens, 64 bytes on their way at a time; the first ones leave before
 // the sines are formed. HBM bounds it: 8192 tokens of 40 heads at d 128 in bf16,
-// 168 MB, take 27 us in a row of calls (6.3 TB/s; 25 at the rate of a copy). CTAs of
+// 168 MB, take 30 us with inputs past the L2 (5.5 TB/s; 25 at the rate of a copy), and 27 in a
+// row of calls on the same inputs, of which the L2 holds a part. CTAs of
 // 1024 vectors: with 2048 the second wave is short of CTAs (32 us, and 25 for 22 at
 // 1501 tokens of 64 heads in fp32), with 512 the sines weigh more (34 us).
 template <typename T, bool kInterleaved>

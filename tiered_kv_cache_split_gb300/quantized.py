@@ -16,7 +16,10 @@ from . import _lib as L
 from .operators import _DTYPES, _I32, _MASK, _On, _at, _dense, _ints, _no_gradient, _tokens
 
 _I8, _F32 = (torch.int8,), (torch.float32,)
-_SHORT_PAGES = 192     # 8 CTAs of a cluster with 24 pages each
+# Up to here (8 CTAs of a cluster with 24 pages each) a call is tried without scratch first. Where it needs
+# none that saves 2 us of 11; where it does after all (more than 16 query heads per KV head, fp32 8; many rows
+# whose logits leave shared memory) the attempt costs 1.5 to 2.5 us of 22.
+_SHORT_PAGES = 192
 
 
 def _like(on, x):
@@ -289,7 +292,6 @@ def quantized_attention(q, pool, scales, page_table, slot_mask, page_counts, out
         else:
             po = _dense(out, "out", (q.dtype,), dev, (batch, hq, d))
         c = _at(counts)
-        # short sequences mostly need no scratch: asking for its size first would take a quarter of the call
         if scratch is None and max(counts, default=0) <= _SHORT_PAGES:
             st = lib.tkv_quantized_attention(batch, hq, hkv, d, dt, pq, pp, ps, pages, pt, pm, c, max_pages, po, pa, None, 0, on.raw)
             if st == L.OK:
